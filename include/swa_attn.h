@@ -64,7 +64,9 @@ typedef enum swa_status {
   SWA_ERR_CUDA = 3,         /* a CUDA runtime/driver call failed                  */
   SWA_ERR_TIMEOUT = 4,      /* device: a bounded pipeline wait ran out            */
   SWA_ERR_WORKSPACE = 5,    /* workspace too small for this problem               */
-  SWA_ERR_DEVICE_CHECK = 6  /* device: a token id outside [0, vocab) was skipped  */
+  SWA_ERR_DEVICE_CHECK = 6  /* device: a token id outside [0, vocab) was skipped; in
+                               the rotary and decode calls also a position, slot,
+                               page, length or request that was refused           */
 } swa_status;
 
 /* Problem description shared by every call. */
@@ -367,6 +369,196 @@ swa_status swa_block_bwd(const swa_params* p, const swa_extras* ex, const swa_bl
                          const int32_t* tok, const void* dout, void* dx, float* dwq, float* dwk,
                          float* dwv, float* dwo, float* dgq, float* dgk, float* dve, void* workspace,
                          size_t ws_bytes, void* stream);
+
+/*
+ * Rotary positions as operators of their own. The _ex and block calls fuse
+ * one form of them (whole heads, channels c and c + d/2 paired, positions
+ * counted from 0); these calls build the tables that form reads, and rotate q
+ * and k in every form: of the whole head or its first `rot` channels, paired
+ * as two halves or side by side, at positions of the caller's. With a
+ * rotation of its own, the attention is called without rotary tables:
+ * swa_rope_apply, swa_attn_fwd, swa_attn_bwd, then swa_rope_apply with
+ * inverse = 1 on dq and dk (the rotation's transpose is its backward).
+ *
+ * swa_rope_tables writes, for the rows t = first .. first + rows - 1,
+ *   cos[t - first][c] = amplitude * cos(t * theta_c), sin likewise,
+ *   fp32 [rows][rot/2], 16-byte aligned, c < rot/2, theta_c = base^(-2c/rot),
+ * with the frequencies scaled for contexts longer than those trained on:
+ *   SWA_ROPE_PLAIN     as they are (factor is not read)
+ *   SWA_ROPE_LINEAR    theta_c / factor (positions interpolated)
+ *   SWA_ROPE_NTK       base * factor^(rot / (rot - 2)) in place of base
+ *   SWA_ROPE_BY_PARTS  (YaRN, Peng et al. 2023, "NTK-by-parts") a column
+ *                      that makes n = orig_len * theta_c / (2 pi) turns over
+ *                      the original context keeps theta_c for n >= fast, gets
+ *                      theta_c / factor for n <= slow, and in between the two
+ *                      mixed by (n - slow) / (fast - slow)
+ * Angles are reduced exactly in 64-bit fixed point: far positions are as
+ * accurate as near ones. Limits: rot a multiple of 16, 16 .. 128; base >= 1;
+ * factor >= 1; 0 <= slow < fast; first + rows < 2^31; amplitude 0 counts as 1
+ * (after a QK-norm a common amplitude cancels when whole heads are turned).
+ */
+#define SWA_ROPE_PLAIN 0
+#define SWA_ROPE_LINEAR 1
+#define SWA_ROPE_NTK 2
+#define SWA_ROPE_BY_PARTS 3
+typedef struct {
+  int rot;
+  int scaling;
+  double base, factor, orig_len, slow, fast, amplitude;
+} swa_rope_freq;
+swa_status swa_rope_tables(const swa_rope_freq* f, int first, int rows, float* cos, float* sin,
+                           void* stream);
+
+/*
+ * Rotary tables as the calls below read them: row t is position t. rot (a
+ * multiple of 16, at most d) channels are turned, the rest are left alone.
+ * interleaved 0: channel c < rot/2 pairs with c + rot/2; 1: 2c with 2c + 1.
+ * The pair (a, b) of column c becomes (a cos + b sin, b cos - a sin), as in
+ * swa_extras.
+ */
+typedef struct {
+  const float* cos;   /* fp32 [rows][rot/2], 16-byte aligned */
+  const float* sin;
+  int rows;
+  int rot;
+  int interleaved;
+} swa_rope;
+
+/*
+ * Rotates q [B, T, Hq, d] into q_out and k [B, T, Hkv, d] into k_out (each
+ * pair may be NULL, and an output may be its input: in place; any other
+ * overlap is undefined). Of p, B, T, Hq, Hkv and d are read (and all checked).
+ *   pos      int32 [B, T] positions, or NULL: row t of the sequence is position
+ *            t (then rows >= T). A token whose position is outside the tables
+ *            keeps its output rows as they were and is reported.
+ *   inverse  1: the transposed rotation, the backward of the forward's
+ *   workspace  at least its 256-byte header, where device checks are reported
+ *            (swa_attn_check_status); NULL: they are not
+ * Sums are fp32, rounded once to elem.
+ */
+swa_status swa_rope_apply(const swa_params* p, const swa_rope* r, const int32_t* pos, const void* q,
+                          const void* k, void* q_out, void* k_out, int inverse, void* workspace,
+                          size_t ws_bytes, void* stream);
+
+/*
+ * The decode path: the same attention for one new token per request, over a
+ * paged cache that holds keys (rotated and normed) and values (with their
+ * value embedding) in 4 bits. The pages have no counterpart of these calls:
+ * the script only trains.
+ *
+ * The cache is one buffer of swa_kv4_cache_size bytes, 16-byte aligned:
+ * [n_pages][Hkv][page/16] tiles of 18 d bytes, page a multiple of 16 tokens.
+ * A tile holds 16 consecutive tokens of one kv head:
+ *   8 d bytes  keys, token by token, d/2 bytes each
+ *   8 d bytes  values, token pair by token pair, d bytes each
+ *   d bytes    the keys' scales: [16 tokens][d/64] pairs (s, z) of bf16
+ *   d bytes    the values' scales, likewise
+ * A number n = 0..15 of 64-channel group g stands for s (n - 8) + z, where
+ *   s = bf16((max - min) / 15), z = bf16(min + 8 s) over the group,
+ *   n = floor((x - z) / s + 8.5) kept within 0..15, 8 where s = 0.
+ * (A group that holds an infinity or a NaN, or whose span overflows fp32, is
+ * held as NaN; steps below 1e-36 count as 0.) Low nibble first, the numbers of
+ * a row are in the order
+ *   keys    [j 0..3][g][i 0..15]:          channel 64 g + 16 j + i
+ *   values  [r 0..7][g][u 0..1][token of the pair][i 0..3]:
+ *                                          channel 64 g + 8 r + 4 u + i
+ * in which the attention's matrix instructions take them.
+ *
+ * A slot is page * (page size) + offset, int64; slot -1 is no slot: padding.
+ * Every number read from device memory (slots, pages, lengths, positions,
+ * token ids) is checked on the device: one out of range is reported in the
+ * workspace status word and skipped as stated, never followed. `workspace` of
+ * plan, append and read is as in swa_rope_apply.
+ */
+typedef struct {
+  void* data;
+  int n_pages;
+  int page;
+} swa_kv4_cache;
+size_t swa_kv4_cache_size(const swa_params* p, int n_pages, int page);
+
+/*
+ * The plan of a step: which pages the requests get, and where each new token
+ * goes, from the requests' lengths, without the host reading any of them.
+ * Request b holds lens[b] tokens and gets new_lens[b] more (NULL: one each).
+ *   table      int32 [B][max_pages], the pages of each request in order; the
+ *              first ceil(lens[b] / page) are read, new ones are written
+ *              behind them, and the rest is left as it was
+ *   free_pages int32 [n_free]; entries from *free_head on are free. Requests
+ *              take what they need from it in order.
+ *   slot (int64), pos, row (int32)  [n_tokens]: slot, position and request of
+ *              each new token, requests one after the other; behind the last
+ *              token slot = -1, pos = 0, row = -1. 16-byte aligned.
+ *   cu         int32 [B + 1]: first token of each request, and their number
+ *              (at most 2^31 - 1)
+ *   lens_out   int32 [B], head_out int32: lengths and list head afterwards
+ *              (not lens and free_head themselves, which every block reads)
+ * A request is refused, and reported, when the pages left do not suffice
+ * (requests behind it that need no page still go), when it would pass
+ * max_pages, when its tokens pass n_tokens, or when its numbers are negative
+ * (a negative count takes no tokens): its tokens get slot -1, its length and
+ * table row stay, and it takes no page (pos is 0 where it would pass the
+ * table row, or the length is negative). A page id outside [0, n_pages) gives
+ * slot -1 and is reported. Limits: B <= 8192, max_pages * page < 2^31.
+ */
+swa_status swa_kv4_plan(int n_pages, int page, int B, int max_pages, const int32_t* lens,
+                        const int32_t* new_lens, int32_t* table, const int32_t* free_pages, int n_free,
+                        const int32_t* free_head, int n_tokens, int64_t* slot, int32_t* pos,
+                        int32_t* row, int32_t* cu, int32_t* lens_out, int32_t* head_out,
+                        void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Puts new rows into the cache: k [B, T, Hkv, d] is rotated (r, NULL: not; at
+ * pos int32 [B, T], NULL: position t), normed and multiplied by gk as in
+ * swa_attn_fwd_ex; v gets its value embedding (ve, tok, ve_gate, or the
+ * learned gate of ex, as there; ex's own rotary tables must be NULL); both
+ * are quantised from fp32 into slot int64 [B, T]. Tokens with slot -1 are
+ * skipped; tokens with a slot outside the cache or (with r) a position
+ * outside the tables are skipped and reported; a token id outside [0, vocab)
+ * is reported and adds no embedding. Two tokens with the same slot in one
+ * call leave that slot's content undefined.
+ */
+swa_status swa_kv4_append(const swa_params* p, const swa_extras* ex, const swa_kv4_cache* c,
+                          const swa_rope* r, const void* k, const void* v, const float* gk,
+                          const void* ve, const int32_t* tok, const float* ve_gate,
+                          const int32_t* pos, const int64_t* slot, void* workspace, size_t ws_bytes,
+                          void* stream);
+
+/*
+ * The keys and values of slots, as the numbers they stand for (keys rotated
+ * and normed): k_out, v_out [B, T, Hkv, d] elem. Rows of slot -1, and of
+ * slots outside the cache (reported), are zero.
+ */
+swa_status swa_kv4_read(const swa_params* p, const swa_kv4_cache* c, const int64_t* slot, void* k_out,
+                        void* v_out, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Attention of one token per request: q [B, Hq, d] is the token at position
+ * lens[b] - 1 (whose key and value are in the cache already), rotated there
+ * (r, NULL: not), normed and multiplied by gq; it sees the cache's keys j with
+ * lens[b] - 1 - window <= j < lens[b] (window -1: all). p->T must be 1 and
+ * p->causal 1; window, softmax_scale and eps as in swa_attn_fwd.
+ *   table    int32 [B][max_pages]; entries behind ceil(lens[b] / page) and in
+ *            front of the window are not read
+ *   lens     int32 [B]; 0: the request's rows of o are 0 and of lse -infinity
+ *   o, lse   [B, Hq, d] elem, [B, Hq] fp32 (natural log)
+ *   ex       NULL, or its wait_limit_ns
+ * A length below 0 counts as 0, one above max_pages * page as that, one
+ * above the rotary tables' rows as 0; keys of a page outside [0, n_pages) are
+ * left out; all four are reported. Several query tokens of one request are as
+ * many rows of B, with the same table row and lengths one apart.
+ *
+ * The workspace (swa_kv4_workspace_size bytes, 256-byte aligned, passed to
+ * swa_kv4_workspace_init once before its first use) holds the status word and
+ * the partial results of long requests that several CTAs share. Calls on one
+ * stream may share it; calls that can overlap need one each.
+ */
+size_t swa_kv4_workspace_size(const swa_params* p, int page, int max_pages);
+swa_status swa_kv4_workspace_init(void* workspace, size_t ws_bytes, void* stream);
+swa_status swa_kv4_attn(const swa_params* p, const swa_extras* ex, const swa_kv4_cache* c,
+                        const swa_rope* r, const void* q, const float* gq, const int32_t* table,
+                        int max_pages, const int32_t* lens, void* o, float* lse, void* workspace,
+                        size_t ws_bytes, void* stream);
 
 /*
  * Synchronises `stream`, reads the workspace status word, clears it, and

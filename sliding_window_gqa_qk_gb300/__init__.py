@@ -31,6 +31,11 @@ __all__ = [
     "make_block_weights", "make_block_extras",
     "swa_attn_check_status", "swa_sssl_window", "swa_has_ve", "swa_strerror",
     "swa_build_info", "attention_forward", "attention_backward", "make_params",
+    "swa_rope", "swa_rope_freq", "swa_kv4_cache", "swa_rope_tables", "swa_rope_apply",
+    "swa_kv4_cache_size", "swa_kv4_plan", "swa_kv4_append", "swa_kv4_read",
+    "swa_kv4_workspace_size", "swa_kv4_workspace_init", "swa_kv4_attn",
+    "rope_tables", "rope_apply", "new_kv4_cache", "new_kv4_workspace", "kv4_plan", "kv4_append",
+    "kv4_read", "kv4_attention",
     "SWA_OK", "SWA_ERR_INVALID_ARG", "SWA_ERR_UNSUPPORTED", "SWA_ERR_CUDA", "SWA_ERR_TIMEOUT",
     "SWA_ERR_WORKSPACE", "SWA_ERR_DEVICE_CHECK", "SWA_REUSE_PROLOGUE", "SWA_BWD_STAGE_PRE",
     "SWA_BWD_STAGE_MAIN", "SWA_BWD_STAGE_POST",
@@ -82,6 +87,23 @@ class swa_block_weights(ctypes.Structure):
                 ("wv", ctypes.c_void_p), ("wo", ctypes.c_void_p)]
 
 
+class swa_rope(ctypes.Structure):
+    """Rotary tables of the rope and kv4 calls (see include/swa_attn.h)."""
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("rows", ctypes.c_int),
+                ("rot", ctypes.c_int), ("interleaved", ctypes.c_int)]
+
+
+class swa_rope_freq(ctypes.Structure):
+    """Frequencies of swa_rope_tables (see include/swa_attn.h)."""
+    _fields_ = [("rot", ctypes.c_int), ("scaling", ctypes.c_int)] + [
+        (n, ctypes.c_double) for n in ("base", "factor", "orig_len", "slow", "fast", "amplitude")]
+
+
+class swa_kv4_cache(ctypes.Structure):
+    """A 4-bit paged cache: device buffer, pages, tokens per page."""
+    _fields_ = [("data", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("page", ctypes.c_int)]
+
+
 _LIBS: dict = {}
 _vp = ctypes.c_void_p
 
@@ -122,6 +144,20 @@ def load(kind: str = "bf16") -> ctypes.CDLL:
     lib.swa_block_fwd.restype = ctypes.c_int
     lib.swa_block_bwd.argtypes = [P, R, W] + [_vp] * 15 + [ctypes.c_size_t, _vp]
     lib.swa_block_bwd.restype = ctypes.c_int
+    C, F, I, Z = (ctypes.POINTER(swa_kv4_cache), ctypes.POINTER(swa_rope), ctypes.c_int, ctypes.c_size_t)
+    for name, args in (
+            ("swa_rope_tables", [ctypes.POINTER(swa_rope_freq), I, I, _vp, _vp, _vp]),
+            ("swa_rope_apply", [P, F] + [_vp] * 5 + [I, _vp, Z, _vp]),
+            ("swa_kv4_plan", [I] * 4 + [_vp] * 4 + [I, _vp, I] + [_vp] * 7 + [Z, _vp]),
+            ("swa_kv4_append", [P, R, C, F] + [_vp] * 9 + [Z, _vp]),
+            ("swa_kv4_read", [P, C] + [_vp] * 4 + [Z, _vp]),
+            ("swa_kv4_workspace_init", [_vp, Z, _vp]),
+            ("swa_kv4_attn", [P, R, C, F, _vp, _vp, _vp, I] + [_vp] * 4 + [Z, _vp])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = I
+    for name, args in (("swa_kv4_cache_size", [P, I, I]), ("swa_kv4_workspace_size", [P, I, I])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = Z
     lib.swa_attn_check_status.argtypes = [_vp, _vp]
     lib.swa_attn_check_status.restype = ctypes.c_int
     lib.swa_sssl_window.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_char_p, ctypes.c_int]
@@ -322,6 +358,76 @@ def swa_block_bwd(p, ex, w, x, gq, gk, ve, tok, dout, dx, dwq, dwk, dwv, dwo, dg
         _ptr(dve), _ptr(ws), n, _stream(stream)))
 
 
+def make_rope(tables, interleaved: bool = False) -> Optional[swa_rope]:
+    """swa_rope from (cos, sin), fp32 device tensors [rows, rot/2]; None: none."""
+    if tables is None:
+        return None
+    cos, sin = tables
+    if cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.dim() != 2 or cos.shape != sin.shape:
+        raise ValueError("rotary tables are two fp32 tensors [rows, rot/2]")
+    return swa_rope(_ptr(cos), _ptr(sin), cos.shape[0], 2 * cos.shape[1], int(bool(interleaved)))
+
+
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def _ws_bytes(ws, ws_bytes):
+    return ws_bytes if ws_bytes is not None else (0 if ws is None else ws.numel())
+
+
+def swa_rope_tables(f: swa_rope_freq, first: int, rows: int, cos, sin, stream=None, kind: str = "bf16") -> int:
+    return int(load(kind).swa_rope_tables(ctypes.byref(f), int(first), int(rows), _ptr(cos), _ptr(sin), _stream(stream)))
+
+
+def swa_rope_apply(p, r, pos, q, k, q_out, k_out, inverse=0, ws=None, ws_bytes=None, stream=None, kind=None) -> int:
+    kind = kind or _kind_of(q if q is not None else k)
+    return int(load(kind).swa_rope_apply(
+        ctypes.byref(p), _ref(r), _ptr(pos), _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), int(inverse), _ptr(ws),
+        _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
+def swa_kv4_cache_size(p: swa_params, n_pages: int, page: int, kind: str = "bf16") -> int:
+    return int(load(kind).swa_kv4_cache_size(ctypes.byref(p), int(n_pages), int(page)))
+
+
+def swa_kv4_plan(n_pages, page, B, max_pages, lens, new_lens, table, free_pages, n_free, free_head, n_tokens, slot, pos,
+                 row, cu, lens_out, head_out, ws=None, ws_bytes=None, stream=None, kind: str = "bf16") -> int:
+    return int(load(kind).swa_kv4_plan(
+        n_pages, page, B, max_pages, _ptr(lens), _ptr(new_lens), _ptr(table), _ptr(free_pages), n_free, _ptr(free_head),
+        n_tokens, _ptr(slot), _ptr(pos), _ptr(row), _ptr(cu), _ptr(lens_out), _ptr(head_out), _ptr(ws),
+        _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
+def swa_kv4_append(p, ex, c, r, k, v, gk, ve, tok, ve_gate, pos, slot, ws=None, ws_bytes=None, stream=None,
+                   kind=None) -> int:
+    kind = kind or _kind_of(k)
+    return int(load(kind).swa_kv4_append(
+        ctypes.byref(p), _ref(ex), _ref(c), _ref(r), _ptr(k), _ptr(v), _ptr(gk), _ptr(ve), _ptr(tok), _ptr(ve_gate),
+        _ptr(pos), _ptr(slot), _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
+def swa_kv4_read(p, c, slot, k_out, v_out, ws=None, ws_bytes=None, stream=None, kind=None) -> int:
+    kind = kind or _kind_of(k_out)
+    return int(load(kind).swa_kv4_read(ctypes.byref(p), _ref(c), _ptr(slot), _ptr(k_out), _ptr(v_out), _ptr(ws),
+                                       _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
+def swa_kv4_workspace_size(p: swa_params, page: int, max_pages: int, kind: str = "bf16") -> int:
+    return int(load(kind).swa_kv4_workspace_size(ctypes.byref(p), int(page), int(max_pages)))
+
+
+def swa_kv4_workspace_init(ws, ws_bytes=None, stream=None, kind: str = "bf16") -> int:
+    return int(load(kind).swa_kv4_workspace_init(_ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
+def swa_kv4_attn(p, ex, c, r, q, gq, table, max_pages, lens, o, lse, ws, ws_bytes=None, stream=None, kind=None) -> int:
+    kind = kind or _kind_of(q)
+    return int(load(kind).swa_kv4_attn(
+        ctypes.byref(p), _ref(ex), _ref(c), _ref(r), _ptr(q), _ptr(gq), _ptr(table), int(max_pages), _ptr(lens),
+        _ptr(o), _ptr(lse), _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
 def swa_attn_check_status(ws, stream=None, kind: str = "bf16") -> int:
     return int(load(kind).swa_attn_check_status(_ptr(ws), _stream(stream)))
 
@@ -423,3 +529,273 @@ def attention_backward(q, k, v, gq, gk, o, lse, dO, *, window: int = -1, causal:
         _check(swa_attn_bwd_ex(p, ex, q, k, v, gq, gk, ve, tok, ve_gate, o, lse, dO, dq, dk, dv, dgq,
                                dgk, dve, ws, flags=flags, stream=stream), "swa_attn_bwd_ex")
     return out
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions and the decode path. These calls check types, shapes and
+# devices before they pass addresses on (the C ABI sees addresses only), run
+# on the device of their tensors, and allocate their outputs on the stream
+# they run on.
+# ---------------------------------------------------------------------------
+
+SWA_ROPE_PLAIN, SWA_ROPE_LINEAR, SWA_ROPE_NTK, SWA_ROPE_BY_PARTS = range(4)
+_SCALINGS = {"none": SWA_ROPE_PLAIN, "linear": SWA_ROPE_LINEAR, "ntk": SWA_ROPE_NTK, "by_parts": SWA_ROPE_BY_PARTS}
+
+
+class _on:
+    """Makes a device, and a stream if one is given, current for a call; does
+    nothing where they are current already."""
+    __slots__ = ("ctx",)
+
+    def __init__(self, device, stream):
+        self.ctx = []
+        if device.type != "cuda":
+            raise ValueError(f"the tensors are on {device}, not on a GPU")
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(device))
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            self.ctx.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+
+
+def _want(name, t, dtype, shape, device):
+    """Checks an argument of the calls below; None passes."""
+    if t is None:
+        return
+    if t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor on {device} is expected, got {t.dtype} on {t.device}"
+                         + ("" if t.is_contiguous() else ", not contiguous"))
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {shape} is expected, got {tuple(t.shape)}")
+
+
+def _elem(name, t):
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name}: bf16 or fp32 is expected, got {t.dtype}")
+
+
+def _want_rope(rope, device):
+    if rope is not None:
+        for name, t in zip(("rope cos", "rope sin"), rope):
+            _want(name, t, torch.float32, None, device)
+
+
+def _want_ws(ws, device):
+    if ws is not None:
+        _want("workspace", ws, torch.uint8, None, device)
+
+
+def rope_tables(rows: int, rot: int, *, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                orig_len: float = 0.0, slow: float = 1.0, fast: float = 32.0, amplitude: float = 1.0,
+                first: int = 0, device=None, stream=None):
+    """cos, sin = rope_tables(rows, rot, ...): fp32 tables [rows, rot/2] of the
+    rotary angles of positions first .. first + rows - 1, with the frequencies
+    scaled for long contexts ("none", "linear", "ntk", "by_parts": the latter
+    wants orig_len, the context trained on). They serve ``rope`` of
+    attention_forward (rot = d), of rope_apply and of the kv4 calls (first =
+    0 there: row t is position t)."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling: one of {sorted(_SCALINGS)} is expected, got {scaling!r}")
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with _on(device, stream):
+        cos = torch.empty(rows, rot // 2, dtype=torch.float32, device=device)
+        sin = torch.empty_like(cos)
+        f = swa_rope_freq(int(rot), _SCALINGS[scaling], base, factor, orig_len, slow, fast, amplitude)
+        _check(swa_rope_tables(f, first, rows, cos, sin), "swa_rope_tables")
+    return cos, sin
+
+
+def rope_apply(q, k, rope, *, pos=None, interleaved: bool = False, inverse: bool = False, out=None, workspace=None,
+               stream=None):
+    """q', k' = rope_apply(q, k, (cos, sin)): q [B, T, Hq, d] and k [B, T, Hkv,
+    d] (either may be None) turned by rotary tables [rows, rot/2], rot <= d,
+    at positions ``pos`` int32 [B, T] (None: t). ``inverse``: the transposed
+    rotation, which turns gradients of q', k' into those of q, k. ``out`` =
+    (q', k') may be (q, k): in place. ``workspace``: where positions outside
+    the tables are reported (swa_attn_check_status); their rows are not
+    written."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("rope_apply: q or k is expected")
+    _elem("q, k", x)
+    B, T, _, d = x.shape
+    dev = x.device
+    Hkv = k.shape[2] if k is not None else 1
+    Hq = q.shape[2] if q is not None else Hkv
+    qo, ko = (None, None) if out is None else out
+    for name, t, H in (("q", q, Hq), ("k", k, Hkv), ("out of q", qo, Hq), ("out of k", ko, Hkv)):
+        _want(name, t, x.dtype, (B, T, H, d), dev)
+    _want("pos", pos, torch.int32, (B, T), dev)
+    _want_rope(rope, dev)
+    _want_ws(workspace, dev)
+    p = make_params(B, T, Hq, Hkv, d)
+    with _on(dev, stream):
+        if q is not None and qo is None:
+            qo = torch.empty_like(q)
+        if k is not None and ko is None:
+            ko = torch.empty_like(k)
+        _check(swa_rope_apply(p, make_rope(rope, interleaved), pos, q, k, qo, ko, inverse, workspace), "swa_rope_apply")
+    return qo, ko
+
+
+def _cache_dims(cache):
+    """n_pages, Hkv, page, d of a cache tensor (new_kv4_cache)."""
+    if cache.dim() != 4 or cache.shape[3] not in (18 * 64, 18 * 128) or cache.dtype != torch.uint8 \
+            or not cache.is_contiguous():
+        raise ValueError("cache: a contiguous uint8 tensor [pages, Hkv, page / 16, 18 d] is expected, d 64 or 128")
+    return cache.shape[0], cache.shape[1], cache.shape[2] * 16, cache.shape[3] // 18
+
+
+def new_kv4_cache(n_pages: int, page: int, Hkv: int, d: int, device):
+    """A 4-bit paged cache of one layer, uint8 [n_pages, Hkv, page/16, 18 d]:
+    ``page`` (a multiple of 16) tokens of keys and values to a page. Zeroed."""
+    p = make_params(1, 1, Hkv, Hkv, d)
+    if swa_kv4_cache_size(p, n_pages, page) == 0:
+        raise SwaError(SWA_ERR_INVALID_ARG, "cache size")
+    return torch.zeros(n_pages, Hkv, page // 16, 18 * d, dtype=torch.uint8, device=device)
+
+
+def new_kv4_workspace(cache, B: int, Hq: int, *, max_pages: int, window: int = -1, kind: str = "bf16", stream=None):
+    """The workspace of kv4_attention for up to B requests of max_pages pages,
+    initialised. kind: "bf16" or "fp32", as q."""
+    _, Hkv, page, d = _cache_dims(cache)
+    p = make_params(B, 1, Hq, Hkv, d, window)
+    n = swa_kv4_workspace_size(p, page, max_pages, kind)
+    if n == 0:
+        raise SwaError(SWA_ERR_INVALID_ARG, "workspace size")
+    with _on(cache.device, stream):
+        ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
+        _check(swa_kv4_workspace_init(ws, n, None, kind), "workspace init")
+    return ws
+
+
+def kv4_plan(lens, new_lens, table, free_pages, free_head, *, page: int, n_pages: int, n_tokens: Optional[int] = None,
+             workspace=None, stream=None) -> dict:
+    """The plan of a serving step, on the GPU: request b holds lens[b] tokens
+    and gets new_lens[b] more (None: one each; all int32). Pages come from
+    free_pages[free_head:] (free_head int32 [1]) and are written into table
+    [B, max_pages] behind those it holds. Returns slot (int64), pos, row
+    (int32) of each new token [n_tokens] (the sum of new_lens, known to the
+    host; more is padding, slot -1), cu [B + 1], and lens and free_head
+    afterwards."""
+    dev = lens.device
+    if table.dim() != 2 or lens.dim() != 1:
+        raise ValueError("lens [B] and table [B, max_pages] are expected")
+    B = lens.shape[0]
+    _want("lens", lens, torch.int32, (B,), dev)
+    _want("new_lens", new_lens, torch.int32, (B,), dev)
+    _want("table", table, torch.int32, (B, table.shape[1]), dev)
+    _want("free_pages", free_pages, torch.int32, (free_pages.numel(),), dev)
+    _want("free_head", free_head, torch.int32, (1,), dev)
+    _want_ws(workspace, dev)
+    if n_tokens is None:
+        if new_lens is not None:
+            raise ValueError("n_tokens: the number of new tokens is expected with new_lens")
+        n_tokens = B
+    with _on(dev, stream):
+        slot = torch.empty(n_tokens, dtype=torch.int64, device=dev)
+        # one buffer for the int32 outputs: fewer allocations a step
+        pad = (n_tokens + 3) // 4 * 4
+        ints = torch.empty(2 * pad + 2 * B + 2, dtype=torch.int32, device=dev)
+        pos, row = ints[:n_tokens], ints[pad:pad + n_tokens]
+        cu, lens_out, head = ints[2 * pad:2 * pad + B + 1], ints[2 * pad + B + 1:-1], ints[-1:]
+        _check(swa_kv4_plan(n_pages, page, B, table.shape[1], lens, new_lens, table, free_pages, free_pages.numel(),
+                            free_head, n_tokens, slot, pos, row, cu, lens_out, head, workspace), "swa_kv4_plan")
+    return {"slot": slot, "pos": pos, "row": row, "cu": cu, "lens": lens_out, "free_head": head}
+
+
+def kv4_append(cache, k, v, slot, *, pos=None, rope=None, interleaved: bool = False, gk=None, eps: float = 1e-6,
+               ve=None, tok=None, ve_gate=None, ve_scale: float = 0.5, gate_x=None, gate_w=None, workspace=None,
+               stream=None) -> None:
+    """Writes new keys and values k, v [B, T, Hkv, d] (as projected: not yet
+    rotated, normed or mixed) into the cache at slot int64 [B, T]; -1 skips a
+    token. Rotary, QK-norm gain, value embedding and gate as in
+    attention_forward, with the rotation at pos int32 [B, T] (None: t)."""
+    n_pages, Hkv, page, d = _cache_dims(cache)
+    _elem("k", k)
+    dev, dt = cache.device, k.dtype
+    if k.dim() != 4:
+        raise ValueError("k: [B, T, Hkv, d] is expected")
+    B, T = k.shape[:2]
+    _want("k", k, dt, (B, T, Hkv, d), dev)
+    _want("v", v, dt, (B, T, Hkv, d), dev)
+    _want("slot", slot, torch.int64, (B, T), dev)
+    _want("pos", pos, torch.int32, (B, T), dev)
+    _want("gk", gk, torch.float32, (d,), dev)
+    vocab, ex = 0, None
+    if ve is not None:
+        vocab = ve.shape[0]
+        _want("ve", ve, dt, (vocab, Hkv * d), dev)
+        _want("tok", tok, torch.int32, (B, T), dev)
+        _want("ve_gate", ve_gate, torch.float32, (B, T, Hkv), dev)
+        if gate_w is not None:
+            _want("gate_w", gate_w, torch.float32, (Hkv, gate_w.shape[1]), dev)
+            if gate_x is None or gate_x.dtype != dt or gate_x.device != dev or gate_x.shape[:2] != (B, T):
+                raise ValueError(f"gate_x: a {dt} tensor [B, T, channels] on {dev} is expected")
+            ex = make_extras(None, gate_x, gate_w)
+    _want_rope(rope, dev)
+    _want_ws(workspace, dev)
+    p = make_params(B, T, Hkv, Hkv, d, eps=eps, ve_scale=ve_scale, vocab=vocab)
+    with _on(dev, stream):
+        _check(swa_kv4_append(p, ex, swa_kv4_cache(cache.data_ptr(), n_pages, page), make_rope(rope, interleaved), k, v,
+                              gk, ve, tok, ve_gate, pos, slot, workspace), "swa_kv4_append")
+
+
+def kv4_read(cache, slot, *, dtype=torch.bfloat16, workspace=None, stream=None):
+    """k, v = kv4_read(cache, slot): the rows that slot int64 [B, T] holds, as
+    ``dtype`` (bf16 or fp32) [B, T, Hkv, d]; keys are rotated and normed.
+    Rows of slot -1 are zero."""
+    n_pages, Hkv, page, d = _cache_dims(cache)
+    dev = cache.device
+    if slot.dim() != 2:
+        raise ValueError("slot: [B, T] is expected")
+    B, T = slot.shape
+    _want("slot", slot, torch.int64, (B, T), dev)
+    _want_ws(workspace, dev)
+    with _on(dev, stream):
+        k = torch.empty(B, T, Hkv, d, dtype=dtype, device=dev)
+        _elem("dtype", k)
+        v = torch.empty_like(k)
+        _check(swa_kv4_read(make_params(B, T, Hkv, Hkv, d), swa_kv4_cache(cache.data_ptr(), n_pages, page), slot, k, v,
+                            workspace), "swa_kv4_read")
+    return k, v
+
+
+def kv4_attention(cache, q, table, lens, *, rope=None, interleaved: bool = False, gq=None, window: int = -1,
+                  softmax_scale: float = 0.0, eps: float = 1e-6, workspace=None, stream=None):
+    """o, lse = kv4_attention(cache, q, table, lens): attention of one token
+    per request, q [B, Hq, d] (as projected), at position lens[b] - 1 over the
+    request's cached keys and values (its own among them), table int32 [B,
+    max_pages]. o as q; lse fp32 [B, Hq]. Rotary, gain, window and scale as in
+    attention_forward. ``workspace``: from new_kv4_workspace, kept by the
+    caller (one per stream); None: one for this call."""
+    n_pages, Hkv, page, d = _cache_dims(cache)
+    _elem("q", q)
+    dev = cache.device
+    if q.dim() != 3 or table.dim() != 2:
+        raise ValueError("q [B, Hq, d] and table [B, max_pages] are expected")
+    B, Hq = q.shape[:2]
+    _want("q", q, q.dtype, (B, Hq, d), dev)
+    _want("table", table, torch.int32, (B, table.shape[1]), dev)
+    _want("lens", lens, torch.int32, (B,), dev)
+    _want("gq", gq, torch.float32, (d,), dev)
+    _want_rope(rope, dev)
+    _want_ws(workspace, dev)
+    p = make_params(B, 1, Hq, Hkv, d, window, True, softmax_scale, eps)
+    with _on(dev, stream):
+        if workspace is None:
+            workspace = new_kv4_workspace(cache, B, Hq, max_pages=table.shape[1], window=window, kind=_kind_of(q))
+        o = torch.empty_like(q)
+        lse = torch.empty(B, Hq, dtype=torch.float32, device=dev)
+        _check(swa_kv4_attn(p, None, swa_kv4_cache(cache.data_ptr(), n_pages, page), make_rope(rope, interleaved), q, gq,
+                            table, table.shape[1], lens, o, lse, workspace), "swa_kv4_attn")
+    return o, lse

@@ -1,0 +1,452 @@
+// The paged cache of keys and values held in 4 bits: its layout, the plan of
+// a serving step (pages, slots, positions), the append that rotates, norms
+// and quantises new rows into it, and the read that turns rows back.
+//
+// Layout: [n_pages][Hkv][page / 16] tiles of 18 d bytes; a tile holds 16
+// consecutive tokens of one kv head:
+//   8 d   keys, token by token, d / 2 bytes each
+//   8 d   values, token pair by token pair, d bytes each
+//   d     16 x d / 64 pairs (s, z) of the keys, bf16
+//   d     16 x d / 64 pairs (s, z) of the values, bf16
+// A stored number n = 0..15 of a 64-channel group stands for s (n - 8) + z.
+// The order of the numbers inside a row is the one in which the attention's
+// matrix instructions take them, so that a lane's 16 bytes of a row are
+// exactly its operand registers (kv4_attn.cuh):
+//   keys    position (j, g, i) of a token's row: channel 64 g + 16 j + i,
+//           j = 0..3, i = 0..15;
+//   values  position (r, g, u, token of the pair, i) of a pair's row: channel
+//           64 g + 8 r + 4 u + i, r = 0..7, u = 0..1, i = 0..3. One token
+//           owns 16-bit pieces, so appends of neighbours never share a store.
+// Low nibble first throughout.
+#pragma once
+
+#include "common.cuh"
+#include "rope.cuh"
+#include "rowwise.cuh"
+
+namespace swa {
+namespace kv4 {
+
+constexpr int kTile = 16;    // tokens of a tile
+
+__host__ __device__ constexpr int tile_bytes(int d) { return 18 * d; }
+
+struct Cache {
+  uint8_t* data;
+  int n_pages, page, Hkv;
+};
+
+// The tile of `slot` (page * page size + offset) of kv head h.
+template <int D>
+__device__ __forceinline__ uint8_t* tile_of(const Cache& c, long long slot, int h) {
+  const long long pg = slot / c.page;
+  const int off = static_cast<int>(slot - pg * c.page);
+  return c.data + ((pg * c.Hkv + h) * (c.page / kTile) + off / kTile) * static_cast<long long>(tile_bytes(D));
+}
+
+// max / min that keep a NaN (fmaxf and fminf drop it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// Quantisation of a row held by RowMap<D> lanes. Per group of 64 channels:
+//   s = bf16((max - min) / 15),  z = bf16(min + 8 s),
+//   n = clamp(floor((x - z) / s + 8 + 1/2), 0, 15),   n = 8 where s = 0.
+// s and z are bf16 (not fp16): values are unnormalised and may pass fp16's
+// range; z is the group's centre rather than its minimum, which makes it
+// small and its rounding finer. A group that holds an infinity or a NaN, or
+// whose span overflows, gets s = z = NaN, so that it reads back as NaN.
+// The quotient comes from the fp32 reciprocal and is then settled by the
+// remainder x - z - n s, which fma gives exactly: values on the border
+// between two numbers (frequent: x, z and s are short bf16 numbers on plain
+// layers) go up, as the formula says, and not where a reciprocal's last bit
+// happens to put them.
+// ---------------------------------------------------------------------------
+// Steps below 1e-36 (whose reciprocal nears fp32's end) count as 0.
+constexpr float kFlatStep = 1e-36f;
+struct Group {
+  float s, z;
+};
+template <int D>
+__device__ __forceinline__ Group group_scale(const float (&x)[RowMap<D>::EPL]) {
+  constexpr int EPL = RowMap<D>::EPL;
+  constexpr int GL = 64 / EPL;   // lanes of a group
+  float lo = x[0], hi = x[0];
+#pragma unroll
+  for (int i = 1; i < EPL; ++i) {
+    lo = min_nan(lo, x[i]);
+    hi = max_nan(hi, x[i]);
+  }
+#pragma unroll
+  for (int o = GL / 2; o > 0; o >>= 1) {
+    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  Group g;
+  g.s = __bfloat162float(__float2bfloat16_rn((hi - lo) / 15.0f));
+  if (g.s < kFlatStep) g.s = 0.0f;
+  g.z = __bfloat162float(__float2bfloat16_rn(fmaf(8.0f, g.s, lo)));
+  if (!isfinite(g.s) || !isfinite(g.z)) g.s = g.z = __int_as_float(0x7fffffff);
+  return g;
+}
+__device__ __forceinline__ uint32_t quantise(float x, const Group& g, float inv, float half) {
+  const float v = x - g.z;
+  float n = rintf(v * inv);
+  const float r = fmaf(-n, g.s, v);
+  n += r >= half ? 1.0f : 0.0f;
+  n -= r < -half ? 1.0f : 0.0f;
+  n = fminf(fmaxf(n, -8.0f), 7.0f);   // a NaN becomes -8
+  return static_cast<uint32_t>(static_cast<int>(n) + 8);
+}
+// The lane's EPL numbers, four bits each, lowest channel lowest.
+template <int D>
+__device__ __forceinline__ uint32_t quantise_lane(const float (&x)[RowMap<D>::EPL], const Group& g) {
+  constexpr int EPL = RowMap<D>::EPL;
+  const bool flat = !(g.s > 0.0f);
+  const float inv = flat ? 0.0f : 1.0f / g.s, half = 0.5f * g.s;
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) w |= (flat ? 8u : quantise(x[i], g, inv, half)) << (4 * i);
+  return w;
+}
+
+// ---------------------------------------------------------------------------
+// Append
+// ---------------------------------------------------------------------------
+struct AppendArgs {
+  Cache c;
+  long long N;                         // tokens: B * T
+  int T;
+  float eps, ve_scale;
+  int vocab;
+  const elem_t* k; const elem_t* v;    // [N, Hkv, D]
+  const float* gk;
+  const elem_t* ve; const int32_t* tok; const float* gate;
+  const elem_t* gx; long long gx_stride; const float* gw; int gch;   // learned gate, gw NULL: none
+  const float* rcos; const float* rsin; int rows, rot, interleaved;  // rcos NULL: none
+  const int32_t* pos; const int64_t* slot;
+  uint32_t* status;                    // or NULL
+};
+
+// Lanes as in the other row-wise kernels: LPR lanes hold one row of D
+// channels, 16 bytes each, and a warp works on RPI rows (token, head) at a
+// time, key and value together.
+template <int D>
+__global__ void __launch_bounds__(kRowWarps * 32) append_kernel(const __grid_constant__ AppendArgs a) {
+  using M = RowMap<D>;
+  constexpr int EPL = M::EPL, NG = D / 64;
+  const int lane = threadIdx.x & 31, cl = lane % M::LPR, c0 = cl * EPL;
+  const int Hkv = a.c.Hkv;
+  const long long rows = a.N * Hkv;
+  const long long cap = static_cast<long long>(a.c.n_pages) * a.c.page;
+  float gk[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) gk[i] = a.gk ? a.gk[c0 + i] : 1.0f;
+  for (long long r0 = grid_warp() * M::RPI; r0 < rows; r0 += grid_warps() * M::RPI) {
+    const long long row = r0 + lane / M::LPR;
+    bool on = row < rows;
+    const long long n = on ? row / Hkv : 0;
+    const int h = static_cast<int>(on ? row - n * Hkv : 0);
+    const long long slot = on ? a.slot[n] : -1;
+    int p = 0;
+    uint32_t bad = 0;
+    if (on && a.rcos != nullptr) {
+      p = a.pos ? a.pos[n] : static_cast<int>(n % a.T);
+      if (slot >= 0 && (p < 0 || p >= a.rows)) bad = DEV_ERR_BOUNDS;
+    }
+    if (on && slot != -1 && (slot < 0 || slot >= cap)) bad = DEV_ERR_BOUNDS;
+    on = on && slot >= 0 && !bad;
+    float x[EPL], y[EPL];
+    {
+      const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+      unpack16(on ? ld16(a.k + row * D + c0) : z, x);
+      unpack16(on ? ld16(a.v + row * D + c0) : z, y);
+    }
+    // key: rotation, then RMSNorm
+    if (a.rcos != nullptr) {
+      const long long at = on ? static_cast<long long>(p) * (a.rot / 2) : 0;
+      rotate_lanes<D>(x, a.rcos + at, a.rsin + at, a.rot, a.interleaved, on);
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) ss = fmaf(x[i], x[i], ss);
+    ss = row_sum<M::LPR>(ss);
+    const float rstd = rsqrtf(ss / D + a.eps);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) x[i] = x[i] * rstd * gk[i];
+    // value: value-embedding mix
+    if (a.ve != nullptr) {
+      float gate = 1.0f;
+      if (a.gw != nullptr) {
+        float z = 0.f;
+        if (on) {
+          const elem_t* xr = a.gx + n * a.gx_stride;
+          for (int c = cl; c < a.gch; c += M::LPR) z = fmaf(a.gw[h * a.gch + c], to_f32(xr[c]), z);
+        }
+        gate = 2.0f / (1.0f + expf(-row_sum<M::LPR>(z)));
+      } else if (on && a.gate != nullptr) {
+        gate = a.gate[n * Hkv + h];
+      }
+      const int tok = on ? a.tok[n] : 0;
+      if (on && tok >= 0 && tok < a.vocab) {
+        float e[EPL];
+        unpack16(ld16(a.ve + (static_cast<long long>(tok) * Hkv + h) * D + c0), e);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) y[i] = fmaf(a.ve_scale * gate, e[i], y[i]);
+      } else if (on) {
+        bad |= DEV_ERR_TOKEN;
+      }
+    }
+    const Group gk4 = group_scale<D>(x), gv4 = group_scale<D>(y);
+    const uint32_t wk = quantise_lane<D>(x, gk4), wv = quantise_lane<D>(y, gv4);
+    if (bad && cl == 0 && a.status) atomicOr(a.status, bad);
+    if (!on) continue;
+    uint8_t* tile = tile_of<D>(a.c, slot, h);
+    const int t = static_cast<int>(slot % a.c.page) % kTile;
+    const int g = c0 / 64, x0 = c0 % 64;
+    // keys: nibble ((x / 16) NG + g) 16 + x % 16 of the row
+    const int nk = ((x0 / 16) * NG + g) * 16 + x0 % 16;
+    uint8_t* krow = tile + t * (D / 2);
+    // values: 16-bit piece (((x / 8) NG + g) 2 + (x / 4) % 2) 2 + token
+    uint16_t* vrow = reinterpret_cast<uint16_t*>(tile + 8 * D + (t / 2) * D);
+    const int pv = (((x0 / 8) * NG + g) * 2 + (x0 / 4) % 2) * 2 + (t & 1);
+    if constexpr (EPL == 8) {
+      reinterpret_cast<uint32_t*>(krow)[nk / 8] = wk;
+      vrow[pv] = static_cast<uint16_t>(wv);
+      vrow[pv + 2] = static_cast<uint16_t>(wv >> 16);
+    } else {
+      reinterpret_cast<uint16_t*>(krow)[nk / 4] = static_cast<uint16_t>(wk);
+      vrow[pv] = static_cast<uint16_t>(wv);
+    }
+    if (x0 == 0) {
+      uint32_t* sc = reinterpret_cast<uint32_t*>(tile + 16 * D);
+      sc[t * NG + g] = pack_bf16x2(gk4.s, gk4.z);
+      sc[(kTile + t) * NG + g] = pack_bf16x2(gv4.s, gv4.z);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Read: the rows of slots as the values they stand for.
+// ---------------------------------------------------------------------------
+struct ReadArgs {
+  Cache c;
+  long long N;
+  const int64_t* slot;
+  elem_t* k; elem_t* v;      // [N, Hkv, D]
+  uint32_t* status;          // or NULL
+};
+
+template <int D>
+__global__ void __launch_bounds__(kRowWarps * 32) read_kernel(const __grid_constant__ ReadArgs a) {
+  using M = RowMap<D>;
+  constexpr int EPL = M::EPL, NG = D / 64;
+  const int lane = threadIdx.x & 31, cl = lane % M::LPR, c0 = cl * EPL;
+  const int Hkv = a.c.Hkv;
+  const long long rows = a.N * Hkv;
+  const long long cap = static_cast<long long>(a.c.n_pages) * a.c.page;
+  for (long long row = grid_warp() * M::RPI + lane / M::LPR; row < rows; row += grid_warps() * M::RPI) {
+    const long long n = row / Hkv;
+    const int h = static_cast<int>(row - n * Hkv);
+    const long long slot = a.slot[n];
+    float x[EPL] = {}, y[EPL] = {};
+    if (slot >= 0 && slot < cap) {
+      const uint8_t* tile = tile_of<D>(a.c, slot, h);
+      const int t = static_cast<int>(slot % a.c.page) % kTile;
+      const int g = c0 / 64, x0 = c0 % 64;
+      const int nk = ((x0 / 16) * NG + g) * 16 + x0 % 16;
+      const uint8_t* krow = tile + t * (D / 2);
+      const uint16_t* vrow = reinterpret_cast<const uint16_t*>(tile + 8 * D + (t / 2) * D);
+      const int pv = (((x0 / 8) * NG + g) * 2 + (x0 / 4) % 2) * 2 + (t & 1);
+      uint32_t wk, wv;
+      if constexpr (EPL == 8) {
+        wk = reinterpret_cast<const uint32_t*>(krow)[nk / 8];
+        wv = vrow[pv] | static_cast<uint32_t>(vrow[pv + 2]) << 16;
+      } else {
+        wk = reinterpret_cast<const uint16_t*>(krow)[nk / 4];
+        wv = vrow[pv];
+      }
+      const uint32_t* sc = reinterpret_cast<const uint32_t*>(tile + 16 * D);
+      const uint32_t a0 = sc[t * NG + g], b0 = sc[(kTile + t) * NG + g];
+      const float ks = __uint_as_float(a0 << 16), kz = __uint_as_float(a0 & 0xFFFF0000u);
+      const float vs = __uint_as_float(b0 << 16), vz = __uint_as_float(b0 & 0xFFFF0000u);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        x[i] = fmaf(ks, static_cast<float>(static_cast<int>((wk >> (4 * i)) & 15u) - 8), kz);
+        y[i] = fmaf(vs, static_cast<float>(static_cast<int>((wv >> (4 * i)) & 15u) - 8), vz);
+      }
+    } else if (slot != -1 && cl == 0 && a.status) {
+      atomicOr(a.status, DEV_ERR_BOUNDS);
+    }
+    st16(a.k + row * D + c0, pack16(x));
+    st16(a.v + row * D + c0, pack16(y));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Plan of a step: request b holds lens[b] tokens and gets new_lens[b] more.
+//   held_b = ceil(lens_b / P), want_b = ceil((lens_b + new_b) / P) - held_b,
+//   off_b = sum of the wants before b; its new pages are
+//   free[head + off_b ..], its tokens' slots follow.
+// Every block does the whole scan itself (a few thousand requests at most,
+// two integers each, from L2) and keeps it in shared memory, so one launch
+// serves every token and no block waits on another.
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 512;
+constexpr int kPlanMaxB = 8192;      // 12 bytes of shared memory per request
+constexpr int kPlanTokens = 4;       // consecutive tokens of a thread
+
+struct PlanArgs {
+  int B, page, n_pages, max_pages, n_free, n_tokens;
+  const int32_t* lens; const int32_t* new_lens;    // new_lens NULL: one each
+  int32_t* table;                                  // [B][max_pages]
+  const int32_t* free_pages; const int32_t* head;
+  int64_t* slot; int32_t* pos; int32_t* row;       // [n_tokens]
+  int32_t* cu; int32_t* lens_out; int32_t* head_out;
+  uint32_t* status;
+};
+
+struct PlanReq {
+  int len, fresh, held, want;
+  bool ok;      // plausible, and fits its table row
+};
+__device__ __forceinline__ PlanReq plan_req(const PlanArgs& a, int b) {
+  PlanReq r;
+  r.len = a.lens[b];
+  r.fresh = a.new_lens ? a.new_lens[b] : 1;
+  const long long end = static_cast<long long>(r.len) + r.fresh;
+  r.ok = r.len >= 0 && r.fresh >= 0 && end <= static_cast<long long>(a.max_pages) * a.page;
+  r.fresh = r.fresh < 0 ? 0 : r.fresh;
+  r.held = r.ok ? (r.len + a.page - 1) / a.page : 0;
+  r.want = r.ok ? static_cast<int>((end + a.page - 1) / a.page) - r.held : 0;
+  return r;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgs a) {
+  extern __shared__ int plan_smem[];
+  int* s_cu = plan_smem;              // [B + 1], clamped to INT_MAX
+  int* s_off = plan_smem + a.B + 1;   // [B]: off_b, or -1 for a refused request
+  int* s_len = s_off + a.B;           // [B]
+  __shared__ long long s_wn[kPlanThreads / 32], s_ww[kPlanThreads / 32];
+  __shared__ unsigned long long s_head;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int per = (a.B + kPlanThreads - 1) / kPlanThreads;
+  const int b0 = tid * per < a.B ? tid * per : a.B, b1 = b0 + per < a.B ? b0 + per : a.B;
+  const int head = *a.head;
+  const long long avail = head >= 0 && head <= a.n_free ? a.n_free - head : 0;
+  long long sn = 0, sw = 0;
+  for (int b = b0; b < b1; ++b) {
+    const PlanReq r = plan_req(a, b);
+    sn += r.fresh;
+    sw += r.want;
+  }
+  long long en = sn, ew = sw;   // inclusive over the warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, en, o), y = __shfl_up_sync(0xffffffffu, ew, o);
+    if (lane >= o) { en += x; ew += y; }
+  }
+  if (lane == 31) { s_wn[wid] = en; s_ww[wid] = ew; }
+  if (tid == 0) s_head = 0;
+  __syncthreads();
+  for (int w = 0; w < wid; ++w) { en += s_wn[w]; ew += s_ww[w]; }
+  en -= sn;
+  ew -= sw;
+  uint32_t bad = head < 0 || head > a.n_free ? DEV_ERR_BOUNDS : 0u;
+  unsigned long long last = 0;   // pages given out
+  for (int b = b0; b < b1; ++b) {
+    const PlanReq r = plan_req(a, b);
+    const bool fits = r.ok && (r.want == 0 || ew + r.want <= avail) && en + r.fresh <= a.n_tokens;
+    if (!fits) bad |= DEV_ERR_BOUNDS;
+    s_cu[b] = static_cast<int>(en < INT32_MAX ? en : INT32_MAX);
+    s_off[b] = fits ? static_cast<int>(r.want ? ew : 0) : -1;
+    s_len[b] = r.len;
+    if (fits && r.want && static_cast<unsigned long long>(ew + r.want) > last) last = ew + r.want;
+    if (blockIdx.x == 0) {
+      a.cu[b] = s_cu[b];
+      a.lens_out[b] = fits ? r.len + r.fresh : r.len;
+    }
+    en += r.fresh;
+    ew += r.want;
+  }
+  if (last) atomicMax(&s_head, last);
+  if (b1 == a.B && b0 < a.B) s_cu[a.B] = static_cast<int>(en < INT32_MAX ? en : INT32_MAX);
+  if (a.B == 0 && tid == 0) s_cu[0] = 0;
+  __syncthreads();
+  if (blockIdx.x == 0 && tid == 0) {
+    a.cu[a.B] = s_cu[a.B];
+    *a.head_out = head + static_cast<int>(s_head);
+  }
+  // the new pages into the table: a warp a request
+  const int nw = gridDim.x * (kPlanThreads / 32);
+  for (int b = blockIdx.x * (kPlanThreads / 32) + wid; b < a.B; b += nw) {
+    if (s_off[b] < 0) continue;
+    const PlanReq r = plan_req(a, b);
+    for (int i = lane; i < r.want; i += 32) {
+      const int pg = a.free_pages[head + s_off[b] + i];
+      if (pg < 0 || pg >= a.n_pages) bad |= DEV_ERR_BOUNDS;
+      a.table[static_cast<long long>(b) * a.max_pages + r.held + i] = pg;
+    }
+  }
+  // tokens
+  const int total = s_cu[a.B];
+  const long long nt = (a.n_tokens + kPlanTokens - 1) / kPlanTokens;
+  for (long long u = static_cast<long long>(blockIdx.x) * kPlanThreads + tid; u < nt;
+       u += static_cast<long long>(gridDim.x) * kPlanThreads) {
+    const int i0 = static_cast<int>(u * kPlanTokens);
+    int b = -1;
+    long long slot[kPlanTokens];
+    int pos[kPlanTokens], row[kPlanTokens];
+#pragma unroll
+    for (int j = 0; j < kPlanTokens; ++j) {
+      const int i = i0 + j;
+      slot[j] = -1; pos[j] = 0; row[j] = -1;
+      if (i >= total || i >= a.n_tokens) continue;
+      if (b < 0) {   // the last request that begins at or before i
+        int lo = 0, hi = a.B - 1;
+        while (lo < hi) {
+          const int m = (lo + hi + 1) >> 1;
+          if (s_cu[m] <= i) lo = m; else hi = m - 1;
+        }
+        b = lo;
+      }
+      while (s_cu[b + 1] <= i) ++b;
+      const int len = s_len[b];
+      const long long t64 = static_cast<long long>(len) + (i - s_cu[b]);
+      const int t = len >= 0 && t64 < static_cast<long long>(a.max_pages) * a.page ? static_cast<int>(t64) : 0;
+      row[j] = b;
+      pos[j] = t;
+      if (s_off[b] < 0) continue;   // (a request that goes lies inside its row)
+      const int held = (len + a.page - 1) / a.page, pj = t / a.page;
+      const int pg = pj < held ? a.table[static_cast<long long>(b) * a.max_pages + pj]
+                               : a.free_pages[head + s_off[b] + (pj - held)];
+      if (pg >= 0 && pg < a.n_pages) slot[j] = static_cast<long long>(pg) * a.page + (t - pj * a.page);
+      else bad |= DEV_ERR_BOUNDS;
+    }
+    if (i0 + kPlanTokens <= a.n_tokens) {
+      longlong2* sp = reinterpret_cast<longlong2*>(a.slot + i0);
+      sp[0] = make_longlong2(slot[0], slot[1]);
+      sp[1] = make_longlong2(slot[2], slot[3]);
+      *reinterpret_cast<int4*>(a.pos + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      *reinterpret_cast<int4*>(a.row + i0) = make_int4(row[0], row[1], row[2], row[3]);
+    } else {
+      for (int j = 0; j < kPlanTokens && i0 + j < a.n_tokens; ++j) {
+        a.slot[i0 + j] = slot[j];
+        a.pos[i0 + j] = pos[j];
+        a.row[i0 + j] = row[j];
+      }
+    }
+  }
+  if (bad && a.status) atomicOr(a.status, bad);
+}
+
+}  // namespace kv4
+}  // namespace swa

@@ -966,7 +966,7 @@ const char* swa_strerror(swa_status s) {
     case SWA_ERR_CUDA: return "CUDA call failed";
     case SWA_ERR_TIMEOUT: return "a device pipeline wait ran out of time";
     case SWA_ERR_WORKSPACE: return "workspace too small";
-    case SWA_ERR_DEVICE_CHECK: return "device check failed (token id outside the table)";
+    case SWA_ERR_DEVICE_CHECK: return "device check failed (a token id, position, slot, page or length out of range)";
   }
   return "unknown status";
 }
@@ -980,3 +980,5 @@ const char* swa_build_info(void) {
 }
 
 }  // extern "C"
+
+#include "decode_api.cuh"
