@@ -55,6 +55,36 @@ int flat_grid(long long items, long long per, long long cap) {
 
 constexpr int kKv4BlocksPerSm = 8;
 
+// Workspace of the decode attention: header, counters of finished chunks,
+// partial results. There are at most B * Hq <= 65535 counters, and the
+// initialisation zeroes room for all of them (or the whole of a smaller one).
+constexpr size_t kKv4Zeroed = 256 + 65536 * sizeof(unsigned);
+struct Kv4Ws {
+  size_t count, part, end;
+};
+Kv4Ws kv4_ws(const kv4::AttnSplit& s, int d) {
+  Kv4Ws w;
+  w.count = 256;
+  w.part = align256(w.count + static_cast<size_t>(s.items) * sizeof(unsigned));
+  w.end = s.splits > 1 ? align256(w.part + static_cast<size_t>(s.items) * s.splits * s.heads * (d + 2) * sizeof(float)) : w.part;
+  return w;
+}
+
+template <int D, int NT, bool kPolled>
+swa_status launch_attn(const kv4::AttnArgs& a, int heads_kv, cudaStream_t st) {
+  auto kern = kv4::attn_kernel<D, NT, kPolled>;
+  constexpr int smem = kv4::AttnSmem<D, NT>::bytes;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return SWA_ERR_CUDA;
+  kern<<<dim3(a.splits, heads_kv * a.groups, a.B), kv4::kAttnWarps * 32, smem, st>>>(a);
+  return launched();
+}
+template <bool kPolled>
+swa_status launch_attn(const kv4::AttnArgs& a, int d, int heads, int heads_kv, cudaStream_t st) {
+  if (d == 64)
+    return heads == kv4::kColQ ? launch_attn<64, 1, kPolled>(a, heads_kv, st) : launch_attn<64, 2, kPolled>(a, heads_kv, st);
+  return heads == kv4::kColQ ? launch_attn<128, 1, kPolled>(a, heads_kv, st) : launch_attn<128, 2, kPolled>(a, heads_kv, st);
+}
+
 template <typename F64, typename F128>
 void by_head_dim(int d, F64 f64, F128 f128) {
   if (d == 64) f64(); else f128();
@@ -255,11 +285,14 @@ size_t swa_kv4_workspace_size(const swa_params* p, int page, int max_pages) {
   if (check_params(p) != SWA_OK || check_pages(1, page) != SWA_OK || max_pages < 1 ||
       static_cast<long long>(max_pages) * page > INT32_MAX)
     return 0;
-  return 256;
+  return kv4_ws(kv4::attn_split(p->B, p->Hq, p->Hkv, page, max_pages, p->window), p->d).end;
 }
 
 swa_status swa_kv4_workspace_init(void* workspace, size_t ws_bytes, void* stream) {
-  return swa_attn_workspace_init(workspace, ws_bytes, stream);
+  if (workspace == nullptr || !aligned(workspace, 256) || ws_bytes < 256) return SWA_ERR_INVALID_ARG;
+  const size_t n = ws_bytes < kKv4Zeroed ? ws_bytes : kKv4Zeroed;
+  if (cudaMemsetAsync(workspace, 0, n, static_cast<cudaStream_t>(stream)) != cudaSuccess) return SWA_ERR_CUDA;
+  return SWA_OK;
 }
 
 swa_status swa_kv4_attn(const swa_params* p, const swa_extras* ex, const swa_kv4_cache* c, const swa_rope* r,
@@ -275,7 +308,9 @@ swa_status swa_kv4_attn(const swa_params* p, const swa_extras* ex, const swa_kv4
   if (ex != nullptr && (ex->rope_cos != nullptr || ex->rope_sin != nullptr)) return SWA_ERR_INVALID_ARG;
   if (max_pages < 1 || static_cast<long long>(max_pages) * c->page > INT32_MAX) return SWA_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, 256)) return SWA_ERR_INVALID_ARG;
-  if (ws_bytes < swa_kv4_workspace_size(p, c->page, max_pages)) return SWA_ERR_WORKSPACE;
+  const kv4::AttnSplit sp = kv4::attn_split(p->B, p->Hq, p->Hkv, c->page, max_pages, p->window);
+  const Kv4Ws w = kv4_ws(sp, p->d);
+  if (ws_bytes < w.end) return SWA_ERR_WORKSPACE;
   if (p->B == 0) return SWA_OK;
   if (!tensor_ok(q) || !tensor_ok(o) || lse == nullptr || table == nullptr || lens == nullptr) return SWA_ERR_INVALID_ARG;
   if (!aligned(lse, 4) || !aligned(table, 4) || !aligned(lens, 4)) return SWA_ERR_INVALID_ARG;
@@ -290,11 +325,13 @@ swa_status swa_kv4_attn(const swa_params* p, const swa_extras* ex, const swa_kv4
   a.table = table; a.lens = lens;
   a.o = static_cast<elem_t*>(o); a.lse = lse;
   a.status = static_cast<uint32_t*>(workspace);
+  a.chunk = sp.chunk; a.splits = sp.splits; a.groups = sp.groups;
+  a.count = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(workspace) + w.count);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.part);
+  a.wait_limit_ns = ex != nullptr && ex->wait_limit_ns != 0 ? ex->wait_limit_ns : kWaitLimitNs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int grid = (p->B * p->Hq + 3) / 4;
-  by_head_dim(p->d, [&] { kv4::attn_kernel<64><<<grid, 128, 0, st>>>(a); },
-              [&] { kv4::attn_kernel<128><<<grid, 128, 0, st>>>(a); });
-  return launched();
+  return a.wait_limit_ns < kPollBelowNs ? launch_attn<true>(a, p->d, sp.heads, p->Hkv, st)
+                                        : launch_attn<false>(a, p->d, sp.heads, p->Hkv, st);
 }
 
 }  // extern "C"

@@ -1,94 +1,550 @@
 // Attention of one new token per request over the 4-bit paged cache.
+//
+// o = sum_j p_j v_j / sum_j p_j, p_j = exp(scale <q, k_j>): each key and value
+// is read once, so the bytes of the cache bound it, and everything else has
+// to stay below what a tile's 18 D bytes cost the memory (about 100 clocks of
+// an SM at D = 128).
+//
+// What that asks for, and what is done:
+//   - Loads. A tile (16 tokens of one kv head, keys, values and scales) is
+//     one contiguous block, fetched by one bulk copy into the warp's own ring
+//     of kStages buffers: no registers and no address arithmetic are spent on
+//     bytes in flight. A warp walks its tiles alone; the warps of a CTA meet
+//     only at the end.
+//   - Products. Per 4-bit number one multiply-add for every query head of the
+//     group is more than the fp32 units have time for, so both products run
+//     on matrix instructions with the cache as the 16-row operand: S^T = K Q^T
+//     (16 keys x 8 columns) and O^T += V^T P^T (16 channels x 8 columns). The
+//     operand registers are made straight from the numbers' bits: (x & 15) |
+//     0x6400 is the fp16 number 1024 + n (0x4300: bf16, 128 + n), and one
+//     exact subtraction leaves n - 8. The cache's order of numbers makes a
+//     lane's 16 bytes of a row exactly its operand registers, so there is no
+//     exchange between lanes. (tcgen05 takes its operands from shared or
+//     tensor memory: the converted tiles, four times the bytes, would have to
+//     be written there first, and its 128-row tiles would hold 8 useful
+//     columns as well.)
+//   - Precision. A group has few query heads, so the eight columns hold four
+//     heads as two terms each: q as fp16 hi + lo (scaled by a power of two
+//     into fp16's range), P as bf16 hi + lo (bf16, because P times a step has
+//     any size). Products of n - 8 with them are exact in the accumulators;
+//     the second terms cost nothing where a group has at most four heads.
+//   - Scales. s and z of a (token, 64 channels) leave the products:
+//     <q, k> = sum_g s_g <q, n - 8>_g + z_g sum(q)_g, and sum_j p_j v_j =
+//     sum_j (p_j s_j) (n_j - 8) + sum_j p_j z_j, the last one number per group.
+//   - Softmax. The running maximum is raised only when a logit passes it by
+//     2^8 (in base 2), which a vote of the warp finds out: the reduction over
+//     lanes and the rescaling are left out of nearly every tile.
+//   - Few requests. A request's tiles are split into chunks of one CTA each;
+//     with more than one, each writes its partial result, and the CTA that
+//     finishes last joins them in the order of the chunks.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "kv4.cuh"
 
 namespace swa {
 namespace kv4 {
 
+constexpr int kAttnWarps = 4;
+constexpr int kStages = 4;               // tiles in flight per warp
+constexpr int kColQ = 4;                 // query heads of one 8-column operand
+constexpr int kAttnCtas = 152 * 8;       // CTAs aimed at: two rounds of the four a GB300's SM holds
+constexpr int kMinChunk = 16, kMaxChunk = 128;   // tiles of a CTA
+
 struct AttnArgs {
   Cache c;
-  int B, Hq, max_pages, window;        // window < 0: none
+  int B, Hq, max_pages, window;          // window < 0: none
   float scale, eps;
-  const elem_t* q;                     // [B, Hq, D]
+  const elem_t* q;                       // [B, Hq, D]
   const float* gq;
   const float* rcos; const float* rsin; int rows, rot, interleaved;   // rcos NULL: none
   const int32_t* table; const int32_t* lens;
-  elem_t* o; float* lse;               // [B, Hq, D], [B, Hq]
+  elem_t* o; float* lse;                 // [B, Hq, D], [B, Hq]
+  int chunk, splits;                     // tiles of a CTA, CTAs of a request
+  int groups;                            // CTAs that share a kv head's query heads
+  unsigned* count;                       // [B * Hkv * groups] finished chunks, 0 between calls
+  float* part;                           // [B * Hkv * groups][splits][heads][D + 2]: O, M, L
   uint32_t* status;
+  uint64_t wait_limit_ns;
 };
 
-// One warp per query head, a key at a time.
 template <int D>
-__global__ void __launch_bounds__(128) attn_kernel(const __grid_constant__ AttnArgs a) {
-  constexpr int NG = D / 64, E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int item = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (item >= a.B * a.Hq) return;
-  const int b = item / a.Hq, hq = item - b * a.Hq, G = a.Hq / a.c.Hkv, h = hq / G;
-  int len = a.lens[b];
+struct AttnShape {
+  static constexpr int TB = tile_bytes(D);
+  static constexpr int NG = D / 64;
+  static constexpr int W = D / 32;       // 32-bit words of a lane's piece of a row
+};
+
+// Shared memory of a CTA: rings (re-used for the join), queries, barriers.
+template <int D, int NT>
+struct AttnSmem {
+  static constexpr int ring = kAttnWarps * kStages * AttnShape<D>::TB;
+  static constexpr int join = kAttnWarps * NT * kColQ * (D + 2) * 4;
+  static constexpr int bars = (ring > join ? ring : join + 127) / 128 * 128;
+  static constexpr int qs = bars + kAttnWarps * kStages * 8;
+  static constexpr int qf = qs + NT * kColQ * 2 * D * 2;        // fp16 hi, lo rows
+  static constexpr int flags = qf + NT * kColQ * 4 * 4;         // factor, sums per group
+  static constexpr int bytes = flags + 16;
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 8x8 transpose of 16-bit elements across the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+// Eight numbers of a word as four fp16 pairs (number i, number i + 4) - 8.
+__device__ __forceinline__ void widen_f16(uint32_t x, uint32_t (&h)[4]) {
+  const __half2 low = __floats2half2_rn(-1032.f, -1032.f), sixteenth = __floats2half2_rn(0.0625f, 0.0625f),
+                high = __floats2half2_rn(-72.f, -72.f);
+  auto h2 = [](uint32_t v) { return *reinterpret_cast<__half2*>(&v); };
+  auto u = [](__half2 v) { return *reinterpret_cast<uint32_t*>(&v); };
+  const uint32_t y = x >> 8;
+  h[0] = u(__hadd2(h2((x & 0x000F000Fu) | 0x64006400u), low));                  // 1024 + n
+  h[1] = u(__hfma2(h2((x & 0x00F000F0u) | 0x64006400u), sixteenth, high));     // 1024 + 16 n
+  h[2] = u(__hadd2(h2((y & 0x000F000Fu) | 0x64006400u), low));
+  h[3] = u(__hfma2(h2((y & 0x00F000F0u) | 0x64006400u), sixteenth, high));
+}
+// The same as bf16 (whose 7 fraction bits leave no place for the second form).
+__device__ __forceinline__ void widen_bf16(uint32_t x, uint32_t (&h)[4]) {
+  const __nv_bfloat162 off = __floats2bfloat162_rn(-136.f, -136.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t v = ((x >> (4 * i)) & 0x000F000Fu) | 0x43004300u;                  // 128 + n
+    const __nv_bfloat162 r = __hadd2(*reinterpret_cast<__nv_bfloat162*>(&v), off);
+    h[i] = *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+
+template <int W>
+__device__ __forceinline__ void ld_words(const uint8_t* p, uint32_t (&w)[W]) {
+  if constexpr (W == 4) {
+    const uint4 t = *reinterpret_cast<const uint4*>(p);
+    w[0] = t.x; w[1] = t.y; w[2] = t.z; w[3] = t.w;
+  } else {
+    const uint2 t = *reinterpret_cast<const uint2*>(p);
+    w[0] = t.x; w[1] = t.y;
+  }
+}
+// The (s, z) pairs of one token, NG groups.
+template <int NG>
+__device__ __forceinline__ void ld_scales(const uint8_t* p, float (&s)[NG], float (&z)[NG]) {
+  uint32_t w[NG];
+  if constexpr (NG == 2) {
+    const uint2 t = *reinterpret_cast<const uint2*>(p);
+    w[0] = t.x; w[1] = t.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    s[g] = __uint_as_float(w[g] << 16);
+    z[g] = __uint_as_float(w[g] & 0xFFFF0000u);
+  }
+}
+
+// A query row by one warp: rotation, norm, gain, softmax scale and log2 e, a
+// power of two that brings the largest entry into [2^13, 2^14), and the two
+// fp16 terms, into shared memory; f[0] = the inverse power, f[1 + g] = the
+// sum over group g. x == NULL: a row of zeros.
+template <int D>
+__device__ __forceinline__ void query_row(const AttnArgs& a, const elem_t* q, int pos, __half* dst, float* f) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, c0 = lane * E;
+  float x[E] = {}, ss = 0.f;
+  if (q != nullptr) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int c = c0 + i;
+      x[i] = to_f32(q[c]);
+      if (a.rcos != nullptr && c < a.rot) {
+        const int half = a.rot / 2;
+        const int col = a.interleaved ? c / 2 : (c < half ? c : c - half);
+        const int to = a.interleaved ? c ^ 1 : (c < half ? c + half : c - half);
+        const bool first = a.interleaved ? (c & 1) == 0 : c < half;
+        const long long at = static_cast<long long>(pos) * half + col;
+        x[i] = fmaf(x[i], a.rcos[at], (first ? 1.f : -1.f) * to_f32(q[to]) * a.rsin[at]);
+      }
+      ss = fmaf(x[i], x[i], ss);
+    }
+  }
+  const float mul = rsqrtf(warp_sum(ss) / D + a.eps) * (a.scale * 1.4426950408889634f);
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    x[i] *= mul * (a.gq ? a.gq[c0 + i] : 1.0f);
+    if (q == nullptr) x[i] = 0.f;
+    top = fmaxf(top, fabsf(x[i]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  // exponent of top, kept where both the power and its inverse are normal
+  int e = static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127;
+  e = e < -100 ? -100 : (e > 100 ? 100 : e);
+  const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23);
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const float v = x[i] * up;
+    const __half hi = __float2half_rn(v);
+    const __half lo = __float2half_rn(v - __half2float(hi));
+    dst[c0 + i] = hi;
+    dst[D + c0 + i] = lo;
+    sum += v;
+  }
+  // lanes of one group: 64 / E
+#pragma unroll
+  for (int o = 32 / E; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) {
+    f[0] = __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23);
+    f[1] = sum;
+  }
+  if (D == 128 && lane == 16) f[2] = sum;
+}
+
+template <int D, int NT, bool kPolled>
+__global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 ? 4 : 2) attn_kernel(const __grid_constant__ AttnArgs a) {
+  using S = AttnShape<D>;
+  using M = AttnSmem<D, NT>;
+  constexpr int NG = S::NG, W = S::W, NQ = NT * kColQ;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int r = lane >> 2, j = lane & 3;
+  const int b = blockIdx.z, h = blockIdx.y / a.groups, qg = blockIdx.y - h * a.groups;
+  const int G = a.Hq / a.c.Hkv;
+  const int nq = min(NQ, G - qg * NQ);                     // query heads of this CTA
+  const long long hq0 = static_cast<long long>(b) * a.Hq + h * G + qg * NQ;
+
+  // what of the request this chunk holds
   uint32_t bad = 0;
+  int len = a.lens[b];
   const long long cap = static_cast<long long>(a.max_pages) * a.c.page;
   if (len < 0 || len > cap) {
     bad = DEV_ERR_BOUNDS;
     len = len < 0 ? 0 : static_cast<int>(cap);
   }
-  if (a.rcos != nullptr && len > a.rows) { bad = DEV_ERR_BOUNDS; len = 0; }
-  const elem_t* q = a.q + static_cast<long long>(item) * D;
-  float x[E], ss = 0.f;
-  const int c0 = lane * E;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int c = c0 + i;
-    x[i] = to_f32(q[c]);
-    if (a.rcos != nullptr && c < a.rot && len > 0) {
-      const int half = a.rot / 2;
-      const int col = a.interleaved ? c / 2 : c % half;
-      const int to = a.interleaved ? c ^ 1 : (c < half ? c + half : c - half);
-      const bool first = a.interleaved ? (c & 1) == 0 : c < half;
-      const long long at = static_cast<long long>(len - 1) * half + col;
-      x[i] = x[i] * a.rcos[at] + (first ? 1.f : -1.f) * to_f32(q[to]) * a.rsin[at];
-    }
-    ss = fmaf(x[i], x[i], ss);
+  if (a.rcos != nullptr && len > a.rows) {
+    bad = DEV_ERR_BOUNDS;
+    len = 0;
   }
-  const float f = rsqrtf(warp_sum(ss) / D + a.eps) * a.scale;
-#pragma unroll
-  for (int i = 0; i < E; ++i) x[i] *= f * (a.gq ? a.gq[c0 + i] : 1.0f);
-  float m = -INFINITY, l = 0.f, acc[E] = {};
-  const int g = c0 / 64, x0 = c0 % 64;
   const int lo = a.window >= 0 && len - 1 - a.window > 0 ? len - 1 - a.window : 0;
-  for (int j = lo; j < len; ++j) {
-    const int pg = a.table[static_cast<long long>(b) * a.max_pages + j / a.c.page];
-    if (pg < 0 || pg >= a.c.n_pages) { bad = DEV_ERR_BOUNDS; continue; }
-    const uint8_t* tile = tile_of<D>(a.c, static_cast<long long>(pg) * a.c.page + j % a.c.page, h);
-    const int t = j % a.c.page % kTile;
-    const uint32_t* sc = reinterpret_cast<const uint32_t*>(tile + 16 * D);
-    const uint32_t ka = sc[t * NG + g], va = sc[(kTile + t) * NG + g];
-    float s = 0.f, v[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int c = x0 + i;
-      const int nk = ((c / 16) * NG + g) * 16 + c % 16;
-      const int kn = tile[t * (D / 2) + nk / 2] >> (4 * (nk & 1)) & 15;
-      const int nv = (((c / 8) * NG + g) * 2 + (c / 4) % 2) * 8 + (t & 1) * 4 + c % 4;
-      const int vn = tile[8 * D + (t / 2) * D + nv / 2] >> (4 * (nv & 1)) & 15;
-      s = fmaf(x[i], fmaf(__uint_as_float(ka << 16), static_cast<float>(kn - 8), __uint_as_float(ka & 0xFFFF0000u)), s);
-      v[i] = fmaf(__uint_as_float(va << 16), static_cast<float>(vn - 8), __uint_as_float(va & 0xFFFF0000u));
-    }
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s), al = expf(m - mn), p = expf(s - mn);
-    l = l * al + p;
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = fmaf(p, v[i], acc[i] * al);
-    m = mn;
-  }
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
-#pragma unroll
-  for (int i = 0; i < E; ++i) a.o[static_cast<long long>(item) * D + c0 + i] = from_f32<elem_t>(acc[i] * inv);
+  const int t_lo = lo / kTile, t_hi = (len + kTile - 1) / kTile;     // tiles [t_lo, t_hi)
+  const int chunks = max(1, (t_hi - t_lo + a.chunk - 1) / a.chunk);
+  if (blockIdx.x >= chunks) return;
+  const int t0 = t_lo + blockIdx.x * a.chunk, t1 = min(t_hi, t0 + a.chunk);
+
+  const uint32_t bars = smem_u32(smem + M::bars) + wid * kStages * 8;
+  uint32_t* flags = reinterpret_cast<uint32_t*>(smem + M::flags);    // [0] abort, [1] last
   if (lane == 0) {
-    a.lse[item] = l > 0.f ? m + logf(l) : -INFINITY;
-    if (bad) atomicOr(a.status, bad);
+    for (int s = 0; s < kStages; ++s) mbar_init(bars + 8 * s, 1);
+    fence_mbar_init();
   }
+  if (tid == 0) flags[0] = 0;
+  __syncwarp();
+
+  // Tile n of this warp is t0 + wid + n * kAttnWarps; its page is looked up
+  // 32 tiles at a time, a lane a tile.
+  const int n_mine = t1 - t0 > wid ? (t1 - t0 - wid + kAttnWarps - 1) / kAttnWarps : 0;
+  uint8_t* ring = smem + wid * kStages * S::TB;
+  const uint32_t ring_u = smem_u32(ring);
+  const int per_page = a.c.page / kTile;
+  int pages = -1, within = 0;
+  uint32_t gone = 0;       // per stage: its tile's page is not there
+  auto issue = [&](int n) {
+    if ((n & 31) == 0) {
+      const int t = t0 + wid + (n + lane) * kAttnWarps;
+      pages = -1;
+      if (t < t1) {
+        const int pi = t / per_page;
+        within = t - pi * per_page;
+        pages = a.table[static_cast<long long>(b) * a.max_pages + pi];
+        if (pages < 0 || pages >= a.c.n_pages) {
+          pages = -1;
+          bad = DEV_ERR_BOUNDS;
+        }
+      }
+    }
+    const int pg = __shfl_sync(0xffffffffu, pages, n & 31), in = __shfl_sync(0xffffffffu, within, n & 31);
+    const int st = n % kStages;
+    gone = (gone & ~(1u << st)) | (pg < 0 ? 1u << st : 0u);
+    if (lane == 0) {
+      if (pg >= 0) {
+        const uint8_t* src = a.c.data + ((static_cast<long long>(pg) * a.c.Hkv + h) * per_page + in) * S::TB;
+        mbar_arrive_expect_tx(bars + 8 * st, S::TB);
+        bulk_load(ring_u + st * S::TB, src, S::TB, bars + 8 * st);
+      } else {
+        mbar_arrive(bars + 8 * st);      // nothing to come, but the phase goes on
+      }
+    }
+  };
+  for (int n = 0; n < kStages && n < n_mine; ++n) issue(n);
+
+  // the queries
+  __half* qs = reinterpret_cast<__half*>(smem + M::qs);
+  float* qf = reinterpret_cast<float*>(smem + M::qf);
+  for (int i = wid; i < NQ; i += kAttnWarps)
+    query_row<D>(a, i < nq && len > 0 ? a.q + (hq0 + i) * D : nullptr, len - 1, qs + i * 2 * D, qf + i * 4);
+  __syncthreads();
+  uint32_t qb[NT][2 * W][2];       // operand registers: column lane / 4 = 2 head + term
+  float qfac[NT], qsum[NT][NG];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const uint16_t* row = reinterpret_cast<const uint16_t*>(qs) + (nt * kColQ + (r >> 1)) * 2 * D + (r & 1) * D;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const uint16_t* c = row + (w / 2) * 64 + j * 16 + (w & 1) * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qb[nt][2 * w + i / 2][i & 1] = c[i] | static_cast<uint32_t>(c[i + 4]) << 16;
+    }
+    qfac[nt] = qf[(nt * kColQ + j) * 4];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) qsum[nt][g] = qf[(nt * kColQ + j) * 4 + 1 + g];
+  }
+
+  const WaitCtl<kPolled> ctl{flags, a.status, a.wait_limit_ns};
+  float acc[NT][2 * W][4] = {};
+  float m[NT], l[NT] = {}, zs[NT][NG] = {};
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) m[nt] = -1e30f;
+  int n = 0;
+  for (; n < n_mine; ++n) {
+    const int st = n % kStages;
+    if (!mbar_wait_warp(bars + 8 * st, (n / kStages) & 1, ctl)) break;
+    if (!(gone >> st & 1u)) {
+      const uint8_t* tile = ring + st * S::TB;
+      const int key0 = (t0 + wid + n * kAttnWarps) * kTile;
+      float s[NT][2];      // logits (base 2) of keys r and r + 8
+      {
+        uint32_t ka[W], kb[W];
+        ld_words<W>(tile + r * (D / 2) + j * (D / 8), ka);
+        ld_words<W>(tile + (r + 8) * (D / 2) + j * (D / 8), kb);
+        float sa[NG], za[NG], sb[NG], zb[NG];
+        ld_scales<NG>(tile + 16 * D + r * (4 * NG), sa, za);
+        ld_scales<NG>(tile + 16 * D + (r + 8) * (4 * NG), sb, zb);
+        float d[NT][NG][4] = {};
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          uint32_t x[4], y[4];
+          widen_f16(ka[w], x);
+          widen_f16(kb[w], y);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16(d[nt][w / 2], x[0], y[0], x[1], y[1], qb[nt][2 * w][0], qb[nt][2 * w][1]);
+            mma_f16(d[nt][w / 2], x[2], y[2], x[3], y[3], qb[nt][2 * w + 1][0], qb[nt][2 * w + 1][1]);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float u = 0.f, v = 0.f;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            u = fmaf(sa[g], d[nt][g][0] + d[nt][g][1], fmaf(za[g], qsum[nt][g], u));
+            v = fmaf(sb[g], d[nt][g][2] + d[nt][g][3], fmaf(zb[g], qsum[nt][g], v));
+          }
+          s[nt][0] = u * qfac[nt];
+          s[nt][1] = v * qfac[nt];
+        }
+      }
+      float sv[2][NG], zv[2][NG];
+      ld_scales<NG>(tile + 17 * D + r * (4 * NG), sv[0], zv[0]);
+      ld_scales<NG>(tile + 17 * D + (r + 8) * (4 * NG), sv[1], zv[1]);
+      if (key0 < lo || key0 + kTile > len) {       // the first or last tile: keys outside count nothing
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int key = key0 + r + 8 * i;
+          if (key < lo || key >= len) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[nt][i] = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) sv[i][g] = zv[i][g] = 0.f;
+          }
+        }
+      }
+      bool raise = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) raise |= fmaxf(s[nt][0], s[nt][1]) > m[nt] + 8.f;
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float x = fmaxf(s[nt][0], s[nt][1]);
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+          const float mn = fmaxf(m[nt], x), al = ex2_approx(m[nt] - mn);
+          m[nt] = mn;
+          l[nt] *= al;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) zs[nt][g] *= al;
+#pragma unroll
+          for (int i = 0; i < 2 * W; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[nt][i][k] *= al;
+        }
+      }
+      uint32_t pb[NT][NG][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float p = ex2_approx(s[nt][i] - m[nt]);
+          l[nt] += p;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            zs[nt][g] = fmaf(p, zv[i][g], zs[nt][g]);
+            const float w = p * sv[i][g];
+            const float hi = __uint_as_float(pack_bf16x2(0.f, w));       // rounded, in the high half
+            pb[nt][g][i] = transpose8(pack_bf16x2(hi, w - hi));
+          }
+        }
+      }
+      uint32_t va[W], vb[W];
+      ld_words<W>(tile + 8 * D + j * D + r * (D / 8), va);
+      ld_words<W>(tile + 8 * D + (j + 4) * D + r * (D / 8), vb);
+      __syncwarp();
+      if (n + kStages < n_mine) issue(n + kStages);   // every lane has its words
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        uint32_t x[4], y[4];
+        widen_bf16(va[w], x);
+        widen_bf16(vb[w], y);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_bf16(acc[nt][2 * w], x[0], x[1], y[0], y[1], pb[nt][w / 2][0], pb[nt][w / 2][1]);
+          mma_bf16(acc[nt][2 * w + 1], x[2], x[3], y[2], y[3], pb[nt][w / 2][0], pb[nt][w / 2][1]);
+        }
+      }
+    } else if (n + kStages < n_mine) {
+      issue(n + kStages);
+    }
+  }
+  // a wait that ran out: the copies still on their way land before the memory is used again
+  for (int k = n; k < n_mine && k < n + kStages; ++k) mbar_wait_drain(bars + 8 * (k % kStages), (k / kStages) & 1, kDrainLimitNs);
+  if (bad) atomicOr(a.status, bad);
+
+  // join the warps: O, M, L of each query head into shared memory
+  __syncthreads();
+  float* jo = reinterpret_cast<float*>(smem);                    // [warp][NQ][D]
+  float* jm = jo + kAttnWarps * NQ * D;                          // [warp][NQ][2]: M, L
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], o);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) zs[nt][g] += __shfl_xor_sync(0xffffffffu, zs[nt][g], o);
+    }
+    const int i = wid * NQ + nt * kColQ + j;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float(&x)[4] = acc[nt][2 * w], (&y)[4] = acc[nt][2 * w + 1];
+      const float z = zs[nt][w / 2];
+      *reinterpret_cast<float4*>(jo + i * D + (w / 2) * 64 + r * 8 + (w & 1) * 4) =
+          make_float4(x[0] + x[1] + z, x[2] + x[3] + z, y[0] + y[1] + z, y[2] + y[3] + z);
+    }
+    if (r == 0) {
+      jm[2 * i] = m[nt];
+      jm[2 * i + 1] = l[nt];
+    }
+  }
+  __syncthreads();
+  constexpr int E = D / 32;
+  const int item = (b * a.c.Hkv + h) * a.groups + qg;
+  float* part = a.part + static_cast<long long>(item) * a.splits * NQ * (D + 2);
+  for (int i = wid; i < nq; i += kAttnWarps) {      // a warp a head, E channels a lane
+    float top = -1e30f, sum = 0.f, o[E] = {};
+#pragma unroll
+    for (int k = 0; k < kAttnWarps; ++k) top = fmaxf(top, jm[2 * (k * NQ + i)]);
+#pragma unroll
+    for (int k = 0; k < kAttnWarps; ++k) {
+      const float f = ex2_approx(jm[2 * (k * NQ + i)] - top);
+      sum = fmaf(f, jm[2 * (k * NQ + i) + 1], sum);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(f, jo[(k * NQ + i) * D + lane * E + e], o[e]);
+    }
+    if (chunks == 1) {
+      const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;     // a NaN stays one
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= inv;
+      store_vec<E>(a.o + (hq0 + i) * D + lane * E, o);
+      if (lane == 0) a.lse[hq0 + i] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    } else {
+      float* dst = part + (static_cast<long long>(blockIdx.x) * NQ + i) * (D + 2);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(dst + lane * E + e) = make_float2(o[e], o[e + 1]);
+      if (lane == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(top, sum);
+    }
+  }
+  if (chunks == 1) return;
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) flags[1] = atomicAdd(a.count + item, 1u) == static_cast<unsigned>(chunks - 1);
+  __syncthreads();
+  if (!flags[1]) return;
+  __threadfence();
+  if (tid == 0) a.count[item] = 0;        // for the next call
+  for (int i = wid; i < nq; i += kAttnWarps) {
+    const float* src = part + i * (D + 2);
+    const long long step = static_cast<long long>(NQ) * (D + 2);
+    float top = -1e30f;
+    for (int k = lane; k < chunks; k += 32) top = fmaxf(top, __ldcg(src + k * step + D));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float sum = 0.f, o[E] = {};
+#pragma unroll 4
+    for (int k = 0; k < chunks; ++k) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(src + k * step + D));
+      const float f = ex2_approx(ml.x - top);
+      sum = fmaf(f, ml.y, sum);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(src + k * step + lane * E + e));
+        o[e] = fmaf(f, v.x, o[e]);
+        o[e + 1] = fmaf(f, v.y, o[e + 1]);
+      }
+    }
+    const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= inv;
+    store_vec<E>(a.o + (hq0 + i) * D + lane * E, o);
+    if (lane == 0) a.lse[hq0 + i] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  }
+}
+
+// Chunks: a CTA's tiles and the CTAs of the longest request, from what the
+// host knows (the table's width and the window, not the lengths).
+struct AttnSplit {
+  int heads, groups;     // query heads of a CTA, CTAs per kv head
+  int chunk, splits;
+  long long items;
+};
+inline AttnSplit attn_split(int B, int Hq, int Hkv, int page, int max_pages, int window) {
+  AttnSplit s;
+  const int G = Hq / Hkv;
+  s.heads = G <= kColQ ? kColQ : 2 * kColQ;
+  s.groups = (G + s.heads - 1) / s.heads;
+  s.items = static_cast<long long>(B) * Hkv * s.groups;
+  const long long cap = static_cast<long long>(max_pages) * page;
+  long long keys = cap;
+  if (window >= 0 && window + 1LL + kTile < cap) keys = window + 1LL + kTile;    // the window may begin inside a tile
+  const long long tiles = (keys + kTile - 1) / kTile;
+  long long c = (tiles * s.items + kAttnCtas - 1) / kAttnCtas;
+  c = c < kMinChunk ? kMinChunk : (c > kMaxChunk ? kMaxChunk : c);
+  c = (c + kAttnWarps - 1) / kAttnWarps * kAttnWarps;
+  s.chunk = static_cast<int>(c);
+  s.splits = static_cast<int>((tiles + c - 1) / c);
+  return s;
 }
 
 }  // namespace kv4
