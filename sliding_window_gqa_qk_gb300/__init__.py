@@ -535,63 +535,71 @@ def attention_backward(q, k, v, gq, gk, o, lse, dO, *, window: int = -1, causal:
 # Rotary positions and the decode path. These calls check types, shapes and
 # devices before they pass addresses on (the C ABI sees addresses only), run
 # on the device of their tensors, and allocate their outputs on the stream
-# they run on.
+# they run on. A decode step is a few microseconds of GPU work, so they are
+# written to cost the host little: one check per tensor, which also yields its
+# address, and one call.
 # ---------------------------------------------------------------------------
 
 SWA_ROPE_PLAIN, SWA_ROPE_LINEAR, SWA_ROPE_NTK, SWA_ROPE_BY_PARTS = range(4)
 _SCALINGS = {"none": SWA_ROPE_PLAIN, "linear": SWA_ROPE_LINEAR, "ntk": SWA_ROPE_NTK, "by_parts": SWA_ROPE_BY_PARTS}
+_F32, _BF16, _I32, _I64, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8
+# torch's own lookup of the current stream's handle by device index; the
+# public one builds a Stream object each time (2.9 us against 0.1 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-class _on:
-    """Makes a device, and a stream if one is given, current for a call; does
-    nothing where they are current already."""
-    __slots__ = ("ctx",)
-
-    def __init__(self, device, stream):
-        self.ctx = []
-        if device.type != "cuda":
-            raise ValueError(f"the tensors are on {device}, not on a GPU")
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.ctx.append(torch.cuda.device(device))
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device)
-            self.ctx.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
-
-    def __exit__(self, *exc):
-        for c in reversed(self.ctx):
-            c.__exit__(*exc)
-
-
-def _want(name, t, dtype, shape, device):
-    """Checks an argument of the calls below; None passes."""
+def _at(name, t, dtype, shape, device):
+    """Address of an argument of the calls below after its checks; None passes."""
     if t is None:
-        return
-    if t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous {dtype} tensor on {device} is expected, got {t.dtype} on {t.device}"
-                         + ("" if t.is_contiguous() else ", not contiguous"))
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {shape} is expected, got {tuple(t.shape)}")
+        return None
+    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on {device} is expected, got "
+                         f"{t.dtype}, {tuple(t.shape)}, on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
+    return t.data_ptr()
 
 
-def _elem(name, t):
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"{name}: bf16 or fp32 is expected, got {t.dtype}")
+def _kind(name, dtype):
+    if dtype is _BF16:
+        return "bf16"
+    if dtype is _F32:
+        return "fp32"
+    raise ValueError(f"{name}: bf16 or fp32 is expected, got {dtype}")
 
 
-def _want_rope(rope, device):
-    if rope is not None:
-        for name, t in zip(("rope cos", "rope sin"), rope):
-            _want(name, t, torch.float32, None, device)
+def _rope_at(rope, interleaved, device):
+    if rope is None:
+        return None
+    cos, sin = rope
+    c = _at("rope cos", cos, _F32, cos.shape, device)
+    if cos.dim() != 2:
+        raise ValueError("rope: two fp32 tensors [rows, rot/2] are expected")
+    return swa_rope(c, _at("rope sin", sin, _F32, cos.shape, device), cos.shape[0], 2 * cos.shape[1], 1 if interleaved else 0)
 
 
-def _want_ws(ws, device):
-    if ws is not None:
-        _want("workspace", ws, torch.uint8, None, device)
+def _ws_at(ws, device):
+    """Address and bytes of a workspace; None: none."""
+    if ws is None:
+        return None, 0
+    n = ws.numel()
+    return _at("workspace", ws, _U8, (n,), device), n
+
+
+def _run(device, stream, call):
+    """call(handle of the stream) with ``device`` current, and with ``stream``
+    (a torch stream or a raw handle; None: the current one), so that what the
+    call allocates belongs to the stream it runs on."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors are on {device}, not on a GPU")
+    here = device.index is None or device.index == torch.cuda.current_device()
+    if stream is None and here and _raw_stream is not None:
+        return call(_raw_stream(device.index if device.index is not None else torch.cuda.current_device()))
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
 
 
 def rope_tables(rows: int, rot: int, *, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -605,13 +613,19 @@ def rope_tables(rows: int, rot: int, *, base: float = 10000.0, scaling: str = "n
     0 there: row t is position t)."""
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling: one of {sorted(_SCALINGS)} is expected, got {scaling!r}")
+    if rows < 0 or rot < 0:
+        raise ValueError("rows, rot: not below 0")
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    with _on(device, stream):
-        cos = torch.empty(rows, rot // 2, dtype=torch.float32, device=device)
+    f = swa_rope_freq(rot, _SCALINGS[scaling], base, factor, orig_len, slow, fast, amplitude)
+
+    def call(st):
+        cos = torch.empty((rows, rot // 2), dtype=_F32, device=device)
         sin = torch.empty_like(cos)
-        f = swa_rope_freq(int(rot), _SCALINGS[scaling], base, factor, orig_len, slow, fast, amplitude)
-        _check(swa_rope_tables(f, first, rows, cos, sin), "swa_rope_tables")
-    return cos, sin
+        s = load("bf16").swa_rope_tables(ctypes.byref(f), first, rows, cos.data_ptr() or 256, sin.data_ptr() or 256, st)
+        if s:
+            raise SwaError(s, "swa_rope_tables")
+        return cos, sin
+    return _run(device, stream, call)
 
 
 def rope_apply(q, k, rope, *, pos=None, interleaved: bool = False, inverse: bool = False, out=None, workspace=None,
@@ -624,35 +638,38 @@ def rope_apply(q, k, rope, *, pos=None, interleaved: bool = False, inverse: bool
     the tables are reported (swa_attn_check_status); their rows are not
     written."""
     x = q if q is not None else k
-    if x is None:
-        raise ValueError("rope_apply: q or k is expected")
-    _elem("q, k", x)
-    B, T, _, d = x.shape
-    dev = x.device
-    Hkv = k.shape[2] if k is not None else 1
-    Hq = q.shape[2] if q is not None else Hkv
+    if x is None or x.dim() != 4:
+        raise ValueError("rope_apply: q or k [B, T, H, d] is expected")
+    dt, dev = x.dtype, x.device
+    lib = load(_kind("q, k", dt))
+    B, T, Hq, d = x.shape
+    Hkv = k.shape[2] if q is not None and k is not None else (1 if k is None else Hq)
     qo, ko = (None, None) if out is None else out
-    for name, t, H in (("q", q, Hq), ("k", k, Hkv), ("out of q", qo, Hq), ("out of k", ko, Hkv)):
-        _want(name, t, x.dtype, (B, T, H, d), dev)
-    _want("pos", pos, torch.int32, (B, T), dev)
-    _want_rope(rope, dev)
-    _want_ws(workspace, dev)
+    sq, sk = (B, T, Hq, d), (B, T, Hkv, d)
+    qa, ka, qoa, koa = _at("q", q, dt, sq, dev), _at("k", k, dt, sk, dev), _at("out of q", qo, dt, sq, dev), \
+        _at("out of k", ko, dt, sk, dev)
+    pa = _at("pos", pos, _I32, (B, T), dev)
+    r = _rope_at(rope, interleaved, dev)
+    ws, nws = _ws_at(workspace, dev)
     p = make_params(B, T, Hq, Hkv, d)
-    with _on(dev, stream):
-        if q is not None and qo is None:
-            qo = torch.empty_like(q)
-        if k is not None and ko is None:
-            ko = torch.empty_like(k)
-        _check(swa_rope_apply(p, make_rope(rope, interleaved), pos, q, k, qo, ko, inverse, workspace), "swa_rope_apply")
-    return qo, ko
+
+    def call(st):
+        qy = torch.empty_like(q) if q is not None and qo is None else qo
+        ky = torch.empty_like(k) if k is not None and ko is None else ko
+        s = lib.swa_rope_apply(ctypes.byref(p), _ref(r), pa, qa, ka, qy.data_ptr() if qoa is None and qy is not None else qoa,
+                               ky.data_ptr() if koa is None and ky is not None else koa, 1 if inverse else 0, ws, nws, st)
+        if s:
+            raise SwaError(s, "swa_rope_apply")
+        return qy, ky
+    return _run(dev, stream, call)
 
 
 def _cache_dims(cache):
     """n_pages, Hkv, page, d of a cache tensor (new_kv4_cache)."""
-    if cache.dim() != 4 or cache.shape[3] not in (18 * 64, 18 * 128) or cache.dtype != torch.uint8 \
-            or not cache.is_contiguous():
+    n, Hkv, tiles, row = cache.shape if cache.dim() == 4 else (0, 0, 0, 0)
+    if row not in (18 * 64, 18 * 128) or cache.dtype is not _U8 or not cache.is_contiguous():
         raise ValueError("cache: a contiguous uint8 tensor [pages, Hkv, page / 16, 18 d] is expected, d 64 or 128")
-    return cache.shape[0], cache.shape[1], cache.shape[2] * 16, cache.shape[3] // 18
+    return n, Hkv, 16 * tiles, row // 18
 
 
 def new_kv4_cache(n_pages: int, page: int, Hkv: int, d: int, device):
@@ -665,17 +682,18 @@ def new_kv4_cache(n_pages: int, page: int, Hkv: int, d: int, device):
 
 
 def new_kv4_workspace(cache, B: int, Hq: int, *, max_pages: int, window: int = -1, kind: str = "bf16", stream=None):
-    """The workspace of kv4_attention for up to B requests of max_pages pages,
-    initialised. kind: "bf16" or "fp32", as q."""
+    """The workspace of kv4_attention for B requests of max_pages pages and
+    this window, initialised. kind: "bf16" or "fp32", as q."""
     _, Hkv, page, d = _cache_dims(cache)
-    p = make_params(B, 1, Hq, Hkv, d, window)
-    n = swa_kv4_workspace_size(p, page, max_pages, kind)
+    n = swa_kv4_workspace_size(make_params(B, 1, Hq, Hkv, d, window), page, max_pages, kind)
     if n == 0:
         raise SwaError(SWA_ERR_INVALID_ARG, "workspace size")
-    with _on(cache.device, stream):
+
+    def call(st):
         ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
-        _check(swa_kv4_workspace_init(ws, n, None, kind), "workspace init")
-    return ws
+        _check(swa_kv4_workspace_init(ws, n, st, kind), "workspace init")
+        return ws
+    return _run(cache.device, stream, call)
 
 
 def kv4_plan(lens, new_lens, table, free_pages, free_head, *, page: int, n_pages: int, n_tokens: Optional[int] = None,
@@ -690,27 +708,35 @@ def kv4_plan(lens, new_lens, table, free_pages, free_head, *, page: int, n_pages
     dev = lens.device
     if table.dim() != 2 or lens.dim() != 1:
         raise ValueError("lens [B] and table [B, max_pages] are expected")
-    B = lens.shape[0]
-    _want("lens", lens, torch.int32, (B,), dev)
-    _want("new_lens", new_lens, torch.int32, (B,), dev)
-    _want("table", table, torch.int32, (B, table.shape[1]), dev)
-    _want("free_pages", free_pages, torch.int32, (free_pages.numel(),), dev)
-    _want("free_head", free_head, torch.int32, (1,), dev)
-    _want_ws(workspace, dev)
+    B, max_pages = table.shape
+    row_b, n_free = (B,), free_pages.numel()
+    la, na = _at("lens", lens, _I32, row_b, dev), _at("new_lens", new_lens, _I32, row_b, dev)
+    ta, fa = _at("table", table, _I32, table.shape, dev), _at("free_pages", free_pages, _I32, (n_free,), dev)
+    ha = _at("free_head", free_head, _I32, (1,), dev)
+    ws, nws = _ws_at(workspace, dev)
     if n_tokens is None:
         if new_lens is not None:
             raise ValueError("n_tokens: the number of new tokens is expected with new_lens")
         n_tokens = B
-    with _on(dev, stream):
-        slot = torch.empty(n_tokens, dtype=torch.int64, device=dev)
-        # one buffer for the int32 outputs: fewer allocations a step
+    if n_tokens < 0:
+        raise ValueError("n_tokens: not below 0")
+
+    def call(st):
+        # one buffer for all outputs: slots first, then the int32 ones, 16-byte aligned pieces
         pad = (n_tokens + 3) // 4 * 4
-        ints = torch.empty(2 * pad + 2 * B + 2, dtype=torch.int32, device=dev)
-        pos, row = ints[:n_tokens], ints[pad:pad + n_tokens]
-        cu, lens_out, head = ints[2 * pad:2 * pad + B + 1], ints[2 * pad + B + 1:-1], ints[-1:]
-        _check(swa_kv4_plan(n_pages, page, B, table.shape[1], lens, new_lens, table, free_pages, free_pages.numel(),
-                            free_head, n_tokens, slot, pos, row, cu, lens_out, head, workspace), "swa_kv4_plan")
-    return {"slot": slot, "pos": pos, "row": row, "cu": cu, "lens": lens_out, "free_head": head}
+        ints = torch.empty(4 * pad + 2 * B + 2, dtype=_I32, device=dev)
+        base = ints.data_ptr()
+        slot, pos, row, cu, lens_out, head = torch.split(ints, (2 * pad, pad, pad, B + 1, B, 1))
+        s = load("bf16").swa_kv4_plan(n_pages, page, B, max_pages, la, na, ta, fa, n_free, ha, n_tokens, base,
+                                      base + 8 * pad, base + 12 * pad, base + 16 * pad, base + 16 * pad + 4 * (B + 1),
+                                      base + 16 * pad + 4 * (2 * B + 1), ws, nws, st)
+        if s:
+            raise SwaError(s, "swa_kv4_plan")
+        slot = slot.view(_I64)
+        if pad != n_tokens:
+            slot, pos, row = slot[:n_tokens], pos[:n_tokens], row[:n_tokens]
+        return {"slot": slot, "pos": pos, "row": row, "cu": cu, "lens": lens_out, "free_head": head}
+    return _run(dev, stream, call)
 
 
 def kv4_append(cache, k, v, slot, *, pos=None, rope=None, interleaved: bool = False, gk=None, eps: float = 1e-6,
@@ -721,33 +747,38 @@ def kv4_append(cache, k, v, slot, *, pos=None, rope=None, interleaved: bool = Fa
     token. Rotary, QK-norm gain, value embedding and gate as in
     attention_forward, with the rotation at pos int32 [B, T] (None: t)."""
     n_pages, Hkv, page, d = _cache_dims(cache)
-    _elem("k", k)
     dev, dt = cache.device, k.dtype
+    lib = load(_kind("k", dt))
     if k.dim() != 4:
         raise ValueError("k: [B, T, Hkv, d] is expected")
     B, T = k.shape[:2]
-    _want("k", k, dt, (B, T, Hkv, d), dev)
-    _want("v", v, dt, (B, T, Hkv, d), dev)
-    _want("slot", slot, torch.int64, (B, T), dev)
-    _want("pos", pos, torch.int32, (B, T), dev)
-    _want("gk", gk, torch.float32, (d,), dev)
-    vocab, ex = 0, None
+    rows, tokens = (B, T, Hkv, d), (B, T)
+    ka, va = _at("k", k, dt, rows, dev), _at("v", v, dt, rows, dev)
+    sa, pa = _at("slot", slot, _I64, tokens, dev), _at("pos", pos, _I32, tokens, dev)
+    ga = _at("gk", gk, _F32, (d,), dev)
+    vocab, ex, ea, ta, gta = 0, None, None, None, None
     if ve is not None:
         vocab = ve.shape[0]
-        _want("ve", ve, dt, (vocab, Hkv * d), dev)
-        _want("tok", tok, torch.int32, (B, T), dev)
-        _want("ve_gate", ve_gate, torch.float32, (B, T, Hkv), dev)
+        ea, ta = _at("ve", ve, dt, (vocab, Hkv * d), dev), _at("tok", tok, _I32, tokens, dev)
+        gta = _at("ve_gate", ve_gate, _F32, (B, T, Hkv), dev)
         if gate_w is not None:
-            _want("gate_w", gate_w, torch.float32, (Hkv, gate_w.shape[1]), dev)
-            if gate_x is None or gate_x.dtype != dt or gate_x.device != dev or gate_x.shape[:2] != (B, T):
+            if gate_w.dim() != 2:
+                raise ValueError("gate_w: [Hkv, channels] is expected")
+            _at("gate_w", gate_w, _F32, (Hkv, gate_w.shape[1]), dev)
+            if gate_x is None or gate_x.dtype is not dt or gate_x.device != dev or gate_x.dim() != 3 \
+                    or gate_x.shape[:2] != tokens or gate_x.shape[2] < gate_w.shape[1]:
                 raise ValueError(f"gate_x: a {dt} tensor [B, T, channels] on {dev} is expected")
             ex = make_extras(None, gate_x, gate_w)
-    _want_rope(rope, dev)
-    _want_ws(workspace, dev)
-    p = make_params(B, T, Hkv, Hkv, d, eps=eps, ve_scale=ve_scale, vocab=vocab)
-    with _on(dev, stream):
-        _check(swa_kv4_append(p, ex, swa_kv4_cache(cache.data_ptr(), n_pages, page), make_rope(rope, interleaved), k, v,
-                              gk, ve, tok, ve_gate, pos, slot, workspace), "swa_kv4_append")
+    r = _rope_at(rope, interleaved, dev)
+    ws, nws = _ws_at(workspace, dev)
+    p = swa_params(B, T, Hkv, Hkv, d, -1, 1, 0.0, eps, ve_scale, vocab)
+    c = swa_kv4_cache(cache.data_ptr(), n_pages, page)
+
+    def call(st):
+        s = lib.swa_kv4_append(ctypes.byref(p), _ref(ex), ctypes.byref(c), _ref(r), ka, va, ga, ea, ta, gta, pa, sa, ws, nws, st)
+        if s:
+            raise SwaError(s, "swa_kv4_append")
+    _run(dev, stream, call)
 
 
 def kv4_read(cache, slot, *, dtype=torch.bfloat16, workspace=None, stream=None):
@@ -756,18 +787,22 @@ def kv4_read(cache, slot, *, dtype=torch.bfloat16, workspace=None, stream=None):
     Rows of slot -1 are zero."""
     n_pages, Hkv, page, d = _cache_dims(cache)
     dev = cache.device
+    lib = load(_kind("dtype", dtype))
     if slot.dim() != 2:
         raise ValueError("slot: [B, T] is expected")
     B, T = slot.shape
-    _want("slot", slot, torch.int64, (B, T), dev)
-    _want_ws(workspace, dev)
-    with _on(dev, stream):
-        k = torch.empty(B, T, Hkv, d, dtype=dtype, device=dev)
-        _elem("dtype", k)
+    sa = _at("slot", slot, _I64, (B, T), dev)
+    ws, nws = _ws_at(workspace, dev)
+    p, c = swa_params(B, T, Hkv, Hkv, d, -1, 1, 0.0, 0.0, 0.0, 0), swa_kv4_cache(cache.data_ptr(), n_pages, page)
+
+    def call(st):
+        k = torch.empty((B, T, Hkv, d), dtype=dtype, device=dev)
         v = torch.empty_like(k)
-        _check(swa_kv4_read(make_params(B, T, Hkv, Hkv, d), swa_kv4_cache(cache.data_ptr(), n_pages, page), slot, k, v,
-                            workspace), "swa_kv4_read")
-    return k, v
+        s = lib.swa_kv4_read(ctypes.byref(p), ctypes.byref(c), sa, k.data_ptr(), v.data_ptr(), ws, nws, st)
+        if s:
+            raise SwaError(s, "swa_kv4_read")
+        return k, v
+    return _run(dev, stream, call)
 
 
 def kv4_attention(cache, q, table, lens, *, rope=None, interleaved: bool = False, gq=None, window: int = -1,
@@ -779,23 +814,28 @@ def kv4_attention(cache, q, table, lens, *, rope=None, interleaved: bool = False
     attention_forward. ``workspace``: from new_kv4_workspace, kept by the
     caller (one per stream); None: one for this call."""
     n_pages, Hkv, page, d = _cache_dims(cache)
-    _elem("q", q)
-    dev = cache.device
+    dev, dt = cache.device, q.dtype
+    kind = _kind("q", dt)
     if q.dim() != 3 or table.dim() != 2:
         raise ValueError("q [B, Hq, d] and table [B, max_pages] are expected")
     B, Hq = q.shape[:2]
-    _want("q", q, q.dtype, (B, Hq, d), dev)
-    _want("table", table, torch.int32, (B, table.shape[1]), dev)
-    _want("lens", lens, torch.int32, (B,), dev)
-    _want("gq", gq, torch.float32, (d,), dev)
-    _want_rope(rope, dev)
-    _want_ws(workspace, dev)
-    p = make_params(B, 1, Hq, Hkv, d, window, True, softmax_scale, eps)
-    with _on(dev, stream):
-        if workspace is None:
-            workspace = new_kv4_workspace(cache, B, Hq, max_pages=table.shape[1], window=window, kind=_kind_of(q))
+    max_pages = table.shape[1]
+    qa, ga = _at("q", q, dt, (B, Hq, d), dev), _at("gq", gq, _F32, (d,), dev)
+    ta, la = _at("table", table, _I32, (B, max_pages), dev), _at("lens", lens, _I32, (B,), dev)
+    r = _rope_at(rope, interleaved, dev)
+    p = swa_params(B, 1, Hq, Hkv, d, window, 1, softmax_scale, eps, 0.0, 0)
+    c = swa_kv4_cache(cache.data_ptr(), n_pages, page)
+
+    def call(st):
+        w = workspace
+        if w is None:
+            w = new_kv4_workspace(cache, B, Hq, max_pages=max_pages, window=window, kind=kind)
+        ws, nws = _ws_at(w, dev)
         o = torch.empty_like(q)
-        lse = torch.empty(B, Hq, dtype=torch.float32, device=dev)
-        _check(swa_kv4_attn(p, None, swa_kv4_cache(cache.data_ptr(), n_pages, page), make_rope(rope, interleaved), q, gq,
-                            table, table.shape[1], lens, o, lse, workspace), "swa_kv4_attn")
-    return o, lse
+        lse = torch.empty((B, Hq), dtype=_F32, device=dev)
+        s = load(kind).swa_kv4_attn(ctypes.byref(p), None, ctypes.byref(c), _ref(r), qa, ga, ta, max_pages, la, o.data_ptr(),
+                                    lse.data_ptr(), ws, nws, st)
+        if s:
+            raise SwaError(s, "swa_kv4_attn")
+        return o, lse
+    return _run(dev, stream, call)

@@ -75,8 +75,18 @@ constexpr float kFlatStep = 1e-36f;
 struct Group {
   float s, z;
 };
+__device__ __forceinline__ float to_bf16(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
+
+// Distance of x from the nearest border between two bf16 roundings, given
+// its rounding y.
+__device__ __forceinline__ float bf16_margin(float x, float y) {
+  return __uint_as_float(__float_as_uint(x) & 0x7F800000u) * 0.00390625f - fabsf(x - y);   // half a step: 2^(e - 8)
+}
+
+// step and centre; err: what the fp32 entries may be off by, of the group's
+// largest; near is set where that reaches a rounding border of either.
 template <int D>
-__device__ __forceinline__ Group group_scale(const float (&x)[RowMap<D>::EPL]) {
+__device__ __forceinline__ Group group_scale(const float (&x)[RowMap<D>::EPL], float err, float& slack, bool& near) {
   constexpr int EPL = RowMap<D>::EPL;
   constexpr int GL = 64 / EPL;   // lanes of a group
   float lo = x[0], hi = x[0];
@@ -91,16 +101,24 @@ __device__ __forceinline__ Group group_scale(const float (&x)[RowMap<D>::EPL]) {
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
   Group g;
-  g.s = __bfloat162float(__float2bfloat16_rn((hi - lo) / 15.0f));
+  const float s = (hi - lo) / 15.0f;
+  g.s = to_bf16(s);
   if (g.s < kFlatStep) g.s = 0.0f;
-  g.z = __bfloat162float(__float2bfloat16_rn(fmaf(8.0f, g.s, lo)));
+  const float z = fmaf(8.0f, g.s, lo);
+  g.z = to_bf16(z);
   if (!isfinite(g.s) || !isfinite(g.z)) g.s = g.z = __int_as_float(0x7fffffff);
+  float top = fmaxf(fabsf(lo), fabsf(hi));
+  if (D == 128) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, GL));   // a rotated pair may span the groups
+  slack = err * top;
+  near = bf16_margin(s, g.s) <= 0.2f * slack || bf16_margin(z, g.z) <= 1.25f * slack;
   return g;
 }
-__device__ __forceinline__ uint32_t quantise(float x, const Group& g, float inv, float half) {
+// One number; gap is lowered to the distance of x from the nearest border.
+__device__ __forceinline__ uint32_t quantise(float x, const Group& g, float inv, float half, float& gap) {
   const float v = x - g.z;
   float n = rintf(v * inv);
   const float r = fmaf(-n, g.s, v);
+  gap = fminf(gap, fabsf(fabsf(r) - half));
   n += r >= half ? 1.0f : 0.0f;
   n -= r < -half ? 1.0f : 0.0f;
   n = fminf(fmaxf(n, -8.0f), 7.0f);   // a NaN becomes -8
@@ -108,13 +126,53 @@ __device__ __forceinline__ uint32_t quantise(float x, const Group& g, float inv,
 }
 // The lane's EPL numbers, four bits each, lowest channel lowest.
 template <int D>
-__device__ __forceinline__ uint32_t quantise_lane(const float (&x)[RowMap<D>::EPL], const Group& g) {
+__device__ __forceinline__ uint32_t quantise_lane(const float (&x)[RowMap<D>::EPL], const Group& g, float& gap) {
   constexpr int EPL = RowMap<D>::EPL;
   const bool flat = !(g.s > 0.0f);
   const float inv = flat ? 0.0f : 1.0f / g.s, half = 0.5f * g.s;
   uint32_t w = 0;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) w |= (flat ? 8u : quantise(x[i], g, inv, half)) << (4 * i);
+  for (int i = 0; i < EPL; ++i) w |= (flat ? 8u : quantise(x[i], g, inv, half, gap)) << (4 * i);
+  return w;
+}
+
+// The same in fp64, for rows that fp32 leaves too close to a border: which of
+// two numbers (and, worse, of two steps) a row gets then follows the formula
+// and not the rounding of a particular kernel. About one row in a hundred
+// takes this way; its price is this GPU's slow fp64.
+template <int D>
+__device__ __noinline__ uint32_t quantise_f64(const double (&x)[RowMap<D>::EPL], Group& g) {
+  constexpr int EPL = RowMap<D>::EPL;
+  constexpr int GL = 64 / EPL;
+  double lo = x[0], hi = x[0];
+#pragma unroll
+  for (int i = 1; i < EPL; ++i) {
+    lo = x[i] < lo ? x[i] : lo;
+    hi = x[i] > hi ? x[i] : hi;
+  }
+#pragma unroll
+  for (int o = GL / 2; o > 0; o >>= 1) {
+    const double a = __shfl_xor_sync(0xffffffffu, lo, o), b = __shfl_xor_sync(0xffffffffu, hi, o);
+    lo = a < lo ? a : lo;
+    hi = b > hi ? b : hi;
+  }
+  g.s = to_bf16(static_cast<float>((hi - lo) / 15.0));
+  if (g.s < kFlatStep) g.s = 0.0f;
+  g.z = to_bf16(static_cast<float>(lo + 8.0 * static_cast<double>(g.s)));
+  const bool flat = !(g.s > 0.0f);
+  const float inv = flat ? 0.0f : 1.0f / g.s;
+  const double half = 0.5 * static_cast<double>(g.s);
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const double v = x[i] - static_cast<double>(g.z);
+    float n = rintf(static_cast<float>(v) * inv);
+    const double r = fma(-static_cast<double>(n), static_cast<double>(g.s), v);
+    n += r >= half ? 1.0f : 0.0f;
+    n -= r < -half ? 1.0f : 0.0f;
+    n = fminf(fmaxf(n, -8.0f), 7.0f);
+    w |= (flat ? 8u : static_cast<uint32_t>(static_cast<int>(n) + 8)) << (4 * i);
+  }
   return w;
 }
 
@@ -135,6 +193,42 @@ struct AppendArgs {
   const int32_t* pos; const int64_t* slot;
   uint32_t* status;                    // or NULL
 };
+
+// The rotated and normed key row in fp64 (row: its index, p its position),
+// quantised; every lane of the warp calls it.
+template <int D>
+__device__ __noinline__ uint32_t key_f64(const AppendArgs& a, long long row, int p, bool on, Group& g) {
+  using M = RowMap<D>;
+  constexpr int EPL = M::EPL;
+  const int cl = (threadIdx.x & 31) % M::LPR, c0 = cl * EPL, half = a.rot / 2;
+  const elem_t* k = a.k + (on ? row : 0) * D;
+  double x[EPL], ss = 0.0;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int c = c0 + i;
+    x[i] = on ? to_f32(k[c]) : 0.0;
+    if (a.rcos != nullptr && c < a.rot && on) {
+      const int col = a.interleaved ? c / 2 : (c < half ? c : c - half);
+      const int to = a.interleaved ? c ^ 1 : (c < half ? c + half : c - half);
+      const bool first = a.interleaved ? (c & 1) == 0 : c < half;
+      const long long at = static_cast<long long>(p) * half + col;
+      const double o = static_cast<double>(to_f32(k[to])) * a.rsin[at];
+      x[i] = x[i] * a.rcos[at] + (first ? o : -o);
+    }
+    ss = fma(x[i], x[i], ss);
+  }
+#pragma unroll
+  for (int o = M::LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  const double rstd = 1.0 / sqrt(ss / D + static_cast<double>(a.eps));
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) x[i] = x[i] * rstd * (a.gk ? a.gk[c0 + i] : 1.0f);
+  return quantise_f64<D>(x, g);
+}
+
+// What fp32 arithmetic may leave an entry off by, as a multiple of the row's
+// largest: rotation, norm and gain are some five roundings of 2^-24.
+constexpr float kKeyErr = 8.0f * 5.9604645e-8f;
+constexpr float kMixErr = 3.0f * 5.9604645e-8f;
 
 // Lanes as in the other row-wise kernels: LPR lanes hold one row of D
 // channels, 16 bytes each, and a warp works on RPI rows (token, head) at a
@@ -183,6 +277,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) append_kernel(const __grid_con
 #pragma unroll
     for (int i = 0; i < EPL; ++i) x[i] = x[i] * rstd * gk[i];
     // value: value-embedding mix
+    float mix = 0.f, e[EPL] = {};
     if (a.ve != nullptr) {
       float gate = 1.0f;
       if (a.gw != nullptr) {
@@ -197,16 +292,52 @@ __global__ void __launch_bounds__(kRowWarps * 32) append_kernel(const __grid_con
       }
       const int tok = on ? a.tok[n] : 0;
       if (on && tok >= 0 && tok < a.vocab) {
-        float e[EPL];
         unpack16(ld16(a.ve + (static_cast<long long>(tok) * Hkv + h) * D + c0), e);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) y[i] = fmaf(a.ve_scale * gate, e[i], y[i]);
+        mix = gate;
       } else if (on) {
         bad |= DEV_ERR_TOKEN;
       }
     }
-    const Group gk4 = group_scale<D>(x), gv4 = group_scale<D>(y);
-    const uint32_t wk = quantise_lane<D>(x, gk4), wv = quantise_lane<D>(y, gv4);
+    float slack, gap = INFINITY;
+    bool near;
+    Group gk4 = group_scale<D>(x, kKeyErr, slack, near);
+    uint32_t wk = quantise_lane<D>(x, gk4, gap);
+    const unsigned rows_mask = M::LPR == 32 ? 0xffffffffu : ((1u << M::LPR) - 1u) << (lane / M::LPR * M::LPR);
+    unsigned close = __ballot_sync(0xffffffffu, on && (near || gap <= slack));
+    if (close) {
+      Group g2;
+      const uint32_t w2 = key_f64<D>(a, row, p, on, g2);
+      if (close & rows_mask) {
+        wk = w2;
+        gk4 = g2;
+      }
+    }
+    Group gv4;
+    uint32_t wv;
+    if (a.ve == nullptr) {
+      gv4 = group_scale<D>(y, 0.f, slack, near);
+      wv = quantise_lane<D>(y, gv4, gap);
+    } else {
+      float v[EPL];
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[i] = fmaf(a.ve_scale * mix, e[i], y[i]);
+      gap = INFINITY;
+      gv4 = group_scale<D>(v, kMixErr, slack, near);
+      wv = quantise_lane<D>(v, gv4, gap);
+      close = __ballot_sync(0xffffffffu, on && (near || gap <= slack));
+      if (close) {
+        double v64[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          v64[i] = static_cast<double>(y[i]) + static_cast<double>(a.ve_scale) * mix * static_cast<double>(e[i]);
+        Group g2;
+        const uint32_t w2 = quantise_f64<D>(v64, g2);
+        if (close & rows_mask) {
+          wv = w2;
+          gv4 = g2;
+        }
+      }
+    }
     if (bad && cl == 0 && a.status) atomicOr(a.status, bad);
     if (!on) continue;
     uint8_t* tile = tile_of<D>(a.c, slot, h);
