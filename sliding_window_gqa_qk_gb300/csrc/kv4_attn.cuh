@@ -47,7 +47,9 @@ namespace swa {
 namespace kv4 {
 
 constexpr int kAttnWarps = 4;
-constexpr int kStages = 4;               // tiles in flight per warp
+constexpr int kStages = 2;               // steps of two tiles in flight per warp
+// P in fp32 calls: a third term, or the second's rounding would show in o
+constexpr bool kThreeTerms = sizeof(elem_t) == 4;
 constexpr int kColQ = 4;                 // query heads of one 8-column operand
 constexpr int kAttnCtas = 152 * 8;       // CTAs aimed at: two rounds of the four a GB300's SM holds
 constexpr int kMinChunk = 16, kMaxChunk = 128;   // tiles of a CTA
@@ -79,7 +81,7 @@ struct AttnShape {
 // Shared memory of a CTA: rings (re-used for the join), queries, barriers.
 template <int D, int NT>
 struct AttnSmem {
-  static constexpr int ring = kAttnWarps * kStages * AttnShape<D>::TB;
+  static constexpr int ring = kAttnWarps * kStages * 2 * AttnShape<D>::TB;
   static constexpr int join = kAttnWarps * NT * kColQ * (D + 2) * 4;
   static constexpr int bars = (ring > join ? ring : join + 127) / 128 * 128;
   static constexpr int qs = bars + kAttnWarps * kStages * 8;
@@ -201,8 +203,9 @@ __device__ __forceinline__ void query_row(const AttnArgs& a, const elem_t* q, in
     const float v = x[i] * up;
     const __half hi = __float2half_rn(v);
     const __half lo = __float2half_rn(v - __half2float(hi));
-    dst[c0 + i] = hi;
-    dst[D + c0 + i] = lo;
+    const int at = ((c0 + i) & ~7) + ((c0 + i) & 3) * 2 + (((c0 + i) >> 2) & 1);   // pairs (i, i + 4) side by side
+    dst[at] = hi;
+    dst[D + at] = lo;
     sum += v;
   }
   // lanes of one group: 64 / E
@@ -255,40 +258,36 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 ? 4 : 2) attn_kernel(
   if (tid == 0) flags[0] = 0;
   __syncwarp();
 
-  // Tile n of this warp is t0 + wid + n * kAttnWarps; its page is looked up
-  // 32 tiles at a time, a lane a tile.
-  const int n_mine = t1 - t0 > wid ? (t1 - t0 - wid + kAttnWarps - 1) / kAttnWarps : 0;
-  uint8_t* ring = smem + wid * kStages * S::TB;
+  // Step n of this warp is the tiles t0 + 2 (wid + n * kAttnWarps) and the one
+  // behind it, which share a stage. Pages are looked up 32 tiles (16 steps)
+  // at a time, a lane a tile.
+  const int n_mine = (t1 - t0 + 1) / 2 > wid ? ((t1 - t0 + 1) / 2 - wid + kAttnWarps - 1) / kAttnWarps : 0;
+  uint8_t* ring = smem + wid * kStages * 2 * S::TB;
   const uint32_t ring_u = smem_u32(ring);
   const int per_page = a.c.page / kTile;
-  int pages = -1, within = 0;
-  uint32_t gone = 0;       // per stage: its tile's page is not there
+  const long long head_off = static_cast<long long>(h) * per_page;
+  long long tile_at = -1;  // of the lane's tile in the cache; -1: none
+  uint32_t gone = 0;       // two bits per stage: tiles that are not there
   auto issue = [&](int n) {
-    if ((n & 31) == 0) {
-      const int t = t0 + wid + (n + lane) * kAttnWarps;
-      pages = -1;
+    if ((n & 15) == 0) {
+      const int t = t0 + 2 * (wid + (n + (lane >> 1)) * kAttnWarps) + (lane & 1);
+      tile_at = -1;
       if (t < t1) {
         const int pi = t / per_page;
-        within = t - pi * per_page;
-        pages = a.table[static_cast<long long>(b) * a.max_pages + pi];
-        if (pages < 0 || pages >= a.c.n_pages) {
-          pages = -1;
+        const int pg = a.table[static_cast<long long>(b) * a.max_pages + pi];
+        if (pg >= 0 && pg < a.c.n_pages)
+          tile_at = static_cast<long long>(pg) * a.c.Hkv * per_page + head_off + (t - pi * per_page);
+        else
           bad = DEV_ERR_BOUNDS;
-        }
       }
     }
-    const int pg = __shfl_sync(0xffffffffu, pages, n & 31), in = __shfl_sync(0xffffffffu, within, n & 31);
     const int st = n % kStages;
-    gone = (gone & ~(1u << st)) | (pg < 0 ? 1u << st : 0u);
-    if (lane == 0) {
-      if (pg >= 0) {
-        const uint8_t* src = a.c.data + ((static_cast<long long>(pg) * a.c.Hkv + h) * per_page + in) * S::TB;
-        mbar_arrive_expect_tx(bars + 8 * st, S::TB);
-        bulk_load(ring_u + st * S::TB, src, S::TB, bars + 8 * st);
-      } else {
-        mbar_arrive(bars + 8 * st);      // nothing to come, but the phase goes on
-      }
-    }
+    const long long at = __shfl_sync(0xffffffffu, tile_at, ((2 * n) & 31) + (lane & 1));
+    const uint32_t there = __ballot_sync(0xffffffffu, at >= 0) & 3u;
+    gone = (gone & ~(3u << (2 * st))) | ((there ^ 3u) << (2 * st));
+    if (lane == 0) mbar_arrive_expect_tx(bars + 8 * st, __popc(there) * S::TB);
+    __syncwarp();
+    if (lane < 2 && at >= 0) bulk_load(ring_u + (st * 2 + lane) * S::TB, a.c.data + at * S::TB, S::TB, bars + 8 * st);
   };
   for (int n = 0; n < kStages && n < n_mine; ++n) issue(n);
 
@@ -302,12 +301,12 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 ? 4 : 2) attn_kernel(
   float qfac[NT], qsum[NT][NG];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const uint16_t* row = reinterpret_cast<const uint16_t*>(qs) + (nt * kColQ + (r >> 1)) * 2 * D + (r & 1) * D;
+    const __half* row = qs + (nt * kColQ + (r >> 1)) * 2 * D + (r & 1) * D;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const uint16_t* c = row + (w / 2) * 64 + j * 16 + (w & 1) * 8;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) qb[nt][2 * w + i / 2][i & 1] = c[i] | static_cast<uint32_t>(c[i + 4]) << 16;
+      const uint4 c = *reinterpret_cast<const uint4*>(row + (w / 2) * 64 + j * 16 + (w & 1) * 8);
+      qb[nt][2 * w][0] = c.x; qb[nt][2 * w][1] = c.y;
+      qb[nt][2 * w + 1][0] = c.z; qb[nt][2 * w + 1][1] = c.w;
     }
     qfac[nt] = qf[(nt * kColQ + j) * 4];
 #pragma unroll
@@ -323,110 +322,130 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 ? 4 : 2) attn_kernel(
   for (; n < n_mine; ++n) {
     const int st = n % kStages;
     if (!mbar_wait_warp(bars + 8 * st, (n / kStages) & 1, ctl)) break;
-    if (!(gone >> st & 1u)) {
-      const uint8_t* tile = ring + st * S::TB;
-      const int key0 = (t0 + wid + n * kAttnWarps) * kTile;
-      float s[NT][2];      // logits (base 2) of keys r and r + 8
-      {
-        uint32_t ka[W], kb[W];
-        ld_words<W>(tile + r * (D / 2) + j * (D / 8), ka);
-        ld_words<W>(tile + (r + 8) * (D / 2) + j * (D / 8), kb);
-        float sa[NG], za[NG], sb[NG], zb[NG];
-        ld_scales<NG>(tile + 16 * D + r * (4 * NG), sa, za);
-        ld_scales<NG>(tile + 16 * D + (r + 8) * (4 * NG), sb, zb);
-        float d[NT][NG][4] = {};
+    const uint8_t* tile = ring + st * 2 * S::TB;
+    const int key0 = (t0 + 2 * (wid + n * kAttnWarps)) * kTile;
+    float s[2][NT][2];       // logits (base 2): tile, column, key r or r + 8
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-          uint32_t x[4], y[4];
-          widen_f16(ka[w], x);
-          widen_f16(kb[w], y);
+    for (int q = 0; q < 2; ++q) {
+      uint32_t ka[W], kb[W];
+      ld_words<W>(tile + q * S::TB + r * (D / 2) + j * (D / 8), ka);
+      ld_words<W>(tile + q * S::TB + (r + 8) * (D / 2) + j * (D / 8), kb);
+      float sa[NG], za[NG], sb[NG], zb[NG];
+      ld_scales<NG>(tile + q * S::TB + 16 * D + r * (4 * NG), sa, za);
+      ld_scales<NG>(tile + q * S::TB + 16 * D + (r + 8) * (4 * NG), sb, zb);
+      float d[NT][NG][4] = {};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_f16(d[nt][w / 2], x[0], y[0], x[1], y[1], qb[nt][2 * w][0], qb[nt][2 * w][1]);
-            mma_f16(d[nt][w / 2], x[2], y[2], x[3], y[3], qb[nt][2 * w + 1][0], qb[nt][2 * w + 1][1]);
-          }
-        }
+      for (int w = 0; w < W; ++w) {
+        uint32_t x[4], y[4];
+        widen_f16(ka[w], x);
+        widen_f16(kb[w], y);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float u = 0.f, v = 0.f;
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            u = fmaf(sa[g], d[nt][g][0] + d[nt][g][1], fmaf(za[g], qsum[nt][g], u));
-            v = fmaf(sb[g], d[nt][g][2] + d[nt][g][3], fmaf(zb[g], qsum[nt][g], v));
-          }
-          s[nt][0] = u * qfac[nt];
-          s[nt][1] = v * qfac[nt];
+          mma_f16(d[nt][w / 2], x[0], y[0], x[1], y[1], qb[nt][2 * w][0], qb[nt][2 * w][1]);
+          mma_f16(d[nt][w / 2], x[2], y[2], x[3], y[3], qb[nt][2 * w + 1][0], qb[nt][2 * w + 1][1]);
         }
       }
-      float sv[2][NG], zv[2][NG];
-      ld_scales<NG>(tile + 17 * D + r * (4 * NG), sv[0], zv[0]);
-      ld_scales<NG>(tile + 17 * D + (r + 8) * (4 * NG), sv[1], zv[1]);
-      if (key0 < lo || key0 + kTile > len) {       // the first or last tile: keys outside count nothing
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float u = 0.f, v = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          u = fmaf(sa[g], d[nt][g][0] + d[nt][g][1], fmaf(za[g], qsum[nt][g], u));
+          v = fmaf(sb[g], d[nt][g][2] + d[nt][g][3], fmaf(zb[g], qsum[nt][g], v));
+        }
+        s[q][nt][0] = u * qfac[nt];
+        s[q][nt][1] = v * qfac[nt];
+      }
+    }
+    float sv[2][2][NG], zv[2][2][NG];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      ld_scales<NG>(tile + q * S::TB + 17 * D + r * (4 * NG), sv[q][0], zv[q][0]);
+      ld_scales<NG>(tile + q * S::TB + 17 * D + (r + 8) * (4 * NG), sv[q][1], zv[q][1]);
+    }
+    const uint32_t miss = gone >> (2 * st) & 3u;
+    if (key0 < lo || key0 + 2 * kTile > len || miss) {       // keys outside, or not there, count nothing
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int key = key0 + r + 8 * i;
-          if (key < lo || key >= len) {
+          const int key = key0 + q * kTile + r + 8 * i;
+          if (key < lo || key >= len || (miss >> q & 1u)) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) s[nt][i] = -INFINITY;
+            for (int nt = 0; nt < NT; ++nt) s[q][nt][i] = -INFINITY;
 #pragma unroll
-            for (int g = 0; g < NG; ++g) sv[i][g] = zv[i][g] = 0.f;
+            for (int g = 0; g < NG; ++g) sv[q][i][g] = zv[q][i][g] = 0.f;
           }
         }
       }
-      bool raise = false;
+    }
+    float top[NT];
+    bool raise = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) raise |= fmaxf(s[nt][0], s[nt][1]) > m[nt] + 8.f;
-      if (__any_sync(0xffffffffu, raise)) {
+    for (int nt = 0; nt < NT; ++nt) {
+      top[nt] = fmaxf(fmax3(s[0][nt][0], s[0][nt][1], s[1][nt][0]), s[1][nt][1]);
+      raise |= top[nt] > m[nt] + 8.f;
+    }
+    if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float x = fmaxf(s[nt][0], s[nt][1]);
+      for (int nt = 0; nt < NT; ++nt) {
+        float x = top[nt];
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-          const float mn = fmaxf(m[nt], x), al = ex2_approx(m[nt] - mn);
-          m[nt] = mn;
-          l[nt] *= al;
+        for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+        const float mn = fmaxf(m[nt], x), al = ex2_approx(m[nt] - mn);
+        m[nt] = mn;
+        l[nt] *= al;
 #pragma unroll
-          for (int g = 0; g < NG; ++g) zs[nt][g] *= al;
+        for (int g = 0; g < NG; ++g) zs[nt][g] *= al;
 #pragma unroll
-          for (int i = 0; i < 2 * W; ++i)
+        for (int i = 0; i < 2 * W; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) acc[nt][i][k] *= al;
-        }
+          for (int k = 0; k < 4; ++k) acc[nt][i][k] *= al;
       }
-      uint32_t pb[NT][NG][2];
+    }
+    uint32_t va[2][W], vb[2][W];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      ld_words<W>(tile + q * S::TB + 8 * D + j * D + r * (D / 8), va[q]);
+      ld_words<W>(tile + q * S::TB + 8 * D + (j + 4) * D + r * (D / 8), vb[q]);
+    }
+    __syncwarp();
+    if (n + kStages < n_mine) issue(n + kStages);   // every lane has its words
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      uint32_t pb[NT][NG][2], pc[NT][NG][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float p = ex2_approx(s[nt][i] - m[nt]);
+          const float p = ex2_approx(s[q][nt][i] - m[nt]);
           l[nt] += p;
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
-            zs[nt][g] = fmaf(p, zv[i][g], zs[nt][g]);
-            const float w = p * sv[i][g];
+            zs[nt][g] = fmaf(p, zv[q][i][g], zs[nt][g]);
+            const float w = p * sv[q][i][g];
             const float hi = __uint_as_float(pack_bf16x2(0.f, w));       // rounded, in the high half
-            pb[nt][g][i] = transpose8(pack_bf16x2(hi, w - hi));
+            const uint32_t both = pack_bf16x2(hi, w - hi);
+            pb[nt][g][i] = transpose8(both);
+            if (kThreeTerms) pc[nt][g][i] = transpose8(pack_bf16x2(w - hi - __uint_as_float(both & 0xFFFF0000u), 0.f));
           }
         }
       }
-      uint32_t va[W], vb[W];
-      ld_words<W>(tile + 8 * D + j * D + r * (D / 8), va);
-      ld_words<W>(tile + 8 * D + (j + 4) * D + r * (D / 8), vb);
-      __syncwarp();
-      if (n + kStages < n_mine) issue(n + kStages);   // every lane has its words
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         uint32_t x[4], y[4];
-        widen_bf16(va[w], x);
-        widen_bf16(vb[w], y);
+        widen_bf16(va[q][w], x);
+        widen_bf16(vb[q][w], y);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           mma_bf16(acc[nt][2 * w], x[0], x[1], y[0], y[1], pb[nt][w / 2][0], pb[nt][w / 2][1]);
           mma_bf16(acc[nt][2 * w + 1], x[2], x[3], y[2], y[3], pb[nt][w / 2][0], pb[nt][w / 2][1]);
+          if (kThreeTerms) {
+            mma_bf16(acc[nt][2 * w], x[0], x[1], y[0], y[1], pc[nt][w / 2][0], pc[nt][w / 2][1]);
+            mma_bf16(acc[nt][2 * w + 1], x[2], x[3], y[2], y[3], pc[nt][w / 2][0], pc[nt][w / 2][1]);
+          }
         }
       }
-    } else if (n + kStages < n_mine) {
-      issue(n + kStages);
     }
   }
   // a wait that ran out: the copies still on their way land before the memory is used again
@@ -541,7 +560,7 @@ inline AttnSplit attn_split(int B, int Hq, int Hkv, int page, int max_pages, int
   const long long tiles = (keys + kTile - 1) / kTile;
   long long c = (tiles * s.items + kAttnCtas - 1) / kAttnCtas;
   c = c < kMinChunk ? kMinChunk : (c > kMaxChunk ? kMaxChunk : c);
-  c = (c + kAttnWarps - 1) / kAttnWarps * kAttnWarps;
+  c = (c + 2 * kAttnWarps - 1) / (2 * kAttnWarps) * (2 * kAttnWarps);
   s.chunk = static_cast<int>(c);
   s.splits = static_cast<int>((tiles + c - 1) / c);
   return s;
