@@ -96,6 +96,13 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// the same onto zeros
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -108,6 +115,12 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
+// (x & mask) | bits as the one instruction it is
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(mask), "r"(bits));
+  return r;
+}
 // Eight numbers of a word as four fp16 pairs (number i, number i + 4) - 8.
 __device__ __forceinline__ void widen_f16(uint32_t x, uint32_t (&h)[4]) {
   const __half2 low = __floats2half2_rn(-1032.f, -1032.f), sixteenth = __floats2half2_rn(0.0625f, 0.0625f),
@@ -115,17 +128,17 @@ __device__ __forceinline__ void widen_f16(uint32_t x, uint32_t (&h)[4]) {
   auto h2 = [](uint32_t v) { return *reinterpret_cast<__half2*>(&v); };
   auto u = [](__half2 v) { return *reinterpret_cast<uint32_t*>(&v); };
   const uint32_t y = x >> 8;
-  h[0] = u(__hadd2(h2((x & 0x000F000Fu) | 0x64006400u), low));                  // 1024 + n
-  h[1] = u(__hfma2(h2((x & 0x00F000F0u) | 0x64006400u), sixteenth, high));     // 1024 + 16 n
-  h[2] = u(__hadd2(h2((y & 0x000F000Fu) | 0x64006400u), low));
-  h[3] = u(__hfma2(h2((y & 0x00F000F0u) | 0x64006400u), sixteenth, high));
+  h[0] = u(__hadd2(h2(and_or(x, 0x000F000Fu, 0x64006400u)), low));                  // 1024 + n
+  h[1] = u(__hfma2(h2(and_or(x, 0x00F000F0u, 0x64006400u)), sixteenth, high));     // 1024 + 16 n
+  h[2] = u(__hadd2(h2(and_or(y, 0x000F000Fu, 0x64006400u)), low));
+  h[3] = u(__hfma2(h2(and_or(y, 0x00F000F0u, 0x64006400u)), sixteenth, high));
 }
 // The same as bf16 (whose 7 fraction bits leave no place for the second form).
 __device__ __forceinline__ void widen_bf16(uint32_t x, uint32_t (&h)[4]) {
   const __nv_bfloat162 off = __floats2bfloat162_rn(-136.f, -136.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t v = ((x >> (4 * i)) & 0x000F000Fu) | 0x43004300u;                  // 128 + n
+    uint32_t v = and_or(x >> (4 * i), 0x000F000Fu, 0x43004300u);                    // 128 + n
     const __nv_bfloat162 r = __hadd2(*reinterpret_cast<__nv_bfloat162*>(&v), off);
     h[i] = *reinterpret_cast<const uint32_t*>(&r);
   }
@@ -333,7 +346,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 ? 4 : 2) attn_kernel(
       float sa[NG], za[NG], sb[NG], zb[NG];
       ld_scales<NG>(tile + q * S::TB + 16 * D + r * (4 * NG), sa, za);
       ld_scales<NG>(tile + q * S::TB + 16 * D + (r + 8) * (4 * NG), sb, zb);
-      float d[NT][NG][4] = {};
+      float d[NT][NG][4];
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         uint32_t x[4], y[4];
@@ -341,7 +354,10 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 ? 4 : 2) attn_kernel(
         widen_f16(kb[w], y);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(d[nt][w / 2], x[0], y[0], x[1], y[1], qb[nt][2 * w][0], qb[nt][2 * w][1]);
+          if (w & 1)
+            mma_f16(d[nt][w / 2], x[0], y[0], x[1], y[1], qb[nt][2 * w][0], qb[nt][2 * w][1]);
+          else
+            mma_f16_first(d[nt][w / 2], x[0], y[0], x[1], y[1], qb[nt][2 * w][0], qb[nt][2 * w][1]);
           mma_f16(d[nt][w / 2], x[2], y[2], x[3], y[3], qb[nt][2 * w + 1][0], qb[nt][2 * w + 1][1]);
         }
       }
