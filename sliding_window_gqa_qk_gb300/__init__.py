@@ -545,7 +545,8 @@ _SCALINGS = {"none": SWA_ROPE_PLAIN, "linear": SWA_ROPE_LINEAR, "ntk": SWA_ROPE_
 _F32, _BF16, _I32, _I64, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8
 # torch's own lookup of the current stream's handle by device index; the
 # public one builds a Stream object each time (2.9 us against 0.1 us)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _at(name, t, dtype, shape, device):
@@ -584,22 +585,27 @@ def _ws_at(ws, device):
     return _at("workspace", ws, _U8, (n,), device), n
 
 
-def _run(device, stream, call):
-    """call(handle of the stream) with ``device`` current, and with ``stream``
-    (a torch stream or a raw handle; None: the current one), so that what the
-    call allocates belongs to the stream it runs on."""
+def _stream_here(device, stream):
+    """The current stream's handle, where ``device`` is the current device and
+    no other stream is asked for; else None (see _there)."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return _raw_stream(device.index)
+    return None
+
+
+def _there(device, stream, call):
+    """call() with ``device`` current, and with ``stream`` (a torch stream or a
+    raw handle) if one is given, so that what it allocates belongs to the
+    stream it runs on."""
     if device.type != "cuda":
         raise ValueError(f"the tensors are on {device}, not on a GPU")
-    here = device.index is None or device.index == torch.cuda.current_device()
-    if stream is None and here and _raw_stream is not None:
-        return call(_raw_stream(device.index if device.index is not None else torch.cuda.current_device()))
     with torch.cuda.device(device):
         if stream is None:
-            return call(torch.cuda.current_stream().cuda_stream)
+            return call()
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
         with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+            return call()
 
 
 def rope_tables(rows: int, rot: int, *, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -615,17 +621,23 @@ def rope_tables(rows: int, rot: int, *, base: float = 10000.0, scaling: str = "n
         raise ValueError(f"scaling: one of {sorted(_SCALINGS)} is expected, got {scaling!r}")
     if rows < 0 or rot < 0:
         raise ValueError("rows, rot: not below 0")
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    index = torch.cuda.current_device()
+    device = torch.device("cuda", index) if device is None else torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", index)
+    st = _stream_here(device, stream)
+    if st is None:
+        return _there(device, stream, lambda: rope_tables(
+            rows, rot, base=base, scaling=scaling, factor=factor, orig_len=orig_len, slow=slow, fast=fast,
+            amplitude=amplitude, first=first, device=device))
     f = swa_rope_freq(rot, _SCALINGS[scaling], base, factor, orig_len, slow, fast, amplitude)
-
-    def call(st):
-        cos = torch.empty((rows, rot // 2), dtype=_F32, device=device)
-        sin = torch.empty_like(cos)
-        s = load("bf16").swa_rope_tables(ctypes.byref(f), first, rows, cos.data_ptr() or 256, sin.data_ptr() or 256, st)
-        if s:
-            raise SwaError(s, "swa_rope_tables")
-        return cos, sin
-    return _run(device, stream, call)
+    cos = torch.empty((rows, rot // 2), dtype=_F32, device=device)
+    sin = torch.empty_like(cos)
+    # (an empty tensor has no address; nothing is written then)
+    s = load("bf16").swa_rope_tables(f, first, rows, cos.data_ptr() or 256, sin.data_ptr() or 256, st)
+    if s:
+        raise SwaError(s, "swa_rope_tables")
+    return cos, sin
 
 
 def rope_apply(q, k, rope, *, pos=None, interleaved: bool = False, inverse: bool = False, out=None, workspace=None,
@@ -651,17 +663,21 @@ def rope_apply(q, k, rope, *, pos=None, interleaved: bool = False, inverse: bool
     pa = _at("pos", pos, _I32, (B, T), dev)
     r = _rope_at(rope, interleaved, dev)
     ws, nws = _ws_at(workspace, dev)
-    p = make_params(B, T, Hq, Hkv, d)
-
-    def call(st):
-        qy = torch.empty_like(q) if q is not None and qo is None else qo
-        ky = torch.empty_like(k) if k is not None and ko is None else ko
-        s = lib.swa_rope_apply(ctypes.byref(p), _ref(r), pa, qa, ka, qy.data_ptr() if qoa is None and qy is not None else qoa,
-                               ky.data_ptr() if koa is None and ky is not None else koa, 1 if inverse else 0, ws, nws, st)
-        if s:
-            raise SwaError(s, "swa_rope_apply")
-        return qy, ky
-    return _run(dev, stream, call)
+    st = _stream_here(dev, stream)
+    if st is None:
+        return _there(dev, stream, lambda: rope_apply(q, k, rope, pos=pos, interleaved=interleaved, inverse=inverse, out=out,
+                                                      workspace=workspace))
+    if q is not None and qo is None:
+        qo = torch.empty_like(q)
+        qoa = qo.data_ptr()
+    if k is not None and ko is None:
+        ko = torch.empty_like(k)
+        koa = ko.data_ptr()
+    s = lib.swa_rope_apply(swa_params(B, T, Hq, Hkv, d, -1, 1, 0.0, 0.0, 0.0, 0), r, pa, qa, ka, qoa, koa,
+                           1 if inverse else 0, ws, nws, st)
+    if s:
+        raise SwaError(s, "swa_rope_apply")
+    return qo, ko
 
 
 def _cache_dims(cache):
@@ -689,11 +705,12 @@ def new_kv4_workspace(cache, B: int, Hq: int, *, max_pages: int, window: int = -
     if n == 0:
         raise SwaError(SWA_ERR_INVALID_ARG, "workspace size")
 
-    def call(st):
+
+    def call():
         ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
-        _check(swa_kv4_workspace_init(ws, n, st, kind), "workspace init")
+        _check(swa_kv4_workspace_init(ws, n, None, kind), "workspace init")
         return ws
-    return _run(cache.device, stream, call)
+    return _there(cache.device, stream, call)
 
 
 def kv4_plan(lens, new_lens, table, free_pages, free_head, *, page: int, n_pages: int, n_tokens: Optional[int] = None,
@@ -721,22 +738,24 @@ def kv4_plan(lens, new_lens, table, free_pages, free_head, *, page: int, n_pages
     if n_tokens < 0:
         raise ValueError("n_tokens: not below 0")
 
-    def call(st):
-        # one buffer for all outputs: slots first, then the int32 ones, 16-byte aligned pieces
-        pad = (n_tokens + 3) // 4 * 4
-        ints = torch.empty(4 * pad + 2 * B + 2, dtype=_I32, device=dev)
-        base = ints.data_ptr()
-        slot, pos, row, cu, lens_out, head = torch.split(ints, (2 * pad, pad, pad, B + 1, B, 1))
-        s = load("bf16").swa_kv4_plan(n_pages, page, B, max_pages, la, na, ta, fa, n_free, ha, n_tokens, base,
-                                      base + 8 * pad, base + 12 * pad, base + 16 * pad, base + 16 * pad + 4 * (B + 1),
-                                      base + 16 * pad + 4 * (2 * B + 1), ws, nws, st)
-        if s:
-            raise SwaError(s, "swa_kv4_plan")
-        slot = slot.view(_I64)
-        if pad != n_tokens:
-            slot, pos, row = slot[:n_tokens], pos[:n_tokens], row[:n_tokens]
-        return {"slot": slot, "pos": pos, "row": row, "cu": cu, "lens": lens_out, "free_head": head}
-    return _run(dev, stream, call)
+    st = _stream_here(dev, stream)
+    if st is None:
+        return _there(dev, stream, lambda: kv4_plan(lens, new_lens, table, free_pages, free_head, page=page, n_pages=n_pages,
+                                                    n_tokens=n_tokens, workspace=workspace))
+    # one buffer for all outputs: slots first, then the int32 ones, in 16-byte aligned pieces
+    pad = (n_tokens + 3) // 4 * 4
+    ints = torch.empty((4 * pad + 2 * B + 2,), dtype=_I32, device=dev)
+    at = ints.data_ptr()
+    s = load("bf16").swa_kv4_plan(n_pages, page, B, max_pages, la, na, ta, fa, n_free, ha, n_tokens, at, at + 8 * pad,
+                                  at + 12 * pad, at + 16 * pad, at + 16 * pad + 4 * (B + 1), at + 16 * pad + 4 * (2 * B + 1),
+                                  ws, nws, st)
+    if s:
+        raise SwaError(s, "swa_kv4_plan")
+    slot, pos, row, cu, lens_out, head = ints.split_with_sizes((2 * pad, pad, pad, B + 1, B, 1))
+    slot = slot.view(_I64)
+    if pad != n_tokens:
+        slot, pos, row = slot[:n_tokens], pos[:n_tokens], row[:n_tokens]
+    return {"slot": slot, "pos": pos, "row": row, "cu": cu, "lens": lens_out, "free_head": head}
 
 
 def kv4_append(cache, k, v, slot, *, pos=None, rope=None, interleaved: bool = False, gk=None, eps: float = 1e-6,
@@ -771,14 +790,15 @@ def kv4_append(cache, k, v, slot, *, pos=None, rope=None, interleaved: bool = Fa
             ex = make_extras(None, gate_x, gate_w)
     r = _rope_at(rope, interleaved, dev)
     ws, nws = _ws_at(workspace, dev)
-    p = swa_params(B, T, Hkv, Hkv, d, -1, 1, 0.0, eps, ve_scale, vocab)
-    c = swa_kv4_cache(cache.data_ptr(), n_pages, page)
-
-    def call(st):
-        s = lib.swa_kv4_append(ctypes.byref(p), _ref(ex), ctypes.byref(c), _ref(r), ka, va, ga, ea, ta, gta, pa, sa, ws, nws, st)
-        if s:
-            raise SwaError(s, "swa_kv4_append")
-    _run(dev, stream, call)
+    st = _stream_here(dev, stream)
+    if st is None:
+        return _there(dev, stream, lambda: kv4_append(
+            cache, k, v, slot, pos=pos, rope=rope, interleaved=interleaved, gk=gk, eps=eps, ve=ve, tok=tok, ve_gate=ve_gate,
+            ve_scale=ve_scale, gate_x=gate_x, gate_w=gate_w, workspace=workspace))
+    s = lib.swa_kv4_append(swa_params(B, T, Hkv, Hkv, d, -1, 1, 0.0, eps, ve_scale, vocab), ex,
+                           swa_kv4_cache(cache.data_ptr(), n_pages, page), r, ka, va, ga, ea, ta, gta, pa, sa, ws, nws, st)
+    if s:
+        raise SwaError(s, "swa_kv4_append")
 
 
 def kv4_read(cache, slot, *, dtype=torch.bfloat16, workspace=None, stream=None):
@@ -793,16 +813,16 @@ def kv4_read(cache, slot, *, dtype=torch.bfloat16, workspace=None, stream=None):
     B, T = slot.shape
     sa = _at("slot", slot, _I64, (B, T), dev)
     ws, nws = _ws_at(workspace, dev)
-    p, c = swa_params(B, T, Hkv, Hkv, d, -1, 1, 0.0, 0.0, 0.0, 0), swa_kv4_cache(cache.data_ptr(), n_pages, page)
-
-    def call(st):
-        k = torch.empty((B, T, Hkv, d), dtype=dtype, device=dev)
-        v = torch.empty_like(k)
-        s = lib.swa_kv4_read(ctypes.byref(p), ctypes.byref(c), sa, k.data_ptr(), v.data_ptr(), ws, nws, st)
-        if s:
-            raise SwaError(s, "swa_kv4_read")
-        return k, v
-    return _run(dev, stream, call)
+    st = _stream_here(dev, stream)
+    if st is None:
+        return _there(dev, stream, lambda: kv4_read(cache, slot, dtype=dtype, workspace=workspace))
+    k = torch.empty((B, T, Hkv, d), dtype=dtype, device=dev)
+    v = torch.empty_like(k)
+    s = lib.swa_kv4_read(swa_params(B, T, Hkv, Hkv, d, -1, 1, 0.0, 0.0, 0.0, 0),
+                         swa_kv4_cache(cache.data_ptr(), n_pages, page), sa, k.data_ptr(), v.data_ptr(), ws, nws, st)
+    if s:
+        raise SwaError(s, "swa_kv4_read")
+    return k, v
 
 
 def kv4_attention(cache, q, table, lens, *, rope=None, interleaved: bool = False, gq=None, window: int = -1,
@@ -823,19 +843,19 @@ def kv4_attention(cache, q, table, lens, *, rope=None, interleaved: bool = False
     qa, ga = _at("q", q, dt, (B, Hq, d), dev), _at("gq", gq, _F32, (d,), dev)
     ta, la = _at("table", table, _I32, (B, max_pages), dev), _at("lens", lens, _I32, (B,), dev)
     r = _rope_at(rope, interleaved, dev)
-    p = swa_params(B, 1, Hq, Hkv, d, window, 1, softmax_scale, eps, 0.0, 0)
-    c = swa_kv4_cache(cache.data_ptr(), n_pages, page)
-
-    def call(st):
-        w = workspace
-        if w is None:
-            w = new_kv4_workspace(cache, B, Hq, max_pages=max_pages, window=window, kind=kind)
-        ws, nws = _ws_at(w, dev)
-        o = torch.empty_like(q)
-        lse = torch.empty((B, Hq), dtype=_F32, device=dev)
-        s = load(kind).swa_kv4_attn(ctypes.byref(p), None, ctypes.byref(c), _ref(r), qa, ga, ta, max_pages, la, o.data_ptr(),
-                                    lse.data_ptr(), ws, nws, st)
-        if s:
-            raise SwaError(s, "swa_kv4_attn")
-        return o, lse
-    return _run(dev, stream, call)
+    st = _stream_here(dev, stream)
+    if st is None:
+        return _there(dev, stream, lambda: kv4_attention(
+            cache, q, table, lens, rope=rope, interleaved=interleaved, gq=gq, window=window, softmax_scale=softmax_scale,
+            eps=eps, workspace=workspace))
+    if workspace is None:
+        workspace = new_kv4_workspace(cache, B, Hq, max_pages=max_pages, window=window, kind=kind)
+    ws, nws = _ws_at(workspace, dev)
+    o = torch.empty_like(q)
+    lse = torch.empty((B, Hq), dtype=_F32, device=dev)
+    s = load(kind).swa_kv4_attn(swa_params(B, 1, Hq, Hkv, d, window, 1, softmax_scale, eps, 0.0, 0), None,
+                                swa_kv4_cache(cache.data_ptr(), n_pages, page), r, qa, ga, ta, max_pages, la, o.data_ptr(),
+                                lse.data_ptr(), ws, nws, st)
+    if s:
+        raise SwaError(s, "swa_kv4_attn")
+    return o, lse

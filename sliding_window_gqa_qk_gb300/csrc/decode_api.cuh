@@ -70,11 +70,25 @@ Kv4Ws kv4_ws(const kv4::AttnSplit& s, int d) {
   return w;
 }
 
+// Raises a kernel's shared-memory limit, once per device. `done`: a word per
+// kernel, one bit per device; a device past its bits is set every time.
+swa_status allow_smem(const void* kern, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SWA_ERR_CUDA;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return SWA_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return SWA_ERR_CUDA;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return SWA_OK;
+}
+
 template <int D, int NT, bool kPolled>
 swa_status launch_attn(const kv4::AttnArgs& a, int heads_kv, cudaStream_t st) {
   auto kern = kv4::attn_kernel<D, NT, kPolled>;
   constexpr int smem = kv4::AttnSmem<D, NT>::bytes;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return SWA_ERR_CUDA;
+  static std::atomic<uint64_t> done;
+  const swa_status s = allow_smem(reinterpret_cast<const void*>(kern), smem, done);
+  if (s != SWA_OK) return s;
   kern<<<dim3(a.splits, heads_kv * a.groups, a.B), kv4::kAttnWarps * 32, smem, st>>>(a);
   return launched();
 }
@@ -209,9 +223,10 @@ swa_status swa_kv4_plan(int n_pages, int page, int B, int max_pages, const int32
   a.slot = slot; a.pos = pos; a.row = row; a.cu = cu; a.lens_out = lens_out; a.head_out = head_out;
   a.status = static_cast<uint32_t*>(workspace);
   const size_t smem = (static_cast<size_t>(B) * 3 + 1) * sizeof(int);
-  if (cudaFuncSetAttribute(kv4::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (3 * kv4::kPlanMaxB + 1) * static_cast<int>(sizeof(int))) != cudaSuccess)
-    return SWA_ERR_CUDA;
+  static std::atomic<uint64_t> done;
+  s = allow_smem(reinterpret_cast<const void*>(kv4::plan_kernel), (3 * kv4::kPlanMaxB + 1) * static_cast<int>(sizeof(int)),
+                 done);
+  if (s != SWA_OK) return s;
   const int grid = flat_grid(n_tokens, kv4::kPlanThreads * kv4::kPlanTokens, num_sms());
   kv4::plan_kernel<<<grid, kv4::kPlanThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
   return launched();

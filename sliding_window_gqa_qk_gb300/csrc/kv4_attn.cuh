@@ -52,7 +52,7 @@ constexpr int kStages = 2;               // steps of two tiles in flight per war
 constexpr bool kThreeTerms = sizeof(elem_t) == 4;
 constexpr int kColQ = 4;                 // query heads of one 8-column operand
 constexpr int kAttnCtas = 152 * 8;       // CTAs aimed at: two rounds of the four a GB300's SM holds
-constexpr int kMinChunk = 16, kMaxChunk = 128;   // tiles of a CTA
+constexpr int kMinChunk = 16, kMaxChunk = 256;   // tiles of a CTA
 
 struct AttnArgs {
   Cache c;
@@ -522,9 +522,11 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 ? 4 : 2) attn_kernel(
     }
   }
   if (chunks == 1) return;
-  __threadfence();
   __syncthreads();
-  if (tid == 0) flags[1] = atomicAdd(a.count + item, 1u) == static_cast<unsigned>(chunks - 1);
+  if (tid == 0) {
+    __threadfence();      // after the barrier it covers what the CTA wrote
+    flags[1] = atomicAdd(a.count + item, 1u) == static_cast<unsigned>(chunks - 1);
+  }
   __syncthreads();
   if (!flags[1]) return;
   __threadfence();

@@ -3,6 +3,7 @@
 //
 // Built twice from this file: with SWA_ELEM_FP32 (fp32 SIMT debug library)
 // and without (bf16 tcgen05 library).
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -99,13 +100,20 @@ swa_status check_params(const swa_params* p) {
 }
 
 swa_status check_device() {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> known[kMaxDev];   // 1: a GB300, 2: another GPU (asked once per device)
   int dev = 0, major = 0, minor = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return SWA_ERR_CUDA;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-    return SWA_ERR_CUDA;
-  if (major != 10 || minor != 3) return SWA_ERR_UNSUPPORTED;  // built for sm_103a only
-  return SWA_OK;
+  const bool slot = dev >= 0 && dev < kMaxDev;
+  int k = slot ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (k == 0) {
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+      return SWA_ERR_CUDA;
+    k = major == 10 && minor == 3 ? 1 : 2;  // built for sm_103a only
+    if (slot) known[dev].store(k, std::memory_order_relaxed);
+  }
+  return k == 1 ? SWA_OK : SWA_ERR_UNSUPPORTED;
 }
 
 swa_status begin(Call& c, const swa_params* p, void* workspace, size_t ws_bytes, bool bwd,
