@@ -588,7 +588,7 @@ def _ws_at(ws, device):
 def _stream_here(device, stream):
     """The current stream's handle, where ``device`` is the current device and
     no other stream is asked for; else None (see _there)."""
-    if stream is None and device.index == torch.cuda.current_device():
+    if stream is None and device.type == "cuda" and device.index == torch.cuda.current_device():
         return _raw_stream(device.index)
     return None
 
@@ -621,10 +621,9 @@ def rope_tables(rows: int, rot: int, *, base: float = 10000.0, scaling: str = "n
         raise ValueError(f"scaling: one of {sorted(_SCALINGS)} is expected, got {scaling!r}")
     if rows < 0 or rot < 0:
         raise ValueError("rows, rot: not below 0")
-    index = torch.cuda.current_device()
-    device = torch.device("cuda", index) if device is None else torch.device(device)
+    device = torch.device("cuda" if device is None else device)
     if device.type == "cuda" and device.index is None:
-        device = torch.device("cuda", index)
+        device = torch.device("cuda", torch.cuda.current_device())
     st = _stream_here(device, stream)
     if st is None:
         return _there(device, stream, lambda: rope_tables(

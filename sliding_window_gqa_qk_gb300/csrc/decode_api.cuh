@@ -33,7 +33,9 @@ constexpr int kMaxPage = 1 << 20;
 
 swa_status check_pages(int n_pages, int page) {
   if (n_pages < 1 || page < kv4::kTile || page % kv4::kTile != 0) return SWA_ERR_INVALID_ARG;
-  return page > kMaxPage ? SWA_ERR_UNSUPPORTED : SWA_OK;
+  // tiles are counted in 31 bits (2^31 of them are 2.4 TB and more)
+  if (page > kMaxPage || static_cast<long long>(n_pages) * (page / kv4::kTile) > INT32_MAX) return SWA_ERR_UNSUPPORTED;
+  return SWA_OK;
 }
 
 swa_status check_cache(const swa_params* p, const swa_kv4_cache* c, kv4::Cache& out) {
@@ -44,6 +46,7 @@ swa_status check_cache(const swa_params* p, const swa_kv4_cache* c, kv4::Cache& 
   out.n_pages = c->n_pages;
   out.page = c->page;
   out.Hkv = p->Hkv;
+  out.per_page = kv4::fast_div(static_cast<uint32_t>(c->page / kv4::kTile));
   return SWA_OK;
 }
 
@@ -70,25 +73,11 @@ Kv4Ws kv4_ws(const kv4::AttnSplit& s, int d) {
   return w;
 }
 
-// Raises a kernel's shared-memory limit, once per device. `done`: a word per
-// kernel, one bit per device; a device past its bits is set every time.
-swa_status allow_smem(const void* kern, int bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return SWA_ERR_CUDA;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return SWA_OK;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return SWA_ERR_CUDA;
-  done.fetch_or(bit, std::memory_order_relaxed);
-  return SWA_OK;
-}
-
 template <int D, int NT, bool kPolled>
 swa_status launch_attn(const kv4::AttnArgs& a, int heads_kv, cudaStream_t st) {
   auto kern = kv4::attn_kernel<D, NT, kPolled>;
   constexpr int smem = kv4::AttnSmem<D, NT>::bytes;
-  static std::atomic<uint64_t> done;
-  const swa_status s = allow_smem(reinterpret_cast<const void*>(kern), smem, done);
-  if (s != SWA_OK) return s;
+  static_assert(smem <= 48 * 1024, "within what a launch gets unasked");
   kern<<<dim3(a.splits, heads_kv * a.groups, a.B), kv4::kAttnWarps * 32, smem, st>>>(a);
   return launched();
 }
@@ -103,6 +92,9 @@ template <typename F64, typename F128>
 void by_head_dim(int d, F64 f64, F128 f128) {
   if (d == 64) f64(); else f128();
 }
+
+// Tokens of one launch of the row kernels, whose rows count in 31 bits.
+long long launch_tokens(int Hkv) { return (1LL << 30) / Hkv; }
 
 }  // namespace
 
@@ -223,10 +215,9 @@ swa_status swa_kv4_plan(int n_pages, int page, int B, int max_pages, const int32
   a.slot = slot; a.pos = pos; a.row = row; a.cu = cu; a.lens_out = lens_out; a.head_out = head_out;
   a.status = static_cast<uint32_t*>(workspace);
   const size_t smem = (static_cast<size_t>(B) * 3 + 1) * sizeof(int);
-  static std::atomic<uint64_t> done;
-  s = allow_smem(reinterpret_cast<const void*>(kv4::plan_kernel), (3 * kv4::kPlanMaxB + 1) * static_cast<int>(sizeof(int)),
-                 done);
-  if (s != SWA_OK) return s;
+  if (smem > 48 * 1024 - 1024 &&     // what a launch gets unasked, less the kernel's own arrays
+      cudaFuncSetAttribute(kv4::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return SWA_ERR_CUDA;
   const int grid = flat_grid(n_tokens, kv4::kPlanThreads * kv4::kPlanTokens, num_sms());
   kv4::plan_kernel<<<grid, kv4::kPlanThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
   return launched();
@@ -253,24 +244,40 @@ swa_status swa_kv4_append(const swa_params* p, const swa_extras* ex, const swa_k
   if (p->B == 0 || p->T == 0) return SWA_OK;
   if (!tensor_ok(k) || !tensor_ok(v) || slot == nullptr) return SWA_ERR_INVALID_ARG;
   if ((s = check_device()) != SWA_OK) return s;
-  a.N = static_cast<long long>(p->B) * p->T;
-  a.T = p->T; a.eps = p->eps; a.ve_scale = p->ve_scale; a.vocab = p->vocab;
-  a.k = static_cast<const elem_t*>(k); a.v = static_cast<const elem_t*>(v); a.gk = gk;
+  a.heads = kv4::fast_div(static_cast<uint32_t>(p->Hkv));
+  a.seq = kv4::fast_div(static_cast<uint32_t>(p->T));
+  a.eps = p->eps; a.ve_scale = p->ve_scale; a.vocab = p->vocab;
+  a.gk = gk;
   if (ve != nullptr) {
-    a.ve = static_cast<const elem_t*>(ve); a.tok = tok; a.gate = ve_gate;
-    a.gx = call.gx; a.gx_stride = call.gx_stride; a.gw = call.gw; a.gch = call.gch;
+    a.ve = static_cast<const elem_t*>(ve);
+    a.gx_stride = call.gx_stride; a.gw = call.gw; a.gch = call.gch;
   }
   if (rope) {
     a.rcos = r->cos; a.rsin = r->sin; a.rows = r->rows; a.rot = r->rot; a.interleaved = r->interleaved;
   }
-  a.pos = pos; a.slot = slot;
   a.status = static_cast<uint32_t*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const long long cap = static_cast<long long>(num_sms()) * kKv4BlocksPerSm;
-  by_head_dim(p->d,
-      [&] { kv4::append_kernel<64><<<flat_grid(a.N * p->Hkv, kRowWarps * RowMap<64>::RPI, cap), kRowWarps * 32, 0, st>>>(a); },
-      [&] { kv4::append_kernel<128><<<flat_grid(a.N * p->Hkv, kRowWarps * RowMap<128>::RPI, cap), kRowWarps * 32, 0, st>>>(a); });
-  return launched();
+  const long long tokens = static_cast<long long>(p->B) * p->T, step = launch_tokens(p->Hkv);
+  for (long long n0 = 0; n0 < tokens; n0 += step) {
+    a.N = static_cast<uint32_t>(tokens - n0 < step ? tokens - n0 : step);
+    a.t0 = static_cast<uint32_t>(n0 % p->T);
+    const long long row0 = n0 * p->Hkv * p->d;
+    a.k = static_cast<const elem_t*>(k) + row0; a.v = static_cast<const elem_t*>(v) + row0;
+    a.pos = pos ? pos + n0 : nullptr; a.slot = slot + n0;
+    if (ve != nullptr) {
+      a.tok = tok + n0;
+      a.gate = ve_gate ? ve_gate + n0 * p->Hkv : nullptr;
+      a.gx = call.gx ? call.gx + n0 * call.gx_stride : nullptr;
+    }
+    const long long rows = static_cast<long long>(a.N) * p->Hkv;
+    auto launch = [&](auto kern, int rpi) { kern<<<flat_grid(rows, kRowWarps * rpi, cap), kRowWarps * 32, 0, st>>>(a); };
+    by_head_dim(p->d,
+        [&] { ve ? launch(kv4::append_kernel<64, true>, RowMap<64>::RPI) : launch(kv4::append_kernel<64, false>, RowMap<64>::RPI); },
+        [&] { ve ? launch(kv4::append_kernel<128, true>, RowMap<128>::RPI) : launch(kv4::append_kernel<128, false>, RowMap<128>::RPI); });
+    if ((s = launched()) != SWA_OK) return s;
+  }
+  return SWA_OK;
 }
 
 swa_status swa_kv4_read(const swa_params* p, const swa_kv4_cache* c, const int64_t* slot, void* k_out, void* v_out,
@@ -284,16 +291,22 @@ swa_status swa_kv4_read(const swa_params* p, const swa_kv4_cache* c, const int64
   if (p->B == 0 || p->T == 0) return SWA_OK;
   if (!tensor_ok(k_out) || !tensor_ok(v_out) || slot == nullptr) return SWA_ERR_INVALID_ARG;
   if ((s = check_device()) != SWA_OK) return s;
-  a.N = static_cast<long long>(p->B) * p->T;
-  a.slot = slot;
-  a.k = static_cast<elem_t*>(k_out); a.v = static_cast<elem_t*>(v_out);
+  a.heads = kv4::fast_div(static_cast<uint32_t>(p->Hkv));
   a.status = static_cast<uint32_t*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const long long cap = static_cast<long long>(num_sms()) * kKv4BlocksPerSm;
-  by_head_dim(p->d,
-      [&] { kv4::read_kernel<64><<<flat_grid(a.N * p->Hkv, kRowWarps * RowMap<64>::RPI, cap), kRowWarps * 32, 0, st>>>(a); },
-      [&] { kv4::read_kernel<128><<<flat_grid(a.N * p->Hkv, kRowWarps * RowMap<128>::RPI, cap), kRowWarps * 32, 0, st>>>(a); });
-  return launched();
+  const long long tokens = static_cast<long long>(p->B) * p->T, step = launch_tokens(p->Hkv);
+  for (long long n0 = 0; n0 < tokens; n0 += step) {
+    a.N = static_cast<uint32_t>(tokens - n0 < step ? tokens - n0 : step);
+    a.slot = slot + n0;
+    a.k = static_cast<elem_t*>(k_out) + n0 * p->Hkv * p->d;
+    a.v = static_cast<elem_t*>(v_out) + n0 * p->Hkv * p->d;
+    const long long rows = static_cast<long long>(a.N) * p->Hkv;
+    auto launch = [&](auto kern, int rpi) { kern<<<flat_grid(rows, kRowWarps * rpi, cap), kRowWarps * 32, 0, st>>>(a); };
+    by_head_dim(p->d, [&] { launch(kv4::read_kernel<64>, RowMap<64>::RPI); }, [&] { launch(kv4::read_kernel<128>, RowMap<128>::RPI); });
+    if ((s = launched()) != SWA_OK) return s;
+  }
+  return SWA_OK;
 }
 
 size_t swa_kv4_workspace_size(const swa_params* p, int page, int max_pages) {

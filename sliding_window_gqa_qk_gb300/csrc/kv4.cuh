@@ -31,17 +31,37 @@ constexpr int kTile = 16;    // tokens of a tile
 
 __host__ __device__ constexpr int tile_bytes(int d) { return 18 * d; }
 
+// n / d for n < 2^31 by a multiplication: with l = ceil(log2 d) and
+// m = ceil(2^(31 + l) / d), n m 2^-(31 + l) exceeds n / d by less than 1 / d.
+struct FastDiv {
+  uint32_t d, mul;
+  int shift;
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return d == 1 ? n : __umulhi(n, mul) >> shift; }
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0, 0};
+  int l = 0;
+  while ((1ull << l) < d) ++l;
+  if (l > 0) {
+    f.mul = static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d);
+    f.shift = l - 1;
+  }
+  return f;
+}
+
 struct Cache {
   uint8_t* data;
   int n_pages, page, Hkv;
+  FastDiv per_page;      // tiles of a page and kv head; there are fewer than 2^31 such tiles
 };
 
 // The tile of `slot` (page * page size + offset) of kv head h.
 template <int D>
 __device__ __forceinline__ uint8_t* tile_of(const Cache& c, long long slot, int h) {
-  const long long pg = slot / c.page;
-  const int off = static_cast<int>(slot - pg * c.page);
-  return c.data + ((pg * c.Hkv + h) * (c.page / kTile) + off / kTile) * static_cast<long long>(tile_bytes(D));
+  const uint32_t t = static_cast<uint32_t>(slot / kTile);
+  const uint32_t pg = c.per_page.div(t);
+  const long long at = (static_cast<long long>(pg) * c.Hkv + h) * c.per_page.d + (t - pg * c.per_page.d);
+  return c.data + at * tile_bytes(D);
 }
 
 // max / min that keep a NaN (fmaxf and fminf drop it).
@@ -64,11 +84,18 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 // range; z is the group's centre rather than its minimum, which makes it
 // small and its rounding finer. A group that holds an infinity or a NaN, or
 // whose span overflows, gets s = z = NaN, so that it reads back as NaN.
-// The quotient comes from the fp32 reciprocal and is then settled by the
-// remainder x - z - n s, which fma gives exactly: values on the border
-// between two numbers (frequent: x, z and s are short bf16 numbers on plain
-// layers) go up, as the formula says, and not where a reciprocal's last bit
-// happens to put them.
+//
+// A border between two numbers, or between two bf16 steps, splits values that
+// fp32 arithmetic cannot always tell apart. Two cases:
+//   - Values of plain layers enter exactly (bf16), and many sit on a border:
+//     x, z and s are short numbers. The number found with an approximate
+//     reciprocal is settled by the remainder x - z - n s, which fma gives
+//     exactly (kExact).
+//   - Keys, and values with an embedding, are results of fp32 arithmetic. A
+//     row with an entry, a step or a centre closer to a border than that
+//     arithmetic is good for is done again in fp64: what a row is held as
+//     then follows the formula, not the rounding of a kernel. That is about
+//     one row in a hundred.
 // ---------------------------------------------------------------------------
 // Steps below 1e-36 (whose reciprocal nears fp32's end) count as 0.
 constexpr float kFlatStep = 1e-36f;
@@ -76,6 +103,11 @@ struct Group {
   float s, z;
 };
 __device__ __forceinline__ float to_bf16(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
 // Distance of x from the nearest border between two bf16 roundings, given
 // its rounding y.
@@ -83,9 +115,16 @@ __device__ __forceinline__ float bf16_margin(float x, float y) {
   return __uint_as_float(__float_as_uint(x) & 0x7F800000u) * 0.00390625f - fabsf(x - y);   // half a step: 2^(e - 8)
 }
 
-// step and centre; err: what the fp32 entries may be off by, of the group's
-// largest; near is set where that reaches a rounding border of either.
-template <int D>
+// x / 15 correctly rounded: the product with 1 / 15 and one correction by its remainder.
+__device__ __forceinline__ float over_15(float x) {
+  const float q = x * (1.0f / 15.0f);
+  return fmaf(fmaf(-15.0f, q, x), 1.0f / 15.0f, q);
+}
+
+// step and centre. Unless kExact, err is what the entries may be off by, as a
+// multiple of the row's largest: slack becomes that, and near is set where it
+// reaches a rounding border of the step or the centre.
+template <int D, bool kExact>
 __device__ __forceinline__ Group group_scale(const float (&x)[RowMap<D>::EPL], float err, float& slack, bool& near) {
   constexpr int EPL = RowMap<D>::EPL;
   constexpr int GL = 64 / EPL;   // lanes of a group
@@ -101,47 +140,56 @@ __device__ __forceinline__ Group group_scale(const float (&x)[RowMap<D>::EPL], f
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
   Group g;
-  const float s = (hi - lo) / 15.0f;
+  const float s = over_15(hi - lo);
   g.s = to_bf16(s);
   if (g.s < kFlatStep) g.s = 0.0f;
   const float z = fmaf(8.0f, g.s, lo);
   g.z = to_bf16(z);
   if (!isfinite(g.s) || !isfinite(g.z)) g.s = g.z = __int_as_float(0x7fffffff);
-  float top = fmaxf(fabsf(lo), fabsf(hi));
-  if (D == 128) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, GL));   // a rotated pair may span the groups
-  slack = err * top;
-  near = bf16_margin(s, g.s) <= 0.2f * slack || bf16_margin(z, g.z) <= 1.25f * slack;
+  if (!kExact) {
+    float top = fmaxf(fabsf(lo), fabsf(hi));
+    if (D == 128) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, GL));   // a rotated pair may span the groups
+    slack = err * top;
+    near = bf16_margin(s, g.s) <= 0.2f * slack || bf16_margin(z, g.z) <= 1.25f * slack;
+  }
   return g;
 }
-// One number; gap is lowered to the distance of x from the nearest border.
-__device__ __forceinline__ uint32_t quantise(float x, const Group& g, float inv, float half, float& gap) {
-  const float v = x - g.z;
-  float n = rintf(v * inv);
-  const float r = fmaf(-n, g.s, v);
-  gap = fminf(gap, fabsf(fabsf(r) - half));
-  n += r >= half ? 1.0f : 0.0f;
-  n -= r < -half ? 1.0f : 0.0f;
-  n = fminf(fmaxf(n, -8.0f), 7.0f);   // a NaN becomes -8
-  return static_cast<uint32_t>(static_cast<int>(n) + 8);
-}
-// The lane's EPL numbers, four bits each, lowest channel lowest.
-template <int D>
+
+// The lane's EPL numbers, four bits each, lowest channel lowest. Adding
+// 1.5 * 2^23 rounds to an integer and leaves it in the low bits; the words
+// then add up as whole numbers. Unless kExact, gap becomes the least distance
+// of an entry from a border.
+template <int D, bool kExact>
 __device__ __forceinline__ uint32_t quantise_lane(const float (&x)[RowMap<D>::EPL], const Group& g, float& gap) {
   constexpr int EPL = RowMap<D>::EPL;
-  const bool flat = !(g.s > 0.0f);
-  const float inv = flat ? 0.0f : 1.0f / g.s, half = 0.5f * g.s;
-  uint32_t w = 0;
+  constexpr float kRound = 12582912.0f;
+  const bool flat = !(g.s > 0.0f);       // step 0, or NaN
+  const float inv = rcp_approx(g.s), half = 0.5f * g.s;
+  uint32_t w = 0, ones = 0;
+  float far = 0.0f;                      // largest distance from a number, in steps
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) w |= (flat ? 8u : quantise(x[i], g, inv, half, gap)) << (4 * i);
-  return w;
+  for (int i = 0; i < EPL; ++i) {
+    const float v = x[i] - g.z;
+    float n = fminf(fmaxf(fmaf(v, inv, 8.0f), 0.0f), 15.0f);
+    float b = n + kRound;
+    if (kExact) {
+      const float r = fmaf(8.0f - (b - kRound), g.s, v);      // x - z - (n - 8) s
+      b += r >= half ? 1.0f : 0.0f;
+      b -= r < -half ? 1.0f : 0.0f;
+      b = fminf(fmaxf(b, kRound), kRound + 15.0f);
+    } else {
+      far = fmaxf(far, fabsf(n - (b - kRound)));
+    }
+    w += __float_as_uint(b) << (4 * i);
+    ones += __float_as_uint(kRound) << (4 * i);
+  }
+  if (!kExact) gap = flat ? INFINITY : (0.5f - far) * g.s;
+  return flat ? 0x88888888u >> (32 - 4 * EPL) : w - ones;
 }
 
-// The same in fp64, for rows that fp32 leaves too close to a border: which of
-// two numbers (and, worse, of two steps) a row gets then follows the formula
-// and not the rounding of a particular kernel. About one row in a hundred
-// takes this way; its price is this GPU's slow fp64.
+// The same in fp64. Every lane of the warp calls it.
 template <int D>
-__device__ __noinline__ uint32_t quantise_f64(const double (&x)[RowMap<D>::EPL], Group& g) {
+__device__ __forceinline__ uint32_t quantise_f64(const double (&x)[RowMap<D>::EPL], Group& g) {
   constexpr int EPL = RowMap<D>::EPL;
   constexpr int GL = 64 / EPL;
   double lo = x[0], hi = x[0];
@@ -156,11 +204,11 @@ __device__ __noinline__ uint32_t quantise_f64(const double (&x)[RowMap<D>::EPL],
     lo = a < lo ? a : lo;
     hi = b > hi ? b : hi;
   }
-  g.s = to_bf16(static_cast<float>((hi - lo) / 15.0));
+  g.s = to_bf16(static_cast<float>((hi - lo) * (1.0 / 15.0)));
   if (g.s < kFlatStep) g.s = 0.0f;
-  g.z = to_bf16(static_cast<float>(lo + 8.0 * static_cast<double>(g.s)));
+  g.z = to_bf16(static_cast<float>(fma(8.0, static_cast<double>(g.s), lo)));
   const bool flat = !(g.s > 0.0f);
-  const float inv = flat ? 0.0f : 1.0f / g.s;
+  const float inv = flat ? 0.0f : rcp_approx(g.s);
   const double half = 0.5 * static_cast<double>(g.s);
   uint32_t w = 0;
 #pragma unroll
@@ -181,8 +229,9 @@ __device__ __noinline__ uint32_t quantise_f64(const double (&x)[RowMap<D>::EPL],
 // ---------------------------------------------------------------------------
 struct AppendArgs {
   Cache c;
-  long long N;                         // tokens: B * T
-  int T;
+  uint32_t N;                          // tokens of this launch: N * Hkv < 2^31
+  FastDiv heads, seq;                  // by Hkv, by T
+  uint32_t t0;                         // position of the launch's first token where pos is NULL
   float eps, ve_scale;
   int vocab;
   const elem_t* k; const elem_t* v;    // [N, Hkv, D]
@@ -194,14 +243,20 @@ struct AppendArgs {
   uint32_t* status;                    // or NULL
 };
 
+// What fp32 arithmetic may leave an entry off by, as a multiple of the row's
+// largest: rotation, norm and gain are some five roundings of 2^-24, and the
+// number's own product with the reciprocal two more.
+constexpr float kKeyErr = 8.0f * 5.9604645e-8f;
+constexpr float kMixErr = 5.0f * 5.9604645e-8f;
+
 // The rotated and normed key row in fp64 (row: its index, p its position),
 // quantised; every lane of the warp calls it.
 template <int D>
-__device__ __noinline__ uint32_t key_f64(const AppendArgs& a, long long row, int p, bool on, Group& g) {
+__device__ __noinline__ uint32_t key_f64(const AppendArgs& a, uint32_t row, int p, bool on, Group* out) {
   using M = RowMap<D>;
   constexpr int EPL = M::EPL;
   const int cl = (threadIdx.x & 31) % M::LPR, c0 = cl * EPL, half = a.rot / 2;
-  const elem_t* k = a.k + (on ? row : 0) * D;
+  const elem_t* k = a.k + static_cast<long long>(on ? row : 0) * D;
   double x[EPL], ss = 0.0;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
@@ -213,58 +268,101 @@ __device__ __noinline__ uint32_t key_f64(const AppendArgs& a, long long row, int
       const bool first = a.interleaved ? (c & 1) == 0 : c < half;
       const long long at = static_cast<long long>(p) * half + col;
       const double o = static_cast<double>(to_f32(k[to])) * a.rsin[at];
-      x[i] = x[i] * a.rcos[at] + (first ? o : -o);
+      x[i] = fma(x[i], static_cast<double>(a.rcos[at]), first ? o : -o);
     }
     ss = fma(x[i], x[i], ss);
   }
 #pragma unroll
   for (int o = M::LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const double rstd = 1.0 / sqrt(ss / D + static_cast<double>(a.eps));
+  // 1 / sqrt by one Newton step from the fp32 one: 2^-22 squared is enough here
+  const double mean = fma(ss, 1.0 / D, static_cast<double>(a.eps));
+  const double r0 = rsqrtf(static_cast<float>(mean));
+  const double rstd = r0 * fma(-0.5 * mean * r0, r0, 1.5);
 #pragma unroll
   for (int i = 0; i < EPL; ++i) x[i] = x[i] * rstd * (a.gk ? a.gk[c0 + i] : 1.0f);
-  return quantise_f64<D>(x, g);
+  Group g;
+  const uint32_t w = quantise_f64<D>(x, g);
+  *out = g;
+  return w;
 }
-
-// What fp32 arithmetic may leave an entry off by, as a multiple of the row's
-// largest: rotation, norm and gain are some five roundings of 2^-24.
-constexpr float kKeyErr = 8.0f * 5.9604645e-8f;
-constexpr float kMixErr = 3.0f * 5.9604645e-8f;
+// A value row with its embedding in fp64, from its fp32 parts.
+template <int D>
+__device__ __noinline__ uint32_t mix_f64(const AppendArgs& a, uint32_t row, const elem_t* ve, float gate, bool on, Group* out) {
+  constexpr int EPL = RowMap<D>::EPL;
+  const int c0 = ((threadIdx.x & 31) % RowMap<D>::LPR) * EPL;
+  double x[EPL];
+  const double f = static_cast<double>(a.ve_scale) * gate;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    x[i] = on ? to_f32(a.v[static_cast<long long>(row) * D + c0 + i]) : 0.0;
+    if (on && ve != nullptr) x[i] = fma(f, static_cast<double>(to_f32(ve[c0 + i])), x[i]);
+  }
+  Group g;
+  const uint32_t w = quantise_f64<D>(x, g);
+  *out = g;
+  return w;
+}
 
 // Lanes as in the other row-wise kernels: LPR lanes hold one row of D
 // channels, 16 bytes each, and a warp works on RPI rows (token, head) at a
-// time, key and value together.
-template <int D>
+// time, key and value together. MIX: a value embedding.
+template <int D, bool MIX>
 __global__ void __launch_bounds__(kRowWarps * 32) append_kernel(const __grid_constant__ AppendArgs a) {
   using M = RowMap<D>;
   constexpr int EPL = M::EPL, NG = D / 64;
+  constexpr bool kPlainExact = !MIX && sizeof(elem_t) == 2;    // fp32 values: x - z may round
   const int lane = threadIdx.x & 31, cl = lane % M::LPR, c0 = cl * EPL;
-  const int Hkv = a.c.Hkv;
-  const long long rows = a.N * Hkv;
+  const uint32_t Hkv = a.heads.d, rows = a.N * Hkv;
   const long long cap = static_cast<long long>(a.c.n_pages) * a.c.page;
+  const unsigned rows_mask = M::LPR == 32 ? 0xffffffffu : ((1u << M::LPR) - 1u) << (lane / M::LPR * M::LPR);
   float gk[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) gk[i] = a.gk ? a.gk[c0 + i] : 1.0f;
-  for (long long r0 = grid_warp() * M::RPI; r0 < rows; r0 += grid_warps() * M::RPI) {
-    const long long row = r0 + lane / M::LPR;
+  for (uint32_t r0 = static_cast<uint32_t>(grid_warp()) * M::RPI; r0 < rows;
+       r0 += static_cast<uint32_t>(grid_warps()) * M::RPI) {
+    const uint32_t row = r0 + lane / M::LPR;
     bool on = row < rows;
-    const long long n = on ? row / Hkv : 0;
+    const uint32_t n = on ? a.heads.div(row) : 0;
     const int h = static_cast<int>(on ? row - n * Hkv : 0);
     const long long slot = on ? a.slot[n] : -1;
+    uint4 kr = make_uint4(0u, 0u, 0u, 0u), vr = kr, er = kr;
+    if (on) {
+      kr = ld16(a.k + static_cast<long long>(row) * D + c0);
+      vr = ld16(a.v + static_cast<long long>(row) * D + c0);
+    }
     int p = 0;
     uint32_t bad = 0;
     if (on && a.rcos != nullptr) {
-      p = a.pos ? a.pos[n] : static_cast<int>(n % a.T);
+      const uint32_t t = a.t0 + n;
+      p = a.pos ? a.pos[n] : static_cast<int>(t - a.seq.div(t) * a.seq.d);
       if (slot >= 0 && (p < 0 || p >= a.rows)) bad = DEV_ERR_BOUNDS;
     }
     if (on && slot != -1 && (slot < 0 || slot >= cap)) bad = DEV_ERR_BOUNDS;
     on = on && slot >= 0 && !bad;
-    float x[EPL], y[EPL];
-    {
-      const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-      unpack16(on ? ld16(a.k + row * D + c0) : z, x);
-      unpack16(on ? ld16(a.v + row * D + c0) : z, y);
+    const elem_t* ve = nullptr;
+    float gate = 1.0f;
+    if (MIX) {
+      const int tok = on ? a.tok[n] : 0;
+      if (on && tok >= 0 && tok < a.vocab) {
+        ve = a.ve + (static_cast<long long>(tok) * Hkv + h) * D;
+        er = ld16(ve + c0);
+      } else if (on) {
+        bad |= DEV_ERR_TOKEN;
+      }
+      if (a.gw != nullptr) {
+        float z = 0.f;
+        if (on) {
+          const elem_t* xr = a.gx + n * a.gx_stride;
+          for (int c = cl; c < a.gch; c += M::LPR) z = fmaf(a.gw[h * a.gch + c], to_f32(xr[c]), z);
+        }
+        gate = 2.0f / (1.0f + expf(-row_sum<M::LPR>(z)));
+      } else if (on && a.gate != nullptr) {
+        gate = a.gate[static_cast<long long>(n) * Hkv + h];
+      }
     }
-    // key: rotation, then RMSNorm
+    // key: rotation, RMSNorm
+    float x[EPL];
+    unpack16(kr, x);
     if (a.rcos != nullptr) {
       const long long at = on ? static_cast<long long>(p) * (a.rot / 2) : 0;
       rotate_lanes<D>(x, a.rcos + at, a.rsin + at, a.rot, a.interleaved, on);
@@ -276,72 +374,45 @@ __global__ void __launch_bounds__(kRowWarps * 32) append_kernel(const __grid_con
     const float rstd = rsqrtf(ss / D + a.eps);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) x[i] = x[i] * rstd * gk[i];
-    // value: value-embedding mix
-    float mix = 0.f, e[EPL] = {};
-    if (a.ve != nullptr) {
-      float gate = 1.0f;
-      if (a.gw != nullptr) {
-        float z = 0.f;
-        if (on) {
-          const elem_t* xr = a.gx + n * a.gx_stride;
-          for (int c = cl; c < a.gch; c += M::LPR) z = fmaf(a.gw[h * a.gch + c], to_f32(xr[c]), z);
-        }
-        gate = 2.0f / (1.0f + expf(-row_sum<M::LPR>(z)));
-      } else if (on && a.gate != nullptr) {
-        gate = a.gate[n * Hkv + h];
-      }
-      const int tok = on ? a.tok[n] : 0;
-      if (on && tok >= 0 && tok < a.vocab) {
-        unpack16(ld16(a.ve + (static_cast<long long>(tok) * Hkv + h) * D + c0), e);
-        mix = gate;
-      } else if (on) {
-        bad |= DEV_ERR_TOKEN;
-      }
-    }
-    float slack, gap = INFINITY;
-    bool near;
-    Group gk4 = group_scale<D>(x, kKeyErr, slack, near);
-    uint32_t wk = quantise_lane<D>(x, gk4, gap);
-    const unsigned rows_mask = M::LPR == 32 ? 0xffffffffu : ((1u << M::LPR) - 1u) << (lane / M::LPR * M::LPR);
+    float slack = 0.f, gap = 0.f;
+    bool near = false;
+    Group sk = group_scale<D, false>(x, kKeyErr, slack, near);
+    uint32_t wk = quantise_lane<D, false>(x, sk, gap);
     unsigned close = __ballot_sync(0xffffffffu, on && (near || gap <= slack));
     if (close) {
-      Group g2;
-      const uint32_t w2 = key_f64<D>(a, row, p, on, g2);
+      Group s2;
+      const uint32_t w2 = key_f64<D>(a, row, p, on, &s2);
       if (close & rows_mask) {
         wk = w2;
-        gk4 = g2;
+        sk = s2;
       }
     }
-    Group gv4;
-    uint32_t wv;
-    if (a.ve == nullptr) {
-      gv4 = group_scale<D>(y, 0.f, slack, near);
-      wv = quantise_lane<D>(y, gv4, gap);
-    } else {
-      float v[EPL];
+    // value, with its embedding
+    unpack16(vr, x);
+    if (MIX) {
+      float e[EPL];
+      unpack16(er, e);
+      const float f = a.ve_scale * gate;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) v[i] = fmaf(a.ve_scale * mix, e[i], y[i]);
-      gap = INFINITY;
-      gv4 = group_scale<D>(v, kMixErr, slack, near);
-      wv = quantise_lane<D>(v, gv4, gap);
+      for (int i = 0; i < EPL; ++i) x[i] = fmaf(f, e[i], x[i]);
+    }
+    Group sv = group_scale<D, kPlainExact>(x, kMixErr, slack, near);
+    uint32_t wv = quantise_lane<D, kPlainExact>(x, sv, gap);
+    if (!kPlainExact) {
       close = __ballot_sync(0xffffffffu, on && (near || gap <= slack));
       if (close) {
-        double v64[EPL];
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          v64[i] = static_cast<double>(y[i]) + static_cast<double>(a.ve_scale) * mix * static_cast<double>(e[i]);
-        Group g2;
-        const uint32_t w2 = quantise_f64<D>(v64, g2);
+        Group s2;
+        const uint32_t w2 = mix_f64<D>(a, row, ve, gate, on, &s2);
         if (close & rows_mask) {
           wv = w2;
-          gv4 = g2;
+          sv = s2;
         }
       }
     }
     if (bad && cl == 0 && a.status) atomicOr(a.status, bad);
     if (!on) continue;
     uint8_t* tile = tile_of<D>(a.c, slot, h);
-    const int t = static_cast<int>(slot % a.c.page) % kTile;
+    const int t = static_cast<int>(slot) & (kTile - 1);
     const int g = c0 / 64, x0 = c0 % 64;
     // keys: nibble ((x / 16) NG + g) 16 + x % 16 of the row
     const int nk = ((x0 / 16) * NG + g) * 16 + x0 % 16;
@@ -359,8 +430,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) append_kernel(const __grid_con
     }
     if (x0 == 0) {
       uint32_t* sc = reinterpret_cast<uint32_t*>(tile + 16 * D);
-      sc[t * NG + g] = pack_bf16x2(gk4.s, gk4.z);
-      sc[(kTile + t) * NG + g] = pack_bf16x2(gv4.s, gv4.z);
+      sc[t * NG + g] = pack_bf16x2(sk.s, sk.z);
+      sc[(kTile + t) * NG + g] = pack_bf16x2(sv.s, sv.z);
     }
   }
 }
@@ -370,7 +441,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) append_kernel(const __grid_con
 // ---------------------------------------------------------------------------
 struct ReadArgs {
   Cache c;
-  long long N;
+  uint32_t N;                // tokens of this launch: N * Hkv < 2^31
+  FastDiv heads;             // by Hkv
   const int64_t* slot;
   elem_t* k; elem_t* v;      // [N, Hkv, D]
   uint32_t* status;          // or NULL
@@ -381,19 +453,19 @@ __global__ void __launch_bounds__(kRowWarps * 32) read_kernel(const __grid_const
   using M = RowMap<D>;
   constexpr int EPL = M::EPL, NG = D / 64;
   const int lane = threadIdx.x & 31, cl = lane % M::LPR, c0 = cl * EPL;
-  const int Hkv = a.c.Hkv;
-  const long long rows = a.N * Hkv;
+  const uint32_t Hkv = a.heads.d, rows = a.N * Hkv;
   const long long cap = static_cast<long long>(a.c.n_pages) * a.c.page;
-  for (long long row = grid_warp() * M::RPI + lane / M::LPR; row < rows; row += grid_warps() * M::RPI) {
-    const long long n = row / Hkv;
+  const int g = c0 / 64, x0 = c0 % 64;
+  const int nk = ((x0 / 16) * NG + g) * 16 + x0 % 16;
+  for (uint32_t row = static_cast<uint32_t>(grid_warp()) * M::RPI + lane / M::LPR; row < rows;
+       row += static_cast<uint32_t>(grid_warps()) * M::RPI) {
+    const uint32_t n = a.heads.div(row);
     const int h = static_cast<int>(row - n * Hkv);
     const long long slot = a.slot[n];
     float x[EPL] = {}, y[EPL] = {};
     if (slot >= 0 && slot < cap) {
       const uint8_t* tile = tile_of<D>(a.c, slot, h);
-      const int t = static_cast<int>(slot % a.c.page) % kTile;
-      const int g = c0 / 64, x0 = c0 % 64;
-      const int nk = ((x0 / 16) * NG + g) * 16 + x0 % 16;
+      const int t = static_cast<int>(slot) & (kTile - 1);
       const uint8_t* krow = tile + t * (D / 2);
       const uint16_t* vrow = reinterpret_cast<const uint16_t*>(tile + 8 * D + (t / 2) * D);
       const int pv = (((x0 / 8) * NG + g) * 2 + (x0 / 4) % 2) * 2 + (t & 1);
@@ -417,8 +489,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) read_kernel(const __grid_const
     } else if (slot != -1 && cl == 0 && a.status) {
       atomicOr(a.status, DEV_ERR_BOUNDS);
     }
-    st16(a.k + row * D + c0, pack16(x));
-    st16(a.v + row * D + c0, pack16(y));
+    st16(a.k + static_cast<long long>(row) * D + c0, pack16(x));
+    st16(a.v + static_cast<long long>(row) * D + c0, pack16(y));
   }
 }
 
