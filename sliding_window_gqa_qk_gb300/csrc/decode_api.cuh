@@ -57,6 +57,7 @@ int flat_grid(long long items, long long per, long long cap) {
 }
 
 constexpr int kKv4BlocksPerSm = 8;
+constexpr int kAppendBlocksPerSm = 64;
 
 // Workspace of the decode attention: header, counters of finished chunks,
 // partial results. There are at most B * Hq <= 65535 counters, and the
@@ -257,7 +258,7 @@ swa_status swa_kv4_append(const swa_params* p, const swa_extras* ex, const swa_k
   }
   a.status = static_cast<uint32_t*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const long long cap = static_cast<long long>(num_sms()) * kKv4BlocksPerSm;
+  const long long cap = static_cast<long long>(num_sms()) * kAppendBlocksPerSm;
   const long long tokens = static_cast<long long>(p->B) * p->T, step = launch_tokens(p->Hkv);
   for (long long n0 = 0; n0 < tokens; n0 += step) {
     a.N = static_cast<uint32_t>(tokens - n0 < step ? tokens - n0 : step);
@@ -271,7 +272,7 @@ swa_status swa_kv4_append(const swa_params* p, const swa_extras* ex, const swa_k
       a.gx = call.gx ? call.gx + n0 * call.gx_stride : nullptr;
     }
     const long long rows = static_cast<long long>(a.N) * p->Hkv;
-    auto launch = [&](auto kern, int rpi) { kern<<<flat_grid(rows, kRowWarps * rpi, cap), kRowWarps * 32, 0, st>>>(a); };
+    auto launch = [&](auto kern, int rpi) { kern<<<flat_grid(rows, kv4::kAppendWarps * rpi, cap), kv4::kAppendWarps * 32, 0, st>>>(a); };
     by_head_dim(p->d,
         [&] { ve ? launch(kv4::append_kernel<64, true>, RowMap<64>::RPI) : launch(kv4::append_kernel<64, false>, RowMap<64>::RPI); },
         [&] { ve ? launch(kv4::append_kernel<128, true>, RowMap<128>::RPI) : launch(kv4::append_kernel<128, false>, RowMap<128>::RPI); });

@@ -92,10 +92,13 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 //     reciprocal is settled by the remainder x - z - n s, which fma gives
 //     exactly (kExact).
 //   - Keys, and values with an embedding, are results of fp32 arithmetic. A
-//     row with an entry, a step or a centre closer to a border than that
-//     arithmetic is good for is done again in fp64: what a row is held as
-//     then follows the formula, not the rounding of a kernel. That is about
-//     one row in a hundred.
+//     row with an entry or a step closer to a border than that arithmetic is
+//     good for is done again in fp64: the numbers a row is held as then
+//     follow the formula, not the rounding of a kernel. A centre close to a
+//     border of its own counts only where the other rounding would change a
+//     number (most centres lie near 0, where bf16's steps are fine); else it
+//     may stay one rounding off, by less than 2^-8 of itself. About one row
+//     in 500 takes that way.
 // ---------------------------------------------------------------------------
 // Steps below 1e-36 (whose reciprocal nears fp32's end) count as 0.
 constexpr float kFlatStep = 1e-36f;
@@ -122,8 +125,8 @@ __device__ __forceinline__ float over_15(float x) {
 }
 
 // step and centre. Unless kExact, err is what the entries may be off by, as a
-// multiple of the row's largest: slack becomes that, and near is set where it
-// reaches a rounding border of the step or the centre.
+// multiple of the row's largest: slack becomes that, plus a step of the
+// centre's where it may round either way, and near is set where the step may.
 template <int D, bool kExact>
 __device__ __forceinline__ Group group_scale(const float (&x)[RowMap<D>::EPL], float err, float& slack, bool& near) {
   constexpr int EPL = RowMap<D>::EPL;
@@ -150,7 +153,8 @@ __device__ __forceinline__ Group group_scale(const float (&x)[RowMap<D>::EPL], f
     float top = fmaxf(fabsf(lo), fabsf(hi));
     if (D == 128) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, GL));   // a rotated pair may span the groups
     slack = err * top;
-    near = bf16_margin(s, g.s) <= 0.2f * slack || bf16_margin(z, g.z) <= 1.25f * slack;
+    near = bf16_margin(s, g.s) <= 0.2f * slack;      // both ends over 15, and a rounding
+    if (bf16_margin(z, g.z) <= 1.25f * slack) slack += __uint_as_float(__float_as_uint(z) & 0x7F800000u) * 0.0078125f;
   }
   return g;
 }
@@ -244,10 +248,12 @@ struct AppendArgs {
 };
 
 // What fp32 arithmetic may leave an entry off by, as a multiple of the row's
-// largest: rotation, norm and gain are some five roundings of 2^-24, and the
-// number's own product with the reciprocal two more.
-constexpr float kKeyErr = 8.0f * 5.9604645e-8f;
-constexpr float kMixErr = 5.0f * 5.9604645e-8f;
+// largest: five roundings of rotation, norm and gain, of half of 2^-23 each
+// and of either sign, and two of the number's product with the reciprocal,
+// come to 2 to 3 units of 2^-24 at most on the rows measured.
+constexpr float kKeyErr = 4.0f * 5.9604645e-8f;
+constexpr float kMixErr = 4.0f * 5.9604645e-8f;
+constexpr int kAppendWarps = 4;      // a small block: one slow row holds up few others
 
 // The rotated and normed key row in fp64 (row: its index, p its position),
 // quantised; every lane of the warp calls it.
@@ -307,7 +313,7 @@ __device__ __noinline__ uint32_t mix_f64(const AppendArgs& a, uint32_t row, cons
 // channels, 16 bytes each, and a warp works on RPI rows (token, head) at a
 // time, key and value together. MIX: a value embedding.
 template <int D, bool MIX>
-__global__ void __launch_bounds__(kRowWarps * 32) append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_constant__ AppendArgs a) {
   using M = RowMap<D>;
   constexpr int EPL = M::EPL, NG = D / 64;
   constexpr bool kPlainExact = !MIX && sizeof(elem_t) == 2;    // fp32 values: x - z may round
