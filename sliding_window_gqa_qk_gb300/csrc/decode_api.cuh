@@ -57,6 +57,7 @@ int flat_grid(long long items, long long per, long long cap) {
 }
 
 constexpr int kKv4BlocksPerSm = 8;
+constexpr long long kFewThreads = 512;   // per SM
 constexpr int kAppendBlocksPerSm = 64;
 
 // Workspace of the decode attention: header, counters of finished chunks,
@@ -136,7 +137,7 @@ swa_status swa_rope_tables(const swa_rope_freq* f, int first, int rows, float* c
   a.n = static_cast<long long>(rows) * a.half / 4;
   a.first = static_cast<unsigned>(first);
   a.amplitude = f->amplitude > 0.0 ? static_cast<float>(f->amplitude) : 1.0f;
-  rope_table_kernel<<<flat_grid(a.n, kRopeThreads, num_sms() * 8LL), kRopeThreads, 0,
+  rope_table_kernel<<<flat_grid(a.n, kTableThreads, num_sms() * 8LL), kTableThreads, 0,
                       static_cast<cudaStream_t>(stream)>>>(a);
   return launched();
 }
@@ -172,7 +173,9 @@ swa_status swa_rope_apply(const swa_params* p, const swa_rope* r, const int32_t*
   const int H = a.Hq + a.Hkv;
   const long long threads = a.N * a.units;
   if (threads / kRopeThreads >= INT32_MAX) return SWA_ERR_UNSUPPORTED;
-  a.heads = H;
+  // One thread for all heads of its unit reads the angles once; few positions
+  // are spread over the heads instead, so that no thread goes round twice.
+  a.heads = threads >= num_sms() * kFewThreads ? H : kRopeBatch[r->interleaved];
   const dim3 grid(static_cast<unsigned>((threads + kRopeThreads - 1) / kRopeThreads), (H + a.heads - 1) / a.heads);
   if (r->interleaved)
     rope_kernel<true><<<grid, kRopeThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);

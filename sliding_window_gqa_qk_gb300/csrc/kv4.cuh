@@ -70,6 +70,16 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float min_nan(float a, float b) {
   float r;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -131,11 +141,11 @@ template <int D, bool kExact>
 __device__ __forceinline__ Group group_scale(const float (&x)[RowMap<D>::EPL], float err, float& slack, bool& near) {
   constexpr int EPL = RowMap<D>::EPL;
   constexpr int GL = 64 / EPL;   // lanes of a group
-  float lo = x[0], hi = x[0];
+  float lo = min_nan(x[0], x[1]), hi = max_nan(x[0], x[1]);
 #pragma unroll
-  for (int i = 1; i < EPL; ++i) {
-    lo = min_nan(lo, x[i]);
-    hi = max_nan(hi, x[i]);
+  for (int i = 2; i < EPL; i += 2) {
+    lo = min_nan(lo, x[i], x[i + 1]);
+    hi = max_nan(hi, x[i], x[i + 1]);
   }
 #pragma unroll
   for (int o = GL / 2; o > 0; o >>= 1) {
@@ -159,30 +169,30 @@ __device__ __forceinline__ Group group_scale(const float (&x)[RowMap<D>::EPL], f
   return g;
 }
 
-// The lane's EPL numbers, four bits each, lowest channel lowest. Adding
-// 1.5 * 2^23 rounds to an integer and leaves it in the low bits; the words
-// then add up as whole numbers. Unless kExact, gap becomes the least distance
-// of an entry from a border.
+// The lane's EPL numbers, four bits each, lowest channel lowest. A saturating
+// multiply-add keeps (x - z) / (15 s) + 8 / 15 within [0, 1]; 15 times that
+// plus 1.5 * 2^23 is rounded to an integer, which sits in the low bits, and the
+// words add up as whole numbers. kExact: rounded a little low, so that only
+// a remainder of half a step or more is left to settle, upwards. Otherwise gap
+// becomes the least distance of an entry from a border.
 template <int D, bool kExact>
 __device__ __forceinline__ uint32_t quantise_lane(const float (&x)[RowMap<D>::EPL], const Group& g, float& gap) {
   constexpr int EPL = RowMap<D>::EPL;
-  constexpr float kRound = 12582912.0f;
+  constexpr float kRound = 12582912.0f, kLow = kExact ? 1.0f / 4096.0f : 0.0f;
   const bool flat = !(g.s > 0.0f);       // step 0, or NaN
-  const float inv = rcp_approx(g.s), half = 0.5f * g.s;
+  const float inv = rcp_approx(g.s) * (1.0f / 15.0f), half = 0.5f * g.s;
+  const float off = fmaf(-g.z, inv, (8.0f - kLow) / 15.0f);
   uint32_t w = 0, ones = 0;
   float far = 0.0f;                      // largest distance from a number, in steps
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const float v = x[i] - g.z;
-    float n = fminf(fmaxf(fmaf(v, inv, 8.0f), 0.0f), 15.0f);
-    float b = n + kRound;
+    float n = kExact ? __saturatef(fmaf(x[i] - g.z, inv, (8.0f - kLow) / 15.0f)) : __saturatef(fmaf(x[i], inv, off));
+    float b = fmaf(n, 15.0f, kRound);
     if (kExact) {
-      const float r = fmaf(8.0f - (b - kRound), g.s, v);      // x - z - (n - 8) s
-      b += r >= half ? 1.0f : 0.0f;
-      b -= r < -half ? 1.0f : 0.0f;
-      b = fminf(fmaxf(b, kRound), kRound + 15.0f);
+      const float r = fmaf((kRound + 8.0f) - b, g.s, x[i] - g.z);      // x - z - (n - 8) s
+      b = fminf(b + (r >= half ? 1.0f : 0.0f), kRound + 15.0f);
     } else {
-      far = fmaxf(far, fabsf(n - (b - kRound)));
+      far = fmaxf(far, fabsf(fmaf(n, 15.0f, kRound - b)));
     }
     w += __float_as_uint(b) << (4 * i);
     ones += __float_as_uint(kRound) << (4 * i);

@@ -12,7 +12,8 @@
 namespace swa {
 
 constexpr int kMaxRot = 128;        // channels turned at most (the largest head)
-constexpr int kRopeThreads = 256;
+constexpr int kTableThreads = 256;
+constexpr int kRopeThreads = 128;
 
 // ---------------------------------------------------------------------------
 // Tables: cos[t][c], sin[t][c] of t * theta_c.
@@ -22,8 +23,10 @@ constexpr int kRopeThreads = 256;
 // turns as a 64-bit fixed-point fraction instead: phi_c = theta_c / (2 pi)
 // scaled by 2^64 and multiplied by the integer t modulo 2^64 leaves the
 // fraction of a turn exactly, with no floating-point reduction and no fp64
-// arithmetic (this GPU has little of it). Its top 32 bits, as a signed
-// number, are the angle in [-1/2, 1/2) turns.
+// arithmetic (this GPU has little of it). Its top 32 bits are the angle; the
+// nearest quarter turn comes off as an integer, and what is left, at most an
+// eighth of a turn either way, goes through the Taylor polynomials of sine
+// (to x^9) and cosine (to x^8), which are good to 2 10^-9 and 3 10^-8 there.
 // ---------------------------------------------------------------------------
 struct RopeTableArgs {
   unsigned long long turn[kMaxRot / 2];  // theta_c / (2 pi) * 2^64
@@ -35,21 +38,33 @@ struct RopeTableArgs {
   float amplitude;
 };
 
-__global__ void __launch_bounds__(kRopeThreads) rope_table_kernel(const __grid_constant__ RopeTableArgs a) {
+// Sine and cosine of frac / 2^32 turns.
+__device__ __forceinline__ void sincos_turn(uint32_t frac, float& sn, float& cs) {
+  const uint32_t q = (frac + 0x20000000u) >> 30;                       // nearest quarter
+  const float x = static_cast<float>(static_cast<int>(frac - (q << 30))) * 1.4629180792671596e-9f;   // 2 pi / 2^32
+  const float y = x * x;
+  const float s = fmaf(x * y, fmaf(y, fmaf(y, fmaf(y, 1.0f / 362880.0f, -1.0f / 5040.0f), 1.0f / 120.0f), -1.0f / 6.0f), x);
+  const float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, 1.0f / 40320.0f, -1.0f / 720.0f), 1.0f / 24.0f), -0.5f), 1.0f);
+  const float a = q & 1u ? c : s, b = q & 1u ? s : c;
+  sn = __uint_as_float(__float_as_uint(a) ^ ((q & 2u) << 30));
+  cs = __uint_as_float(__float_as_uint(b) ^ (((q + 1u) & 2u) << 30));
+}
+
+__global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_constant__ RopeTableArgs a) {
   __shared__ unsigned long long turn[kMaxRot / 2];
   if (threadIdx.x < kMaxRot / 2) turn[threadIdx.x] = a.turn[threadIdx.x];
   __syncthreads();
   const int q = a.half / 4;
-  for (long long i = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x; i < a.n;
-       i += static_cast<long long>(gridDim.x) * kRopeThreads) {
-    const unsigned row = static_cast<unsigned>(i / q);
+  for (long long i = static_cast<long long>(blockIdx.x) * kTableThreads + threadIdx.x; i < a.n;
+       i += static_cast<long long>(gridDim.x) * kTableThreads) {
+    // rows < 2^31 and q <= 16: the quotient by a 64-bit division only where i is that large
+    const unsigned row = i < UINT32_MAX ? static_cast<unsigned>(i) / q : static_cast<unsigned>(i / q);
     const int c = static_cast<int>(i - static_cast<long long>(row) * q) * 4;
     const unsigned long long t = a.first + row;
     float cs[4], sn[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int frac = static_cast<int>(static_cast<unsigned>((turn[c + j] * t) >> 32));
-      sincospif(static_cast<float>(frac) * 4.656612873077393e-10f, &sn[j], &cs[j]);  // 2^-31: half turns
+      sincos_turn(static_cast<uint32_t>((turn[c + j] * t) >> 32), sn[j], cs[j]);
       cs[j] *= a.amplitude;
       sn[j] *= a.amplitude;
     }
@@ -65,11 +80,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_table_kernel(const __grid_c
 // channels c.. and their partners (split-half), 16 bytes that hold whole
 // pairs (interleaved), or 16 bytes past the turned part (copied when the
 // output is another tensor). It reads the unit's cosines and sines once and
-// walks over some of the position's heads with them, kRopeBatch heads' loads
-// in flight at a time. Every element is read and written by the same thread,
+// walks over some of the position's heads with them, a batch of heads' loads
+// in flight at a time (six 16-byte loads where a unit is two pieces, four where
+// it is one: 24 more registers for eight cost 9 % on a layer of 16 x 2048
+// positions). Every element is read and written by the same thread,
 // reads first, so the rotation also runs in place.
 // ---------------------------------------------------------------------------
-constexpr int kRopeBatch = 4;
+constexpr int kRopeBatch[2] = {3, 4};    // split-half, interleaved
 
 struct RopeArgs {
   const elem_t* q; const elem_t* k;   // [N, Hq, d], [N, Hkv, d] or NULL
@@ -87,7 +104,7 @@ struct RopeArgs {
 
 template <bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int EPL = 16 / static_cast<int>(sizeof(elem_t));
+  constexpr int EPL = 16 / static_cast<int>(sizeof(elem_t)), kBatch = kRopeBatch[INTER];
   const long long id = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
   const long long n = id / a.units;
   if (n >= a.N) return;
@@ -116,11 +133,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   }
   const int H = a.Hq + a.Hkv;
   const int h0 = blockIdx.y * a.heads, h1 = h0 + a.heads < H ? h0 + a.heads : H;
-  for (int h = h0; h < h1; h += kRopeBatch) {
-    uint4 x[kRopeBatch], y[kRopeBatch];
-    elem_t* out[kRopeBatch];
+  for (int h = h0; h < h1; h += kBatch) {
+    uint4 x[kBatch], y[kBatch];
+    elem_t* out[kBatch];
 #pragma unroll
-    for (int i = 0; i < kRopeBatch; ++i) {
+    for (int i = 0; i < kBatch; ++i) {
       if (h + i >= h1) continue;
       const bool is_q = h + i < a.Hq;
       const long long off = is_q ? (n * a.Hq + h + i) * a.d + c : (n * a.Hkv + (h + i - a.Hq)) * a.d + c;
@@ -130,7 +147,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
       if (!INTER && turn) y[i] = ld16(src + half);
     }
 #pragma unroll
-    for (int i = 0; i < kRopeBatch; ++i) {
+    for (int i = 0; i < kBatch; ++i) {
       if (h + i >= h1) continue;
       if (!turn) {
         st16(out[i], x[i]);
