@@ -51,8 +51,9 @@ constexpr int kStages = 2;               // steps of two tiles in flight per war
 // P in fp32 calls: a third term, or the second's rounding would show in o
 constexpr bool kThreeTerms = sizeof(elem_t) == 4;
 constexpr int kColQ = 4;                 // query heads of one 8-column operand
-constexpr int kAttnCtas = 152 * 8;       // CTAs aimed at: two rounds of the four a GB300's SM holds
-constexpr int kMinChunk = 16, kMaxChunk = 256;   // tiles of a CTA
+constexpr int kMaxSplits = 512;          // CTAs of one request and kv head
+// CTAs an SM holds (registers: 128 a thread with one operand, 255 with two)
+constexpr int attn_ctas_per_sm(int operands) { return operands == 1 ? 4 : 2; }
 
 struct AttnArgs {
   Cache c;
@@ -232,7 +233,7 @@ __device__ __forceinline__ void query_row(const AttnArgs& a, const elem_t* q, in
 }
 
 template <int D, int NT, bool kPolled>
-__global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 ? 4 : 2) attn_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kAttnWarps * 32, attn_ctas_per_sm(NT)) attn_kernel(const __grid_constant__ AttnArgs a) {
   using S = AttnShape<D>;
   using M = AttnSmem<D, NT>;
   constexpr int NG = S::NG, W = S::W, NQ = NT * kColQ;
@@ -560,13 +561,23 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 ? 4 : 2) attn_kernel(
 }
 
 // Chunks: a CTA's tiles and the CTAs of the longest request, from what the
-// host knows (the table's width and the window, not the lengths).
+// host knows (the table's width and the window, not the lengths). The number
+// of splits is the one with the least estimated time, in tiles of one CTA: a
+// chunk and the set-up of a CTA, as often as the CTAs fill the GPU, and for
+// more than one split the join, a tail of the last CTA; the mean of a batch
+// of full-length requests (whole rounds of CTAs) and of one that is ragged
+// (half the CTAs have work). Measured on 32 requests x 4096 tiles, 4 kv
+// heads: chunks of 64, 96, 216, 256 and 432 tiles take 243, 226, 212, 216 and
+// 214 us; 16 ragged requests of at most 313 tiles, 6 kv heads: chunks of 32 and
+// 56 tiles 14.9 and 18.4 us; one request of 10 tiles 3.9 us in one CTA, 5.4 us
+// in two.
 struct AttnSplit {
   int heads, groups;     // query heads of a CTA, CTAs per kv head
   int chunk, splits;
   long long items;
 };
 inline AttnSplit attn_split(int B, int Hq, int Hkv, int page, int max_pages, int window) {
+  constexpr long long kSetup = 12, kJoin = 6, kStep = 2 * kAttnWarps;
   AttnSplit s;
   const int G = Hq / Hkv;
   s.heads = G <= kColQ ? kColQ : 2 * kColQ;
@@ -576,11 +587,21 @@ inline AttnSplit attn_split(int B, int Hq, int Hkv, int page, int max_pages, int
   long long keys = cap;
   if (window >= 0 && window + 1LL + kTile < cap) keys = window + 1LL + kTile;    // the window may begin inside a tile
   const long long tiles = (keys + kTile - 1) / kTile;
-  long long c = (tiles * s.items + kAttnCtas - 1) / kAttnCtas;
-  c = c < kMinChunk ? kMinChunk : (c > kMaxChunk ? kMaxChunk : c);
-  c = (c + 2 * kAttnWarps - 1) / (2 * kAttnWarps) * (2 * kAttnWarps);
-  s.chunk = static_cast<int>(c);
-  s.splits = static_cast<int>((tiles + c - 1) / c);
+  const long long slots = 152LL * attn_ctas_per_sm(s.heads / kColQ);             // of a GB300
+  long long best = 0, chunk = 0;
+  for (long long n = 1; n <= kMaxSplits; ++n) {
+    const long long c = ((tiles + n - 1) / n + kStep - 1) / kStep * kStep, real = (tiles + c - 1) / c;
+    const long long own = (c < tiles ? c : tiles) + kSetup, half = s.items * real / 2;
+    const long long t = (half > slots ? half * own / slots : own) + (s.items * real + slots - 1) / slots * own +
+                        (real > 1 ? kJoin + real / 2 : 0);
+    if (n == 1 || t < best) {
+      best = t;
+      chunk = c;
+    }
+    if (c == kStep) break;
+  }
+  s.chunk = static_cast<int>(chunk);
+  s.splits = static_cast<int>((tiles + chunk - 1) / chunk);
   return s;
 }
 
