@@ -492,7 +492,8 @@ size_t swa_kv4_cache_size(const swa_params* p, int n_pages, int page);
  *   cu         int32 [B + 1]: first token of each request, and their number
  *              (at most 2^31 - 1)
  *   lens_out   int32 [B], head_out int32: lengths and list head afterwards
- *              (not lens and free_head themselves, which every block reads)
+ *              (not lens, new_lens and free_head themselves, which every block
+ *              reads)
  * A request is refused, and reported, when the pages left do not suffice
  * (requests behind it that need no page still go), when it would pass
  * max_pages, when its tokens pass n_tokens, or when its numbers are negative
@@ -548,10 +549,15 @@ swa_status swa_kv4_read(const swa_params* p, const swa_kv4_cache* c, const int64
  * left out; all four are reported. Several query tokens of one request are as
  * many rows of B, with the same table row and lengths one apart.
  *
- * The workspace (swa_kv4_workspace_size bytes, 256-byte aligned, passed to
- * swa_kv4_workspace_init once before its first use) holds the status word and
- * the partial results of long requests that several CTAs share. Calls on one
- * stream may share it; calls that can overlap need one each.
+ * The workspace (256-byte aligned, passed to swa_kv4_workspace_init once
+ * before its first use) holds the status word, counters, and the partial
+ * results of long requests that several CTAs share. Calls of any shapes and
+ * captured graphs of them may share it as long as they run one after the
+ * other (one stream, or events) and it has the bytes of each
+ * (swa_kv4_workspace_size; a smaller batch can need more: fewer requests are
+ * split into more parts); calls that can overlap need one each. The partial
+ * results of a request are joined in a fixed order: a call gives the same bits
+ * every time.
  */
 size_t swa_kv4_workspace_size(const swa_params* p, int page, int max_pages);
 swa_status swa_kv4_workspace_init(void* workspace, size_t ws_bytes, void* stream);

@@ -61,18 +61,14 @@ constexpr long long kFewThreads = 512;   // per SM
 constexpr int kAppendBlocksPerSm = 64;
 
 // Workspace of the decode attention: header, counters of finished chunks,
-// partial results. There are at most B * Hq <= 65535 counters, and the
-// initialisation zeroes room for all of them (or the whole of a smaller one).
-constexpr size_t kKv4Zeroed = 256 + 65536 * sizeof(unsigned);
-struct Kv4Ws {
-  size_t count, part, end;
-};
-Kv4Ws kv4_ws(const kv4::AttnSplit& s, int d) {
-  Kv4Ws w;
-  w.count = 256;
-  w.part = align256(w.count + static_cast<size_t>(s.items) * sizeof(unsigned));
-  w.end = s.splits > 1 ? align256(w.part + static_cast<size_t>(s.items) * s.splits * s.heads * (d + 2) * sizeof(float)) : w.part;
-  return w;
+// partial results. Calls of any size may follow one another on a workspace,
+// so the counters, which each call leaves at zero, have a place of their own
+// at a fixed size (a call has at most B * Hq <= 65535 of them), where no
+// call's partial results ever lie.
+constexpr size_t kKv4Count = 256, kKv4Part = kKv4Count + 65536 * sizeof(unsigned);
+size_t kv4_ws_bytes(const kv4::AttnSplit& s, int d) {
+  if (s.splits == 1) return kKv4Part;
+  return align256(kKv4Part + static_cast<size_t>(s.items) * s.splits * s.heads * (d + 2) * sizeof(float));
 }
 
 template <int D, int NT, bool kPolled>
@@ -210,7 +206,7 @@ swa_status swa_kv4_plan(int n_pages, int page, int B, int max_pages, const int32
                         static_cast<const void*>(head_out)})
     if (!aligned(x, 4)) return SWA_ERR_INVALID_ARG;
   // every block reads the inputs for itself while block 0 writes the outputs
-  if ((B > 0 && lens_out == lens) || head_out == free_head) return SWA_ERR_INVALID_ARG;
+  if ((B > 0 && (lens_out == lens || lens_out == new_lens)) || head_out == free_head) return SWA_ERR_INVALID_ARG;
   if ((s = check_header(workspace, ws_bytes)) != SWA_OK) return s;
   if ((s = check_device()) != SWA_OK) return s;
   kv4::PlanArgs a{};
@@ -317,13 +313,13 @@ size_t swa_kv4_workspace_size(const swa_params* p, int page, int max_pages) {
   if (check_params(p) != SWA_OK || check_pages(1, page) != SWA_OK || max_pages < 1 ||
       static_cast<long long>(max_pages) * page > INT32_MAX)
     return 0;
-  return kv4_ws(kv4::attn_split(p->B, p->Hq, p->Hkv, page, max_pages, p->window), p->d).end;
+  return kv4_ws_bytes(kv4::attn_split(p->B, p->Hq, p->Hkv, page, max_pages, p->window), p->d);
 }
 
 swa_status swa_kv4_workspace_init(void* workspace, size_t ws_bytes, void* stream) {
-  if (workspace == nullptr || !aligned(workspace, 256) || ws_bytes < 256) return SWA_ERR_INVALID_ARG;
-  const size_t n = ws_bytes < kKv4Zeroed ? ws_bytes : kKv4Zeroed;
-  if (cudaMemsetAsync(workspace, 0, n, static_cast<cudaStream_t>(stream)) != cudaSuccess) return SWA_ERR_CUDA;
+  if (workspace == nullptr || !aligned(workspace, 256)) return SWA_ERR_INVALID_ARG;
+  if (ws_bytes < kKv4Part) return SWA_ERR_WORKSPACE;
+  if (cudaMemsetAsync(workspace, 0, kKv4Part, static_cast<cudaStream_t>(stream)) != cudaSuccess) return SWA_ERR_CUDA;
   return SWA_OK;
 }
 
@@ -341,8 +337,7 @@ swa_status swa_kv4_attn(const swa_params* p, const swa_extras* ex, const swa_kv4
   if (max_pages < 1 || static_cast<long long>(max_pages) * c->page > INT32_MAX) return SWA_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, 256)) return SWA_ERR_INVALID_ARG;
   const kv4::AttnSplit sp = kv4::attn_split(p->B, p->Hq, p->Hkv, c->page, max_pages, p->window);
-  const Kv4Ws w = kv4_ws(sp, p->d);
-  if (ws_bytes < w.end) return SWA_ERR_WORKSPACE;
+  if (ws_bytes < kv4_ws_bytes(sp, p->d)) return SWA_ERR_WORKSPACE;
   if (p->B == 0) return SWA_OK;
   if (!tensor_ok(q) || !tensor_ok(o) || lse == nullptr || table == nullptr || lens == nullptr) return SWA_ERR_INVALID_ARG;
   if (!aligned(lse, 4) || !aligned(table, 4) || !aligned(lens, 4)) return SWA_ERR_INVALID_ARG;
@@ -358,8 +353,8 @@ swa_status swa_kv4_attn(const swa_params* p, const swa_extras* ex, const swa_kv4
   a.o = static_cast<elem_t*>(o); a.lse = lse;
   a.status = static_cast<uint32_t*>(workspace);
   a.chunk = sp.chunk; a.splits = sp.splits; a.groups = sp.groups;
-  a.count = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(workspace) + w.count);
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.part);
+  a.count = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(workspace) + kKv4Count);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kKv4Part);
   a.wait_limit_ns = ex != nullptr && ex->wait_limit_ns != 0 ? ex->wait_limit_ns : kWaitLimitNs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return a.wait_limit_ns < kPollBelowNs ? launch_attn<true>(a, p->d, sp.heads, p->Hkv, st)

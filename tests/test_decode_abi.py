@@ -113,7 +113,10 @@ def test_cache_and_workspace_sizes():
     assert swa.swa_kv4_cache_size(params(d=96), 7, 48) == 0
     assert swa.swa_kv4_workspace_init(None, 256) == BAD
     assert swa.swa_kv4_workspace_init(A + 1, 256) == BAD
-    assert swa.swa_kv4_workspace_init(A, 100) == BAD
+    assert swa.swa_kv4_workspace_init(A, 256) == WS
+    # the counters alone: what every call needs
+    least = swa.swa_kv4_workspace_size(params(T=1, B=1, Hq=1, Hkv=1), 16, 1)
+    assert swa.swa_kv4_workspace_init(A, least - 1) == WS
 
 
 def plan(**kw):
@@ -131,7 +134,7 @@ def test_plan_refuses():
                dict(max_pages=1 << 27), dict(n_tokens=2 ** 31 - 1), dict(lens=None), dict(table=None), dict(free=None),
                dict(head=None), dict(slot=None), dict(pos=None), dict(row=None), dict(cu=None), dict(lens_out=None),
                dict(head_out=None), dict(slot=A + 8), dict(pos=A + 4), dict(row=A + 4), dict(lens=A + 2),
-               dict(lens_out=A), dict(head_out=A), dict(ws=A + 8, ws_bytes=256)):
+               dict(lens_out=A), dict(lens=3 * A, lens_out=A), dict(head_out=A), dict(ws=A + 8, ws_bytes=256)):
         assert plan(**kw) == BAD, kw
     assert plan(B=8193) == UNS
     assert plan(ws=A, ws_bytes=8) == WS

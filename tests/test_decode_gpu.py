@@ -635,6 +635,47 @@ def test_long_request_split_over_many_blocks_repeats_its_bits():
         assert np.all(np.abs(f64(o)[0] - ro) <= 2.0 ** -8 * np.abs(ro) + 1.7e-4 * np.abs(v).max())
 
 
+def test_one_workspace_serves_calls_of_other_shapes():
+    # a few long requests (split, partial results), many short ones, long ones
+    # again: nothing of one call is taken for another's
+    shapes = [([3000, 2900], 4, 2, 128, 64), ([30] * 300, 4, 2, 128, 16), ([1800], 9, 1, 64, 32), ([2000, 5, 0, 700], 2, 2, 64, 16)]
+    sizes = [swa.swa_kv4_workspace_size(swa.make_params(len(x), 1, hq, hkv, d), page, max(-(-n // page) for n in x) + 1)
+             for x, hq, hkv, d, page in shapes]
+    ws = torch.full((max(sizes),), 255, dtype=torch.uint8, device=dev())
+    assert swa.swa_kv4_workspace_init(ws) == swa.SWA_OK
+    for i in (0, 1, 2, 3, 1, 0, 3, 2):
+        lens, Hq, Hkv, d, page = shapes[i]
+        check_attention("bf16", lens, Hq, Hkv, d, page, workspace=ws, seed=10 + i)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_waits_that_run_out_are_reported_and_the_workspace_stays_usable(kind):
+    # a limit of 1 ns, on requests whose 150 MB all come from memory: the
+    # copies all land, only later than the limit allows
+    d, page, n, Hkv, Hq, B = 128, 64, 8192, 2, 4, 64
+    per = n // page
+    cache = torch.randint(0, 256, (B * per, Hkv, page // 16, 18 * d), dtype=torch.uint8, device=dev())
+    sc = cache[..., 16 * d:].view(torch.bfloat16)
+    sc[..., 0::2], sc[..., 1::2] = 0.2, 0.1
+    table = torch.arange(B * per, dtype=torch.int32, device=dev()).view(B, per)
+    lens = torch.full((B,), n, dtype=torch.int32, device=dev())
+    q = randn(6, B, Hq, d, dtype=DT[kind]).to(dev())
+    ws = swa.new_kv4_workspace(cache, B, Hq, max_pages=per, kind=kind)
+    want = swa.kv4_attention(cache, q, table, lens, workspace=ws)
+    assert swa.swa_attn_check_status(ws, kind=kind) == swa.SWA_OK
+    p, c = swa.make_params(B, 1, Hq, Hkv, d), swa.swa_kv4_cache(cache.data_ptr(), B * per, page)
+    o, lse = torch.empty_like(q), torch.empty(B, Hq, device=dev())
+    short = swa.make_extras(wait_limit_ns=1)
+    for _ in range(3):
+        st = swa.swa_kv4_attn(p, short, c, None, q, None, table, per, lens, o, lse, ws)
+        assert st == swa.SWA_OK
+        assert swa.swa_attn_check_status(ws, kind=kind) == swa.SWA_ERR_TIMEOUT
+        assert swa.swa_attn_check_status(ws, kind=kind) == swa.SWA_OK      # read and cleared
+        got = swa.kv4_attention(cache, q, table, lens, workspace=ws)
+        assert swa.swa_attn_check_status(ws, kind=kind) == swa.SWA_OK
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_cache_past_32_bits():
     # pages whose byte offsets, and slots, need more than 32 bits
     d, page, Hkv = 64, 512, 1
