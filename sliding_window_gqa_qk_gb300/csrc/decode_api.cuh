@@ -234,7 +234,7 @@ swa_status swa_kv4_append(const swa_params* p, const swa_extras* ex, const swa_k
   bool rope = false;
   if ((s = check_rope(r, p->d, rope)) != SWA_OK) return s;
   if (rope && pos == nullptr && r->rows < p->T) return SWA_ERR_INVALID_ARG;
-  if (!aligned(pos, 4) || !aligned(slot, 8)) return SWA_ERR_INVALID_ARG;
+  if (!aligned(pos, 4) || !aligned(slot, 8) || !aligned(gk, 4)) return SWA_ERR_INVALID_ARG;
   if (ex != nullptr && (ex->rope_cos != nullptr || ex->rope_sin != nullptr)) return SWA_ERR_INVALID_ARG;
   Call call;
   call.p = *p;
@@ -313,7 +313,7 @@ size_t swa_kv4_workspace_size(const swa_params* p, int page, int max_pages) {
   if (check_params(p) != SWA_OK || check_pages(1, page) != SWA_OK || max_pages < 1 ||
       static_cast<long long>(max_pages) * page > INT32_MAX)
     return 0;
-  return kv4_ws_bytes(kv4::attn_split(p->B, p->Hq, p->Hkv, page, max_pages, p->window), p->d);
+  return kv4_ws_bytes(kv4::attn_split(p->B, p->Hq, p->Hkv, p->d, page, max_pages, p->window), p->d);
 }
 
 swa_status swa_kv4_workspace_init(void* workspace, size_t ws_bytes, void* stream) {
@@ -336,11 +336,11 @@ swa_status swa_kv4_attn(const swa_params* p, const swa_extras* ex, const swa_kv4
   if (ex != nullptr && (ex->rope_cos != nullptr || ex->rope_sin != nullptr)) return SWA_ERR_INVALID_ARG;
   if (max_pages < 1 || static_cast<long long>(max_pages) * c->page > INT32_MAX) return SWA_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, 256)) return SWA_ERR_INVALID_ARG;
-  const kv4::AttnSplit sp = kv4::attn_split(p->B, p->Hq, p->Hkv, c->page, max_pages, p->window);
+  const kv4::AttnSplit sp = kv4::attn_split(p->B, p->Hq, p->Hkv, p->d, c->page, max_pages, p->window);
   if (ws_bytes < kv4_ws_bytes(sp, p->d)) return SWA_ERR_WORKSPACE;
   if (p->B == 0) return SWA_OK;
   if (!tensor_ok(q) || !tensor_ok(o) || lse == nullptr || table == nullptr || lens == nullptr) return SWA_ERR_INVALID_ARG;
-  if (!aligned(lse, 4) || !aligned(table, 4) || !aligned(lens, 4)) return SWA_ERR_INVALID_ARG;
+  if (!aligned(lse, 4) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(gq, 16)) return SWA_ERR_INVALID_ARG;
   if ((s = check_device()) != SWA_OK) return s;
   a.B = p->B; a.Hq = p->Hq; a.max_pages = max_pages; a.window = p->window;
   a.scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt(static_cast<float>(p->d));
@@ -355,6 +355,7 @@ swa_status swa_kv4_attn(const swa_params* p, const swa_extras* ex, const swa_kv4
   a.chunk = sp.chunk; a.splits = sp.splits; a.groups = sp.groups;
   a.count = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(workspace) + kKv4Count);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kKv4Part);
+  a.part_ml = reinterpret_cast<float2*>(a.part + sp.items * sp.splits * sp.heads * p->d);
   a.wait_limit_ns = ex != nullptr && ex->wait_limit_ns != 0 ? ex->wait_limit_ns : kWaitLimitNs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return a.wait_limit_ns < kPollBelowNs ? launch_attn<true>(a, p->d, sp.heads, p->Hkv, st)

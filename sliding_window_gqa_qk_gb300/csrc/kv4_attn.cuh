@@ -37,6 +37,15 @@
 //   - Few requests. A request's tiles are split into chunks of one CTA each;
 //     with more than one, each writes its partial result, and the CTA that
 //     finishes last joins them in the order of the chunks.
+//
+// Measured (GB300, graph of calls, bf16): 32 requests of 57k to 65k tokens, 16 / 4
+// heads of 128: 212 us, 5.33 TB/s, 78 % of the measured copy rate. The same
+// kernel with the arithmetic taken out streams the cache in 166 us (the copy
+// rate), with the copies taken out it computes in 184 us; the two overlap but
+// not wholly. About 300 instructions a warp and tile, 160 of them turning
+// numbers into operands; 57 % of the ALU pipe, 24 % of the tensor pipe. At d =
+// 64 a token has half the bytes and the same softmax: 48 % of the copy rate.
+// Short requests pay a CTA's set-up and end, about 3 us.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -52,8 +61,12 @@ constexpr int kStages = 2;               // steps of two tiles in flight per war
 constexpr bool kThreeTerms = sizeof(elem_t) == 4;
 constexpr int kColQ = 4;                 // query heads of one 8-column operand
 constexpr int kMaxSplits = 512;          // CTAs of one request and kv head
-// CTAs an SM holds (registers: 128 a thread with one operand, 255 with two)
-constexpr int attn_ctas_per_sm(int operands) { return operands == 1 ? 4 : 2; }
+// CTAs an SM holds, by head dim and 8-column operands; it bounds the registers
+// of a thread (128, or 255 for two). Measured on 16 requests of 32768 tokens, 4 kv
+// heads: d = 128, eight query heads a kv head: two 92.6 us, three (spills) 97; d =
+// 64, eight: two 67.2, three 56.9, four 55.3; d = 64, four: four 43.2, five 43.2,
+// six 46.1.
+constexpr int attn_ctas_per_sm(int d, int operands) { return operands == 1 || d == 64 ? 4 : 2; }
 
 struct AttnArgs {
   Cache c;
@@ -67,7 +80,8 @@ struct AttnArgs {
   int chunk, splits;                     // tiles of a CTA, CTAs of a request
   int groups;                            // CTAs that share a kv head's query heads
   unsigned* count;                       // [B * Hkv * groups] finished chunks, 0 between calls
-  float* part;                           // [B * Hkv * groups][splits][heads][D + 2]: O, M, L
+  float* part;                           // [B * Hkv * groups][splits][heads][D]: partial O
+  float2* part_ml;                       // [B * Hkv * groups][splits][heads]: their M, L
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
@@ -180,28 +194,47 @@ template <int D>
 __device__ __forceinline__ void query_row(const AttnArgs& a, const elem_t* q, int pos, __half* dst, float* f) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31, c0 = lane * E;
-  float x[E] = {}, ss = 0.f;
-  if (q != nullptr) {
+  float x[E] = {}, g[E], ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int c = c0 + i;
-      x[i] = to_f32(q[c]);
-      if (a.rcos != nullptr && c < a.rot) {
-        const int half = a.rot / 2;
-        const int col = a.interleaved ? c / 2 : (c < half ? c : c - half);
-        const int to = a.interleaved ? c ^ 1 : (c < half ? c + half : c - half);
-        const bool first = a.interleaved ? (c & 1) == 0 : c < half;
-        const long long at = static_cast<long long>(pos) * half + col;
-        x[i] = fmaf(x[i], a.rcos[at], (first ? 1.f : -1.f) * to_f32(q[to]) * a.rsin[at]);
+  for (int i = 0; i < E; ++i) g[i] = 1.0f;
+  if (q != nullptr) {
+    // all loads before any use: this is latency in front of every CTA
+    load_vec<E>(q + c0, x);
+    if (a.gq != nullptr) load_vec<E>(a.gq + c0, g);
+    if (a.rcos != nullptr && c0 < a.rot) {
+      const int half = a.rot / 2;
+      const long long row = static_cast<long long>(pos) * half;
+      if (a.interleaved) {
+        float c[E / 2], s[E / 2];
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+          c[i] = a.rcos[row + c0 / 2 + i];
+          s[i] = a.rsin[row + c0 / 2 + i];
+        }
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+          const float u = x[2 * i], v = x[2 * i + 1];
+          x[2 * i] = fmaf(u, c[i], v * s[i]);
+          x[2 * i + 1] = fmaf(v, c[i], -u * s[i]);
+        }
+      } else {      // half is a multiple of 8: the lane's channels lie on one side of it
+        const bool first = c0 < half;
+        float y[E], c[E], s[E];
+        load_vec<E>(q + (first ? c0 + half : c0 - half), y);
+        load_vec<E>(a.rcos + row + (first ? c0 : c0 - half), c);
+        load_vec<E>(a.rsin + row + (first ? c0 : c0 - half), s);
+#pragma unroll
+        for (int i = 0; i < E; ++i) x[i] = fmaf(x[i], c[i], (first ? y[i] : -y[i]) * s[i]);
       }
-      ss = fmaf(x[i], x[i], ss);
     }
+#pragma unroll
+    for (int i = 0; i < E; ++i) ss = fmaf(x[i], x[i], ss);
   }
   const float mul = rsqrtf(warp_sum(ss) / D + a.eps) * (a.scale * 1.4426950408889634f);
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < E; ++i) {
-    x[i] *= mul * (a.gq ? a.gq[c0 + i] : 1.0f);
+    x[i] *= mul * g[i];
     if (q == nullptr) x[i] = 0.f;
     top = fmaxf(top, fabsf(x[i]));
   }
@@ -232,8 +265,21 @@ __device__ __forceinline__ void query_row(const AttnArgs& a, const elem_t* q, in
   if (D == 128 && lane == 16) f[2] = sum;
 }
 
+// o and lse of one head from its sums, by one warp. No key: 0 and -infinity;
+// a NaN stays one.
+template <int D>
+__device__ __forceinline__ void finish_head(const AttnArgs& a, long long head, float (&o)[D / 32], float top, float sum) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] *= inv;
+  store_vec<E>(a.o + head * D + lane * E, o);
+  if (lane == 0) a.lse[head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
 template <int D, int NT, bool kPolled>
-__global__ void __launch_bounds__(kAttnWarps * 32, attn_ctas_per_sm(NT)) attn_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kAttnWarps * 32, attn_ctas_per_sm(D, NT)) attn_kernel(const __grid_constant__ AttnArgs a) {
   using S = AttnShape<D>;
   using M = AttnSmem<D, NT>;
   constexpr int NG = S::NG, W = S::W, NQ = NT * kColQ;
@@ -497,7 +543,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, attn_ctas_per_sm(NT)) attn_ke
   __syncthreads();
   constexpr int E = D / 32;
   const int item = (b * a.c.Hkv + h) * a.groups + qg;
-  float* part = a.part + static_cast<long long>(item) * a.splits * NQ * (D + 2);
+  const long long part0 = static_cast<long long>(item) * a.splits * NQ;
   for (int i = wid; i < nq; i += kAttnWarps) {      // a warp a head, E channels a lane
     float top = -1e30f, sum = 0.f, o[E] = {};
 #pragma unroll
@@ -506,20 +552,17 @@ __global__ void __launch_bounds__(kAttnWarps * 32, attn_ctas_per_sm(NT)) attn_ke
     for (int k = 0; k < kAttnWarps; ++k) {
       const float f = ex2_approx(jm[2 * (k * NQ + i)] - top);
       sum = fmaf(f, jm[2 * (k * NQ + i) + 1], sum);
+      float x[E];
+      load_vec<E>(jo + (k * NQ + i) * D + lane * E, x);
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(f, jo[(k * NQ + i) * D + lane * E + e], o[e]);
+      for (int e = 0; e < E; ++e) o[e] = fmaf(f, x[e], o[e]);
     }
     if (chunks == 1) {
-      const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;     // a NaN stays one
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] *= inv;
-      store_vec<E>(a.o + (hq0 + i) * D + lane * E, o);
-      if (lane == 0) a.lse[hq0 + i] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+      finish_head<D>(a, hq0 + i, o, top, sum);
     } else {
-      float* dst = part + (static_cast<long long>(blockIdx.x) * NQ + i) * (D + 2);
-#pragma unroll
-      for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(dst + lane * E + e) = make_float2(o[e], o[e + 1]);
-      if (lane == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(top, sum);
+      const long long at = part0 + static_cast<long long>(blockIdx.x) * NQ + i;
+      store_vec<E>(a.part + at * D + lane * E, o);
+      if (lane == 0) a.part_ml[at] = make_float2(top, sum);
     }
   }
   if (chunks == 1) return;
@@ -532,31 +575,62 @@ __global__ void __launch_bounds__(kAttnWarps * 32, attn_ctas_per_sm(NT)) attn_ke
   if (!flags[1]) return;
   __threadfence();
   if (tid == 0) a.count[item] = 0;        // for the next call
-  for (int i = wid; i < nq; i += kAttnWarps) {
-    const float* src = part + i * (D + 2);
-    const long long step = static_cast<long long>(NQ) * (D + 2);
-    float top = -1e30f;
-    for (int k = lane; k < chunks; k += 32) top = fmaxf(top, __ldcg(src + k * step + D));
+
+  // join the chunks: a warp every fourth one, all heads of it at once (their
+  // loads wait together), then the warps as above, with M common to all
+  float top[NQ], sum[NQ] = {}, o[NQ][E] = {};
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float sum = 0.f, o[E] = {};
+  for (int i = 0; i < NQ; ++i) top[i] = -1e30f;
+  for (int k = lane; k < chunks; k += 32) {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+      if (i < nq) top[i] = fmaxf(top[i], __ldcg(a.part_ml + part0 + k * NQ + i).x);
+  }
+#pragma unroll
+  for (int i = 0; i < NQ; ++i)
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], x));
 #pragma unroll 4
-    for (int k = 0; k < chunks; ++k) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(src + k * step + D));
-      const float f = ex2_approx(ml.x - top);
-      sum = fmaf(f, ml.y, sum);
+  for (int k = wid; k < chunks; k += kAttnWarps) {
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(src + k * step + lane * E + e));
-        o[e] = fmaf(f, v.x, o[e]);
-        o[e + 1] = fmaf(f, v.y, o[e + 1]);
+    for (int i = 0; i < NQ; ++i) {
+      if (i >= nq) continue;
+      const long long at = part0 + static_cast<long long>(k) * NQ + i;
+      const float2 ml = __ldcg(a.part_ml + at);
+      float x[E];
+      if constexpr (E == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + at * D + lane * E));
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part + at * D + lane * E));
+        x[0] = v.x; x[1] = v.y;
       }
-    }
-    const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
+      const float f = ex2_approx(ml.x - top[i]);
+      sum[i] = fmaf(f, ml.y, sum[i]);
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= inv;
-    store_vec<E>(a.o + (hq0 + i) * D + lane * E, o);
-    if (lane == 0) a.lse[hq0 + i] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+      for (int e = 0; e < E; ++e) o[i][e] = fmaf(f, x[e], o[i][e]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    store_vec<E>(jo + (wid * NQ + i) * D + lane * E, o[i]);
+    if (lane == 0) {
+      jm[2 * (wid * NQ + i)] = top[i];
+      jm[2 * (wid * NQ + i) + 1] = sum[i];
+    }
+  }
+  __syncthreads();
+  for (int i = wid; i < nq; i += kAttnWarps) {
+    float total = 0.f, y[E] = {};
+#pragma unroll
+    for (int k = 0; k < kAttnWarps; ++k) {
+      total += jm[2 * (k * NQ + i) + 1];
+      float x[E];
+      load_vec<E>(jo + (k * NQ + i) * D + lane * E, x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] += x[e];
+    }
+    finish_head<D>(a, hq0 + i, y, jm[2 * i], total);
   }
 }
 
@@ -576,7 +650,7 @@ struct AttnSplit {
   int chunk, splits;
   long long items;
 };
-inline AttnSplit attn_split(int B, int Hq, int Hkv, int page, int max_pages, int window) {
+inline AttnSplit attn_split(int B, int Hq, int Hkv, int d, int page, int max_pages, int window) {
   constexpr long long kSetup = 12, kJoin = 6, kStep = 2 * kAttnWarps;
   AttnSplit s;
   const int G = Hq / Hkv;
@@ -587,7 +661,7 @@ inline AttnSplit attn_split(int B, int Hq, int Hkv, int page, int max_pages, int
   long long keys = cap;
   if (window >= 0 && window + 1LL + kTile < cap) keys = window + 1LL + kTile;    // the window may begin inside a tile
   const long long tiles = (keys + kTile - 1) / kTile;
-  const long long slots = 152LL * attn_ctas_per_sm(s.heads / kColQ);             // of a GB300
+  const long long slots = 152LL * attn_ctas_per_sm(d, s.heads / kColQ);          // of a GB300
   long long best = 0, chunk = 0;
   for (long long n = 1; n <= kMaxSplits; ++n) {
     const long long c = ((tiles + n - 1) / n + kStep - 1) / kStep * kStep, real = (tiles + c - 1) / c;

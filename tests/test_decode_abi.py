@@ -172,7 +172,7 @@ def test_cache_calls_refuse(kind):
     assert append(p, cache(page=1 << 21), kind=kind) == UNS
     assert append(params(d=96), cache(), kind=kind) == UNS and attn(params(d=96, T=1), cache(), kind=kind) == UNS
     for kw in (dict(k=None), dict(v=None), dict(slot=None), dict(k=A + 8), dict(v=A + 4), dict(slot=A + 4), dict(pos=A + 1),
-               dict(ws=A + 1, ws_bytes=256)):
+               dict(gk=A + 2), dict(ws=A + 1, ws_bytes=256)):
         assert append(p, cache(), kind=kind, **kw) == BAD, kw
     assert append(p, cache(), kind=kind, ws=A, ws_bytes=128) == WS
     assert append(p, cache(), rope(rows=2), kind=kind) == BAD
@@ -195,7 +195,7 @@ def test_cache_calls_refuse(kind):
     for kw in (dict(slot=None), dict(k=None), dict(v=A + 8), dict(slot=A + 4), dict(ws=A + 2, ws_bytes=256)):
         assert read(p, cache(), kind, **kw) == BAD, kw
     for kw in (dict(q=None), dict(table=None), dict(lens=None), dict(o=None), dict(lse=None), dict(q=A + 8), dict(lens=A + 2),
-               dict(max_pages=0), dict(max_pages=1 << 27), dict(ws=None), dict(ws=A + 16)):
+               dict(gq=A + 8), dict(lse=A + 2), dict(table=A + 1), dict(max_pages=0), dict(max_pages=1 << 27), dict(ws=None), dict(ws=A + 16)):
         assert attn(one, cache(), kind=kind, **kw) == BAD, kw
     assert attn(one, cache(), kind=kind, ws_bytes=swa.swa_kv4_workspace_size(one, 32, 16, kind) - 1) == WS
     assert attn(params(T=2), cache(), kind=kind) == BAD and attn(params(T=1, causal=False), cache(), kind=kind) == BAD
