@@ -97,8 +97,8 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 //
 // A border between two numbers, or between two bf16 steps, splits values that
 // fp32 arithmetic cannot always tell apart. Two cases:
-//   - Values of plain layers enter exactly (bf16), and many sit on a border:
-//     x, z and s are short numbers. The number found with an approximate
+//   - Values of plain layers enter exactly (bf16), and many sit on a border (one
+//     Gaussian value in 450): x, z and s are short numbers. The number found with an approximate
 //     reciprocal is settled by the remainder x - z - n s, which fma gives
 //     exactly (kExact).
 //   - Keys, and values with an embedding, are results of fp32 arithmetic. A
@@ -257,10 +257,10 @@ struct AppendArgs {
   uint32_t* status;                    // or NULL
 };
 
-// What fp32 arithmetic may leave an entry off by, as a multiple of the row's
-// largest: five roundings of rotation, norm and gain, of half of 2^-23 each
-// and of either sign, and two of the number's product with the reciprocal,
-// come to 2 to 3 units of 2^-24 at most on the rows measured.
+// What fp32 arithmetic may leave an entry off by, in units of 2^-24 of the
+// row's largest entry. Rotation, norm and gain, in fp32 and fp64 on 200,000
+// Gaussian rows: 0.41 rms; more than 3 in one row of 54, more than 4 in one of
+// 2400, 4.7 at most. At 4, one row in 550 goes the slow way.
 constexpr float kKeyErr = 4.0f * 5.9604645e-8f;
 constexpr float kMixErr = 4.0f * 5.9604645e-8f;
 constexpr int kAppendWarps = 4;      // a small block: one slow row holds up few others
@@ -322,6 +322,12 @@ __device__ __noinline__ uint32_t mix_f64(const AppendArgs& a, uint32_t row, cons
 // Lanes as in the other row-wise kernels: LPR lanes hold one row of D
 // channels, 16 bytes each, and a warp works on RPI rows (token, head) at a
 // time, key and value together. MIX: a value embedding.
+// It should be bound by memory (4 D bytes in, 18 D / 16 out per row) and is
+// bound by instructions, about 35 per channel and lane: 16384 tokens of 3 heads of
+// 128 take 24.2 us, 1.3 TB/s, of which the steps and centres (computed by all
+// lanes of a group) are 5.5 us, rotation 2.5, the keys' numbers 2.3, stores 2.1,
+// fp64 rows 0.7. 64 single tokens take 3.0 us, a chain of dependent loads.
+// Blocks of four warps, not persistent: 24.2 us; of eight, eight per SM: 32.
 template <int D, bool MIX>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_constant__ AppendArgs a) {
   using M = RowMap<D>;
@@ -464,6 +470,8 @@ struct ReadArgs {
   uint32_t* status;          // or NULL
 };
 
+// Bound by the rows written: 16384 tokens of 3 heads of 128 take 6.3 us, 5.1
+// TB/s read and written, 75 % of the measured copy rate.
 template <int D>
 __global__ void __launch_bounds__(kRowWarps * 32) read_kernel(const __grid_constant__ ReadArgs a) {
   using M = RowMap<D>;
@@ -517,7 +525,9 @@ __global__ void __launch_bounds__(kRowWarps * 32) read_kernel(const __grid_const
 //   free[head + off_b ..], its tokens' slots follow.
 // Every block does the whole scan itself (a few thousand requests at most,
 // two integers each, from L2) and keeps it in shared memory, so one launch
-// serves every token and no block waits on another.
+// serves every token and no block waits on another. Latency bounds it: 64
+// requests of one token 6.4 us, 1000 requests of 104,000 tokens 7.5 us (their
+// bytes would take 0.3).
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxB = 8192;      // 12 bytes of shared memory per request

@@ -84,7 +84,9 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_
 // in flight at a time (six 16-byte loads where a unit is two pieces, four where
 // it is one: 24 more registers for eight cost 9 % on a layer of 16 x 2048
 // positions). Every element is read and written by the same thread,
-// reads first, so the rotation also runs in place.
+// reads first, so the rotation also runs in place. Bound by memory: 16 x 2048
+// positions, 6 + 3 heads of 128, bf16: 25.0 us, 6.1 TB/s, 90 % of the measured
+// copy rate; 2 x 16384, 16 + 4 heads, fp32: 101 us, 98 %.
 // ---------------------------------------------------------------------------
 constexpr int kRopeBatch[2] = {3, 4};    // split-half, interleaved
 
