@@ -22,6 +22,11 @@ import torch
 
 from . import build as _build
 
+try:  # the short way into the decode calls; everything works without it
+    from . import _fast
+except ImportError:
+    _fast = None
+
 __all__ = [
     "swa_params", "SwaError", "load",
     "swa_attn_workspace_size", "swa_attn_workspace_init", "swa_attn_fwd", "swa_attn_bwd",
@@ -169,6 +174,10 @@ def load(kind: str = "bf16") -> ctypes.CDLL:
     lib.swa_build_info.argtypes = []
     lib.swa_build_info.restype = ctypes.c_char_p
     _LIBS[kind] = lib
+    if _fast is not None:
+        _fast.bind(0 if kind == "bf16" else 1, *(
+            ctypes.cast(getattr(lib, f), _vp).value for f in (
+                "swa_rope_tables", "swa_rope_apply", "swa_kv4_plan", "swa_kv4_append", "swa_kv4_read", "swa_kv4_attn")))
     return lib
 
 
@@ -535,13 +544,14 @@ def attention_backward(q, k, v, gq, gk, o, lse, dO, *, window: int = -1, causal:
 # Rotary positions and the decode path. These calls check types, shapes and
 # devices before they pass addresses on (the C ABI sees addresses only), run
 # on the device of their tensors, and allocate their outputs on the stream
-# they run on. A decode step is a few microseconds of GPU work, so they are
-# written to cost the host little: one check per tensor, which also yields its
-# address, and one call.
+# they run on. A decode step is a few microseconds of GPU work, so the ordinary
+# case goes through csrc/py_fast.cpp, which returns None for every other: the
+# Python below is the whole of each call, the other only its short way.
 # ---------------------------------------------------------------------------
 
 SWA_ROPE_PLAIN, SWA_ROPE_LINEAR, SWA_ROPE_NTK, SWA_ROPE_BY_PARTS = range(4)
 _SCALINGS = {"none": SWA_ROPE_PLAIN, "linear": SWA_ROPE_LINEAR, "ntk": SWA_ROPE_NTK, "by_parts": SWA_ROPE_BY_PARTS}
+_NO_ROPE = (None, None)
 _F32, _BF16, _I32, _I64, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8
 # torch's own lookup of the current stream's handle by device index; the
 # public one builds a Stream object each time (2.9 us against 0.1 us)
@@ -621,6 +631,10 @@ def rope_tables(rows: int, rot: int, *, base: float = 10000.0, scaling: str = "n
         raise ValueError(f"scaling: one of {sorted(_SCALINGS)} is expected, got {scaling!r}")
     if rows < 0 or rot < 0:
         raise ValueError("rows, rot: not below 0")
+    if _fast is not None and device is None and stream is None:
+        r = _fast.rope_tables(rows, rot, _SCALINGS[scaling], base, factor, orig_len, slow, fast, amplitude, first)
+        if r is not None:
+            return r
     device = torch.device("cuda" if device is None else device)
     if device.type == "cuda" and device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
@@ -648,6 +662,10 @@ def rope_apply(q, k, rope, *, pos=None, interleaved: bool = False, inverse: bool
     (q', k') may be (q, k): in place. ``workspace``: where positions outside
     the tables are reported (swa_attn_check_status); their rows are not
     written."""
+    if _fast is not None and stream is None and rope is not None:
+        r = _fast.rope_apply(q, k, *rope, pos, interleaved, inverse, *(_NO_ROPE if out is None else out), workspace)
+        if r is not None:
+            return r
     x = q if q is not None else k
     if x is None or x.dim() != 4:
         raise ValueError("rope_apply: q or k [B, T, H, d] is expected")
@@ -721,6 +739,10 @@ def kv4_plan(lens, new_lens, table, free_pages, free_head, *, page: int, n_pages
     (int32) of each new token [n_tokens] (the sum of new_lens, known to the
     host; more is padding, slot -1), cu [B + 1], and lens and free_head
     afterwards."""
+    if _fast is not None and stream is None and n_tokens is not None:
+        r = _fast.kv4_plan(lens, new_lens, table, free_pages, free_head, page, n_pages, n_tokens, workspace)
+        if r is not None:
+            return r
     dev = lens.device
     if table.dim() != 2 or lens.dim() != 1:
         raise ValueError("lens [B] and table [B, max_pages] are expected")
@@ -764,6 +786,10 @@ def kv4_append(cache, k, v, slot, *, pos=None, rope=None, interleaved: bool = Fa
     rotated, normed or mixed) into the cache at slot int64 [B, T]; -1 skips a
     token. Rotary, QK-norm gain, value embedding and gate as in
     attention_forward, with the rotation at pos int32 [B, T] (None: t)."""
+    if _fast is not None and stream is None and gate_w is None:
+        if _fast.kv4_append(cache, k, v, slot, pos, *(_NO_ROPE if rope is None else rope), interleaved, gk, eps, ve, tok, ve_gate, ve_scale,
+                            workspace):
+            return
     n_pages, Hkv, page, d = _cache_dims(cache)
     dev, dt = cache.device, k.dtype
     lib = load(_kind("k", dt))
@@ -804,6 +830,10 @@ def kv4_read(cache, slot, *, dtype=torch.bfloat16, workspace=None, stream=None):
     """k, v = kv4_read(cache, slot): the rows that slot int64 [B, T] holds, as
     ``dtype`` (bf16 or fp32) [B, T, Hkv, d]; keys are rotated and normed.
     Rows of slot -1 are zero."""
+    if _fast is not None and stream is None and (dtype is _BF16 or dtype is _F32):
+        r = _fast.kv4_read(cache, slot, dtype is _F32, workspace)
+        if r is not None:
+            return r
     n_pages, Hkv, page, d = _cache_dims(cache)
     dev = cache.device
     lib = load(_kind("dtype", dtype))
@@ -832,6 +862,11 @@ def kv4_attention(cache, q, table, lens, *, rope=None, interleaved: bool = False
     max_pages]. o as q; lse fp32 [B, Hq]. Rotary, gain, window and scale as in
     attention_forward. ``workspace``: from new_kv4_workspace, kept by the
     caller (one per stream); None: one for this call."""
+    if _fast is not None and stream is None:
+        r = _fast.kv4_attention(cache, q, table, lens, *(_NO_ROPE if rope is None else rope), interleaved, gq, window,
+                                softmax_scale, eps, workspace)
+        if r is not None:
+            return r
     n_pages, Hkv, page, d = _cache_dims(cache)
     dev, dt = cache.device, q.dtype
     kind = _kind("q", dt)

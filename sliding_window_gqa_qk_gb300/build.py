@@ -3,7 +3,12 @@
   libswaattn.so       bf16 tensors, tcgen05 kernels (the product path)
   libswaattn_fp32.so  fp32 tensors, SIMT debug kernels
 
-Both come from csrc/swa_attn.cu, compiled for sm_103a only.
+Both come from csrc/swa_attn.cu, compiled for sm_103a only. And, with the host
+compiler against the installed torch:
+
+  _fast.so            the binding's short way into the decode calls
+                      (csrc/py_fast.cpp); the binding works without it, only
+                      slower, so a failure to build it is a warning
 """
 
 from __future__ import annotations
@@ -12,6 +17,8 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -46,7 +53,7 @@ def lib_path(kind: str) -> str:
 
 def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-                  + glob.glob(os.path.join(INCLUDE, "*.h")))
+                  + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def _stale(out: str) -> bool:
@@ -54,6 +61,22 @@ def _stale(out: str) -> bool:
         return True
     t = os.path.getmtime(out)
     return any(os.path.getmtime(s) > t for s in _sources())
+
+
+FAST = os.path.join(PKG, "_fast.so")
+
+
+def _fast_cmd(out: str, nvcc: str):
+    """The host compiler's command for _fast.so."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    include = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include"), "/usr/local/cuda/include"]
+    return [shutil.which("g++") or "c++", "-std=c++17", "-O2", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *("-I" + i for i in include), "-o", out,
+            os.path.join(CSRC, "py_fast.cpp"), "-L" + os.path.join(base, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python",
+            "-lc10_cuda"]
 
 
 def build(force: bool = False, verbose: bool = False) -> None:
@@ -71,10 +94,20 @@ def build(force: bool = False, verbose: bool = False) -> None:
             print(" ".join(cmd))
         procs.append((out, tmp, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                  stderr=subprocess.STDOUT, text=True)))
+    if force or _stale(FAST):
+        try:
+            cmd = _fast_cmd(FAST + ".tmp", nvcc)
+            if verbose:
+                print(" ".join(cmd))
+            procs.append((FAST, FAST + ".tmp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+        except (OSError, ImportError, AttributeError) as e:
+            warnings.warn(f"_fast.so is not built: {e}")
     errors = []
     for out, tmp, p in procs:
         log, _ = p.communicate()
-        if p.returncode != 0:
+        if p.returncode != 0 and out == FAST:
+            warnings.warn("_fast.so is not built:\n" + log[-2000:])
+        elif p.returncode != 0:
             errors.append(f"{os.path.basename(out)}:\n{log}")
         else:
             os.replace(tmp, out)

@@ -1,0 +1,334 @@
+// The short way from Python to the rotary and decode entry points.
+//
+// A decode step is 4 to 15 us of GPU work, and the checks, allocations and
+// argument conversions of the binding's Python functions cost 16 to 30 us
+// around it. These functions do the same for the ordinary case (tensors of
+// the right types and shapes on the current device, the current stream) in a
+// few. In every other case, and when the library refuses the call, they
+// return None and the Python function does it all itself: what is wrong is
+// found and told there, and nothing depends on this module but time.
+#include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <ATen/ops/empty_like.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "../../include/swa_attn.h"
+
+namespace {
+
+struct Lib {
+  decltype(&swa_rope_tables) tables;
+  decltype(&swa_rope_apply) apply;
+  decltype(&swa_kv4_plan) plan;
+  decltype(&swa_kv4_append) append;
+  decltype(&swa_kv4_read) read;
+  decltype(&swa_kv4_attn) attn;
+};
+Lib libs[2];   // bf16, fp32; filled by bind()
+
+struct Refused {};   // not the ordinary case
+
+int device_now() { return static_cast<int>(c10::cuda::current_device()); }
+void* stream_now(int dev) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
+
+const at::Tensor& tensor(PyObject* o) {
+  if (!THPVariable_Check(o)) throw Refused{};
+  return THPVariable_Unpack(o);
+}
+// Address of a tensor after its checks; None passes as NULL.
+void* at_(PyObject* o, at::ScalarType type, int dev, at::IntArrayRef shape) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = tensor(o);
+  if (t.scalar_type() != type || !t.is_cuda() || t.get_device() != dev || t.sizes() != shape || !t.is_contiguous())
+    throw Refused{};
+  return t.data_ptr();
+}
+int small(int64_t x) {
+  if (x < 0 || x > INT32_MAX) throw Refused{};
+  return static_cast<int>(x);
+}
+int int_of(PyObject* o) {
+  const long long x = PyLong_AsLongLong(o);
+  if (PyErr_Occurred() || x < INT32_MIN || x > INT32_MAX) throw Refused{};
+  return static_cast<int>(x);
+}
+double double_of(PyObject* o) {
+  const double x = PyFloat_AsDouble(o);
+  if (PyErr_Occurred()) throw Refused{};
+  return x;
+}
+int kind_of(at::ScalarType t) {
+  const int kind = t == at::kBFloat16 ? 0 : (t == at::kFloat ? 1 : -1);
+  if (kind < 0 || libs[kind].attn == nullptr) throw Refused{};   // another type, or its library is not loaded yet
+  return kind;
+}
+// Rotary tables: false where there are none.
+bool rope_of(PyObject* cos, PyObject* sin, PyObject* interleaved, int dev, swa_rope& r) {
+  if (cos == Py_None) return false;
+  const at::Tensor& c = tensor(cos);
+  if (c.dim() != 2) throw Refused{};
+  r.cos = static_cast<const float*>(at_(cos, at::kFloat, dev, c.sizes()));
+  r.sin = static_cast<const float*>(at_(sin, at::kFloat, dev, c.sizes()));
+  if (r.sin == nullptr) throw Refused{};
+  r.rows = small(c.size(0));
+  r.rot = small(2 * c.size(1));
+  r.interleaved = PyObject_IsTrue(interleaved);
+  return true;
+}
+struct Ws {
+  void* at;
+  size_t bytes;
+};
+Ws ws_of(PyObject* o, int dev) {
+  if (o == Py_None) return {nullptr, 0};
+  const at::Tensor& t = tensor(o);
+  return {at_(o, at::kByte, dev, {t.numel()}), static_cast<size_t>(t.numel())};
+}
+struct CacheDims {
+  swa_kv4_cache c;
+  int Hkv, d;
+};
+CacheDims cache_of(PyObject* o, int dev) {
+  const at::Tensor& t = tensor(o);
+  if (t.dim() != 4 || (t.size(3) != 18 * 64 && t.size(3) != 18 * 128)) throw Refused{};
+  CacheDims x{};
+  x.c.data = at_(o, at::kByte, dev, t.sizes());
+  x.c.n_pages = small(t.size(0));
+  x.Hkv = small(t.size(1));
+  x.c.page = small(16 * t.size(2));
+  x.d = small(t.size(3) / 18);
+  return x;
+}
+at::TensorOptions on(int dev, at::ScalarType type) {
+  return at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev)));
+}
+PyObject* pair(const at::Tensor& a, const at::Tensor& b) {
+  PyObject* x = a.defined() ? THPVariable_Wrap(a) : Py_NewRef(Py_None);
+  PyObject* y = b.defined() ? THPVariable_Wrap(b) : Py_NewRef(Py_None);
+  PyObject* t = PyTuple_Pack(2, x, y);
+  Py_DECREF(x);
+  Py_DECREF(y);
+  return t;
+}
+
+// Runs f; anything out of the ordinary is None.
+template <typename F>
+PyObject* guarded(F f) {
+  try {
+    PyObject* r = f();
+    if (r != nullptr) return r;
+  } catch (...) {
+  }
+  PyErr_Clear();
+  Py_RETURN_NONE;
+}
+
+PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 7) Py_RETURN_NONE;
+  return guarded([&]() -> PyObject* {
+    void* f[6];
+    for (int i = 0; i < 6; ++i) f[i] = PyLong_AsVoidPtr(a[i + 1]);
+    if (PyErr_Occurred()) throw Refused{};
+    libs[int_of(a[0]) & 1] = Lib{reinterpret_cast<decltype(&swa_rope_tables)>(f[0]), reinterpret_cast<decltype(&swa_rope_apply)>(f[1]),
+                                 reinterpret_cast<decltype(&swa_kv4_plan)>(f[2]), reinterpret_cast<decltype(&swa_kv4_append)>(f[3]),
+                                 reinterpret_cast<decltype(&swa_kv4_read)>(f[4]), reinterpret_cast<decltype(&swa_kv4_attn)>(f[5])};
+    Py_RETURN_TRUE;
+  });
+}
+
+// rope_tables(rows, rot, scaling, base, factor, orig_len, slow, fast, amplitude, first)
+PyObject* rope_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 10 || libs[0].tables == nullptr) Py_RETURN_NONE;
+  return guarded([&]() -> PyObject* {
+    const int dev = device_now(), rows = int_of(a[0]), first = int_of(a[9]);
+    swa_rope_freq f{int_of(a[1]), int_of(a[2]), double_of(a[3]), double_of(a[4]), double_of(a[5]),
+                    double_of(a[6]), double_of(a[7]), double_of(a[8])};
+    if (rows < 1 || f.rot < 2) throw Refused{};
+    at::Tensor cos = at::empty({rows, f.rot / 2}, on(dev, at::kFloat)), sin = at::empty_like(cos);
+    if (libs[0].tables(&f, first, rows, cos.data_ptr<float>(), sin.data_ptr<float>(), stream_now(dev)) != SWA_OK) throw Refused{};
+    return pair(cos, sin);
+  });
+}
+
+// rope_apply(q, k, cos, sin, pos, interleaved, inverse, q_out, k_out, workspace)
+PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 10) Py_RETURN_NONE;
+  return guarded([&]() -> PyObject* {
+    const bool has_q = a[0] != Py_None, has_k = a[1] != Py_None;
+    const at::Tensor& x = tensor(has_q ? a[0] : a[1]);
+    if (x.dim() != 4) throw Refused{};
+    const int dev = device_now();
+    const auto type = x.scalar_type();
+    const int kind = kind_of(type);
+    const int64_t B = x.size(0), T = x.size(1), d = x.size(3);
+    int64_t Hq = x.size(2), Hkv = Hq;
+    if (has_q) {
+      Hkv = 1;
+      if (has_k) {
+        if (tensor(a[1]).dim() != 4) throw Refused{};
+        Hkv = tensor(a[1]).size(2);
+      }
+    }
+    const void* q = at_(a[0], type, dev, {B, T, Hq, d});
+    const void* k = at_(a[1], type, dev, {B, T, Hkv, d});
+    const int32_t* pos = static_cast<const int32_t*>(at_(a[4], at::kInt, dev, {B, T}));
+    swa_rope r{};
+    if (!rope_of(a[2], a[3], a[5], dev, r)) throw Refused{};
+    void* qo = at_(a[7], type, dev, {B, T, Hq, d});
+    void* ko = at_(a[8], type, dev, {B, T, Hkv, d});
+    const Ws ws = ws_of(a[9], dev);
+    at::Tensor qt, kt;
+    if (has_q && qo == nullptr) {
+      if (a[7] != Py_None) throw Refused{};
+      qt = at::empty_like(tensor(a[0]));
+      qo = qt.data_ptr();
+    } else if (has_q) {
+      qt = tensor(a[7]);
+    }
+    if (has_k && ko == nullptr) {
+      if (a[8] != Py_None) throw Refused{};
+      kt = at::empty_like(tensor(a[1]));
+      ko = kt.data_ptr();
+    } else if (has_k) {
+      kt = tensor(a[8]);
+    }
+    swa_params p{small(B), small(T), small(Hq), small(Hkv), small(d), -1, 1, 0.f, 0.f, 0.f, 0};
+    if (libs[kind].apply(&p, &r, pos, q, k, qo, ko, PyObject_IsTrue(a[6]), ws.at, ws.bytes, stream_now(dev)) != SWA_OK)
+      throw Refused{};
+    return pair(qt, kt);
+  });
+}
+
+// kv4_plan(lens, new_lens, table, free_pages, free_head, page, n_pages, n_tokens, workspace)
+PyObject* kv4_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 9 || libs[0].plan == nullptr) Py_RETURN_NONE;
+  return guarded([&]() -> PyObject* {
+    const int dev = device_now();
+    const at::Tensor &lens = tensor(a[0]), &table = tensor(a[2]), &free = tensor(a[3]);
+    if (lens.dim() != 1 || table.dim() != 2) throw Refused{};
+    const int64_t B = lens.size(0), N = int_of(a[7]);
+    if (N < 0 || B < 1) throw Refused{};
+    const auto* l = static_cast<const int32_t*>(at_(a[0], at::kInt, dev, {B}));
+    const auto* nl = static_cast<const int32_t*>(at_(a[1], at::kInt, dev, {B}));
+    auto* tb = static_cast<int32_t*>(at_(a[2], at::kInt, dev, {B, table.size(1)}));
+    const auto* fr = static_cast<const int32_t*>(at_(a[3], at::kInt, dev, {free.numel()}));
+    const auto* hd = static_cast<const int32_t*>(at_(a[4], at::kInt, dev, {1}));
+    const Ws ws = ws_of(a[8], dev);
+    const auto i32 = on(dev, at::kInt);
+    at::Tensor slot = at::empty({N}, on(dev, at::kLong)), pos = at::empty({N}, i32), row = at::empty({N}, i32),
+               cu = at::empty({B + 1}, i32), lens_out = at::empty({B}, i32), head = at::empty({1}, i32);
+    if (libs[0].plan(int_of(a[6]), int_of(a[5]), small(B), small(table.size(1)), l, nl, tb, fr, small(free.numel()), hd,
+                     static_cast<int>(N), slot.data_ptr<int64_t>(), pos.data_ptr<int32_t>(), row.data_ptr<int32_t>(),
+                     cu.data_ptr<int32_t>(), lens_out.data_ptr<int32_t>(), head.data_ptr<int32_t>(), ws.at, ws.bytes,
+                     stream_now(dev)) != SWA_OK)
+      throw Refused{};
+    PyObject* dict = PyDict_New();
+    const struct { const char* name; const at::Tensor& t; } out[] = {
+        {"slot", slot}, {"pos", pos}, {"row", row}, {"cu", cu}, {"lens", lens_out}, {"free_head", head}};
+    for (const auto& o : out) {
+      PyObject* v = THPVariable_Wrap(o.t);
+      PyDict_SetItemString(dict, o.name, v);
+      Py_DECREF(v);
+    }
+    return dict;
+  });
+}
+
+// kv4_append(cache, k, v, slot, pos, cos, sin, interleaved, gk, eps, ve, tok, ve_gate, ve_scale, workspace)
+PyObject* kv4_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 15) Py_RETURN_NONE;
+  return guarded([&]() -> PyObject* {
+    const int dev = device_now();
+    const CacheDims c = cache_of(a[0], dev);
+    const at::Tensor& k = tensor(a[1]);
+    if (k.dim() != 4) throw Refused{};
+    const auto type = k.scalar_type();
+    const int kind = kind_of(type);
+    const int64_t B = k.size(0), T = k.size(1);
+    const at::DimVector rows{B, T, c.Hkv, c.d};
+    const void *ka = at_(a[1], type, dev, rows), *va = at_(a[2], type, dev, rows);
+    const auto* slot = static_cast<const int64_t*>(at_(a[3], at::kLong, dev, {B, T}));
+    const auto* pos = static_cast<const int32_t*>(at_(a[4], at::kInt, dev, {B, T}));
+    swa_rope r{};
+    const bool rope = rope_of(a[5], a[6], a[7], dev, r);
+    const auto* gk = static_cast<const float*>(at_(a[8], at::kFloat, dev, {c.d}));
+    const void* ve = nullptr;
+    const int32_t* tok = nullptr;
+    const float* gate = nullptr;
+    int vocab = 0;
+    if (a[10] != Py_None) {
+      if (tensor(a[10]).dim() != 2) throw Refused{};
+      vocab = small(tensor(a[10]).size(0));
+      ve = at_(a[10], type, dev, {vocab, static_cast<int64_t>(c.Hkv) * c.d});
+      tok = static_cast<const int32_t*>(at_(a[11], at::kInt, dev, {B, T}));
+      gate = static_cast<const float*>(at_(a[12], at::kFloat, dev, {B, T, c.Hkv}));
+    }
+    const Ws ws = ws_of(a[14], dev);
+    swa_params p{small(B), small(T), c.Hkv, c.Hkv, c.d, -1, 1, 0.f, static_cast<float>(double_of(a[9])),
+                 static_cast<float>(double_of(a[13])), vocab};
+    if (libs[kind].append(&p, nullptr, &c.c, rope ? &r : nullptr, ka, va, gk, ve, tok, gate, pos, slot, ws.at, ws.bytes,
+                          stream_now(dev)) != SWA_OK)
+      throw Refused{};
+    Py_RETURN_TRUE;
+  });
+}
+
+// kv4_read(cache, slot, fp32, workspace)
+PyObject* kv4_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 4) Py_RETURN_NONE;
+  return guarded([&]() -> PyObject* {
+    const int dev = device_now();
+    const CacheDims c = cache_of(a[0], dev);
+    const at::Tensor& s = tensor(a[1]);
+    if (s.dim() != 2) throw Refused{};
+    const int kind = kind_of(PyObject_IsTrue(a[2]) ? at::kFloat : at::kBFloat16);
+    const auto* slot = static_cast<const int64_t*>(at_(a[1], at::kLong, dev, s.sizes()));
+    const Ws ws = ws_of(a[3], dev);
+    at::Tensor k = at::empty({s.size(0), s.size(1), c.Hkv, c.d}, on(dev, kind ? at::kFloat : at::kBFloat16)),
+               v = at::empty_like(k);
+    swa_params p{small(s.size(0)), small(s.size(1)), c.Hkv, c.Hkv, c.d, -1, 1, 0.f, 0.f, 0.f, 0};
+    if (libs[kind].read(&p, &c.c, slot, k.data_ptr(), v.data_ptr(), ws.at, ws.bytes, stream_now(dev)) != SWA_OK) throw Refused{};
+    return pair(k, v);
+  });
+}
+
+// kv4_attention(cache, q, table, lens, cos, sin, interleaved, gq, window, softmax_scale, eps, workspace)
+PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 12) Py_RETURN_NONE;
+  return guarded([&]() -> PyObject* {
+    const int dev = device_now();
+    const CacheDims c = cache_of(a[0], dev);
+    const at::Tensor &q = tensor(a[1]), &table = tensor(a[2]);
+    if (q.dim() != 3 || table.dim() != 2 || a[11] == Py_None) throw Refused{};
+    const auto type = q.scalar_type();
+    const int kind = kind_of(type);
+    const int64_t B = q.size(0), Hq = q.size(1), width = table.size(1);
+    const void* qa = at_(a[1], type, dev, {B, Hq, c.d});
+    const auto* ta = static_cast<const int32_t*>(at_(a[2], at::kInt, dev, {B, width}));
+    const auto* la = static_cast<const int32_t*>(at_(a[3], at::kInt, dev, {B}));
+    swa_rope r{};
+    const bool rope = rope_of(a[4], a[5], a[6], dev, r);
+    const auto* gq = static_cast<const float*>(at_(a[7], at::kFloat, dev, {c.d}));
+    const Ws ws = ws_of(a[11], dev);
+    swa_params p{small(B), 1, small(Hq), c.Hkv, c.d, int_of(a[8]), 1, static_cast<float>(double_of(a[9])),
+                 static_cast<float>(double_of(a[10])), 0.f, 0};
+    at::Tensor o = at::empty_like(q), lse = at::empty({B, Hq}, on(dev, at::kFloat));
+    if (libs[kind].attn(&p, nullptr, &c.c, rope ? &r : nullptr, qa, gq, ta, small(width), la, o.data_ptr(),
+                        lse.data_ptr<float>(), ws.at, ws.bytes, stream_now(dev)) != SWA_OK)
+      throw Refused{};
+    return pair(o, lse);
+  });
+}
+
+#define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {FAST(bind),       FAST(rope_tables), FAST(rope_apply),    FAST(kv4_plan),
+                         FAST(kv4_append), FAST(kv4_read),    FAST(kv4_attention), {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__fast() { return PyModule_Create(&module); }

@@ -855,3 +855,94 @@ def test_several_query_tokens_of_a_request_are_rows():
         ro, rl = dec.attend(f64(q)[i], rows[0][0][:m], rows[0][1][:m])
         assert np.abs(f64(lse)[i] - rl).max() <= 1e-4
         assert np.all(np.abs(f64(o)[i] - ro) <= 2.0 ** -8 * np.abs(ro) + 1.7e-4 * np.abs(rows[0][1]).max())
+
+
+# ---------------------------------------------------------------------------
+# The short way of the binding
+# ---------------------------------------------------------------------------
+
+def test_short_way_is_there_and_gives_the_same_bits(monkeypatch):
+    assert swa._fast is not None, "_fast.so is not built: the decode calls run the long way"
+    swa.load("bf16"), swa.load("fp32")      # loading a library ties it to the module
+    B, Hq, Hkv, d, page = 3, 4, 2, 64, 16
+    lens = torch.tensor([20, 0, 33], dtype=torch.int32, device=dev())
+    new = torch.tensor([2, 40, 1], dtype=torch.int32, device=dev())
+    table0 = torch.arange(24, dtype=torch.int32, device=dev()).view(3, 8)
+    free = torch.arange(40, 60, dtype=torch.int32, device=dev())
+    head = torch.zeros(1, dtype=torch.int32, device=dev())
+    gq, gk = (1 + 0.1 * randn(i, d).to(dev()) for i in (1, 2))
+    tab, gate = randn(3, 11, Hkv * d).to(dev()), torch.rand(43, 1, Hkv, device=dev())
+    tok = torch.randint(0, 11, (43, 1), dtype=torch.int32, device=dev())
+    taken = []
+    kinds = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+    class Watch:      # notes which calls the short way took
+        def __getattr__(self, name):
+            f = getattr(fast, name)
+
+            def call(*a):
+                r = f(*a)
+                taken.append((name, r is not None))
+                return r
+            return call
+
+    fast = swa._fast
+
+    def everything(dt):
+        rope = swa.rope_tables(64, 32, base=5000.0, scaling="by_parts", factor=3.0, orig_len=40)
+        table = table0.clone()
+        plan = swa.kv4_plan(lens, new, table, free, head, page=page, n_pages=60, n_tokens=43)
+        one = swa.kv4_plan(lens, None, table, free, head, page=page, n_pages=60, n_tokens=5)
+        cache = torch.zeros(60, Hkv, 1, 18 * d, dtype=torch.uint8, device=dev())
+        ws = swa.new_kv4_workspace(cache, B, Hq, max_pages=8, kind="fp32" if dt is torch.float32 else "bf16")
+        k, v, q = (randn(i, *s, dtype=dt).to(dev()) for i, s in ((4, (43, 1, Hkv, d)), (5, (43, 1, Hkv, d)), (6, (B, Hq, d))))
+        slot, pos = plan["slot"].view(43, 1), plan["pos"].view(43, 1)
+        swa.kv4_append(cache, k, v, slot, pos=pos, rope=rope, interleaved=True, gk=gk, ve=tab.to(dt), tok=tok, ve_gate=gate,
+                       ve_scale=0.25, eps=1e-3, workspace=ws)
+        swa.kv4_append(cache, k[:1], v[:1], slot[:1])
+        kr, vr = swa.kv4_read(cache, slot, dtype=dt)
+        att = swa.kv4_attention(cache, q, table, plan["lens"], rope=rope, interleaved=True, gq=gq, window=30,
+                                softmax_scale=0.1, eps=1e-3, workspace=ws)
+        bare = swa.kv4_attention(cache, q, table, plan["lens"], workspace=ws)
+        x = randn(7, B, 9, Hq, d, dtype=dt).to(dev())
+        turned = swa.rope_apply(x, x[:, :, :Hkv].contiguous(), rope)
+        back = swa.rope_apply(x, None, rope, pos=torch.full((B, 9), 5, dtype=torch.int32, device=dev()), interleaved=True, inverse=True)
+        swa.rope_apply(None, x, rope, out=(None, x))
+        return [*rope, *plan.values(), *one.values(), table, cache, kr, vr, *att, *bare, *turned, back[0], x]
+
+    for dt in kinds.values():
+        monkeypatch.setattr(swa, "_fast", None)
+        want = everything(dt)
+        monkeypatch.setattr(swa, "_fast", Watch())
+        taken.clear()
+        got = everything(dt)
+        assert len(taken) == 11 and all(ok for _, ok in taken), taken
+        for a, b in zip(got, want):
+            assert a.dtype == b.dtype and a.shape == b.shape and torch.equal(a, b)
+
+
+def test_short_way_leaves_the_unusual_to_the_long_one():
+    c = torch.zeros(4, 2, 1, 18 * 64, dtype=torch.uint8, device=dev())
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16, device=dev())
+    table, lens = torch.zeros(1, 4, dtype=torch.int32, device=dev()), torch.ones(1, dtype=torch.int32, device=dev())
+    ws = swa.new_kv4_workspace(c, 1, 4, max_pages=4)
+    slot, k = torch.zeros(1, 3, dtype=torch.int64, device=dev()), torch.zeros(1, 3, 2, 64, dtype=torch.bfloat16, device=dev())
+    bad = [lambda: swa.kv4_attention(c, q.half(), table, lens, workspace=ws), lambda: swa.kv4_attention(c, q, table.long(), lens, workspace=ws),
+           lambda: swa.kv4_attention(c, q, table, lens, workspace=ws.cpu()), lambda: swa.kv4_attention(c.cpu(), q, table, lens, workspace=ws),
+           lambda: swa.kv4_attention(c, q[:, :3].contiguous(), table, lens, workspace=ws),
+           lambda: swa.kv4_attention(c, q, table, lens, workspace=ws[:256]), lambda: swa.kv4_attention(c, q, table, lens, window=-3, workspace=ws),
+           lambda: swa.kv4_append(c, k, k, slot.int()), lambda: swa.kv4_append(c, k, k[:, :, :1], slot), lambda: swa.kv4_append(c, k, k, None),
+           lambda: swa.kv4_read(c, slot[0]), lambda: swa.kv4_read(c, slot.cpu()), lambda: swa.kv4_read(c, slot, dtype=torch.float16),
+           lambda: swa.kv4_plan(lens, lens, table, lens, lens, page=24, n_pages=4, n_tokens=1),
+           lambda: swa.kv4_plan(lens, lens, table, lens, None, page=16, n_pages=4, n_tokens=1),
+           lambda: swa.rope_tables(8, 24), lambda: swa.rope_tables(-1, 16), lambda: swa.rope_apply(q, None, swa.rope_tables(4, 64)),
+           lambda: swa.rope_apply(k, None, swa.rope_tables(2, 64))]
+    for i, f in enumerate(bad):
+        with pytest.raises((ValueError, TypeError, swa.SwaError)):
+            f()
+            print("call", i, "was taken")
+    # a stream of its own, a raw handle, a row of tables as one tensor
+    o = swa.kv4_attention(c, q, table, lens, workspace=ws, stream=torch.cuda.current_stream())
+    p = swa.kv4_attention(c, q, table, lens, rope=torch.stack(swa.rope_tables(4, 64)), workspace=ws)
+    assert o[0].shape == p[0].shape
+    assert swa.rope_tables(0, 16)[0].shape == (0, 8)
