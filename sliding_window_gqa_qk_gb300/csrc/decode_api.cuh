@@ -218,7 +218,10 @@ swa_status swa_kv4_plan(int n_pages, int page, int B, int max_pages, const int32
   if (smem > 48 * 1024 - 1024 &&     // what a launch gets unasked, less the kernel's own arrays
       cudaFuncSetAttribute(kv4::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
     return SWA_ERR_CUDA;
-  const int grid = flat_grid(n_tokens, kv4::kPlanThreads * kv4::kPlanTokens, num_sms());
+  // as many blocks as the tokens want, or the requests: two to a warp, for their new pages
+  const int by_tokens = flat_grid(n_tokens, kv4::kPlanThreads * kv4::kPlanTokens, num_sms());
+  const int by_requests = flat_grid(B, kv4::kPlanThreads / 16, num_sms());
+  const int grid = by_tokens > by_requests ? by_tokens : by_requests;
   kv4::plan_kernel<<<grid, kv4::kPlanThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
   return launched();
 }
