@@ -526,8 +526,9 @@ __global__ void __launch_bounds__(kRowWarps * 32) read_kernel(const __grid_const
 // Every block does the whole scan itself (a few thousand requests at most,
 // two integers each, from L2) and keeps it in shared memory, so one launch
 // serves every token and no block waits on another. Latency bounds it: 64
-// requests of one token 6.4 us, 1000 requests of 104,000 tokens 7.5 us (their
-// bytes would take 0.3).
+// requests of one token 5.5 us, 1000 requests of 104,000 tokens 7.7 us (their
+// bytes would take 0.3), 633 requests of one token 7.7 us on 20 blocks and 21.4
+// on the one that their tokens fill.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxB = 8192;      // 12 bytes of shared memory per request
