@@ -500,7 +500,8 @@ size_t swa_kv4_cache_size(const swa_params* p, int n_pages, int page);
  * (a negative count takes no tokens): its tokens get slot -1, its length and
  * table row stay, and it takes no page (pos is 0 where it would pass the
  * table row, or the length is negative). A page id outside [0, n_pages) gives
- * slot -1 and is reported. Limits: B <= 8192, max_pages * page < 2^31.
+ * slot -1 and is reported. Limits: B <= 8192, max_pages * page < 2^31 - 64 (in
+ * the attention too).
  */
 swa_status swa_kv4_plan(int n_pages, int page, int B, int max_pages, const int32_t* lens,
                         const int32_t* new_lens, int32_t* table, const int32_t* free_pages, int n_free,

@@ -722,7 +722,6 @@ def new_kv4_workspace(cache, B: int, Hq: int, *, max_pages: int, window: int = -
     if n == 0:
         raise SwaError(SWA_ERR_INVALID_ARG, "workspace size")
 
-
     def call():
         ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
         _check(swa_kv4_workspace_init(ws, n, None, kind), "workspace init")

@@ -38,6 +38,11 @@ swa_status check_pages(int n_pages, int page) {
   return SWA_OK;
 }
 
+// A table row's tokens: positions a step or two past them still fit 32 bits.
+bool width_ok(int max_pages, int page) {
+  return max_pages >= 1 && static_cast<long long>(max_pages) * page <= INT32_MAX - 64;
+}
+
 swa_status check_cache(const swa_params* p, const swa_kv4_cache* c, kv4::Cache& out) {
   if (c == nullptr || c->data == nullptr || !aligned(c->data, 16)) return SWA_ERR_INVALID_ARG;
   const swa_status s = check_pages(c->n_pages, c->page);
@@ -191,8 +196,7 @@ swa_status swa_kv4_plan(int n_pages, int page, int B, int max_pages, const int32
                         void* workspace, size_t ws_bytes, void* stream) {
   swa_status s = check_pages(n_pages, page);
   if (s != SWA_OK) return s;
-  if (B < 0 || max_pages < 1 || n_free < 0 || n_tokens < 0) return SWA_ERR_INVALID_ARG;
-  if (static_cast<long long>(max_pages) * page > INT32_MAX || n_tokens > INT32_MAX - kv4::kPlanTokens)
+  if (B < 0 || !width_ok(max_pages, page) || n_free < 0 || n_tokens < 0 || n_tokens > INT32_MAX - kv4::kPlanTokens)
     return SWA_ERR_INVALID_ARG;
   if (B > kv4::kPlanMaxB) return SWA_ERR_UNSUPPORTED;
   if (free_head == nullptr || head_out == nullptr || cu == nullptr || (n_free > 0 && free_pages == nullptr))
@@ -237,7 +241,8 @@ swa_status swa_kv4_append(const swa_params* p, const swa_extras* ex, const swa_k
   bool rope = false;
   if ((s = check_rope(r, p->d, rope)) != SWA_OK) return s;
   if (rope && pos == nullptr && r->rows < p->T) return SWA_ERR_INVALID_ARG;
-  if (!aligned(pos, 4) || !aligned(slot, 8) || !aligned(gk, 4)) return SWA_ERR_INVALID_ARG;
+  if (!aligned(pos, 4) || !aligned(slot, 8) || !aligned(gk, 4) || !aligned(tok, 4) || !aligned(ve_gate, 4))
+    return SWA_ERR_INVALID_ARG;
   if (ex != nullptr && (ex->rope_cos != nullptr || ex->rope_sin != nullptr)) return SWA_ERR_INVALID_ARG;
   Call call;
   call.p = *p;
@@ -313,9 +318,7 @@ swa_status swa_kv4_read(const swa_params* p, const swa_kv4_cache* c, const int64
 }
 
 size_t swa_kv4_workspace_size(const swa_params* p, int page, int max_pages) {
-  if (check_params(p) != SWA_OK || check_pages(1, page) != SWA_OK || max_pages < 1 ||
-      static_cast<long long>(max_pages) * page > INT32_MAX)
-    return 0;
+  if (check_params(p) != SWA_OK || check_pages(1, page) != SWA_OK || !width_ok(max_pages, page)) return 0;
   return kv4_ws_bytes(kv4::attn_split(p->B, p->Hq, p->Hkv, p->d, page, max_pages, p->window), p->d);
 }
 
@@ -337,7 +340,7 @@ swa_status swa_kv4_attn(const swa_params* p, const swa_extras* ex, const swa_kv4
   bool rope = false;
   if ((s = check_rope(r, p->d, rope)) != SWA_OK) return s;
   if (ex != nullptr && (ex->rope_cos != nullptr || ex->rope_sin != nullptr)) return SWA_ERR_INVALID_ARG;
-  if (max_pages < 1 || static_cast<long long>(max_pages) * c->page > INT32_MAX) return SWA_ERR_INVALID_ARG;
+  if (!width_ok(max_pages, c->page)) return SWA_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, 256)) return SWA_ERR_INVALID_ARG;
   const kv4::AttnSplit sp = kv4::attn_split(p->B, p->Hq, p->Hkv, p->d, c->page, max_pages, p->window);
   if (ws_bytes < kv4_ws_bytes(sp, p->d)) return SWA_ERR_WORKSPACE;

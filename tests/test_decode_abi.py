@@ -131,7 +131,7 @@ def plan(**kw):
 @needs_no_gpu
 def test_plan_refuses():
     for kw in (dict(page=8), dict(page=0), dict(n_pages=0), dict(B=-1), dict(max_pages=0), dict(n_free=-1), dict(n_tokens=-1),
-               dict(max_pages=1 << 27), dict(n_tokens=2 ** 31 - 1), dict(lens=None), dict(table=None), dict(free=None),
+               dict(max_pages=1 << 27), dict(max_pages=(1 << 27) - 4), dict(n_tokens=2 ** 31 - 1), dict(lens=None), dict(table=None), dict(free=None),
                dict(head=None), dict(slot=None), dict(pos=None), dict(row=None), dict(cu=None), dict(lens_out=None),
                dict(head_out=None), dict(slot=A + 8), dict(pos=A + 4), dict(row=A + 4), dict(lens=A + 2),
                dict(lens_out=A), dict(lens=3 * A, lens_out=A), dict(head_out=A), dict(ws=A + 8, ws_bytes=256)):
@@ -172,7 +172,7 @@ def test_cache_calls_refuse(kind):
     assert append(p, cache(page=1 << 21), kind=kind) == UNS
     assert append(params(d=96), cache(), kind=kind) == UNS and attn(params(d=96, T=1), cache(), kind=kind) == UNS
     for kw in (dict(k=None), dict(v=None), dict(slot=None), dict(k=A + 8), dict(v=A + 4), dict(slot=A + 4), dict(pos=A + 1),
-               dict(gk=A + 2), dict(ws=A + 1, ws_bytes=256)):
+               dict(gk=A + 2), dict(tok=A + 2), dict(gate=A + 1), dict(ws=A + 1, ws_bytes=256)):
         assert append(p, cache(), kind=kind, **kw) == BAD, kw
     assert append(p, cache(), kind=kind, ws=A, ws_bytes=128) == WS
     assert append(p, cache(), rope(rows=2), kind=kind) == BAD
@@ -195,7 +195,7 @@ def test_cache_calls_refuse(kind):
     for kw in (dict(slot=None), dict(k=None), dict(v=A + 8), dict(slot=A + 4), dict(ws=A + 2, ws_bytes=256)):
         assert read(p, cache(), kind, **kw) == BAD, kw
     for kw in (dict(q=None), dict(table=None), dict(lens=None), dict(o=None), dict(lse=None), dict(q=A + 8), dict(lens=A + 2),
-               dict(gq=A + 8), dict(lse=A + 2), dict(table=A + 1), dict(max_pages=0), dict(max_pages=1 << 27), dict(ws=None), dict(ws=A + 16)):
+               dict(gq=A + 8), dict(lse=A + 2), dict(table=A + 1), dict(max_pages=0), dict(max_pages=1 << 27), dict(max_pages=(1 << 26) - 2), dict(ws=None), dict(ws=A + 16)):
         assert attn(one, cache(), kind=kind, **kw) == BAD, kw
     assert attn(one, cache(), kind=kind, ws_bytes=swa.swa_kv4_workspace_size(one, 32, 16, kind) - 1) == WS
     assert attn(params(T=2), cache(), kind=kind) == BAD and attn(params(T=1, causal=False), cache(), kind=kind) == BAD
