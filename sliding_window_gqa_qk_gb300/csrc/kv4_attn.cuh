@@ -99,10 +99,11 @@ struct AttnSmem {
   static constexpr int ring = kAttnWarps * kStages * 2 * AttnShape<D>::TB;
   static constexpr int join = kAttnWarps * NT * kColQ * (D + 2) * 4;
   static constexpr int bars = (ring > join ? ring : join + 127) / 128 * 128;
-  static constexpr int qs = bars + kAttnWarps * kStages * 8;
+  static constexpr int qs = bars + (kAttnWarps * kStages * 8 + 15) / 16 * 16;    // read 16 bytes at a time
   static constexpr int qf = qs + NT * kColQ * 2 * D * 2;        // fp16 hi, lo rows
   static constexpr int flags = qf + NT * kColQ * 4 * 4;         // factor, sums per group
   static constexpr int bytes = flags + 16;
+  static_assert(bars % 128 == 0 && qs % 16 == 0 && qf % 16 == 0 && flags % 16 == 0, "");
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
