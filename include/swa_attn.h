@@ -552,13 +552,12 @@ swa_status swa_kv4_read(const swa_params* p, const swa_kv4_cache* c, const int64
  *
  * The workspace (256-byte aligned, passed to swa_kv4_workspace_init once
  * before its first use) holds the status word, counters, and the partial
- * results of long requests that several CTAs share. Calls of any shapes and
- * captured graphs of them may share it as long as they run one after the
- * other (one stream, or events) and it has the bytes of each
- * (swa_kv4_workspace_size; a smaller batch can need more: fewer requests are
- * split into more parts); calls that can overlap need one each. The partial
- * results of a request are joined in a fixed order: a call gives the same bits
- * every time.
+ * results of long requests that several CTAs share (10 MB). Its size,
+ * swa_kv4_workspace_size, is the same for every valid call: calls of any
+ * shapes, layers and windows, and captured graphs of them, may share one as
+ * long as they run one after the other (one stream, or events); calls that can
+ * overlap need one each. The partial results of a request are joined in a
+ * fixed order: a call gives the same bits every time.
  */
 size_t swa_kv4_workspace_size(const swa_params* p, int page, int max_pages);
 swa_status swa_kv4_workspace_init(void* workspace, size_t ws_bytes, void* stream);

@@ -715,8 +715,9 @@ def new_kv4_cache(n_pages: int, page: int, Hkv: int, d: int, device):
 
 
 def new_kv4_workspace(cache, B: int, Hq: int, *, max_pages: int, window: int = -1, kind: str = "bf16", stream=None):
-    """The workspace of kv4_attention for B requests of max_pages pages and
-    this window, initialised. kind: "bf16" or "fp32", as q."""
+    """A workspace of kv4_attention, initialised: 10 MB, the same for every
+    batch, window and head count (the arguments are only checked), for calls
+    that run one after the other. kind: "bf16" or "fp32", as q."""
     _, Hkv, page, d = _cache_dims(cache)
     n = swa_kv4_workspace_size(make_params(B, 1, Hq, Hkv, d, window), page, max_pages, kind)
     if n == 0:

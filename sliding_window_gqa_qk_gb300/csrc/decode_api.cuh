@@ -66,15 +66,21 @@ constexpr long long kFewThreads = 512;   // per SM
 constexpr int kAppendBlocksPerSm = 64;
 
 // Workspace of the decode attention: header, counters of finished chunks,
-// partial results. Calls of any size may follow one another on a workspace,
-// so the counters, which each call leaves at zero, have a place of their own
-// at a fixed size (a call has at most B * Hq <= 65535 of them), where no
-// call's partial results ever lie.
+// partial results; one size for every call. Calls of any shape may follow one
+// another on a workspace, so the counters, which each call leaves at zero,
+// have a place of their own (a call has at most B * Hq <= 65535 of them),
+// where no call's partial results ever lie.
 constexpr size_t kKv4Count = 256, kKv4Part = kKv4Count + 65536 * sizeof(unsigned);
-size_t kv4_ws_bytes(const kv4::AttnSplit& s, int d) {
-  if (s.splits == 1) return kKv4Part;
-  return align256(kKv4Part + static_cast<size_t>(s.items) * s.splits * s.heads * (d + 2) * sizeof(float));
+constexpr size_t kv4_ws_bytes() {
+  long long most = 0;
+  for (int d = 64; d <= 128; d += 64)
+    for (int operands = 1; operands <= 2; ++operands) {
+      const long long n = kv4::attn_part_floats(d, operands);
+      most = n > most ? n : most;
+    }
+  return (kKv4Part + static_cast<size_t>(most) * sizeof(float) + 255) / 256 * 256;
 }
+constexpr size_t kKv4Bytes = kv4_ws_bytes();
 
 template <int D, int NT, bool kPolled>
 swa_status launch_attn(const kv4::AttnArgs& a, int heads_kv, cudaStream_t st) {
@@ -319,12 +325,12 @@ swa_status swa_kv4_read(const swa_params* p, const swa_kv4_cache* c, const int64
 
 size_t swa_kv4_workspace_size(const swa_params* p, int page, int max_pages) {
   if (check_params(p) != SWA_OK || check_pages(1, page) != SWA_OK || !width_ok(max_pages, page)) return 0;
-  return kv4_ws_bytes(kv4::attn_split(p->B, p->Hq, p->Hkv, p->d, page, max_pages, p->window), p->d);
+  return kKv4Bytes;
 }
 
 swa_status swa_kv4_workspace_init(void* workspace, size_t ws_bytes, void* stream) {
   if (workspace == nullptr || !aligned(workspace, 256)) return SWA_ERR_INVALID_ARG;
-  if (ws_bytes < kKv4Part) return SWA_ERR_WORKSPACE;
+  if (ws_bytes < kKv4Bytes) return SWA_ERR_WORKSPACE;
   if (cudaMemsetAsync(workspace, 0, kKv4Part, static_cast<cudaStream_t>(stream)) != cudaSuccess) return SWA_ERR_CUDA;
   return SWA_OK;
 }
@@ -343,7 +349,7 @@ swa_status swa_kv4_attn(const swa_params* p, const swa_extras* ex, const swa_kv4
   if (!width_ok(max_pages, c->page)) return SWA_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, 256)) return SWA_ERR_INVALID_ARG;
   const kv4::AttnSplit sp = kv4::attn_split(p->B, p->Hq, p->Hkv, p->d, c->page, max_pages, p->window);
-  if (ws_bytes < kv4_ws_bytes(sp, p->d)) return SWA_ERR_WORKSPACE;
+  if (ws_bytes < kKv4Bytes) return SWA_ERR_WORKSPACE;
   if (p->B == 0) return SWA_OK;
   if (!tensor_ok(q) || !tensor_ok(o) || lse == nullptr || table == nullptr || lens == nullptr) return SWA_ERR_INVALID_ARG;
   if (!aligned(lse, 4) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(gq, 16)) return SWA_ERR_INVALID_ARG;

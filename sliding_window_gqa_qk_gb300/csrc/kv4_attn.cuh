@@ -646,6 +646,13 @@ __global__ void __launch_bounds__(kAttnWarps * 32, attn_ctas_per_sm(D, NT)) attn
 // 214 us; 16 ragged requests of at most 313 tiles, 6 kv heads: chunks of 32 and
 // 56 tiles 14.9 and 18.4 us; one request of 10 tiles 3.9 us in one CTA, 5.4 us
 // in two.
+// Partial results are kept for at most kPartRounds rounds of CTAs, so that a
+// workspace has one size whatever the batch, the lengths and the window.
+constexpr long long kPartRounds = 8;
+constexpr long long attn_slots(int d, int operands) { return 152LL * attn_ctas_per_sm(d, operands); }   // of a GB300
+constexpr long long attn_part_floats(int d, int operands) {
+  return kPartRounds * attn_slots(d, operands) * operands * kColQ * (d + 2);
+}
 struct AttnSplit {
   int heads, groups;     // query heads of a CTA, CTAs per kv head
   int chunk, splits;
@@ -662,10 +669,11 @@ inline AttnSplit attn_split(int B, int Hq, int Hkv, int d, int page, int max_pag
   long long keys = cap;
   if (window >= 0 && window + 1LL + kTile < cap) keys = window + 1LL + kTile;    // the window may begin inside a tile
   const long long tiles = (keys + kTile - 1) / kTile;
-  const long long slots = 152LL * attn_ctas_per_sm(d, s.heads / kColQ);          // of a GB300
+  const long long slots = attn_slots(d, s.heads / kColQ);
   long long best = 0, chunk = 0;
   for (long long n = 1; n <= kMaxSplits; ++n) {
     const long long c = ((tiles + n - 1) / n + kStep - 1) / kStep * kStep, real = (tiles + c - 1) / c;
+    if (real > 1 && s.items * real > kPartRounds * slots) break;
     const long long own = (c < tiles ? c : tiles) + kSetup, half = s.items * real / 2;
     const long long t = (half > slots ? half * own / slots : own) + (s.items * real + slots - 1) / slots * own +
                         (real > 1 ? kJoin + real / 2 : 0);
