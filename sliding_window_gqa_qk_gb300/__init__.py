@@ -15,6 +15,7 @@ binding picks the one matching the dtype of ``q``.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 from typing import Optional
 
@@ -22,10 +23,17 @@ import torch
 
 from . import build as _build
 
-try:  # the short way into the decode calls; everything works without it
-    from . import _fast
-except ImportError:
-    _fast = None
+
+class _Unloaded:
+    """Stands for the short way into the decode calls (csrc/py_fast.cpp) until
+    load() brings it in with the library it leads to: leaves every call to the
+    long way, and keeps the import of the package free of compiled code."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+_fast = _Unloaded()      # None once load() finds that it is not built: everything works without it
 
 __all__ = [
     "swa_params", "SwaError", "load",
@@ -113,6 +121,15 @@ _LIBS: dict = {}
 _vp = ctypes.c_void_p
 
 
+def _load_fast() -> None:
+    global _fast
+    if isinstance(_fast, _Unloaded):
+        try:
+            _fast = importlib.import_module(__name__ + "._fast")
+        except ImportError:
+            _fast = None
+
+
 def load(kind: str = "bf16") -> ctypes.CDLL:
     """The ctypes handle of the bf16 or fp32 library (loaded once)."""
     if kind in _LIBS:
@@ -174,6 +191,7 @@ def load(kind: str = "bf16") -> ctypes.CDLL:
     lib.swa_build_info.argtypes = []
     lib.swa_build_info.restype = ctypes.c_char_p
     _LIBS[kind] = lib
+    _load_fast()
     if _fast is not None:
         _fast.bind(0 if kind == "bf16" else 1, *(
             ctypes.cast(getattr(lib, f), _vp).value for f in (
