@@ -15,7 +15,7 @@ binding picks the one matching the dtype of ``q``.
 from __future__ import annotations
 
 import ctypes
-import importlib
+import importlib.util
 import os
 from typing import Optional
 
@@ -124,8 +124,13 @@ _vp = ctypes.c_void_p
 def _load_fast() -> None:
     global _fast
     if isinstance(_fast, _Unloaded):
+        path = _build.fast_path()
+        spec = importlib.util.spec_from_file_location(__name__ + "._fast", path)
         try:
-            _fast = importlib.import_module(__name__ + "._fast")
+            if not os.path.exists(path):
+                raise ImportError(path)
+            _fast = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(_fast)
         except ImportError:
             _fast = None
 

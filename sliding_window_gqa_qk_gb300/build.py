@@ -6,15 +6,19 @@
 Both come from csrc/swa_attn.cu, compiled for sm_103a only. And, with the host
 compiler against the installed torch:
 
-  _fast.so            the binding's short way into the decode calls
+  _fast.*.so          the binding's short way into the decode calls
                       (csrc/py_fast.cpp); the binding works without it, only
-                      slower, so a failure to build it is a warning
+                      slower, so a failure to build it is a warning. It reads
+                      Python's and torch's objects by their headers, so its
+                      name holds the versions of both: under another torch or
+                      Python it is not there, and is built again.
 """
 
 from __future__ import annotations
 
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sysconfig
@@ -63,11 +67,15 @@ def _stale(out: str) -> bool:
     return any(os.path.getmtime(s) > t for s in _sources())
 
 
-FAST = os.path.join(PKG, "_fast.so")
+def fast_path() -> str:
+    """The short way's module as built for this Python and this torch."""
+    import torch
+    tag = re.sub(r"[^A-Za-z0-9]+", "_", torch.__version__)
+    return os.path.join(PKG, f"_fast.{sysconfig.get_config_var('SOABI')}.torch_{tag}.so")
 
 
 def _fast_cmd(out: str, nvcc: str):
-    """The host compiler's command for _fast.so."""
+    """The host compiler's command for the short way."""
     import torch
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
@@ -94,19 +102,21 @@ def build(force: bool = False, verbose: bool = False) -> None:
             print(" ".join(cmd))
         procs.append((out, tmp, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                  stderr=subprocess.STDOUT, text=True)))
-    if force or _stale(FAST):
-        try:
-            cmd = _fast_cmd(FAST + ".tmp", nvcc)
+    fast = None
+    try:
+        fast = fast_path()
+        if force or _stale(fast):
+            cmd = _fast_cmd(fast + ".tmp", nvcc)
             if verbose:
                 print(" ".join(cmd))
-            procs.append((FAST, FAST + ".tmp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
-        except (OSError, ImportError, AttributeError) as e:
-            warnings.warn(f"_fast.so is not built: {e}")
+            procs.append((fast, fast + ".tmp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    except (OSError, ImportError, AttributeError) as e:
+        warnings.warn(f"the short way (_fast) is not built: {e}")
     errors = []
     for out, tmp, p in procs:
         log, _ = p.communicate()
-        if p.returncode != 0 and out == FAST:
-            warnings.warn("_fast.so is not built:\n" + log[-2000:])
+        if p.returncode != 0 and out == fast:
+            warnings.warn("the short way (_fast) is not built:\n" + log[-2000:])
         elif p.returncode != 0:
             errors.append(f"{os.path.basename(out)}:\n{log}")
         else:

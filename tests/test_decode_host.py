@@ -28,3 +28,18 @@ def test_an_import_maps_no_library_of_the_package():
     before, after = run(code).splitlines()
     assert before == "[]"
     assert "libswaattn.so" in after and "_fast" in after and after.endswith("True")
+
+
+def test_the_short_way_is_that_of_this_torch_and_python(monkeypatch):
+    here = swa_build.fast_path()
+    assert os.path.exists(here)
+    torch_version = __import__("torch").__version__
+    monkeypatch.setattr("torch.__version__", torch_version + ".other")
+    assert swa_build.fast_path() != here and not os.path.exists(swa_build.fast_path())
+    monkeypatch.setattr("torch.__version__", torch_version)
+    monkeypatch.setattr(swa_build.sysconfig, "get_config_var", lambda name: "cpython-399-other")
+    assert swa_build.fast_path() != here and not os.path.exists(swa_build.fast_path())
+    # one built for another torch, or without a name for any, is left alone
+    code = ("import torch\ntorch.__version__ += '.other'\nimport sliding_window_gqa_qk_gb300 as swa\nswa.load('bf16')\n"
+            "print(swa._fast)\nprint([x for x in open('/proc/self/maps') if '_fast' in x and 'gb300' in x])")
+    assert run(code).split() == ["None", "[]"]
