@@ -198,6 +198,7 @@ def load(kind: str = "bf16") -> ctypes.CDLL:
     _LIBS[kind] = lib
     _load_fast()
     if _fast is not None:
+        _fast.raises(SwaError)
         _fast.bind(0 if kind == "bf16" else 1, *(
             ctypes.cast(getattr(lib, f), _vp).value for f in (
                 "swa_rope_tables", "swa_rope_apply", "swa_kv4_plan", "swa_kv4_append", "swa_kv4_read", "swa_kv4_attn")))
@@ -568,8 +569,9 @@ def attention_backward(q, k, v, gq, gk, o, lse, dO, *, window: int = -1, causal:
 # devices before they pass addresses on (the C ABI sees addresses only), run
 # on the device of their tensors, and allocate their outputs on the stream
 # they run on. A decode step is a few microseconds of GPU work, so the ordinary
-# case goes through csrc/py_fast.cpp, which returns None for every other: the
-# Python below is the whole of each call, the other only its short way.
+# case goes through csrc/py_fast.cpp, which returns None for every other that
+# it has not launched: the Python below is the whole of each call, the other
+# only its short way.
 # ---------------------------------------------------------------------------
 
 SWA_ROPE_PLAIN, SWA_ROPE_LINEAR, SWA_ROPE_NTK, SWA_ROPE_BY_PARTS = range(4)

@@ -4,9 +4,11 @@
 // argument conversions of the binding's Python functions cost 16 to 30 us
 // around it. These functions do the same for the ordinary case (tensors of
 // the right types and shapes on the current device, the current stream) in a
-// few. In every other case, and when the library refuses the call, they
-// return None and the Python function does it all itself: what is wrong is
-// found and told there, and nothing depends on this module but time.
+// few. In every other case, and when the library refuses the call before it
+// launches anything, they return None and the Python function does it all
+// itself: what is wrong is found and told there, and nothing depends on this
+// module but time. A call that may have launched is never made again: its
+// error is raised here.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -30,7 +32,23 @@ struct Lib {
 };
 Lib libs[2];   // bf16, fp32; filled by bind()
 
-struct Refused {};   // not the ordinary case
+struct Refused {};   // not the ordinary case; nothing is launched
+
+PyObject* error_type = nullptr;   // SwaError(status, what); set by raises()
+
+// The library call of a function below: its status, and whether it may have
+// launched.
+struct Call {
+  bool launched = false;
+  swa_status status = SWA_OK;
+  // These three are decided before a launch. Any other status may come after
+  // it: SWA_ERR_CUDA also tells of errors that older calls left behind.
+  void operator()(swa_status s) {
+    if (s == SWA_ERR_INVALID_ARG || s == SWA_ERR_UNSUPPORTED || s == SWA_ERR_WORKSPACE) throw Refused{};
+    launched = true;
+    status = s;
+  }
+};
 
 int device_now() { return static_cast<int>(c10::cuda::current_device()); }
 void* stream_now(int dev) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
@@ -115,21 +133,37 @@ PyObject* pair(const at::Tensor& a, const at::Tensor& b) {
   return t;
 }
 
-// Runs f; anything out of the ordinary is None.
+// Runs f, whose library call is `what`; anything out of the ordinary before
+// the launch is None.
 template <typename F>
-PyObject* guarded(F f) {
+PyObject* guarded(const char* what, F f) {
+  Call call;
+  PyObject* r = nullptr;
   try {
-    PyObject* r = f();
-    if (r != nullptr) return r;
+    r = f(call);
   } catch (...) {
+    r = nullptr;
   }
-  PyErr_Clear();
-  Py_RETURN_NONE;
+  if (!call.launched) {
+    if (r != nullptr) return r;
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
+  if (call.status != SWA_OK) {
+    Py_XDECREF(r);
+    PyErr_Clear();
+    PyObject* e = error_type != nullptr ? PyObject_CallFunction(error_type, "is", static_cast<int>(call.status), what) : nullptr;
+    if (e != nullptr) PyErr_SetObject(error_type, e);
+    Py_XDECREF(e);
+    r = nullptr;
+  }
+  if (r == nullptr && !PyErr_Occurred()) PyErr_Format(PyExc_RuntimeError, "%s: failed after its launch", what);
+  return r;
 }
 
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 7) Py_RETURN_NONE;
-  return guarded([&]() -> PyObject* {
+  return guarded("bind", [&](Call&) -> PyObject* {
     void* f[6];
     for (int i = 0; i < 6; ++i) f[i] = PyLong_AsVoidPtr(a[i + 1]);
     if (PyErr_Occurred()) throw Refused{};
@@ -140,16 +174,24 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+PyObject* raises(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 1 || !PyType_Check(a[0])) Py_RETURN_NONE;
+  Py_INCREF(a[0]);
+  Py_XDECREF(error_type);
+  error_type = a[0];
+  Py_RETURN_TRUE;
+}
+
 // rope_tables(rows, rot, scaling, base, factor, orig_len, slow, fast, amplitude, first)
 PyObject* rope_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 10 || libs[0].tables == nullptr) Py_RETURN_NONE;
-  return guarded([&]() -> PyObject* {
+  return guarded("swa_rope_tables", [&](Call& call) -> PyObject* {
     const int dev = device_now(), rows = int_of(a[0]), first = int_of(a[9]);
     swa_rope_freq f{int_of(a[1]), int_of(a[2]), double_of(a[3]), double_of(a[4]), double_of(a[5]),
                     double_of(a[6]), double_of(a[7]), double_of(a[8])};
     if (rows < 1 || f.rot < 2) throw Refused{};
     at::Tensor cos = at::empty({rows, f.rot / 2}, on(dev, at::kFloat)), sin = at::empty_like(cos);
-    if (libs[0].tables(&f, first, rows, cos.data_ptr<float>(), sin.data_ptr<float>(), stream_now(dev)) != SWA_OK) throw Refused{};
+    call(libs[0].tables(&f, first, rows, cos.data_ptr<float>(), sin.data_ptr<float>(), stream_now(dev)));
     return pair(cos, sin);
   });
 }
@@ -157,7 +199,7 @@ PyObject* rope_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // rope_apply(q, k, cos, sin, pos, interleaved, inverse, q_out, k_out, workspace)
 PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 10) Py_RETURN_NONE;
-  return guarded([&]() -> PyObject* {
+  return guarded("swa_rope_apply", [&](Call& call) -> PyObject* {
     const bool has_q = a[0] != Py_None, has_k = a[1] != Py_None;
     const at::Tensor& x = tensor(has_q ? a[0] : a[1]);
     if (x.dim() != 4) throw Refused{};
@@ -197,8 +239,7 @@ PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
       kt = tensor(a[8]);
     }
     swa_params p{small(B), small(T), small(Hq), small(Hkv), small(d), -1, 1, 0.f, 0.f, 0.f, 0};
-    if (libs[kind].apply(&p, &r, pos, q, k, qo, ko, PyObject_IsTrue(a[6]), ws.at, ws.bytes, stream_now(dev)) != SWA_OK)
-      throw Refused{};
+    call(libs[kind].apply(&p, &r, pos, q, k, qo, ko, PyObject_IsTrue(a[6]), ws.at, ws.bytes, stream_now(dev)));
     return pair(qt, kt);
   });
 }
@@ -206,7 +247,7 @@ PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // kv4_plan(lens, new_lens, table, free_pages, free_head, page, n_pages, n_tokens, workspace)
 PyObject* kv4_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 9 || libs[0].plan == nullptr) Py_RETURN_NONE;
-  return guarded([&]() -> PyObject* {
+  return guarded("swa_kv4_plan", [&](Call& call) -> PyObject* {
     const int dev = device_now();
     const at::Tensor &lens = tensor(a[0]), &table = tensor(a[2]), &free = tensor(a[3]);
     if (lens.dim() != 1 || table.dim() != 2) throw Refused{};
@@ -221,11 +262,10 @@ PyObject* kv4_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto i32 = on(dev, at::kInt);
     at::Tensor slot = at::empty({N}, on(dev, at::kLong)), pos = at::empty({N}, i32), row = at::empty({N}, i32),
                cu = at::empty({B + 1}, i32), lens_out = at::empty({B}, i32), head = at::empty({1}, i32);
-    if (libs[0].plan(int_of(a[6]), int_of(a[5]), small(B), small(table.size(1)), l, nl, tb, fr, small(free.numel()), hd,
+    call(libs[0].plan(int_of(a[6]), int_of(a[5]), small(B), small(table.size(1)), l, nl, tb, fr, small(free.numel()), hd,
                      static_cast<int>(N), slot.data_ptr<int64_t>(), pos.data_ptr<int32_t>(), row.data_ptr<int32_t>(),
                      cu.data_ptr<int32_t>(), lens_out.data_ptr<int32_t>(), head.data_ptr<int32_t>(), ws.at, ws.bytes,
-                     stream_now(dev)) != SWA_OK)
-      throw Refused{};
+                     stream_now(dev)));
     PyObject* dict = PyDict_New();
     const struct { const char* name; const at::Tensor& t; } out[] = {
         {"slot", slot}, {"pos", pos}, {"row", row}, {"cu", cu}, {"lens", lens_out}, {"free_head", head}};
@@ -241,7 +281,7 @@ PyObject* kv4_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // kv4_append(cache, k, v, slot, pos, cos, sin, interleaved, gk, eps, ve, tok, ve_gate, ve_scale, workspace)
 PyObject* kv4_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 15) Py_RETURN_NONE;
-  return guarded([&]() -> PyObject* {
+  return guarded("swa_kv4_append", [&](Call& call) -> PyObject* {
     const int dev = device_now();
     const CacheDims c = cache_of(a[0], dev);
     const at::Tensor& k = tensor(a[1]);
@@ -270,9 +310,8 @@ PyObject* kv4_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Ws ws = ws_of(a[14], dev);
     swa_params p{small(B), small(T), c.Hkv, c.Hkv, c.d, -1, 1, 0.f, static_cast<float>(double_of(a[9])),
                  static_cast<float>(double_of(a[13])), vocab};
-    if (libs[kind].append(&p, nullptr, &c.c, rope ? &r : nullptr, ka, va, gk, ve, tok, gate, pos, slot, ws.at, ws.bytes,
-                          stream_now(dev)) != SWA_OK)
-      throw Refused{};
+    call(libs[kind].append(&p, nullptr, &c.c, rope ? &r : nullptr, ka, va, gk, ve, tok, gate, pos, slot, ws.at, ws.bytes,
+                          stream_now(dev)));
     Py_RETURN_TRUE;
   });
 }
@@ -280,7 +319,7 @@ PyObject* kv4_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // kv4_read(cache, slot, fp32, workspace)
 PyObject* kv4_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 4) Py_RETURN_NONE;
-  return guarded([&]() -> PyObject* {
+  return guarded("swa_kv4_read", [&](Call& call) -> PyObject* {
     const int dev = device_now();
     const CacheDims c = cache_of(a[0], dev);
     const at::Tensor& s = tensor(a[1]);
@@ -291,7 +330,7 @@ PyObject* kv4_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor k = at::empty({s.size(0), s.size(1), c.Hkv, c.d}, on(dev, kind ? at::kFloat : at::kBFloat16)),
                v = at::empty_like(k);
     swa_params p{small(s.size(0)), small(s.size(1)), c.Hkv, c.Hkv, c.d, -1, 1, 0.f, 0.f, 0.f, 0};
-    if (libs[kind].read(&p, &c.c, slot, k.data_ptr(), v.data_ptr(), ws.at, ws.bytes, stream_now(dev)) != SWA_OK) throw Refused{};
+    call(libs[kind].read(&p, &c.c, slot, k.data_ptr(), v.data_ptr(), ws.at, ws.bytes, stream_now(dev)));
     return pair(k, v);
   });
 }
@@ -299,7 +338,7 @@ PyObject* kv4_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // kv4_attention(cache, q, table, lens, cos, sin, interleaved, gq, window, softmax_scale, eps, workspace)
 PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 12) Py_RETURN_NONE;
-  return guarded([&]() -> PyObject* {
+  return guarded("swa_kv4_attn", [&](Call& call) -> PyObject* {
     const int dev = device_now();
     const CacheDims c = cache_of(a[0], dev);
     const at::Tensor &q = tensor(a[1]), &table = tensor(a[2]);
@@ -317,15 +356,14 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     swa_params p{small(B), 1, small(Hq), c.Hkv, c.d, int_of(a[8]), 1, static_cast<float>(double_of(a[9])),
                  static_cast<float>(double_of(a[10])), 0.f, 0};
     at::Tensor o = at::empty_like(q), lse = at::empty({B, Hq}, on(dev, at::kFloat));
-    if (libs[kind].attn(&p, nullptr, &c.c, rope ? &r : nullptr, qa, gq, ta, small(width), la, o.data_ptr(),
-                        lse.data_ptr<float>(), ws.at, ws.bytes, stream_now(dev)) != SWA_OK)
-      throw Refused{};
+    call(libs[kind].attn(&p, nullptr, &c.c, rope ? &r : nullptr, qa, gq, ta, small(width), la, o.data_ptr(),
+                        lse.data_ptr<float>(), ws.at, ws.bytes, stream_now(dev)));
     return pair(o, lse);
   });
 }
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST(bind),       FAST(rope_tables), FAST(rope_apply),    FAST(kv4_plan),
+PyMethodDef methods[] = {FAST(bind),       FAST(raises),      FAST(rope_tables), FAST(rope_apply),    FAST(kv4_plan),
                          FAST(kv4_append), FAST(kv4_read),    FAST(kv4_attention), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
