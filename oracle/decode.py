@@ -73,7 +73,8 @@ def quantise(x):
         s = bf16((hi - lo) / 15.0)
         s = np.where(s < 1e-36, 0.0, s)
         z = bf16(lo + 8.0 * s)
-        bad = ~(np.isfinite(s) & np.isfinite(z))
+        # a span that fp32 cannot hold counts as one that is not finite
+        bad = ~(np.isfinite(s) & np.isfinite(z)) | (hi - lo >= 2.0 ** 128 - 2.0 ** 103)
         s, z = np.where(bad, np.nan, s), np.where(bad, np.nan, z)
         n = np.clip(np.floor((g - z) / np.where(s > 0, s, 1.0) + 8.5), 0, 15)
     n = np.where(s > 0, n, 8)

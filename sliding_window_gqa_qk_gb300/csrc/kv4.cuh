@@ -201,7 +201,8 @@ __device__ __forceinline__ uint32_t quantise_lane(const float (&x)[RowMap<D>::EP
   return flat ? 0x88888888u >> (32 - 4 * EPL) : w - ones;
 }
 
-// The same in fp64. Every lane of the warp calls it.
+// The same in fp64, of a group that is finite: its comparisons would drop a NaN
+// (see settled()). Every lane of the warp calls it.
 template <int D>
 __device__ __forceinline__ uint32_t quantise_f64(const double (&x)[RowMap<D>::EPL], Group& g) {
   constexpr int EPL = RowMap<D>::EPL;
@@ -256,6 +257,11 @@ struct AppendArgs {
   const int32_t* pos; const int64_t* slot;
   uint32_t* status;                    // or NULL
 };
+
+// Whether a lane takes the fp64 result of its row: where the row has a close
+// entry, unless fp32 found the lane's group not finite. The row's other group
+// may be what was close.
+__device__ __forceinline__ bool settled(unsigned close, const Group& fp32) { return close != 0 && !isnan(fp32.s); }
 
 // What fp32 arithmetic may leave an entry off by, in units of 2^-24 of the
 // row's largest entry. Rotation, norm and gain, in fp32 and fp64 on 200,000
@@ -404,7 +410,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
     if (close) {
       Group s2;
       const uint32_t w2 = key_f64<D>(a, row, p, on, &s2);
-      if (close & rows_mask) {
+      if (settled(close & rows_mask, sk)) {
         wk = w2;
         sk = s2;
       }
@@ -425,7 +431,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
       if (close) {
         Group s2;
         const uint32_t w2 = mix_f64<D>(a, row, ve, gate, on, &s2);
-        if (close & rows_mask) {
+        if (settled(close & rows_mask, sv)) {
           wv = w2;
           sv = s2;
         }
