@@ -539,7 +539,8 @@ swa_status swa_kv4_read(const swa_params* p, const swa_kv4_cache* c, const int64
  * lens[b] - 1 (whose key and value are in the cache already), rotated there
  * (r, NULL: not), normed and multiplied by gq; it sees the cache's keys j with
  * lens[b] - 1 - window <= j < lens[b] (window -1: all). p->T must be 1 and
- * p->causal 1; window, softmax_scale and eps as in swa_attn_fwd.
+ * p->causal 1, B * Hq at most 65535; window, softmax_scale and eps as in
+ * swa_attn_fwd.
  *   table    int32 [B][max_pages]; entries behind ceil(lens[b] / page) and in
  *            front of the window are not read
  *   lens     int32 [B]; 0: the request's rows of o are 0 and of lse -infinity

@@ -9,6 +9,17 @@
 
 namespace {
 
+constexpr int kMaxRowHeads = 65535;
+
+// The problem of the calls whose kernels walk flat lists of rows (rotation,
+// append, read): any number of tokens, in any shape. The rotation of few
+// tokens counts batches of three heads and more of q and k in grid y.
+swa_status check_rows(const swa_params* p) {
+  const swa_status s = check_problem(p);
+  if (s != SWA_OK) return s;
+  return p->Hq > kMaxRowHeads ? SWA_ERR_UNSUPPORTED : SWA_OK;
+}
+
 // Rotary tables of the rope and decode calls: r NULL, or both tables NULL:
 // none (on = false).
 swa_status check_rope(const swa_rope* r, int d, bool& on) {
@@ -151,7 +162,7 @@ swa_status swa_rope_tables(const swa_rope_freq* f, int first, int rows, float* c
 
 swa_status swa_rope_apply(const swa_params* p, const swa_rope* r, const int32_t* pos, const void* q, const void* k,
                           void* q_out, void* k_out, int inverse, void* workspace, size_t ws_bytes, void* stream) {
-  swa_status s = check_params(p);
+  swa_status s = check_rows(p);
   if (s != SWA_OK) return s;
   bool on = false;
   if ((s = check_rope(r, p->d, on)) != SWA_OK) return s;
@@ -192,7 +203,7 @@ swa_status swa_rope_apply(const swa_params* p, const swa_rope* r, const int32_t*
 }
 
 size_t swa_kv4_cache_size(const swa_params* p, int n_pages, int page) {
-  if (check_params(p) != SWA_OK || check_pages(n_pages, page) != SWA_OK) return 0;
+  if (check_rows(p) != SWA_OK || check_pages(n_pages, page) != SWA_OK) return 0;
   return static_cast<size_t>(n_pages) * p->Hkv * (page / kv4::kTile) * kv4::tile_bytes(p->d);
 }
 
@@ -240,7 +251,7 @@ swa_status swa_kv4_append(const swa_params* p, const swa_extras* ex, const swa_k
                           const void* k, const void* v, const float* gk, const void* ve, const int32_t* tok,
                           const float* ve_gate, const int32_t* pos, const int64_t* slot, void* workspace,
                           size_t ws_bytes, void* stream) {
-  swa_status s = check_params(p);
+  swa_status s = check_rows(p);
   if (s != SWA_OK) return s;
   kv4::AppendArgs a{};
   if ((s = check_cache(p, c, a.c)) != SWA_OK) return s;
@@ -296,7 +307,7 @@ swa_status swa_kv4_append(const swa_params* p, const swa_extras* ex, const swa_k
 
 swa_status swa_kv4_read(const swa_params* p, const swa_kv4_cache* c, const int64_t* slot, void* k_out, void* v_out,
                         void* workspace, size_t ws_bytes, void* stream) {
-  swa_status s = check_params(p);
+  swa_status s = check_rows(p);
   if (s != SWA_OK) return s;
   kv4::ReadArgs a{};
   if ((s = check_cache(p, c, a.c)) != SWA_OK) return s;

@@ -81,7 +81,8 @@ swa_status set_extras(Call& c, const swa_extras* e, const float* ve_gate) {
   return SWA_OK;
 }
 
-swa_status check_params(const swa_params* p) {
+// What every call asks of its problem.
+swa_status check_problem(const swa_params* p) {
   if (p == nullptr) return SWA_ERR_INVALID_ARG;
   if (p->B < 0 || p->T < 0 || p->Hq < 1 || p->Hkv < 1 || p->d < 1) return SWA_ERR_INVALID_ARG;
   if (p->Hq % p->Hkv != 0) return SWA_ERR_INVALID_ARG;
@@ -91,6 +92,12 @@ swa_status check_params(const swa_params* p) {
   if (!std::isfinite(p->eps) || p->eps < 0.f) return SWA_ERR_INVALID_ARG;
   if (!std::isfinite(p->ve_scale)) return SWA_ERR_INVALID_ARG;
   if (p->d != 64 && p->d != 128) return SWA_ERR_UNSUPPORTED;
+  return SWA_OK;
+}
+
+swa_status check_params(const swa_params* p) {
+  const swa_status s = check_problem(p);
+  if (s != SWA_OK) return s;
   // Grid and index limits: (batch, head) pairs index a grid dimension of at
   // most 65535 blocks in the row-wise kernels, tiles of 128 positions index
   // grid y of the attention kernels (< 65536), positions are 32-bit TMA

@@ -57,3 +57,35 @@ def test_a_group_that_is_not_finite_is_held_as_nan(kind, embedded, rest):
     assert torch.all(vr[~want] == rest) and torch.isfinite(kr).all()
     held = dec.dequantise(*dec.quantise(f64(v)[0, :, 0]))      # and the oracle says the same
     np.testing.assert_array_equal(np.isnan(held), want.numpy())
+
+
+# ---------------------------------------------------------------------------
+# Sizes
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_more_tokens_than_a_grid_dimension_holds(kind):
+    # tokens of a step as n rows of one token, as a plan gives them, are the
+    # same tokens as one row of n
+    n, Hkv, d, page = 40001, 3, 64, 32
+    n_pages = -(-n // page)
+    k, v = (randn(i, n, 1, Hkv, d, dtype=DT[kind]).to(dev()) for i in (1, 2))
+    slot = torch.randperm(n_pages * page, generator=gen(3))[:n].view(n, 1).to(dev())
+    pos = torch.randint(0, 50, (n, 1), generator=gen(4), dtype=torch.int32).to(dev())
+    rope = swa.rope_tables(50, d)
+    got, want = (torch.zeros(n_pages, Hkv, page // 16, 18 * d, dtype=torch.uint8, device=dev()) for _ in range(2))
+    swa.kv4_append(got, k, v, slot, pos=pos, rope=rope)
+    swa.kv4_append(want, k.view(1, n, Hkv, d), v.view(1, n, Hkv, d), slot.view(1, n), pos=pos.view(1, n), rope=rope)
+    assert torch.equal(got, want) and want.any()
+    a, b = swa.kv4_read(got, slot, dtype=DT[kind]), swa.kv4_read(got, slot.view(1, n), dtype=DT[kind])
+    for x, y in zip(a, b):
+        assert x.shape == (n, 1, Hkv, d) and torch.equal(x.view(-1), y.view(-1))
+    a = swa.rope_apply(k, v, rope, pos=pos)
+    b = swa.rope_apply(k.view(1, n, Hkv, d), v.view(1, n, Hkv, d), rope, pos=pos.view(1, n))
+    for x, y in zip(a, b):
+        assert torch.equal(x.view(-1), y.view(-1))
+    # many heads of few tokens
+    q = randn(5, 2, 1, 40000, d, dtype=DT[kind]).to(dev())
+    x, _ = swa.rope_apply(q, None, rope, pos=pos[:2])
+    y, _ = swa.rope_apply(q.view(2, 20000, 2, d), None, rope, pos=pos[:2].expand(2, 20000).contiguous())
+    assert torch.equal(x.view(-1), y.view(-1))

@@ -1,12 +1,15 @@
 """Host side of the decode calls' binding: what an import loads, and which
-build of the short way (csrc/py_fast.cpp) is taken. Nothing here runs on a GPU."""
+build of the short way (csrc/py_fast.cpp) is taken; sizes that the calls take.
+Nothing here runs on a GPU."""
 
 import os
 import subprocess
 import sys
 
 import pytest
+import torch
 
+import sliding_window_gqa_qk_gb300 as swa
 from sliding_window_gqa_qk_gb300 import build as swa_build
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -33,7 +36,7 @@ def test_an_import_maps_no_library_of_the_package():
 def test_the_short_way_is_that_of_this_torch_and_python(monkeypatch):
     here = swa_build.fast_path()
     assert os.path.exists(here)
-    torch_version = __import__("torch").__version__
+    torch_version = torch.__version__
     monkeypatch.setattr("torch.__version__", torch_version + ".other")
     assert swa_build.fast_path() != here and not os.path.exists(swa_build.fast_path())
     monkeypatch.setattr("torch.__version__", torch_version)
@@ -43,3 +46,33 @@ def test_the_short_way_is_that_of_this_torch_and_python(monkeypatch):
     code = ("import torch\ntorch.__version__ += '.other'\nimport sliding_window_gqa_qk_gb300 as swa\nswa.load('bf16')\n"
             "print(swa._fast)\nprint([x for x in open('/proc/self/maps') if '_fast' in x and 'gb300' in x])")
     assert run(code).split() == ["None", "[]"]
+
+
+# ---------------------------------------------------------------------------
+# Sizes
+# ---------------------------------------------------------------------------
+
+A = 1 << 20
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses would be used")
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_the_row_calls_take_any_number_of_tokens(kind):
+    # what the same calls of a few tokens end with on a machine without a GPU
+    cache, rope = swa.swa_kv4_cache(A, 10, 32), swa.swa_rope(A, A, 1 << 23, 64, 0)
+
+    def ends(**kw):
+        p = swa.make_params(**dict(dict(B=2, T=3, Hq=4, Hkv=2, d=128), **kw))
+        return (swa.swa_rope_apply(p, rope, A, A, A, A, A, kind=kind), swa.swa_kv4_append(p, None, cache, rope, A, A, None, None, None, None, A, A, kind=kind),
+                swa.swa_kv4_read(p, cache, A, A, A, kind=kind))
+
+    few = ends()
+    assert few[0] != swa.SWA_OK and len(set(few)) == 1
+    for kw in (dict(B=16384, T=1), dict(B=104000, T=1, Hq=3, Hkv=3), dict(B=2 ** 31 - 1, T=1, Hq=1, Hkv=1), dict(B=1, T=(1 << 22) + 1),
+               dict(B=40000, T=2, Hq=65535, Hkv=1)):
+        assert ends(**kw) == few, kw
+        assert swa.swa_kv4_cache_size(swa.make_params(**dict(dict(B=2, T=3, Hq=4, Hkv=2, d=128), **kw)), 10, 32, kind) > 0
+    assert set(ends(B=1, T=1, Hq=65536)) == {swa.SWA_ERR_UNSUPPORTED}
+    # the attention counts requests and heads in its grid
+    attn = lambda **kw: swa.swa_kv4_attn(swa.make_params(T=1, d=64, **kw), None, cache, None, A, None, A, 4, A, A, A, A, 1 << 40, kind=kind)   # noqa: E731
+    assert attn(B=65536, Hq=1, Hkv=1) == swa.SWA_ERR_UNSUPPORTED and attn(B=65535, Hq=1, Hkv=1) == few[0]
