@@ -550,6 +550,11 @@ struct PlanArgs {
   uint32_t* status;
 };
 
+// Pages of len tokens, len >= 0: the sum may pass 2^31, but not 2^32.
+__device__ __forceinline__ int plan_pages(const PlanArgs& a, int len) {
+  return static_cast<int>((static_cast<uint32_t>(len) + static_cast<uint32_t>(a.page) - 1u) / static_cast<uint32_t>(a.page));
+}
+
 struct PlanReq {
   int len, fresh, held, want;
   bool ok;      // plausible, and fits its table row
@@ -561,8 +566,8 @@ __device__ __forceinline__ PlanReq plan_req(const PlanArgs& a, int b) {
   const long long end = static_cast<long long>(r.len) + r.fresh;
   r.ok = r.len >= 0 && r.fresh >= 0 && end <= static_cast<long long>(a.max_pages) * a.page;
   r.fresh = r.fresh < 0 ? 0 : r.fresh;
-  r.held = r.ok ? (r.len + a.page - 1) / a.page : 0;
-  r.want = r.ok ? static_cast<int>((end + a.page - 1) / a.page) - r.held : 0;
+  r.held = r.ok ? plan_pages(a, r.len) : 0;
+  r.want = r.ok ? plan_pages(a, static_cast<int>(end)) - r.held : 0;
   return r;
 }
 
@@ -661,7 +666,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       row[j] = b;
       pos[j] = t;
       if (s_off[b] < 0) continue;   // (a request that goes lies inside its row)
-      const int held = (len + a.page - 1) / a.page, pj = t / a.page;
+      const int held = plan_pages(a, len), pj = t / a.page;
       const int pg = pj < held ? a.table[static_cast<long long>(b) * a.max_pages + pj]
                                : a.free_pages[head + s_off[b] + (pj - held)];
       if (pg >= 0 && pg < a.n_pages) slot[j] = static_cast<long long>(pg) * a.page + (t - pj * a.page);

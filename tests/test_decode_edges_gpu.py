@@ -89,3 +89,26 @@ def test_more_tokens_than_a_grid_dimension_holds(kind):
     x, _ = swa.rope_apply(q, None, rope, pos=pos[:2])
     y, _ = swa.rope_apply(q.view(2, 20000, 2, d), None, rope, pos=pos[:2].expand(2, 20000).contiguous())
     assert torch.equal(x.view(-1), y.view(-1))
+
+
+def test_plan_of_lengths_near_the_end_of_32_bits():
+    # pages that are no power of two: the length rounded up to whole pages
+    # passes 2^31 although the table row ends below it
+    for page, width, lens, new in ((192, 11184810, [2147483500, 0], [10, 5]), (16000, 134217, [2147471997, 15999], [1, 2]),
+                                   (144, 14913080, [2147483517, 2147483376], [3, 100])):
+        n_pages, n_tokens = 12, sum(new) + 1
+        table = np.full((2, width), -1, np.int32)
+        for b, n in enumerate(lens):
+            table[b, max(-(-n // page) - 2, 0):-(-n // page)] = 3 + b
+        free, head = np.array([7, 8, 9], np.int32), 1
+        ref = dec.plan(np.array(lens, np.int64), np.array(new, np.int64), table, free, head, page, n_pages, n_tokens)
+        assert ref["refused"] == 0
+        t = torch.tensor(table, device=dev())
+        ws = torch.zeros(256, dtype=torch.uint8, device=dev())
+        out = swa.kv4_plan(i32(*lens), i32(*new), t, i32(*free.tolist()), i32(head), page=page, n_pages=n_pages, n_tokens=n_tokens,
+                           workspace=ws)
+        assert swa.swa_attn_check_status(ws) == swa.SWA_OK
+        assert np.array_equal(t.cpu().numpy(), ref["table"])
+        for x in ("slot", "pos", "row", "cu", "lens"):
+            np.testing.assert_array_equal(out[x].cpu().numpy(), ref[x], err_msg=x)
+        assert out["free_head"].item() == ref["free_head"]
