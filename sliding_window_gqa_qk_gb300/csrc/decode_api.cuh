@@ -113,6 +113,11 @@ void by_head_dim(int d, F64 f64, F128 f128) {
   if (d == 64) f64(); else f128();
 }
 
+// Shared memory of a plan of B requests. The limit that the kernel is given
+// is that of the largest plan whatever B is: it holds for the device, and
+// another thread's call may lie between a call's asking and its launch.
+constexpr size_t plan_smem(int B) { return (static_cast<size_t>(B) * 3 + 1) * sizeof(int); }
+
 // Tokens of one launch of the row kernels, whose rows count in 31 bits.
 long long launch_tokens(int Hkv) { return (1LL << 30) / Hkv; }
 
@@ -235,10 +240,13 @@ swa_status swa_kv4_plan(int n_pages, int page, int B, int max_pages, const int32
   a.lens = lens; a.new_lens = new_lens; a.table = table; a.free_pages = free_pages; a.head = free_head;
   a.slot = slot; a.pos = pos; a.row = row; a.cu = cu; a.lens_out = lens_out; a.head_out = head_out;
   a.status = static_cast<uint32_t*>(workspace);
-  const size_t smem = (static_cast<size_t>(B) * 3 + 1) * sizeof(int);
+  const size_t smem = plan_smem(B);
   if (smem > 48 * 1024 - 1024 &&     // what a launch gets unasked, less the kernel's own arrays
-      cudaFuncSetAttribute(kv4::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+      cudaFuncSetAttribute(kv4::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(plan_smem(kv4::kPlanMaxB))) != cudaSuccess) {
+    cudaGetLastError();   // told here, and not again by the next launch
     return SWA_ERR_CUDA;
+  }
   // as many blocks as the tokens want, or the requests: two to a warp, for their new pages
   const int by_tokens = flat_grid(n_tokens, kv4::kPlanThreads * kv4::kPlanTokens, num_sms());
   const int by_requests = flat_grid(B, kv4::kPlanThreads / 16, num_sms());

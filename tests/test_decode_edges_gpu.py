@@ -112,3 +112,60 @@ def test_plan_of_lengths_near_the_end_of_32_bits():
         for x in ("slot", "pos", "row", "cu", "lens"):
             np.testing.assert_array_equal(out[x].cpu().numpy(), ref[x], err_msg=x)
         assert out["free_head"].item() == ref["free_head"]
+
+
+HARNESS = r"""
+#include <pthread.h>
+#include <stdint.h>
+#include "swa_attn.h"
+typedef swa_status (*plan_fn)(int, int, int, int, const int32_t*, const int32_t*, int32_t*, const int32_t*, int, const int32_t*, int,
+                              int64_t*, int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, void*, size_t, void*);
+typedef struct {
+  plan_fn f;
+  int B, n, failed;
+  void *lens, *table, *free_pages, *head, *slot, *pos, *row, *cu, *lens_out, *head_out, *stream;
+} work;
+static void* loop(void* x) {
+  work* w = (work*)x;
+  for (int i = 0; i < w->n; ++i)
+    w->failed += w->f(w->B, 16, w->B, 2, w->lens, 0, w->table, w->free_pages, w->B, w->head, w->B, w->slot, w->pos, w->row, w->cu,
+                      w->lens_out, w->head_out, 0, 0, w->stream) != SWA_OK;
+  return 0;
+}
+void both(work* a, work* b) {
+  pthread_t t, u;
+  pthread_create(&t, 0, loop, a);
+  pthread_create(&u, 0, loop, b);
+  pthread_join(t, 0);
+  pthread_join(u, 0);
+}
+"""
+
+
+def test_plans_of_large_batches_from_two_threads(tmp_path):
+    # both want more shared memory than a launch gets unasked, each its own
+    # amount: neither takes away what the other has asked for
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    (tmp_path / "both.c").write_text(HARNESS)
+    so = os.fspath(tmp_path / "both.so")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-O1", "-pthread", "-I" + include, "-o", so, os.fspath(tmp_path / "both.c")], check=True)
+    names = ("lens", "table", "free_pages", "head", "slot", "pos", "row", "cu", "lens_out", "head_out", "stream")
+
+    class Work(ctypes.Structure):
+        _fields_ = [("f", ctypes.c_void_p)] + [(x, ctypes.c_int) for x in ("B", "n", "failed")] + [(x, ctypes.c_void_p) for x in names]
+
+    works, kept = [], []
+    for B in (8192, 4300):
+        zeros = lambda n, t=torch.int32: torch.zeros(n, dtype=t, device=dev())   # noqa: E731
+        buf = [zeros(B), zeros(2 * B), torch.arange(B, dtype=torch.int32, device=dev()), zeros(1), zeros(B, torch.int64), zeros(B),
+               zeros(B), zeros(B + 1), zeros(B), zeros(1)]
+        stream = torch.cuda.Stream()
+        kept.append((buf, stream))
+        works.append(Work(ctypes.cast(swa.load("bf16").swa_kv4_plan, ctypes.c_void_p).value, B, 20000, 0,
+                          *(t.data_ptr() for t in buf), stream.cuda_stream))
+    torch.cuda.synchronize()
+    ctypes.CDLL(so).both(ctypes.byref(works[0]), ctypes.byref(works[1]))
+    torch.cuda.synchronize()
+    assert [w.failed for w in works] == [0, 0]
+    for (buf, _), w in zip(kept, works):
+        assert torch.equal(buf[4].cpu(), 16 * torch.arange(w.B))
