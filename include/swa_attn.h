@@ -431,11 +431,15 @@ typedef struct {
  *   pos      int32 [B, T] positions, or NULL: row t of the sequence is position
  *            t (then rows >= T). A token whose position is outside the tables
  *            keeps its output rows as they were and is reported.
- *   inverse  1: the transposed rotation, the backward of the forward's
+ *   inverse  1: the transposed rotation, the backward of the forward's; 0: the
+ *            rotation. SWA_ROPE_NEW_OUTPUTS may be added: the outputs hold
+ *            nothing yet (neither may be its input), and the rows of such
+ *            tokens are set to zero
  *   workspace  at least its 256-byte header, where device checks are reported
  *            (swa_attn_check_status); NULL: they are not
  * Sums are fp32, rounded once to elem.
  */
+#define SWA_ROPE_NEW_OUTPUTS 4
 swa_status swa_rope_apply(const swa_params* p, const swa_rope* r, const int32_t* pos, const void* q,
                           const void* k, void* q_out, void* k_out, int inverse, void* workspace,
                           size_t ws_bytes, void* stream);

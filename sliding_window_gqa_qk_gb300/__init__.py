@@ -575,6 +575,7 @@ def attention_backward(q, k, v, gq, gk, o, lse, dO, *, window: int = -1, causal:
 # ---------------------------------------------------------------------------
 
 SWA_ROPE_PLAIN, SWA_ROPE_LINEAR, SWA_ROPE_NTK, SWA_ROPE_BY_PARTS = range(4)
+SWA_ROPE_NEW_OUTPUTS = 4
 _SCALINGS = {"none": SWA_ROPE_PLAIN, "linear": SWA_ROPE_LINEAR, "ntk": SWA_ROPE_NTK, "by_parts": SWA_ROPE_BY_PARTS}
 _NO_ROPE = (None, None)
 _F32, _BF16, _I32, _I64, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.int64, torch.uint8
@@ -685,8 +686,9 @@ def rope_apply(q, k, rope, *, pos=None, interleaved: bool = False, inverse: bool
     at positions ``pos`` int32 [B, T] (None: t). ``inverse``: the transposed
     rotation, which turns gradients of q', k' into those of q, k. ``out`` =
     (q', k') may be (q, k): in place. ``workspace``: where positions outside
-    the tables are reported (swa_attn_check_status); their rows are not
-    written."""
+    the tables are reported (swa_attn_check_status), which nothing tells
+    without one. Their rows are zero in new outputs, and left as they were in
+    those of ``out``."""
     if _fast is not None and stream is None and rope is not None:
         r = _fast.rope_apply(q, k, *rope, pos, interleaved, inverse, *(_NO_ROPE if out is None else out), workspace)
         if r is not None:
@@ -709,14 +711,18 @@ def rope_apply(q, k, rope, *, pos=None, interleaved: bool = False, inverse: bool
     if st is None:
         return _there(dev, stream, lambda: rope_apply(q, k, rope, pos=pos, interleaved=interleaved, inverse=inverse, out=out,
                                                       workspace=workspace))
+    # outputs allocated here hold nothing yet: the call is told so, or, beside
+    # one of the caller's, they begin as zeros where a row may be left out
+    fresh = qo is None and ko is None
+    new = torch.empty_like if fresh or pos is None else torch.zeros_like
     if q is not None and qo is None:
-        qo = torch.empty_like(q)
+        qo = new(q)
         qoa = qo.data_ptr()
     if k is not None and ko is None:
-        ko = torch.empty_like(k)
+        ko = new(k)
         koa = ko.data_ptr()
     s = lib.swa_rope_apply(swa_params(B, T, Hq, Hkv, d, -1, 1, 0.0, 0.0, 0.0, 0), r, pa, qa, ka, qoa, koa,
-                           1 if inverse else 0, ws, nws, st)
+                           (1 if inverse else 0) | (SWA_ROPE_NEW_OUTPUTS if fresh else 0), ws, nws, st)
     if s:
         raise SwaError(s, "swa_rope_apply")
     return qo, ko

@@ -171,8 +171,11 @@ swa_status swa_rope_apply(const swa_params* p, const swa_rope* r, const int32_t*
   if (s != SWA_OK) return s;
   bool on = false;
   if ((s = check_rope(r, p->d, on)) != SWA_OK) return s;
+  const bool fresh = (inverse & SWA_ROPE_NEW_OUTPUTS) != 0;
+  inverse &= ~SWA_ROPE_NEW_OUTPUTS;
   if (!on || (inverse != 0 && inverse != 1)) return SWA_ERR_INVALID_ARG;
   if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr)) return SWA_ERR_INVALID_ARG;
+  if (fresh && ((q != nullptr && q == q_out) || (k != nullptr && k == k_out))) return SWA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(pos, 4))
     return SWA_ERR_INVALID_ARG;
   if (pos == nullptr && r->rows < p->T) return SWA_ERR_INVALID_ARG;
@@ -192,6 +195,7 @@ swa_status swa_rope_apply(const swa_params* p, const swa_rope* r, const int32_t*
   const bool in_place = (q == nullptr || q == q_out) && (k == nullptr || k == k_out);
   a.units = a.turned + (in_place ? 0 : (p->d - r->rot) / EPL);
   a.sgn = inverse ? -1.f : 1.f;
+  a.fresh = fresh;
   a.status = static_cast<uint32_t*>(workspace);
   const int H = a.Hq + a.Hkv;
   const long long threads = a.N * a.units;

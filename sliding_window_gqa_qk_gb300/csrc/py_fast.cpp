@@ -14,6 +14,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
+#include <ATen/ops/zeros_like.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -223,23 +224,27 @@ PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* qo = at_(a[7], type, dev, {B, T, Hq, d});
     void* ko = at_(a[8], type, dev, {B, T, Hkv, d});
     const Ws ws = ws_of(a[9], dev);
+    // Outputs allocated here hold nothing yet: the call is told so, or, beside
+    // one of the caller's, they begin as zeros where a row may be left out.
+    const bool fresh = qo == nullptr && ko == nullptr, zeros = !fresh && pos != nullptr;
     at::Tensor qt, kt;
     if (has_q && qo == nullptr) {
       if (a[7] != Py_None) throw Refused{};
-      qt = at::empty_like(tensor(a[0]));
+      qt = zeros ? at::zeros_like(tensor(a[0])) : at::empty_like(tensor(a[0]));
       qo = qt.data_ptr();
     } else if (has_q) {
       qt = tensor(a[7]);
     }
     if (has_k && ko == nullptr) {
       if (a[8] != Py_None) throw Refused{};
-      kt = at::empty_like(tensor(a[1]));
+      kt = zeros ? at::zeros_like(tensor(a[1])) : at::empty_like(tensor(a[1]));
       ko = kt.data_ptr();
     } else if (has_k) {
       kt = tensor(a[8]);
     }
+    const int mode = (PyObject_IsTrue(a[6]) ? 1 : 0) | (fresh ? SWA_ROPE_NEW_OUTPUTS : 0);
     swa_params p{small(B), small(T), small(Hq), small(Hkv), small(d), -1, 1, 0.f, 0.f, 0.f, 0};
-    call(libs[kind].apply(&p, &r, pos, q, k, qo, ko, PyObject_IsTrue(a[6]), ws.at, ws.bytes, stream_now(dev)));
+    call(libs[kind].apply(&p, &r, pos, q, k, qo, ko, mode, ws.at, ws.bytes, stream_now(dev)));
     return pair(qt, kt);
   });
 }

@@ -101,6 +101,7 @@ struct RopeArgs {
   int turned, units;                  // units of a position: turned, and all
   int heads;                          // heads of one thread
   float sgn;                          // 1, or -1 for the transposed rotation
+  bool fresh;                         // rows that are not turned become zero
   uint32_t* status;                   // or NULL
 };
 
@@ -112,13 +113,23 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   if (n >= a.N) return;
   const int u = static_cast<int>(id - n * a.units);
   const int p = a.pos ? a.pos[n] : static_cast<int>(n % a.T);
-  if (p < 0 || p >= a.rows) {   // left as it was, and reported
-    if (u == 0 && blockIdx.y == 0 && a.status) atomicOr(a.status, DEV_ERR_BOUNDS);
-    return;
-  }
   const int half = a.rot / 2;
   const bool turn = u < a.turned;
   const int c = turn ? u * EPL : a.rot + (u - a.turned) * EPL;
+  const int H = a.Hq + a.Hkv;
+  const int h0 = blockIdx.y * a.heads, h1 = h0 + a.heads < H ? h0 + a.heads : H;
+  if (p < 0 || p >= a.rows) {   // left as it was, or zero, and reported
+    if (u == 0 && blockIdx.y == 0 && a.status) atomicOr(a.status, DEV_ERR_BOUNDS);
+    if (a.fresh) {
+#pragma unroll 1
+      for (int h = h0; h < h1; ++h) {
+        elem_t* out = (h < a.Hq ? a.qo + (n * a.Hq + h) * a.d : a.ko + (n * a.Hkv + (h - a.Hq)) * a.d) + c;
+        st16(out, make_uint4(0u, 0u, 0u, 0u));
+        if (!INTER && turn) st16(out + half, make_uint4(0u, 0u, 0u, 0u));
+      }
+    }
+    return;
+  }
   constexpr int NP = INTER ? EPL / 2 : EPL;   // pairs of the unit
   float cs[NP], sn[NP];
   if (turn) {
@@ -133,8 +144,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 #pragma unroll
     for (int i = 0; i < NP; ++i) sn[i] *= a.sgn;
   }
-  const int H = a.Hq + a.Hkv;
-  const int h0 = blockIdx.y * a.heads, h1 = h0 + a.heads < H ? h0 + a.heads : H;
   for (int h = h0; h < h1; h += kBatch) {
     uint4 x[kBatch], y[kBatch];
     elem_t* out[kBatch];

@@ -169,3 +169,47 @@ def test_plans_of_large_batches_from_two_threads(tmp_path):
     assert [w.failed for w in works] == [0, 0]
     for (buf, _), w in zip(kept, works):
         assert torch.equal(buf[4].cpu(), 16 * torch.arange(w.B))
+
+
+# ---------------------------------------------------------------------------
+# Positions outside the tables
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("short_way", [False, True])
+def test_rows_of_positions_outside_the_tables_are_zero_in_new_outputs(kind, inter, short_way, monkeypatch):
+    swa.load(kind)
+    if not short_way:
+        monkeypatch.setattr(swa, "_fast", None)
+    B, T, Hq, Hkv, d, rot = 2, 40, 5, 1, 128, 48
+    q, k = randn(1, B, T, Hq, d, dtype=DT[kind]).to(dev()), randn(2, B, T, Hkv, d, dtype=DT[kind]).to(dev())
+    rope = swa.rope_tables(30, rot)
+    pos = torch.randint(0, 30, (B, T), generator=gen(3), dtype=torch.int32)
+    bad = torch.rand(B, T, generator=gen(4)) < 0.3
+    pos[bad] = torch.where(torch.rand(int(bad.sum()), generator=gen(5)) < 0.5, -1, 30).int()
+    pd, bad = pos.to(dev()), bad.to(dev())
+    qw, kw = swa.rope_apply(q, k, rope, pos=pd.clamp(0, 29), interleaved=inter)
+    qw[bad], kw[bad] = 0, 0
+
+    def stale():      # what the next allocations of these sizes find in memory
+        a, b = torch.full_like(q, 7.0), torch.full_like(k, 7.0)
+        del a, b
+
+    ws = torch.zeros(256, dtype=torch.uint8, device=dev())
+    for w in (None, ws):
+        stale()
+        qo, ko = swa.rope_apply(q, k, rope, pos=pd, interleaved=inter, workspace=w)
+        assert torch.equal(qo, qw) and torch.equal(ko, kw)
+        stale()
+        assert torch.equal(swa.rope_apply(None, k, rope, pos=pd, interleaved=inter, workspace=w)[1], kw)
+        # an output of the caller's keeps those rows, a new one beside it is zero there
+        mine = torch.full_like(q, 3.0)
+        stale()
+        qo, ko = swa.rope_apply(q, k, rope, pos=pd, interleaved=inter, out=(mine, None), workspace=w)
+        assert qo is mine and torch.all(qo[bad] == 3.0) and torch.equal(qo[~bad], qw[~bad]) and torch.equal(ko, kw)
+        same = k.clone()
+        stale()
+        qo, ko = swa.rope_apply(q, same, rope, pos=pd, interleaved=inter, out=(None, same), workspace=w)
+        assert torch.equal(qo, qw) and torch.equal(ko[bad], k[bad]) and torch.equal(ko[~bad], kw[~bad])
+    assert swa.swa_attn_check_status(ws) == swa.SWA_ERR_DEVICE_CHECK

@@ -76,3 +76,18 @@ def test_the_row_calls_take_any_number_of_tokens(kind):
     # the attention counts requests and heads in its grid
     attn = lambda **kw: swa.swa_kv4_attn(swa.make_params(T=1, d=64, **kw), None, cache, None, A, None, A, 4, A, A, A, A, 1 << 40, kind=kind)   # noqa: E731
     assert attn(B=65536, Hq=1, Hkv=1) == swa.SWA_ERR_UNSUPPORTED and attn(B=65535, Hq=1, Hkv=1) == few[0]
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses would be used")
+def test_new_outputs_of_a_rotation_are_no_inputs():
+    p, rope = swa.make_params(B=2, T=3, Hq=4, Hkv=2, d=128), swa.swa_rope(A, A, 64, 64, 0)
+    new = swa.SWA_ROPE_NEW_OUTPUTS
+    apply = lambda *args: swa.swa_rope_apply(p, rope, None, *args, kind="bf16")   # noqa: E731
+    plain = apply(A, A, 2 * A, 3 * A, 0)
+    for mode in (new, new + 1):
+        assert apply(A, A, 2 * A, 3 * A, mode) == plain
+        for q, k, qo, ko in ((A, A, A, 3 * A), (A, A, 2 * A, A), (None, A, None, A), (A, None, A, None)):
+            assert apply(q, k, qo, ko, mode) == swa.SWA_ERR_INVALID_ARG
+        assert apply(A, None, 2 * A, None, mode) == plain
+    for mode in (2, 3, new + 2, 8, -1):
+        assert apply(A, A, 2 * A, 3 * A, mode) == swa.SWA_ERR_INVALID_ARG
