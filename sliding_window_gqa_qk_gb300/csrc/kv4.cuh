@@ -271,6 +271,18 @@ constexpr float kKeyErr = 4.0f * 5.9604645e-8f;
 constexpr float kMixErr = 4.0f * 5.9604645e-8f;
 constexpr int kAppendWarps = 4;      // a small block: one slow row holds up few others
 
+// 1 / sqrt(x), x >= 0 of any size: an even power of two is taken out, and one
+// Newton step from the fp32 root of the rest squares its 2^-22, which is enough
+// here. Infinity gives 2^-512, which keeps an infinity one and leaves nothing of
+// a number.
+__device__ __forceinline__ double rsqrt_f64(double x) {
+  const int hi = __double2hiint(x), k = ((hi >> 20) - 1023) & ~1;
+  const double m = __hiloint2double(hi - k * (1 << 20), __double2loint(x));   // within [1, 4)
+  const double r0 = rsqrtf(static_cast<float>(m));
+  const double r = r0 * fma(-0.5 * m * r0, r0, 1.5) * __hiloint2double((1023 - k / 2) * (1 << 20), 0);
+  return x > 0.0 ? r : static_cast<double>(rsqrtf(static_cast<float>(x)));     // 0 and NaN
+}
+
 // The rotated and normed key row in fp64 (row: its index, p its position),
 // quantised; every lane of the warp calls it.
 template <int D>
@@ -296,10 +308,7 @@ __device__ __noinline__ uint32_t key_f64(const AppendArgs& a, uint32_t row, int 
   }
 #pragma unroll
   for (int o = M::LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  // 1 / sqrt by one Newton step from the fp32 one: 2^-22 squared is enough here
-  const double mean = fma(ss, 1.0 / D, static_cast<double>(a.eps));
-  const double r0 = rsqrtf(static_cast<float>(mean));
-  const double rstd = r0 * fma(-0.5 * mean * r0, r0, 1.5);
+  const double rstd = rsqrt_f64(fma(ss, 1.0 / D, static_cast<double>(a.eps)));
 #pragma unroll
   for (int i = 0; i < EPL; ++i) x[i] = x[i] * rstd * (a.gk ? a.gk[c0 + i] : 1.0f);
   Group g;
@@ -399,6 +408,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < EPL; ++i) ss = fmaf(x[i], x[i], ss);
     ss = row_sum<M::LPR>(ss);
+    // A mean square past fp32 makes every entry 0 (or NaN), whose step of 0 lies
+    // on a border: such a row is done in fp64.
     const float rstd = rsqrtf(ss / D + a.eps);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) x[i] = x[i] * rstd * gk[i];

@@ -1,6 +1,6 @@
 """The rotary and decode calls where their ranges end, for both builds:
-infinities and NaN beside rows that are settled in 64 bits, rows too large or
-too small for fp32 squares, more tokens than a grid dimension holds, lengths
+infinities and NaN beside rows that are settled in 64 bits, rows too large
+for fp32 squares, more tokens than a grid dimension holds, lengths
 near 2^31, positions outside the tables, block tables much wider than the
 requests. Bounds as in test_decode_gpu.py unless a test derives its own."""
 
@@ -213,3 +213,44 @@ def test_rows_of_positions_outside_the_tables_are_zero_in_new_outputs(kind, inte
         qo, ko = swa.rope_apply(q, same, rope, pos=pd, interleaved=inter, out=(None, same), workspace=w)
         assert torch.equal(qo, qw) and torch.equal(ko[bad], k[bad]) and torch.equal(ko[~bad], kw[~bad])
     assert swa.swa_attn_check_status(ws) == swa.SWA_ERR_DEVICE_CHECK
+
+
+# ---------------------------------------------------------------------------
+# Rows whose squares pass fp32
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("d,rot,inter", [(128, 128, False), (128, 48, True), (64, 0, False)])
+@pytest.mark.parametrize("power,eps", [(100, 1e-6), (70, 0.0), (115, 1e-6)])
+def test_keys_whose_squares_pass_fp32_are_normed(kind, d, rot, inter, power, eps):
+    T, Hkv, page = 23, 3, 32
+    k = randn(1, 1, T, Hkv, d, dtype=DT[kind])
+    k[0, 1::2] *= 2.0 ** power               # beside rows of ordinary size
+    tabs = None if not rot else tuple(torch.tensor(x, dtype=torch.float32) for x in dec.rope_tables(T, rot))
+    gk = 1 + 0.1 * randn(3, d)
+    cache = random_cache(9, 2, Hkv, page, d).to(dev())
+    slot = torch.arange(T, device=dev()).view(1, T)
+    swa.kv4_append(cache, k.to(dev()), randn(2, 1, T, Hkv, d, dtype=DT[kind]).to(dev()), slot, interleaved=inter, eps=eps,
+                   rope=None if tabs is None else tuple(t.to(dev()) for t in tabs), gk=gk.to(dev()))
+    kw = {} if tabs is None else dict(cos=f64(tabs[0])[:T], sin=f64(tabs[1])[:T], interleaved=inter)
+    want, _, _, _ = dec.append_rows(f64(k)[0], f64(k)[0], f64(gk), float(np.float32(eps)), **kw)
+    assert np.abs(want[1]).max() > 1         # normed, not vanished
+    for t in range(T):
+        sc = scales_of(cache.cpu(), page, t)
+        nk, _ = numbers_of(cache.cpu(), page, t)
+        check_held(want[t], nk, sc[0, :, :, 0], sc[0, :, :, 1], False, np.abs(want[t]).max(-1))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_an_infinite_key_entry_stays_in_its_group(kind):
+    # x / inf = 0 beside it, inf / inf = NaN where it is
+    d, page = 128, 16
+    k = randn(1, 1, 4, 1, d, dtype=DT[kind])
+    k[0, 1, 0, 5], k[0, 2, 0, 100] = math.inf, -math.inf
+    cache = random_cache(1, 1, 1, page, d).to(dev())
+    slot = torch.arange(4, device=dev()).view(1, 4)
+    swa.kv4_append(cache, k.to(dev()), k.to(dev()), slot)
+    kr = swa.kv4_read(cache, slot, dtype=torch.float32)[0][0, :, 0].cpu()
+    assert torch.isnan(kr[1, :64]).all() and torch.all(kr[1, 64:] == 0)
+    assert torch.isnan(kr[2, 64:]).all() and torch.all(kr[2, :64] == 0)
+    assert torch.isfinite(kr[[0, 3]]).all()
