@@ -231,7 +231,20 @@ __device__ __forceinline__ void query_row(const AttnArgs& a, const elem_t* q, in
 #pragma unroll
     for (int i = 0; i < E; ++i) ss = fmaf(x[i], x[i], ss);
   }
-  const float mul = rsqrtf(warp_sum(ss) / D + a.eps) * (a.scale * 1.4426950408889634f);
+  ss = warp_sum(ss);
+  float eps = a.eps;
+  if (ss == INFINITY) {      // the squares pass fp32: the same of 2^-80 of the row
+    constexpr float kDown = 0x1p-80f;
+    ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      x[i] *= kDown;
+      ss = fmaf(x[i], x[i], ss);
+    }
+    ss = warp_sum(ss);
+    eps = eps * kDown * kDown;
+  }
+  const float mul = rsqrtf(ss / D + eps) * (a.scale * 1.4426950408889634f);
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < E; ++i) {

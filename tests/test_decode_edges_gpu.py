@@ -254,3 +254,23 @@ def test_an_infinite_key_entry_stays_in_its_group(kind):
     assert torch.isnan(kr[1, :64]).all() and torch.all(kr[1, 64:] == 0)
     assert torch.isnan(kr[2, 64:]).all() and torch.all(kr[2, :64] == 0)
     assert torch.isfinite(kr[[0, 3]]).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("d,rot,inter", [(128, 128, False), (64, 32, True), (64, 0, False)])
+@pytest.mark.parametrize("power,eps", [(100, 1e-6), (70, 0.0), (115, 1e-6)])
+def test_queries_whose_squares_pass_fp32_are_normed(kind, d, rot, inter, power, eps):
+    lens, Hkv, page = [90, 5], 2, 32
+    cache, table, rows = build_cache(lens, Hkv, d, page)
+    q = randn(2, 2, 8, d, dtype=DT[kind])
+    big = q.clone()
+    big[:, 1::2] *= 2.0 ** power
+    tabs = None if not rot else tuple(torch.tensor(x, dtype=torch.float32) for x in dec.rope_tables(90, rot))
+    o, lse = swa.kv4_attention(cache.to(dev()), big.to(dev()), table.to(dev()), i32(*lens), interleaved=inter, eps=eps,
+                               rope=None if tabs is None else tuple(t.to(dev()) for t in tabs))
+    for b, n in enumerate(lens):
+        kw = {} if tabs is None else dict(cos=f64(tabs[0])[n - 1], sin=f64(tabs[1])[n - 1], interleaved=inter)
+        ro, rl = dec.attend(f64(big)[b], *rows[b], eps=float(np.float32(eps)), **kw)
+        assert np.all(np.abs(f64(lse)[b] - rl) <= 1e-4)
+        tol = HALF[kind] * np.abs(ro) + 1.7e-4 * np.abs(rows[b][1]).max()
+        assert np.all(np.abs(f64(o)[b] - ro) <= tol)
