@@ -37,14 +37,28 @@ struct Refused {};   // not the ordinary case; nothing is launched
 
 PyObject* error_type = nullptr;   // SwaError(status, what); set by raises()
 
+// Lets other Python threads run for its life.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // The library call of a function below: its status, and whether it may have
 // launched.
 struct Call {
   bool launched = false;
   swa_status status = SWA_OK;
-  // These three are decided before a launch. Any other status may come after
+  // Runs f, which allocates outputs and makes the call, both of which may wait
+  // for the device; nothing of Python is used in it. INVALID_ARG, UNSUPPORTED
+  // and WORKSPACE are decided before a launch. Any other status may come after
   // it: SWA_ERR_CUDA also tells of errors that older calls left behind.
-  void operator()(swa_status s) {
+  template <typename F>
+  void operator()(F f) {
+    swa_status s;
+    {
+      Unlocked unlocked;
+      s = f();
+    }
     if (s == SWA_ERR_INVALID_ARG || s == SWA_ERR_UNSUPPORTED || s == SWA_ERR_WORKSPACE) throw Refused{};
     launched = true;
     status = s;
@@ -191,8 +205,12 @@ PyObject* rope_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
     swa_rope_freq f{int_of(a[1]), int_of(a[2]), double_of(a[3]), double_of(a[4]), double_of(a[5]),
                     double_of(a[6]), double_of(a[7]), double_of(a[8])};
     if (rows < 1 || f.rot < 2) throw Refused{};
-    at::Tensor cos = at::empty({rows, f.rot / 2}, on(dev, at::kFloat)), sin = at::empty_like(cos);
-    call(libs[0].tables(&f, first, rows, cos.data_ptr<float>(), sin.data_ptr<float>(), stream_now(dev)));
+    at::Tensor cos, sin;
+    call([&] {
+      cos = at::empty({rows, f.rot / 2}, on(dev, at::kFloat));
+      sin = at::empty_like(cos);
+      return libs[0].tables(&f, first, rows, cos.data_ptr<float>(), sin.data_ptr<float>(), stream_now(dev));
+    });
     return pair(cos, sin);
   });
 }
@@ -227,24 +245,23 @@ PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
     // Outputs allocated here hold nothing yet: the call is told so, or, beside
     // one of the caller's, they begin as zeros where a row may be left out.
     const bool fresh = qo == nullptr && ko == nullptr, zeros = !fresh && pos != nullptr;
-    at::Tensor qt, kt;
-    if (has_q && qo == nullptr) {
-      if (a[7] != Py_None) throw Refused{};
-      qt = zeros ? at::zeros_like(tensor(a[0])) : at::empty_like(tensor(a[0]));
-      qo = qt.data_ptr();
-    } else if (has_q) {
-      qt = tensor(a[7]);
-    }
-    if (has_k && ko == nullptr) {
-      if (a[8] != Py_None) throw Refused{};
-      kt = zeros ? at::zeros_like(tensor(a[1])) : at::empty_like(tensor(a[1]));
-      ko = kt.data_ptr();
-    } else if (has_k) {
-      kt = tensor(a[8]);
-    }
+    if ((qo == nullptr && a[7] != Py_None) || (ko == nullptr && a[8] != Py_None)) throw Refused{};
     const int mode = (PyObject_IsTrue(a[6]) ? 1 : 0) | (fresh ? SWA_ROPE_NEW_OUTPUTS : 0);
-    swa_params p{small(B), small(T), small(Hq), small(Hkv), small(d), -1, 1, 0.f, 0.f, 0.f, 0};
-    call(libs[kind].apply(&p, &r, pos, q, k, qo, ko, mode, ws.at, ws.bytes, stream_now(dev)));
+    const swa_params p{small(B), small(T), small(Hq), small(Hkv), small(d), -1, 1, 0.f, 0.f, 0.f, 0};
+    const at::Tensor none;
+    const at::Tensor &qi = has_q ? tensor(a[0]) : none, &ki = has_k ? tensor(a[1]) : none;
+    at::Tensor qt = has_q && qo != nullptr ? tensor(a[7]) : none, kt = has_k && ko != nullptr ? tensor(a[8]) : none;
+    call([&] {
+      if (has_q && qo == nullptr) {
+        qt = zeros ? at::zeros_like(qi) : at::empty_like(qi);
+        qo = qt.data_ptr();
+      }
+      if (has_k && ko == nullptr) {
+        kt = zeros ? at::zeros_like(ki) : at::empty_like(ki);
+        ko = kt.data_ptr();
+      }
+      return libs[kind].apply(&p, &r, pos, q, k, qo, ko, mode, ws.at, ws.bytes, stream_now(dev));
+    });
     return pair(qt, kt);
   });
 }
@@ -264,13 +281,20 @@ PyObject* kv4_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto* fr = static_cast<const int32_t*>(at_(a[3], at::kInt, dev, {free.numel()}));
     const auto* hd = static_cast<const int32_t*>(at_(a[4], at::kInt, dev, {1}));
     const Ws ws = ws_of(a[8], dev);
-    const auto i32 = on(dev, at::kInt);
-    at::Tensor slot = at::empty({N}, on(dev, at::kLong)), pos = at::empty({N}, i32), row = at::empty({N}, i32),
-               cu = at::empty({B + 1}, i32), lens_out = at::empty({B}, i32), head = at::empty({1}, i32);
-    call(libs[0].plan(int_of(a[6]), int_of(a[5]), small(B), small(table.size(1)), l, nl, tb, fr, small(free.numel()), hd,
-                     static_cast<int>(N), slot.data_ptr<int64_t>(), pos.data_ptr<int32_t>(), row.data_ptr<int32_t>(),
-                     cu.data_ptr<int32_t>(), lens_out.data_ptr<int32_t>(), head.data_ptr<int32_t>(), ws.at, ws.bytes,
-                     stream_now(dev)));
+    const int page = int_of(a[5]), n_pages = int_of(a[6]), b = small(B), width = small(table.size(1)), n_free = small(free.numel());
+    at::Tensor slot, pos, row, cu, lens_out, head;
+    call([&] {
+      const auto i32 = on(dev, at::kInt);
+      slot = at::empty({N}, on(dev, at::kLong));
+      pos = at::empty({N}, i32);
+      row = at::empty({N}, i32);
+      cu = at::empty({B + 1}, i32);
+      lens_out = at::empty({B}, i32);
+      head = at::empty({1}, i32);
+      return libs[0].plan(n_pages, page, b, width, l, nl, tb, fr, n_free, hd, static_cast<int>(N), slot.data_ptr<int64_t>(),
+                          pos.data_ptr<int32_t>(), row.data_ptr<int32_t>(), cu.data_ptr<int32_t>(), lens_out.data_ptr<int32_t>(),
+                          head.data_ptr<int32_t>(), ws.at, ws.bytes, stream_now(dev));
+    });
     PyObject* dict = PyDict_New();
     const struct { const char* name; const at::Tensor& t; } out[] = {
         {"slot", slot}, {"pos", pos}, {"row", row}, {"cu", cu}, {"lens", lens_out}, {"free_head", head}};
@@ -313,10 +337,12 @@ PyObject* kv4_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       gate = static_cast<const float*>(at_(a[12], at::kFloat, dev, {B, T, c.Hkv}));
     }
     const Ws ws = ws_of(a[14], dev);
-    swa_params p{small(B), small(T), c.Hkv, c.Hkv, c.d, -1, 1, 0.f, static_cast<float>(double_of(a[9])),
-                 static_cast<float>(double_of(a[13])), vocab};
-    call(libs[kind].append(&p, nullptr, &c.c, rope ? &r : nullptr, ka, va, gk, ve, tok, gate, pos, slot, ws.at, ws.bytes,
-                          stream_now(dev)));
+    const swa_params p{small(B), small(T), c.Hkv, c.Hkv, c.d, -1, 1, 0.f, static_cast<float>(double_of(a[9])),
+                       static_cast<float>(double_of(a[13])), vocab};
+    call([&] {
+      return libs[kind].append(&p, nullptr, &c.c, rope ? &r : nullptr, ka, va, gk, ve, tok, gate, pos, slot, ws.at, ws.bytes,
+                               stream_now(dev));
+    });
     Py_RETURN_TRUE;
   });
 }
@@ -332,10 +358,13 @@ PyObject* kv4_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int kind = kind_of(PyObject_IsTrue(a[2]) ? at::kFloat : at::kBFloat16);
     const auto* slot = static_cast<const int64_t*>(at_(a[1], at::kLong, dev, s.sizes()));
     const Ws ws = ws_of(a[3], dev);
-    at::Tensor k = at::empty({s.size(0), s.size(1), c.Hkv, c.d}, on(dev, kind ? at::kFloat : at::kBFloat16)),
-               v = at::empty_like(k);
-    swa_params p{small(s.size(0)), small(s.size(1)), c.Hkv, c.Hkv, c.d, -1, 1, 0.f, 0.f, 0.f, 0};
-    call(libs[kind].read(&p, &c.c, slot, k.data_ptr(), v.data_ptr(), ws.at, ws.bytes, stream_now(dev)));
+    const swa_params p{small(s.size(0)), small(s.size(1)), c.Hkv, c.Hkv, c.d, -1, 1, 0.f, 0.f, 0.f, 0};
+    at::Tensor k, v;
+    call([&] {
+      k = at::empty({p.B, p.T, c.Hkv, c.d}, on(dev, kind ? at::kFloat : at::kBFloat16));
+      v = at::empty_like(k);
+      return libs[kind].read(&p, &c.c, slot, k.data_ptr(), v.data_ptr(), ws.at, ws.bytes, stream_now(dev));
+    });
     return pair(k, v);
   });
 }
@@ -358,11 +387,16 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const bool rope = rope_of(a[4], a[5], a[6], dev, r);
     const auto* gq = static_cast<const float*>(at_(a[7], at::kFloat, dev, {c.d}));
     const Ws ws = ws_of(a[11], dev);
-    swa_params p{small(B), 1, small(Hq), c.Hkv, c.d, int_of(a[8]), 1, static_cast<float>(double_of(a[9])),
-                 static_cast<float>(double_of(a[10])), 0.f, 0};
-    at::Tensor o = at::empty_like(q), lse = at::empty({B, Hq}, on(dev, at::kFloat));
-    call(libs[kind].attn(&p, nullptr, &c.c, rope ? &r : nullptr, qa, gq, ta, small(width), la, o.data_ptr(),
-                        lse.data_ptr<float>(), ws.at, ws.bytes, stream_now(dev)));
+    const swa_params p{small(B), 1, small(Hq), c.Hkv, c.d, int_of(a[8]), 1, static_cast<float>(double_of(a[9])),
+                       static_cast<float>(double_of(a[10])), 0.f, 0};
+    const int max_pages = small(width);
+    at::Tensor o, lse;
+    call([&] {
+      o = at::empty_like(q);
+      lse = at::empty({B, Hq}, on(dev, at::kFloat));
+      return libs[kind].attn(&p, nullptr, &c.c, rope ? &r : nullptr, qa, gq, ta, max_pages, la, o.data_ptr(), lse.data_ptr<float>(),
+                             ws.at, ws.bytes, stream_now(dev));
+    });
     return pair(o, lse);
   });
 }

@@ -3,6 +3,10 @@ with functions bound in place of the library's: a call is made once, its errors
 are told, and other Python threads run beside it. No call here fails on the GPU."""
 
 import ctypes
+import os
+import subprocess
+import threading
+import time
 
 import pytest
 import torch
@@ -77,3 +81,38 @@ def test_rotation_in_place_that_meets_an_older_error_turns_once(bind):
     with pytest.raises(swa.SwaError):
         swa.rope_apply(q, k, rope, out=(q, k))
     assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+
+
+STUB = r"""
+#include <unistd.h>
+volatile int entered = 0, go = 0, waited = 0;
+int stub(const void* a, int b, int c, void* d, void* e, void* f) {
+  entered = 1;
+  for (int i = 0; i < 5000 && !go; ++i) usleep(1000);   /* at most 5 s */
+  waited = go ? 1 : -1;
+  return 0;
+}
+"""
+
+
+def test_other_threads_run_beside_a_call(bind, tmp_path):
+    # a call that waits, as one does on a full launch queue, until another
+    # Python thread has let it go on
+    (tmp_path / "stub.c").write_text(STUB)
+    so = os.fspath(tmp_path / "stub.so")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-O1", "-o", so, os.fspath(tmp_path / "stub.c")], check=True)
+    lib = ctypes.CDLL(so)
+    entered, go, waited = (ctypes.c_int.in_dll(lib, n) for n in ("entered", "go", "waited"))
+    bind("swa_rope_tables", lib.stub)
+
+    def let_go():
+        while not entered.value and time.monotonic() < end:
+            time.sleep(0.001)
+        go.value = 1
+
+    end = time.monotonic() + 20
+    t = threading.Thread(target=let_go)
+    t.start()
+    swa.rope_tables(8, 64)
+    t.join()
+    assert waited.value == 1, "the call held the interpreter"
