@@ -15,7 +15,7 @@ import torch
 
 import sliding_window_gqa_qk_gb300 as swa
 from oracle import decode as dec
-from test_decode_gpu import (DT, EPS, HALF, U, build_cache, check_attention, check_held, dev, f64, gen, numbers_of, randn,
+from test_decode_gpu import (DT, EPS, HALF, U, build_cache, check_held, dev, f64, gen, numbers_of, randn,
                              random_cache, scales_of)
 
 pytestmark = pytest.mark.gpu
@@ -274,3 +274,114 @@ def test_queries_whose_squares_pass_fp32_are_normed(kind, d, rot, inter, power, 
         assert np.all(np.abs(f64(lse)[b] - rl) <= 1e-4)
         tol = HALF[kind] * np.abs(ro) + 1.7e-4 * np.abs(rows[b][1]).max()
         assert np.all(np.abs(f64(o)[b] - ro) <= tol)
+
+
+# ---------------------------------------------------------------------------
+# Tighter bounds
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rot,rows,first,kw", [
+    (128, 3000, 0, {}), (64, 500, 2 ** 20, {}), (16, 4000, 12345, {}), (128, 700, 1000, dict(base=500000.0)),
+    (96, 700, 4000, dict(scaling="ntk", factor=8.0)), (64, 900, 65536, dict(scaling="by_parts", factor=16.0, orig_len=4096))])
+def test_tables_keep_their_polynomials_error(rot, rows, first, kw):
+    """With u = 2^-24 and |x| <= pi/4 the reduced angle: cutting the angle to 32
+    bits costs 2 pi 2^-32 = 0.025 u; the integer's rounding, the constant's and
+    the product's 3 u x, of which cosine sees 3 u x sin x <= 1.67 u and sine 3 u
+    x cos x <= 1.67 u; Taylor's remainder x^10 / 10! = 2.5e-8 = 0.42 u (cosine),
+    x^11 / 11! = 0.03 u (sine); x x rounded: y / 2 u = 0.31 u; the polynomial's
+    last steps 0.5 u (the result lies within [1/2, 1]) + 0.2 u for the ones
+    before. Sum 3.2 u. The oracle's own angle is off by its 2^-53 part."""
+    cos, sin = swa.rope_tables(rows, rot, first=first, **kw)
+    rc, rs = dec.rope_tables(rows, rot, first=first, **kw)
+    tol = 3.2 * U + (first + rows) * 2.0 ** -52
+    assert np.abs(f64(cos) - rc).max() <= tol
+    assert np.abs(f64(sin) - rs).max() <= tol
+
+
+def test_attention_in_fp32_keeps_the_third_term_of_p():
+    """Two keys, logits so small (softmax_scale 2^-9) that their error does not
+    count: the products of a logit sum to at most 0.15 in absolute value, so
+    (see the attention's bound) it is off by 0.15 * 2.6e-6 = 4e-7, and by 2^-22
+    through exp2 (2 ulp) = 2.4e-7; both enter o twice (numerator and sum). P
+    times a step as three bf16 terms keeps 2^-24. The matrix instructions add
+    three terms to sums that are rounded down to 2^-23 of them at most, four
+    times; six fp32 roundings follow. Together 2 * 6.4e-7 + 4 * 2^-23 + 8 * 2^-24
+    = 2.3e-6 of sum_j p_j (|s (n - 8)| + |z|) / sum_j p_j. Two terms alone would
+    leave up to 2^-17 = 7.6e-6."""
+    B, Hq, d, page = 64, 4, 64, 16
+    cache, table, rows = build_cache([2] * B, 1, d, page)
+    sc = cache[..., 16 * d:].view(torch.bfloat16).view(-1, 1, 1, 2, 16, 1, 2)
+    for b in range(B):        # centres 0, numbers far from 8: the step's term is all there is
+        pg = int(table[b, 0])
+        sc[pg, 0, 0, 1, :2, 0, 1] = 0.0
+        rows[b] = (rows[b][0], np.array([dec.read_row(cache.numpy()[pg:pg + 1], page, j, 0)[1] for j in range(2)])[:, None])
+    q = randn(5, B, Hq, d)
+    o, lse = swa.kv4_attention(cache.to(dev()), q.to(dev()), table.to(dev()), i32(*[2] * B), softmax_scale=2.0 ** -9)
+    worst = 0.0
+    for b in range(B):
+        ro, rl = dec.attend(f64(q)[b], *rows[b], scale=2.0 ** -9)
+        z = dec.rms_norm(f64(q)[b], None, EPS) @ rows[b][0][:, 0].T * 2.0 ** -9
+        p = np.exp(z - z.max(-1, keepdims=True))
+        weight = (p / p.sum(-1, keepdims=True)) @ np.abs(rows[b][1][:, 0])
+        worst = max(worst, float((np.abs(f64(o)[b] - ro) / np.maximum(weight, 1e-30)).max()))
+        assert np.abs(f64(lse)[b] - rl).max() <= 1e-6
+    assert worst <= 2.5e-6, worst
+
+
+# ---------------------------------------------------------------------------
+# Block tables wider than the requests, and the largest batch
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("B,width,window", [(1, 8192, -1), (32, 4096, -1), (3, 8192, 700)])
+def test_attention_with_a_table_much_wider_than_the_requests(B, width, window):
+    # the parts of a request follow the table's width; its result is that of a
+    # table of its own width to the rounding of the sums
+    d, page, Hkv, Hq = 128, 16, 2, 8
+    lens = [int(n) for n in np.random.default_rng(B).integers(1, 3000, B)]
+    lens[0] = 3000
+    held = [-(-n // page) for n in lens]
+    cache = random_cache(1, sum(held), Hkv, page, d)
+    sc = cache[..., 16 * d:].view(torch.bfloat16)
+    sc[..., 0::2], sc[..., 1::2] = 0.2, (0.2 * randn(4, *sc[..., 1::2].shape)).bfloat16()
+    ids, at = torch.randperm(sum(held), generator=gen(2)).int(), 0
+    wide = torch.full((B, width), -1, dtype=torch.int32)
+    for b in range(B):
+        wide[b, :held[b]] = ids[at:at + held[b]]
+        at += held[b]
+    cd, q = cache.to(dev()), randn(3, B, Hq, d).to(dev())
+    ws = swa.new_kv4_workspace(cd, B, Hq, max_pages=width, window=window, kind="fp32")
+    got = swa.kv4_attention(cd, q, wide.to(dev()), i32(*lens), window=window, workspace=ws)
+    want = swa.kv4_attention(cd, q, wide[:, :max(held)].contiguous().to(dev()), i32(*lens), window=window, workspace=ws)
+    assert swa.swa_attn_check_status(ws, kind="fp32") == swa.SWA_OK
+    # the same logits bit for bit; exp2 over other maxima (2^-22) and sums of 3000
+    # terms in another order, 24 roundings deep on either side, of nothing past 16
+    for a, b in zip(got, want):
+        assert (a - b).abs().max().item() <= 24 * 2 * U * 16
+    slot = (wide[0].long().clamp(min=0)[:, None] * page + torch.arange(page)).view(1, -1)[:, :lens[0]].contiguous().to(dev())
+    k, v = (x[0].double().cpu().numpy() for x in swa.kv4_read(cd, slot, dtype=torch.float32))
+    ro, rl = dec.attend(f64(q)[0], k, v, window=window)
+    assert np.abs(f64(got[1])[0] - rl).max() <= 1e-4
+    assert np.all(np.abs(f64(got[0])[0] - ro) <= U * np.abs(ro) + 1.7e-4 * np.abs(v).max())
+
+
+def test_attention_of_the_largest_batch():
+    # 65535 rows of B, eight distinct ones repeated
+    lens = [33, 1, 0, 64, 17, 90, 16, 5]
+    cache, table, rows = build_cache(lens, 1, 64, 16)
+    B = 65535
+    at = torch.arange(B) % 8
+    q = randn(2, 8, 1, 64, dtype=torch.bfloat16)
+    cd = cache.to(dev())
+    o, lse = swa.kv4_attention(cd, q[at].to(dev()), table[at].to(dev()), torch.tensor(lens, dtype=torch.int32)[at].to(dev()))
+    small = swa.kv4_attention(cd, q.to(dev()), table.to(dev()), i32(*lens))
+    for b in range(8):
+        n = lens[b]
+        if n:
+            ro, rl = dec.attend(f64(q)[b], *rows[b])
+            assert np.abs(f64(small[1])[b] - rl).max() <= 1e-4
+            assert np.all(np.abs(f64(small[0])[b] - ro) <= 2.0 ** -8 * np.abs(ro) + 1.7e-4 * np.abs(rows[b][1]).max())
+    at = at.to(dev())
+    assert torch.equal(o, small[0][at]) and torch.equal(lse, small[1][at])
+    with pytest.raises(swa.SwaError):
+        swa.kv4_attention(cd, q[torch.zeros(65536, dtype=torch.long)].to(dev()), table[:1].expand(65536, -1).contiguous().to(dev()),
+                          torch.ones(65536, dtype=torch.int32, device=dev()))

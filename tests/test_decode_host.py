@@ -2,7 +2,9 @@
 build of the short way (csrc/py_fast.cpp) is taken; sizes that the calls take.
 Nothing here runs on a GPU."""
 
+import ctypes
 import os
+import re
 import subprocess
 import sys
 
@@ -91,3 +93,37 @@ def test_new_outputs_of_a_rotation_are_no_inputs():
         assert apply(A, None, 2 * A, None, mode) == plain
     for mode in (2, 3, new + 2, 8, -1):
         assert apply(A, A, 2 * A, 3 * A, mode) == swa.SWA_ERR_INVALID_ARG
+
+
+# ---------------------------------------------------------------------------
+# Arithmetic
+# ---------------------------------------------------------------------------
+
+OVER_15 = r"""
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+%s
+static float at(uint32_t bits) { float f; memcpy(&f, &bits, 4); return f; }
+/* wrong quotients of every fp32 number of `n` binades from exponent e0 on */
+extern "C" long wrong(int e0, int n) {
+  long bad = 0;
+  for (uint32_t b = (uint32_t)e0 << 23; b < (uint32_t)(e0 + n) << 23; ++b) bad += over_15(at(b)) != at(b) / 15.0f;
+  return bad;
+}
+"""
+
+
+def test_a_span_over_15_is_correctly_rounded(tmp_path):
+    # the kernel's own function, compiled for the host: every span of the
+    # binades that a step's fraction can come from (the quotient's takes in
+    # two), at the ends of the range of steps that do not count as 0 and at 1
+    source = open(os.path.join(ROOT, "sliding_window_gqa_qk_gb300", "csrc", "kv4.cuh")).read()
+    code = re.search(r"__device__ __forceinline__ (float over_15\(float x\) \{.*?\n\})", source, re.S).group(1)
+    (tmp_path / "over.cpp").write_text(OVER_15 % code)
+    so = os.fspath(tmp_path / "over.so")
+    subprocess.run(["g++", "-O2", "-ffp-contract=off", "-shared", "-fPIC", "-o", so, os.fspath(tmp_path / "over.cpp")], check=True)
+    wrong = ctypes.CDLL(so).wrong
+    wrong.restype = ctypes.c_long
+    for e0 in (127 - 116, 126, 253):       # 15e-36 is 2^-115.7
+        assert wrong(e0, 2) == 0, e0
