@@ -391,16 +391,6 @@ def swa_block_bwd(p, ex, w, x, gq, gk, ve, tok, dout, dx, dwq, dwk, dwv, dwo, dg
         _ptr(dve), _ptr(ws), n, _stream(stream)))
 
 
-def make_rope(tables, interleaved: bool = False) -> Optional[swa_rope]:
-    """swa_rope from (cos, sin), fp32 device tensors [rows, rot/2]; None: none."""
-    if tables is None:
-        return None
-    cos, sin = tables
-    if cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.dim() != 2 or cos.shape != sin.shape:
-        raise ValueError("rotary tables are two fp32 tensors [rows, rot/2]")
-    return swa_rope(_ptr(cos), _ptr(sin), cos.shape[0], 2 * cos.shape[1], int(bool(interleaved)))
-
-
 def _ref(s):
     return None if s is None else ctypes.byref(s)
 
