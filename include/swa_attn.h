@@ -437,7 +437,8 @@ typedef struct {
  *            tokens are set to zero
  *   workspace  at least its 256-byte header, where device checks are reported
  *            (swa_attn_check_status); NULL: they are not
- * Sums are fp32, rounded once to elem.
+ * Sums are fp32, rounded once to elem. Limit: Hq <= 65535, here and in the
+ * append, the read and swa_kv4_cache_size, which take any number of tokens B * T.
  */
 #define SWA_ROPE_NEW_OUTPUTS 4
 swa_status swa_rope_apply(const swa_params* p, const swa_rope* r, const int32_t* pos, const void* q,
@@ -460,9 +461,11 @@ swa_status swa_rope_apply(const swa_params* p, const swa_rope* r, const int32_t*
  * A number n = 0..15 of 64-channel group g stands for s (n - 8) + z, where
  *   s = bf16((max - min) / 15), z = bf16(min + 8 s) over the group,
  *   n = floor((x - z) / s + 8.5) kept within 0..15, 8 where s = 0.
- * (A group that holds an infinity or a NaN, or whose span overflows fp32, is
- * held as NaN; steps below 1e-36 count as 0.) Low nibble first, the numbers of
- * a row are in the order
+ * Keys, and values with an embedding, come out of fp32 arithmetic: the z of one
+ * may be bf16's other neighbour of min + 8 s where no number depends on it. (A
+ * group that holds an infinity or a NaN, or whose span overflows fp32, is held
+ * as NaN; steps below 1e-36 count as 0.) Low nibble first, the numbers of a row
+ * are in the order
  *   keys    [j 0..3][g][i 0..15]:          channel 64 g + 16 j + i
  *   values  [r 0..7][g][u 0..1][token of the pair][i 0..3]:
  *                                          channel 64 g + 8 r + 4 u + i
@@ -522,7 +525,8 @@ swa_status swa_kv4_plan(int n_pages, int page, int B, int max_pages, const int32
  * skipped; tokens with a slot outside the cache or (with r) a position
  * outside the tables are skipped and reported; a token id outside [0, vocab)
  * is reported and adds no embedding. Two tokens with the same slot in one
- * call leave that slot's content undefined.
+ * call leave that slot's content undefined. A key whose squares pass fp32's
+ * range is normed all the same.
  */
 swa_status swa_kv4_append(const swa_params* p, const swa_extras* ex, const swa_kv4_cache* c,
                           const swa_rope* r, const void* k, const void* v, const float* gk,
@@ -544,7 +548,7 @@ swa_status swa_kv4_read(const swa_params* p, const swa_kv4_cache* c, const int64
  * (r, NULL: not), normed and multiplied by gq; it sees the cache's keys j with
  * lens[b] - 1 - window <= j < lens[b] (window -1: all). p->T must be 1 and
  * p->causal 1, B * Hq at most 65535; window, softmax_scale and eps as in
- * swa_attn_fwd.
+ * swa_attn_fwd. gq is 16-byte aligned.
  *   table    int32 [B][max_pages]; entries behind ceil(lens[b] / page) and in
  *            front of the window are not read
  *   lens     int32 [B]; 0: the request's rows of o are 0 and of lse -infinity

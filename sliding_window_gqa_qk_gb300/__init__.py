@@ -806,7 +806,9 @@ def kv4_append(cache, k, v, slot, *, pos=None, rope=None, interleaved: bool = Fa
     """Writes new keys and values k, v [B, T, Hkv, d] (as projected: not yet
     rotated, normed or mixed) into the cache at slot int64 [B, T]; -1 skips a
     token. Rotary, QK-norm gain, value embedding and gate as in
-    attention_forward, with the rotation at pos int32 [B, T] (None: t)."""
+    attention_forward, with the rotation at pos int32 [B, T] (None: t). A token
+    whose slot or position is out of range is skipped, which only a
+    ``workspace`` tells (swa_attn_check_status)."""
     if _fast is not None and stream is None and gate_w is None:
         if _fast.kv4_append(cache, k, v, slot, pos, *(_NO_ROPE if rope is None else rope), interleaved, gk, eps, ve, tok, ve_gate, ve_scale,
                             workspace):
@@ -850,7 +852,8 @@ def kv4_append(cache, k, v, slot, *, pos=None, rope=None, interleaved: bool = Fa
 def kv4_read(cache, slot, *, dtype=torch.bfloat16, workspace=None, stream=None):
     """k, v = kv4_read(cache, slot): the rows that slot int64 [B, T] holds, as
     ``dtype`` (bf16 or fp32) [B, T, Hkv, d]; keys are rotated and normed.
-    Rows of slot -1 are zero."""
+    Rows of slot -1, and of slots outside the cache (reported in
+    ``workspace``), are zero."""
     if _fast is not None and stream is None and (dtype is _BF16 or dtype is _F32):
         r = _fast.kv4_read(cache, slot, dtype is _F32, workspace)
         if r is not None:
@@ -882,7 +885,8 @@ def kv4_attention(cache, q, table, lens, *, rope=None, interleaved: bool = False
     request's cached keys and values (its own among them), table int32 [B,
     max_pages]. o as q; lse fp32 [B, Hq]. Rotary, gain, window and scale as in
     attention_forward. ``workspace``: from new_kv4_workspace, kept by the
-    caller (one per stream); None: one for this call."""
+    caller (one per stream), where numbers out of range are reported; None: one
+    for this call, and its reports are lost."""
     if _fast is not None and stream is None:
         r = _fast.kv4_attention(cache, q, table, lens, *(_NO_ROPE if rope is None else rope), interleaved, gq, window,
                                 softmax_scale, eps, workspace)

@@ -100,7 +100,9 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 //   - Values of plain layers enter exactly (bf16), and many sit on a border (one
 //     Gaussian value in 450): x, z and s are short numbers. The number found with an approximate
 //     reciprocal is settled by the remainder x - z - n s, which fma gives
-//     exactly (kExact).
+//     exactly (kExact). (x - z itself rounds where x is far smaller than z; that
+//     decides only for a border at 0 and an x within 2^-25 z of it, which goes
+//     up from either side, both numbers being as near.)
 //   - Keys, and values with an embedding, are results of fp32 arithmetic. A
 //     row with an entry or a step closer to a border than that arithmetic is
 //     good for is done again in fp64: the numbers a row is held as then
@@ -128,7 +130,9 @@ __device__ __forceinline__ float bf16_margin(float x, float y) {
   return __uint_as_float(__float_as_uint(x) & 0x7F800000u) * 0.00390625f - fabsf(x - y);   // half a step: 2^(e - 8)
 }
 
-// x / 15 correctly rounded: the product with 1 / 15 and one correction by its remainder.
+// x / 15, correctly rounded where the quotient is a normal number (compared with
+// the division over every fraction, which a power of two does not change): the
+// product with 1 / 15 and one correction by its remainder.
 __device__ __forceinline__ float over_15(float x) {
   const float q = x * (1.0f / 15.0f);
   return fmaf(fmaf(-15.0f, q, x), 1.0f / 15.0f, q);
@@ -339,10 +343,10 @@ __device__ __noinline__ uint32_t mix_f64(const AppendArgs& a, uint32_t row, cons
 // time, key and value together. MIX: a value embedding.
 // It should be bound by memory (4 D bytes in, 18 D / 16 out per row) and is
 // bound by instructions, about 35 per channel and lane: 16384 tokens of 3 heads of
-// 128 take 24.2 us, 1.3 TB/s, of which the steps and centres (computed by all
+// 128 take 24.8 us, 1.3 TB/s, of which the steps and centres (computed by all
 // lanes of a group) are 5.5 us, rotation 2.5, the keys' numbers 2.3, stores 2.1,
 // fp64 rows 0.7. 64 single tokens take 3.0 us, a chain of dependent loads.
-// Blocks of four warps, not persistent: 24.2 us; of eight, eight per SM: 32.
+// Blocks of four warps, not persistent, against eight, eight per SM: 32 us.
 template <int D, bool MIX>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const __grid_constant__ AppendArgs a) {
   using M = RowMap<D>;
@@ -543,8 +547,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) read_kernel(const __grid_const
 // Every block does the whole scan itself (a few thousand requests at most,
 // two integers each, from L2) and keeps it in shared memory, so one launch
 // serves every token and no block waits on another. Latency bounds it: 64
-// requests of one token 5.5 us, 1000 requests of 104,000 tokens 7.7 us (their
-// bytes would take 0.3), 633 requests of one token 7.7 us on 20 blocks and 21.4
+// requests of one token 5.3 us, 1000 requests of 104,000 tokens 7.1 us (their
+// bytes would take 0.3), 633 requests of one token 7.3 us on 20 blocks and 21.4
 // on the one that their tokens fill.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 512;

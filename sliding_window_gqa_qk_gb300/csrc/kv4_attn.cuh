@@ -17,7 +17,9 @@
 //     (16 keys x 8 columns) and O^T += V^T P^T (16 channels x 8 columns). The
 //     operand registers are made straight from the numbers' bits: (x & 15) |
 //     0x6400 is the fp16 number 1024 + n (0x4300: bf16, 128 + n), and one
-//     exact subtraction leaves n - 8. The cache's order of numbers makes a
+//     exact subtraction leaves n - 8 (numbers as the low bits of a float of a
+//     known power of two: Kim, Henry, Fahim and Awadalla 2022, "Who Says
+//     Elephants Can't Run"). The cache's order of numbers makes a
 //     lane's 16 bytes of a row exactly its operand registers, so there is no
 //     exchange between lanes. (tcgen05 takes its operands from shared or
 //     tensor memory: the converted tiles, four times the bytes, would have to
@@ -27,7 +29,11 @@
 //     heads as two terms each: q as fp16 hi + lo (scaled by a power of two
 //     into fp16's range), P as bf16 hi + lo (bf16, because P times a step has
 //     any size). Products of n - 8 with them are exact in the accumulators;
-//     the second terms cost nothing where a group has at most four heads.
+//     the second terms cost nothing where a group has at most four heads. That
+//     is 22 bits of q, whose 2^-22 of a logit is below what the norm's and
+//     the sum's fp32 roundings leave (a third term would be a product more),
+//     and 16 bits of P, far below a bf16 o's 8; an fp32 o's 24 get a third term
+//     of P.
 //   - Scales. s and z of a (token, 64 channels) leave the products:
 //     <q, k> = sum_g s_g <q, n - 8>_g + z_g sum(q)_g, and sum_j p_j v_j =
 //     sum_j (p_j s_j) (n_j - 8) + sum_j p_j z_j, the last one number per group.
