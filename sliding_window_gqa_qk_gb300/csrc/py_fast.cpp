@@ -94,6 +94,11 @@ double double_of(PyObject* o) {
   if (PyErr_Occurred()) throw Refused{};
   return x;
 }
+bool truth_of(PyObject* o) {
+  const int x = PyObject_IsTrue(o);
+  if (x < 0) throw Refused{};
+  return x != 0;
+}
 int kind_of(at::ScalarType t) {
   const int kind = t == at::kBFloat16 ? 0 : (t == at::kFloat ? 1 : -1);
   if (kind < 0 || libs[kind].attn == nullptr) throw Refused{};   // another type, or its library is not loaded yet
@@ -109,7 +114,7 @@ bool rope_of(PyObject* cos, PyObject* sin, PyObject* interleaved, int dev, swa_r
   if (r.sin == nullptr) throw Refused{};
   r.rows = small(c.size(0));
   r.rot = small(2 * c.size(1));
-  r.interleaved = PyObject_IsTrue(interleaved);
+  r.interleaved = truth_of(interleaved);
   return true;
 }
 struct Ws {
@@ -246,7 +251,7 @@ PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
     // one of the caller's, they begin as zeros where a row may be left out.
     const bool fresh = qo == nullptr && ko == nullptr, zeros = !fresh && pos != nullptr;
     if ((qo == nullptr && a[7] != Py_None) || (ko == nullptr && a[8] != Py_None)) throw Refused{};
-    const int mode = (PyObject_IsTrue(a[6]) ? 1 : 0) | (fresh ? SWA_ROPE_NEW_OUTPUTS : 0);
+    const int mode = (truth_of(a[6]) ? 1 : 0) | (fresh ? SWA_ROPE_NEW_OUTPUTS : 0);
     const swa_params p{small(B), small(T), small(Hq), small(Hkv), small(d), -1, 1, 0.f, 0.f, 0.f, 0};
     const at::Tensor none;
     const at::Tensor &qi = has_q ? tensor(a[0]) : none, &ki = has_k ? tensor(a[1]) : none;
@@ -355,7 +360,7 @@ PyObject* kv4_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const CacheDims c = cache_of(a[0], dev);
     const at::Tensor& s = tensor(a[1]);
     if (s.dim() != 2) throw Refused{};
-    const int kind = kind_of(PyObject_IsTrue(a[2]) ? at::kFloat : at::kBFloat16);
+    const int kind = kind_of(truth_of(a[2]) ? at::kFloat : at::kBFloat16);
     const auto* slot = static_cast<const int64_t*>(at_(a[1], at::kLong, dev, s.sizes()));
     const Ws ws = ws_of(a[3], dev);
     const swa_params p{small(s.size(0)), small(s.size(1)), c.Hkv, c.Hkv, c.d, -1, 1, 0.f, 0.f, 0.f, 0};

@@ -116,3 +116,15 @@ def test_other_threads_run_beside_a_call(bind, tmp_path):
     swa.rope_tables(8, 64)
     t.join()
     assert waited.value == 1, "the call held the interpreter"
+
+
+def test_an_argument_without_a_truth_value_stops_the_call(bind):
+    made = []
+    bind("swa_rope_apply", lambda *a: made.append(1) or swa.SWA_OK)
+    rope = swa.rope_tables(9, 64)
+    q = randn(1, 1, 9, 2, 64, dtype=torch.bfloat16).to(dev())
+    before = q.clone()
+    for kw in (dict(inverse=torch.ones(2)), dict(interleaved=torch.ones(2))):
+        with pytest.raises(RuntimeError, match="ambiguous"):
+            swa.rope_apply(q, None, rope, out=(q, None), **kw)
+    assert not made and torch.equal(q, before)
