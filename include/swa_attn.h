@@ -576,6 +576,118 @@ swa_status swa_kv4_attn(const swa_params* p, const swa_extras* ex, const swa_kv4
                         size_t ws_bytes, void* stream);
 
 /*
+ * Several drafted tokens of a request at once (speculative decoding): a tree of
+ * them, each the continuation of its parent. A step's tokens lie one request
+ * behind the other, as swa_kv4_plan lays them out: those of request b are rows
+ * cu[b] .. cu[b + 1] - 1 (at most max_new, 1 .. 64), their slots are the last ones
+ * of its lens[b], in order. The rest of lens[b] is its context. Rows behind
+ * cu[B] are padding.
+ *
+ * swa_kv4_tree: what the tokens see, and where they stand, from their parents.
+ *   parent  int32 [n_tokens], the index of the token's parent among its request's
+ *           (in front of it), or -1: it follows the context
+ *   pos     int32 [n_tokens]: the context's length and the token's depth. Both
+ *           swa_kv4_append (with the plan's slots) and the attention rotate there.
+ *   seen    int64 [n_tokens]: bit t set: the token sees the request's token t
+ *           (itself and those above it)
+ * Padding, tokens whose parent is not in front of them, those below these, and
+ * the tokens of a request that is refused get seen 0 and pos 0; all but the padding
+ * are reported. A request is refused when it has more than max_new tokens, or
+ * more than lens[b], or when lens[b] is negative; where cu itself is not
+ * plausible (negative, falling, beyond n_tokens), its rows are not touched.
+ *
+ * swa_kv4_tree_attn: their attention; q [n_tokens, Hq, d] is rotated at pos,
+ * normed and multiplied by gq as in swa_kv4_attn, whose arguments the others are
+ * (p->T must be 1; p->B counts requests). A token sees its whole context and the
+ * drafted tokens of seen (bits behind the request's last token count nothing),
+ * both only where their position is at least pos - window. seen and pos need not
+ * come from a tree. A row of seen 0 sees nothing, not even the context: o is 0, lse
+ * -infinity, as for padding. So are, and are reported, rows whose position lies
+ * in front of the context's end or outside the rotary tables, and those of refused
+ * requests (as above, or lens[b] > max_pages * page). Keys of a page outside
+ * [0, n_pages) are left out and reported. What a token does not see changes
+ * nothing of its row, a NaN even. The workspace is that of swa_kv4_attn
+ * (swa_kv4_workspace_size, and what is said there of sharing one). Limit: B * Hq
+ * at most 65535.
+ * Rounding: in bf16 calls the probabilities count 8 bits where they multiply
+ * the values (not in their sum, nor in lse). Sums are fp32, joined in a fixed order.
+ *
+ * swa_kv4_move: the tokens of slots src[b][t] become those of dst[b][t] (int64 [p->B,
+ * p->T], T <= 64), in the whole cache of a layer: the accepted path of a tree put
+ * in order behind its context. All of row b are read before any is written; slots
+ * that one row writes and another row reads or writes leave those undefined, as
+ * does the same dst twice in a row. Pairs with a -1 are skipped; with a slot outside
+ * the cache skipped and reported.
+ */
+swa_status swa_kv4_tree(int B, int n_tokens, int max_new, const int32_t* parent, const int32_t* cu, const int32_t* lens,
+                        int32_t* pos, int64_t* seen, void* workspace, size_t ws_bytes, void* stream);
+swa_status swa_kv4_tree_attn(const swa_params* p, const swa_extras* ex, const swa_kv4_cache* c, const swa_rope* r,
+                             int n_tokens, int max_new, const void* q, const float* gq, const int32_t* table, int max_pages,
+                             const int32_t* lens, const int32_t* cu, const int32_t* pos, const int64_t* seen, void* o,
+                             float* lse, void* workspace, size_t ws_bytes, void* stream);
+swa_status swa_kv4_move(const swa_params* p, const swa_kv4_cache* c, const int64_t* src, const int64_t* dst, void* workspace,
+                        size_t ws_bytes, void* stream);
+
+/*
+ * The norm in front of a layer, with the residual's addition, as an operator of
+ * its own (the block calls have one without gain inside):
+ *   h = x + add (rounded to elem),  rstd = 1 / sqrt(mean_c(h^2) + eps),  y = gain h rstd
+ * over rows of C channels (a multiple of 8, at most 65536).
+ *   add    NULL: h = x
+ *   gain   fp32 [C], or NULL (1)
+ *   h      elem [rows, C]; NULL only where add is NULL. May be x or add.
+ *   y      elem [rows, C], may be x or add; or
+ *   y8, scale  y in 8 bits: e4m3 numbers [rows, C], fp32 [rows]; y ~ y8 * scale.
+ *          y8 = e4m3(448 u / max|u|), scale = max|u| rstd / 448 with u = gain h,
+ *          to nearest, ties to even, exactly so. A row that holds a NaN or an
+ *          infinity is NaN in both; one whose entries are all 0 is 0 in both (so is one
+ *          whose gains bring max|u| 2^60 below the entries' own size and fp32's end).
+ *   rstd   fp32 [rows] or NULL (the backward wants it)
+ * Sums are fp32; squares that leave its range are summed of the row times a
+ * power of two.
+ *
+ * swa_rms_norm_bwd, for the loss <y, dy> + <h, dh>:
+ *   dx     elem [rows, C]: gradient of x and of add; may be dy, dh or h
+ *   dgain  fp32 [C] (overwritten), or NULL. It wants the workspace
+ *          (swa_rms_norm_workspace_size, 256-byte aligned; nothing in it is kept or has
+ *          to be set): partial sums, added in a fixed order.
+ *   dh     NULL: h is not used elsewhere
+ * rows == 0 clears dgain.
+ */
+swa_status swa_rms_norm(long long rows, int C, float eps, const void* x, const void* add, const float* gain, void* h, void* y,
+                        void* y8, float* scale, float* rstd, void* stream);
+size_t swa_rms_norm_workspace_size(long long rows, int C);
+swa_status swa_rms_norm_bwd(long long rows, int C, const void* h, const float* rstd, const float* gain, const void* dy,
+                            const void* dh, void* dx, float* dgain, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Projections whose weights are held in 4 bits, for serving:
+ *   y[m][n] = x_scale[m] sum_k x[m][k] W[n][k] + add[m][n]
+ * K a multiple of 8; N, K at most 2^24. The weights are swa_w4_size(N, K) bytes,
+ * 16-byte aligned: [ceil(N / 16)][ceil(K / 64)] tiles of 544 bytes, 512 of numbers
+ * and 16 steps (bf16). A number n = 0..15 stands for s (n - 8), with a step s per
+ * row and 64 columns. Lane = 4 r + j (r 0..7, j 0..3) of a tile has its bytes 16
+ * lane ..; their 32-bit word w has, low nibble first, for e = 0, 1, q = 0, 1, hi
+ * = 0, 1 the number of row r + 8 hi, column 16 j + 4 w + 2 q + e. Step 2 r + hi is
+ * that of row r + 8 hi.
+ *
+ * swa_w4_pack makes them of w [N][K] elem (torch.nn.Linear layout):
+ *   s = bf16(max|w| / 7) (the quotient in fp32) over the group, n = floor(w / s +
+ *   8.5) kept within 0..15, exactly so; n = 8 where s is below 1e-36 (it is 0 then).
+ * A group that holds a NaN or an infinity is NaN. Beyond N and K numbers are 8 and
+ * steps 0. swa_w4_unpack gives w as the numbers it is held as, rounded to elem.
+ *
+ * swa_w4_linear: x [M][K] elem, or e4m3 where x_scale (fp32 [M]) is given: the pair
+ * that swa_rms_norm makes. add [M][N] or NULL; it may be y. x, add and y are 16-byte
+ * aligned. Products are exact, sums fp32.
+ */
+size_t swa_w4_size(int N, int K);
+swa_status swa_w4_pack(int N, int K, const void* w, void* w4, void* stream);
+swa_status swa_w4_unpack(int N, int K, const void* w4, void* w, void* stream);
+swa_status swa_w4_linear(int M, int N, int K, const void* x, const float* x_scale, const void* w4, const void* add, void* y,
+                         void* stream);
+
+/*
  * Synchronises `stream`, reads the workspace status word, clears it, and
  * returns SWA_OK, SWA_ERR_TIMEOUT or SWA_ERR_DEVICE_CHECK (timeout wins).
  * After a timeout it also drops the record of a zeroed dQ accumulator (a

@@ -49,6 +49,9 @@ __all__ = [
     "swa_kv4_workspace_size", "swa_kv4_workspace_init", "swa_kv4_attn",
     "rope_tables", "rope_apply", "new_kv4_cache", "new_kv4_workspace", "kv4_plan", "kv4_append",
     "kv4_read", "kv4_attention",
+    "swa_kv4_tree", "swa_kv4_tree_attn", "swa_kv4_move", "swa_rms_norm", "swa_rms_norm_workspace_size", "swa_rms_norm_bwd",
+    "swa_w4_size", "swa_w4_pack", "swa_w4_unpack", "swa_w4_linear",
+    "kv4_tree", "kv4_tree_attention", "kv4_move", "rms_norm", "rms_norm_backward", "w4_pack", "w4_unpack", "w4_linear",
     "SWA_OK", "SWA_ERR_INVALID_ARG", "SWA_ERR_UNSUPPORTED", "SWA_ERR_CUDA", "SWA_ERR_TIMEOUT",
     "SWA_ERR_WORKSPACE", "SWA_ERR_DEVICE_CHECK", "SWA_REUSE_PROLOGUE", "SWA_BWD_STAGE_PRE",
     "SWA_BWD_STAGE_MAIN", "SWA_BWD_STAGE_POST",
@@ -171,7 +174,7 @@ def load(kind: str = "bf16") -> ctypes.CDLL:
     lib.swa_block_fwd.restype = ctypes.c_int
     lib.swa_block_bwd.argtypes = [P, R, W] + [_vp] * 15 + [ctypes.c_size_t, _vp]
     lib.swa_block_bwd.restype = ctypes.c_int
-    C, F, I, Z = (ctypes.POINTER(swa_kv4_cache), ctypes.POINTER(swa_rope), ctypes.c_int, ctypes.c_size_t)
+    C, F, I, L, Z = (ctypes.POINTER(swa_kv4_cache), ctypes.POINTER(swa_rope), ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t)
     for name, args in (
             ("swa_rope_tables", [ctypes.POINTER(swa_rope_freq), I, I, _vp, _vp, _vp]),
             ("swa_rope_apply", [P, F] + [_vp] * 5 + [I, _vp, Z, _vp]),
@@ -179,10 +182,19 @@ def load(kind: str = "bf16") -> ctypes.CDLL:
             ("swa_kv4_append", [P, R, C, F] + [_vp] * 9 + [Z, _vp]),
             ("swa_kv4_read", [P, C] + [_vp] * 4 + [Z, _vp]),
             ("swa_kv4_workspace_init", [_vp, Z, _vp]),
-            ("swa_kv4_attn", [P, R, C, F, _vp, _vp, _vp, I] + [_vp] * 4 + [Z, _vp])):
+            ("swa_kv4_attn", [P, R, C, F, _vp, _vp, _vp, I] + [_vp] * 4 + [Z, _vp]),
+            ("swa_kv4_tree", [I] * 3 + [_vp] * 6 + [Z, _vp]),
+            ("swa_kv4_tree_attn", [P, R, C, F, I, I, _vp, _vp, _vp, I] + [_vp] * 7 + [Z, _vp]),
+            ("swa_kv4_move", [P, C] + [_vp] * 3 + [Z, _vp]),
+            ("swa_rms_norm", [L, I, ctypes.c_float] + [_vp] * 9),
+            ("swa_rms_norm_bwd", [L, I] + [_vp] * 8 + [Z, _vp]),
+            ("swa_w4_pack", [I, I] + [_vp] * 3),
+            ("swa_w4_unpack", [I, I] + [_vp] * 3),
+            ("swa_w4_linear", [I] * 3 + [_vp] * 6)):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = I
-    for name, args in (("swa_kv4_cache_size", [P, I, I]), ("swa_kv4_workspace_size", [P, I, I])):
+    for name, args in (("swa_kv4_cache_size", [P, I, I]), ("swa_kv4_workspace_size", [P, I, I]),
+                       ("swa_rms_norm_workspace_size", [L, I]), ("swa_w4_size", [I, I])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = Z
     lib.swa_attn_check_status.argtypes = [_vp, _vp]
@@ -449,6 +461,57 @@ def swa_kv4_attn(p, ex, c, r, q, gq, table, max_pages, lens, o, lse, ws, ws_byte
     return int(load(kind).swa_kv4_attn(
         ctypes.byref(p), _ref(ex), _ref(c), _ref(r), _ptr(q), _ptr(gq), _ptr(table), int(max_pages), _ptr(lens),
         _ptr(o), _ptr(lse), _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
+def swa_kv4_tree(B, n_tokens, max_new, parent, cu, lens, pos, seen, ws=None, ws_bytes=None, stream=None, kind: str = "bf16") -> int:
+    return int(load(kind).swa_kv4_tree(B, n_tokens, max_new, _ptr(parent), _ptr(cu), _ptr(lens), _ptr(pos), _ptr(seen), _ptr(ws),
+                                       _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
+def swa_kv4_tree_attn(p, ex, c, r, n_tokens, max_new, q, gq, table, max_pages, lens, cu, pos, seen, o, lse, ws, ws_bytes=None,
+                      stream=None, kind=None) -> int:
+    kind = kind or _kind_of(q)
+    return int(load(kind).swa_kv4_tree_attn(
+        ctypes.byref(p), _ref(ex), _ref(c), _ref(r), int(n_tokens), int(max_new), _ptr(q), _ptr(gq), _ptr(table), int(max_pages),
+        _ptr(lens), _ptr(cu), _ptr(pos), _ptr(seen), _ptr(o), _ptr(lse), _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
+def swa_kv4_move(p, c, src, dst, ws=None, ws_bytes=None, stream=None, kind: str = "bf16") -> int:
+    return int(load(kind).swa_kv4_move(ctypes.byref(p), _ref(c), _ptr(src), _ptr(dst), _ptr(ws), _ws_bytes(ws, ws_bytes),
+                                       _stream(stream)))
+
+
+def swa_rms_norm(rows, C, eps, x, add, gain, h, y, y8, scale, rstd, stream=None, kind=None) -> int:
+    kind = kind or _kind_of(x)
+    return int(load(kind).swa_rms_norm(int(rows), int(C), float(eps), _ptr(x), _ptr(add), _ptr(gain), _ptr(h), _ptr(y), _ptr(y8),
+                                       _ptr(scale), _ptr(rstd), _stream(stream)))
+
+
+def swa_rms_norm_workspace_size(rows: int, C: int, kind: str = "bf16") -> int:
+    return int(load(kind).swa_rms_norm_workspace_size(int(rows), int(C)))
+
+
+def swa_rms_norm_bwd(rows, C, h, rstd, gain, dy, dh, dx, dgain, ws=None, ws_bytes=None, stream=None, kind=None) -> int:
+    kind = kind or _kind_of(h)
+    return int(load(kind).swa_rms_norm_bwd(int(rows), int(C), _ptr(h), _ptr(rstd), _ptr(gain), _ptr(dy), _ptr(dh), _ptr(dx),
+                                           _ptr(dgain), _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
+def swa_w4_size(N: int, K: int, kind: str = "bf16") -> int:
+    return int(load(kind).swa_w4_size(int(N), int(K)))
+
+
+def swa_w4_pack(N, K, w, w4, stream=None, kind=None) -> int:
+    return int(load(kind or _kind_of(w)).swa_w4_pack(int(N), int(K), _ptr(w), _ptr(w4), _stream(stream)))
+
+
+def swa_w4_unpack(N, K, w4, w, stream=None, kind=None) -> int:
+    return int(load(kind or _kind_of(w)).swa_w4_unpack(int(N), int(K), _ptr(w4), _ptr(w), _stream(stream)))
+
+
+def swa_w4_linear(M, N, K, x, x_scale, w4, add, y, stream=None, kind=None) -> int:
+    return int(load(kind or _kind_of(y)).swa_w4_linear(int(M), int(N), int(K), _ptr(x), _ptr(x_scale), _ptr(w4), _ptr(add), _ptr(y),
+                                                       _stream(stream)))
 
 
 def swa_attn_check_status(ws, stream=None, kind: str = "bf16") -> int:
@@ -918,3 +981,217 @@ def kv4_attention(cache, q, table, lens, *, rope=None, interleaved: bool = False
     if s:
         raise SwaError(s, "swa_kv4_attn")
     return o, lse
+
+
+# ---------------------------------------------------------------------------
+# Drafted tokens, the norm and the 4-bit projections of a serving step (and the
+# norm's backward). Checks, devices and streams as above.
+# ---------------------------------------------------------------------------
+
+_F8 = torch.float8_e4m3fn
+
+
+def kv4_tree(parent, cu, lens, *, max_new: int, workspace=None, stream=None):
+    """pos, seen = kv4_tree(parent, cu, lens): positions (int32) and visibility
+    (int64 bits) of a step's drafted tokens, from parent int32 [N] (the index of
+    each token's parent among its request's, -1: the context), cu int32 [B + 1]
+    (rows of the requests; rows behind cu[B] are padding) and lens int32 [B]
+    (cached tokens, the drafted ones among them: cu and lens of kv4_plan). At
+    most ``max_new`` (up to 64) tokens a request."""
+    dev = parent.device
+    if parent.dim() != 1 or cu.dim() != 1 or cu.numel() < 1:
+        raise ValueError("parent [N] and cu [B + 1] are expected")
+    N, B = parent.shape[0], cu.shape[0] - 1
+    pa, ca, la = _at("parent", parent, _I32, (N,), dev), _at("cu", cu, _I32, (B + 1,), dev), _at("lens", lens, _I32, (B,), dev)
+    ws, nws = _ws_at(workspace, dev)
+    st = _stream_here(dev, stream)
+    if st is None:
+        return _there(dev, stream, lambda: kv4_tree(parent, cu, lens, max_new=max_new, workspace=workspace))
+    pos = torch.empty((N,), dtype=_I32, device=dev)
+    seen = torch.empty((N,), dtype=_I64, device=dev)
+    s = load("bf16").swa_kv4_tree(B, N, max_new, pa, ca, la, pos.data_ptr(), seen.data_ptr(), ws, nws, st)
+    if s:
+        raise SwaError(s, "swa_kv4_tree")
+    return pos, seen
+
+
+def kv4_tree_attention(cache, q, table, lens, cu, pos, seen, *, max_new: int, rope=None, interleaved: bool = False, gq=None,
+                       window: int = -1, softmax_scale: float = 0.0, eps: float = 1e-6, workspace=None, stream=None):
+    """o, lse = kv4_tree_attention(cache, q, table, lens, cu, pos, seen):
+    attention of each request's drafted tokens, q [N, Hq, d] (as projected), over
+    its context and the drafted tokens that ``seen`` shows it (kv4_tree), whose keys
+    and values are in the cache already. The other arguments are those of
+    kv4_attention. Rows that see nothing (padding among them) are 0, their lse
+    -infinity."""
+    n_pages, Hkv, page, d = _cache_dims(cache)
+    dev, dt = cache.device, q.dtype
+    kind = _kind("q", dt)
+    if q.dim() != 3 or table.dim() != 2:
+        raise ValueError("q [N, Hq, d] and table [B, max_pages] are expected")
+    N, Hq = q.shape[:2]
+    B, max_pages = table.shape
+    qa, ga = _at("q", q, dt, (N, Hq, d), dev), _at("gq", gq, _F32, (d,), dev)
+    ta, la = _at("table", table, _I32, (B, max_pages), dev), _at("lens", lens, _I32, (B,), dev)
+    ca, pa, sa = _at("cu", cu, _I32, (B + 1,), dev), _at("pos", pos, _I32, (N,), dev), _at("seen", seen, _I64, (N,), dev)
+    r = _rope_at(rope, interleaved, dev)
+    st = _stream_here(dev, stream)
+    if st is None:
+        return _there(dev, stream, lambda: kv4_tree_attention(
+            cache, q, table, lens, cu, pos, seen, max_new=max_new, rope=rope, interleaved=interleaved, gq=gq, window=window,
+            softmax_scale=softmax_scale, eps=eps, workspace=workspace))
+    if workspace is None:
+        workspace = new_kv4_workspace(cache, B, Hq, max_pages=max_pages, window=window, kind=kind)
+    ws, nws = _ws_at(workspace, dev)
+    o = torch.empty_like(q)
+    lse = torch.empty((N, Hq), dtype=_F32, device=dev)
+    s = load(kind).swa_kv4_tree_attn(swa_params(B, 1, Hq, Hkv, d, window, 1, softmax_scale, eps, 0.0, 0), None,
+                                     swa_kv4_cache(cache.data_ptr(), n_pages, page), r, N, max_new, qa, ga, ta, max_pages, la, ca,
+                                     pa, sa, o.data_ptr(), lse.data_ptr(), ws, nws, st)
+    if s:
+        raise SwaError(s, "swa_kv4_tree_attn")
+    return o, lse
+
+
+def kv4_move(cache, src, dst, *, workspace=None, stream=None) -> None:
+    """Moves cached tokens: those of slots src int64 [B, T] (T <= 64) become those of
+    dst. All of a row are read before any is written; rows must not write what
+    others read or write. -1 in either skips a pair; slots outside the cache are
+    skipped, which only a ``workspace`` tells."""
+    n_pages, Hkv, page, d = _cache_dims(cache)
+    dev = cache.device
+    if src.dim() != 2:
+        raise ValueError("src: [B, T] is expected")
+    B, T = src.shape
+    sa, da = _at("src", src, _I64, (B, T), dev), _at("dst", dst, _I64, (B, T), dev)
+    ws, nws = _ws_at(workspace, dev)
+    st = _stream_here(dev, stream)
+    if st is None:
+        return _there(dev, stream, lambda: kv4_move(cache, src, dst, workspace=workspace))
+    s = load("bf16").swa_kv4_move(swa_params(B, T, Hkv, Hkv, d, -1, 1, 0.0, 0.0, 0.0, 0),
+                                  swa_kv4_cache(cache.data_ptr(), n_pages, page), sa, da, ws, nws, st)
+    if s:
+        raise SwaError(s, "swa_kv4_move")
+
+
+def _rows_of(name, x):
+    if x.dim() < 1:
+        raise ValueError(f"{name}: [..., channels] is expected")
+    C = x.shape[-1]
+    return (x.numel() // C if C else 0), C
+
+
+def rms_norm(x, gain=None, *, add=None, eps: float = 1e-6, fp8: bool = False, inplace: bool = False, stream=None) -> dict:
+    """h = x + add, y = gain h / sqrt(mean(h^2) + eps) over the last dimension of
+    x (bf16 or fp32; gain fp32 [C]). Returns y, h (x itself without an ``add``) and
+    rstd fp32 [...]; with ``fp8`` y is float8_e4m3fn and scale fp32 [...] the rows'
+    factors (y ~ y * scale). ``inplace``: h is written over x."""
+    rows, C = _rows_of("x", x)
+    dt, dev = x.dtype, x.device
+    lib = load(_kind("x", dt))
+    xa, aa, ga = _at("x", x, dt, x.shape, dev), _at("add", add, dt, x.shape, dev), _at("gain", gain, _F32, (C,), dev)
+    st = _stream_here(dev, stream)
+    if st is None:
+        return _there(dev, stream, lambda: rms_norm(x, gain, add=add, eps=eps, fp8=fp8, inplace=inplace))
+    h = x if add is None or inplace else torch.empty_like(x)
+    y = torch.empty(x.shape, dtype=_F8 if fp8 else dt, device=dev)
+    rstd = torch.empty(x.shape[:-1], dtype=_F32, device=dev)
+    scale = torch.empty_like(rstd) if fp8 else None
+    # (an empty tensor has no address; nothing is written then)
+    ya = y.data_ptr() or 256
+    s = lib.swa_rms_norm(rows, C, eps, xa, aa, ga, h.data_ptr() if add is not None else None, None if fp8 else ya, ya if fp8 else None,
+                         (scale.data_ptr() or 256) if fp8 else None, rstd.data_ptr(), st)
+    if s:
+        raise SwaError(s, "swa_rms_norm")
+    return {"y": y, "scale": scale, "h": h, "rstd": rstd}
+
+
+def rms_norm_backward(h, rstd, dy, gain=None, *, dh=None, need_gain: bool = True, workspace=None, stream=None) -> dict:
+    """Backward of rms_norm from its h and rstd: dx, the gradient of x and of add
+    (dy's, and dh where h is used elsewhere: the residual), and dgain fp32 [C] (None
+    without ``need_gain``). ``workspace``: uint8, of swa_rms_norm_workspace_size
+    bytes; None: one for this call."""
+    rows, C = _rows_of("h", h)
+    dt, dev = h.dtype, h.device
+    kind = _kind("h", dt)
+    ha, da, ea = _at("h", h, dt, h.shape, dev), _at("dy", dy, dt, h.shape, dev), _at("dh", dh, dt, h.shape, dev)
+    ra, ga = _at("rstd", rstd, _F32, h.shape[:-1], dev), _at("gain", gain, _F32, (C,), dev)
+    st = _stream_here(dev, stream)
+    if st is None:
+        return _there(dev, stream, lambda: rms_norm_backward(h, rstd, dy, gain, dh=dh, need_gain=need_gain, workspace=workspace))
+    dx = torch.empty_like(h)
+    dgain = torch.empty((C,), dtype=_F32, device=dev) if need_gain else None
+    if workspace is None and need_gain:
+        workspace = torch.empty((swa_rms_norm_workspace_size(rows, C, kind),), dtype=_U8, device=dev)
+    ws, nws = _ws_at(workspace, dev)
+    s = load(kind).swa_rms_norm_bwd(rows, C, ha, ra, ga, da, ea, dx.data_ptr(), dgain.data_ptr() if need_gain else None, ws, nws, st)
+    if s:
+        raise SwaError(s, "swa_rms_norm_bwd")
+    return {"dx": dx, "dgain": dgain}
+
+
+def _w4_tiles(N: int, K: int):
+    return -(-N // 16), -(-K // 64), 544
+
+
+def w4_pack(w, *, stream=None):
+    """Weights w [N, K] (torch.nn.Linear layout, bf16 or fp32, K a multiple of 8) in 4
+    bits with a bf16 step per row and 64 columns: uint8 [N / 16, K / 64, 544], both
+    rounded up."""
+    if w.dim() != 2:
+        raise ValueError("w: [N, K] is expected")
+    (N, K), dev = w.shape, w.device
+    lib, wa = load(_kind("w", w.dtype)), _at("w", w, w.dtype, w.shape, w.device)
+    st = _stream_here(dev, stream)
+    if st is None:
+        return _there(dev, stream, lambda: w4_pack(w))
+    w4 = torch.empty(_w4_tiles(N, K), dtype=_U8, device=dev)
+    s = lib.swa_w4_pack(N, K, wa, w4.data_ptr(), st)
+    if s:
+        raise SwaError(s, "swa_w4_pack")
+    return w4
+
+
+def w4_unpack(w4, out_features: int, in_features: int, *, dtype=torch.bfloat16, stream=None):
+    """The weights [out_features, in_features] that w4 holds, as ``dtype``."""
+    lib, dev, N, K = load(_kind("dtype", dtype)), w4.device, out_features, in_features
+    wa = _at("w4", w4, _U8, _w4_tiles(N, K), dev)
+    st = _stream_here(dev, stream)
+    if st is None:
+        return _there(dev, stream, lambda: w4_unpack(w4, N, K, dtype=dtype))
+    w = torch.empty((N, K), dtype=dtype, device=dev)
+    s = lib.swa_w4_unpack(N, K, wa, w.data_ptr(), st)
+    if s:
+        raise SwaError(s, "swa_w4_unpack")
+    return w
+
+
+def w4_linear(x, w4, *, out_features: Optional[int] = None, scale=None, add=None, dtype=None, out=None, stream=None):
+    """y = x W^T (+ add) [..., out_features] for x [..., K] and weights of w4_pack
+    (out_features: N; None: a multiple of 16, all that w4 holds). x is bf16 or fp32, or
+    float8_e4m3fn with ``scale`` fp32 [...] (rms_norm's pair); then ``dtype`` is y's
+    (bf16 by default). ``out``: y, which may be ``add``."""
+    M, K = _rows_of("x", x)
+    dev = x.device
+    if w4.dim() != 3:
+        raise ValueError("w4: uint8 [N / 16, K / 64, 544] is expected")
+    N = 16 * w4.shape[0] if out_features is None else out_features
+    if scale is None:
+        if dtype is not None and dtype is not x.dtype:
+            raise ValueError(f"dtype: that of x, {x.dtype}, is expected, got {dtype}")
+        dt = x.dtype
+    else:
+        dt = _BF16 if dtype is None else dtype
+    lib = load(_kind("dtype" if scale is not None else "x", dt))
+    shape = (*x.shape[:-1], N)
+    xa, wa = _at("x", x, dt if scale is None else _F8, x.shape, dev), _at("w4", w4, _U8, _w4_tiles(N, K), dev)
+    sa, aa, oa = _at("scale", scale, _F32, x.shape[:-1], dev), _at("add", add, dt, shape, dev), _at("out", out, dt, shape, dev)
+    st = _stream_here(dev, stream)
+    if st is None:
+        return _there(dev, stream, lambda: w4_linear(x, w4, out_features=N, scale=scale, add=add, dtype=dt, out=out))
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=dev)
+        oa = out.data_ptr()
+    s = lib.swa_w4_linear(M, N, K, xa, sa, wa, aa, oa, st)
+    if s:
+        raise SwaError(s, "swa_w4_linear")
+    return out

@@ -1,0 +1,761 @@
+// Drafted tokens over the 4-bit paged cache: positions and visibility of a
+// request's tree of drafted tokens, their attention, and the move of the
+// accepted ones to their places.
+//
+// The tokens of a step lie one request behind the other: those of request b are
+// rows cu[b] .. cu[b + 1] - 1 (at most kTreeTokens), and their keys and values
+// are in the cache already, as the last tokens of its lens[b], in their order.
+// The request's context is what is in front of them.
+#pragma once
+
+#include "kv4_attn.cuh"
+
+namespace swa {
+namespace kv4 {
+
+constexpr int kTreeTokens = 64;      // drafted tokens of a request: bits of a mask
+
+// ---------------------------------------------------------------------------
+// Tree: token i sees itself and what its parent sees; its position is the
+// context's length and its depth.
+//   pos[i] = ctx + |above(i)| - 1,  seen[i] = bits of above(i),
+//   above(i) = {i} and above(parent[i]); parent -1: the context.
+// A warp a request; a lane walks up from its two tokens.
+// ---------------------------------------------------------------------------
+struct TreeArgs {
+  int B, N, max_new;                 // N: rows
+  const int32_t* parent; const int32_t* cu; const int32_t* lens;
+  int32_t* pos; int64_t* seen;       // [N]
+  uint32_t* status;                  // or NULL
+};
+
+// A request's rows: false where cu is not plausible (and nothing is to be touched).
+struct TreeReq {
+  int row0, n, ctx;                  // n = 0, all rows hidden: bad
+  int rows;                          // rows that are the request's
+  bool bad;
+};
+__device__ __forceinline__ TreeReq tree_req(const int32_t* cu, const int32_t* lens, int b, int N, int max_new, long long cap) {
+  TreeReq r{cu[b], 0, 0, 0, false};
+  const int end = cu[b + 1], len = lens[b];
+  if (r.row0 < 0 || end < r.row0 || end > N) {
+    r.bad = true;
+    return r;
+  }
+  r.rows = end - r.row0;
+  r.ctx = len - r.rows;
+  if (len < 0 || len > cap || r.rows > max_new || r.ctx < 0) r.bad = true;
+  else r.n = r.rows;
+  return r;
+}
+
+constexpr int kTreeWarps = 4;
+__global__ void __launch_bounds__(kTreeWarps * 32) tree_kernel(const __grid_constant__ TreeArgs a) {
+  __shared__ int up[kTreeWarps][kTreeTokens];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const long long stride = static_cast<long long>(gridDim.x) * kTreeWarps;
+  uint32_t bad = 0;
+  for (long long b = static_cast<long long>(blockIdx.x) * kTreeWarps + wid; b < a.B; b += stride) {
+    const TreeReq q = tree_req(a.cu, a.lens, static_cast<int>(b), a.N, a.max_new, INT32_MAX);
+    if (q.bad) bad = DEV_ERR_BOUNDS;
+    for (int i = lane; i < q.n; i += 32) {
+      const int p = a.parent[q.row0 + i];
+      up[wid][i] = p >= -1 && p < i ? p : -2;
+    }
+    __syncwarp();
+    for (int i = lane; i < q.rows; i += 32) {
+      unsigned long long m = 0;
+      if (i < q.n) {
+        int t = i;
+        while (t >= 0) {               // strictly down: a parent is in front of its child
+          m |= 1ull << t;
+          t = up[wid][t];
+        }
+        if (t != -1) {
+          m = 0;
+          bad = DEV_ERR_BOUNDS;
+        }
+      }
+      a.seen[q.row0 + i] = static_cast<int64_t>(m);
+      a.pos[q.row0 + i] = m ? q.ctx + __popcll(m) - 1 : 0;
+    }
+    __syncwarp();
+  }
+  // rows behind the last request
+  const int used = a.cu[a.B];
+  if (used < 0 || used > a.N) bad = DEV_ERR_BOUNDS;
+  else
+    for (long long i = used + static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < a.N;
+         i += static_cast<long long>(gridDim.x) * blockDim.x) {
+      a.seen[i] = 0;
+      a.pos[i] = 0;
+    }
+  if (bad && a.status) atomicOr(a.status, bad);
+}
+
+// ---------------------------------------------------------------------------
+// Move: the tokens of slots src[b][t] become those of dst[b][t]. All of a row b
+// are read before any is written. A block a (row, kv head).
+// ---------------------------------------------------------------------------
+struct MoveArgs {
+  Cache c;
+  int B, T;
+  const int64_t* src; const int64_t* dst;
+  uint32_t* status;
+};
+constexpr int kMoveThreads = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ MoveArgs a) {
+  constexpr int KW = D / 8, VW = D / 4, SW = D / 64;       // words of a key row, 16-bit pieces of a value row, pairs of each
+  constexpr int RB = D + 8 * SW;                           // bytes of a token
+  __shared__ __align__(16) uint8_t held[kTreeTokens * RB];
+  __shared__ long long to[kTreeTokens];
+  __shared__ long long from[kTreeTokens];
+  const long long slots = static_cast<long long>(a.c.n_pages) * a.c.page;
+  uint32_t bad = 0;
+  const long long items = static_cast<long long>(a.B) * a.c.Hkv;
+  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+    const long long b = it / a.c.Hkv;
+    const int h = static_cast<int>(it - b * a.c.Hkv);
+    for (int t = threadIdx.x; t < a.T; t += kMoveThreads) {
+      long long s = a.src[b * a.T + t], d = a.dst[b * a.T + t];
+      const bool skip = s == -1 || d == -1;
+      if (!skip && (s < 0 || s >= slots || d < 0 || d >= slots)) bad = DEV_ERR_BOUNDS;
+      if (skip || s < 0 || s >= slots || d < 0 || d >= slots || s == d) s = d = -1;
+      from[t] = s;
+      to[t] = d;
+    }
+    __syncthreads();
+    constexpr int UNITS = KW + VW + 2 * SW;
+    for (int u = threadIdx.x; u < a.T * UNITS; u += kMoveThreads) {
+      const int t = u / UNITS, k = u - t * UNITS;
+      if (from[t] < 0) continue;
+      const uint8_t* tile = tile_of<D>(a.c, from[t], h);
+      const int o = static_cast<int>(from[t] & 15);
+      uint8_t* x = held + t * RB;
+      if (k < KW) *reinterpret_cast<uint32_t*>(x + 4 * k) = *reinterpret_cast<const uint32_t*>(tile + o * (D / 2) + 4 * k);
+      else if (k < KW + VW)
+        *reinterpret_cast<uint16_t*>(x + D / 2 + 2 * (k - KW)) =
+            *reinterpret_cast<const uint16_t*>(tile + 8 * D + (o >> 1) * D + 4 * (k - KW) + 2 * (o & 1));
+      else {
+        const int i = k - KW - VW, kv = i / SW, g = i - kv * SW;
+        *reinterpret_cast<uint32_t*>(x + D + 4 * i) = *reinterpret_cast<const uint32_t*>(tile + 16 * D + kv * D + o * (4 * SW) + 4 * g);
+      }
+    }
+    __syncthreads();
+    for (int u = threadIdx.x; u < a.T * UNITS; u += kMoveThreads) {
+      const int t = u / UNITS, k = u - t * UNITS;
+      if (to[t] < 0) continue;
+      uint8_t* tile = tile_of<D>(a.c, to[t], h);
+      const int o = static_cast<int>(to[t] & 15);
+      const uint8_t* x = held + t * RB;
+      if (k < KW) *reinterpret_cast<uint32_t*>(tile + o * (D / 2) + 4 * k) = *reinterpret_cast<const uint32_t*>(x + 4 * k);
+      else if (k < KW + VW)
+        *reinterpret_cast<uint16_t*>(tile + 8 * D + (o >> 1) * D + 4 * (k - KW) + 2 * (o & 1)) =
+            *reinterpret_cast<const uint16_t*>(x + D / 2 + 2 * (k - KW));
+      else {
+        const int i = k - KW - VW, kv = i / SW, g = i - kv * SW;
+        *reinterpret_cast<uint32_t*>(tile + 16 * D + kv * D + o * (4 * SW) + 4 * g) = *reinterpret_cast<const uint32_t*>(x + D + 4 * i);
+      }
+    }
+    __syncthreads();
+  }
+  if (bad && a.status) atomicOr(a.status, bad);
+}
+
+// ---------------------------------------------------------------------------
+// Attention of a request's drafted tokens. Row (token i, query head g of the kv
+// head's group) sees key j of the context where pos_i - j <= window, and drafted
+// token t where bit t of seen_i is set and pos_i - pos_t <= window.
+//
+// The rows of one (request, kv head) share its keys and values: they are the
+// 16-row operand of both products here (S = Q K^T, O += P V), so that each tile
+// of the cache is fetched and widened once for 16 rows, and P goes from one
+// product's result to the other's operand without an exchange between lanes.
+// The cache's words are the eight-column operand as they are (a lane's numbers
+// are of key lane / 4, or of channel lane / 4).
+//   RW   warps that hold 16 rows each of the same keys (1, 2 or 4); the other
+//        4 / RW - 1 groups of warps take other steps of two tiles.
+// Precision: q is two fp16 terms (22 bits: lse is an fp32 output; one term left it
+// 2e-4 off). P is one bf16 term in bf16 calls, whose o has 8 bits itself (as in the
+// training forward), and three in fp32 ones. The products with n - 8 are exact,
+// steps and centres multiply the sums in fp32.
+// ---------------------------------------------------------------------------
+struct TreeAttnArgs : AttnArgs {
+  int N, max_new;
+  const int32_t* cu; const int32_t* pos; const int64_t* seen;
+};
+
+constexpr int kQTerms = 2;
+constexpr int tree_stages(int rw) { return rw == 1 ? 2 : 4; }
+constexpr int tree_ctas_per_sm(int d) { return d == 64 && !kThreeTerms ? 4 : 2; }
+
+template <int D, int RW>
+struct TreeSmem {
+  static constexpr int rows = 16 * RW, groups = kAttnWarps / RW, stages = tree_stages(RW);
+  static constexpr int ring1 = stages * 2 * AttnShape<D>::TB;          // of one group of warps
+  static constexpr int ring = groups * ring1;
+  static constexpr int q = (ring + 15) / 16 * 16;                     // fp16 rows, hi then lo
+  static constexpr int q_end = q + rows * kQTerms * D * 2;
+  static constexpr int join = kAttnWarps * 16 * (D + 2) * 4;          // over the rings and the queries
+  static constexpr int bars = ((q_end > join ? q_end : join) + 127) / 128 * 128;
+  static constexpr int qf = bars + groups * stages * 16;                // full and free barriers
+  static constexpr int row = qf + rows * 16;                          // first visible key, pos, seen of each row
+  static constexpr int tpos = row + rows * 16;                        // positions of the drafted tokens
+  static constexpr int flags = tpos + kTreeTokens * 4;
+  static constexpr int bytes = flags + 16;
+};
+
+struct TreeRow {
+  int lo;                            // first key of the context that it sees; INT_MAX: hidden
+  int pos;
+  unsigned long long seen;
+};
+
+// NR query rows by one warp at once (query_row's arithmetic, row after row the
+// same; their loads wait together).
+template <int D, int NR>
+__device__ __forceinline__ void query_rows(const AttnArgs& a, const elem_t* const (&q)[NR], const int (&pos)[NR], __half* dst,
+                                           float* f) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, c0 = lane * E;
+  float x[NR][E], y[NR][E], cs[NR][E], sn[NR][E], g[E];
+  const bool turned = a.rcos != nullptr && c0 < a.rot;
+  const int half = a.rot / 2;
+  const bool first = c0 < half;
+#pragma unroll
+  for (int i = 0; i < E; ++i) g[i] = 1.0f;
+  if (a.gq != nullptr) load_vec<E>(a.gq + c0, g);
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[n][i] = y[n][i] = sn[n][i] = 0.f, cs[n][i] = 1.f;
+    if (q[n] == nullptr) continue;
+    load_vec<E>(q[n] + c0, x[n]);
+    if (turned) {
+      const long long row = static_cast<long long>(pos[n]) * half;
+      if (a.interleaved) {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+          cs[n][2 * i] = cs[n][2 * i + 1] = a.rcos[row + c0 / 2 + i];
+          sn[n][2 * i] = sn[n][2 * i + 1] = a.rsin[row + c0 / 2 + i];
+        }
+      } else {
+        load_vec<E>(q[n] + (first ? c0 + half : c0 - half), y[n]);
+        load_vec<E>(a.rcos + row + (first ? c0 : c0 - half), cs[n]);
+        load_vec<E>(a.rsin + row + (first ? c0 : c0 - half), sn[n]);
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+    float ss = 0.f;
+    if (turned) {
+      if (a.interleaved) {
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+          const float u = x[n][i], v = x[n][i + 1];
+          x[n][i] = fmaf(u, cs[n][i], v * sn[n][i]);
+          x[n][i + 1] = fmaf(v, cs[n][i], -u * sn[n][i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) x[n][i] = fmaf(x[n][i], cs[n][i], (first ? y[n][i] : -y[n][i]) * sn[n][i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) ss = fmaf(x[n][i], x[n][i], ss);
+    ss = warp_sum(ss);
+    float eps = a.eps;
+    if (ss == INFINITY) {      // the squares pass fp32: the same of 2^-80 of the row
+      constexpr float kDown = 0x1p-80f;
+      ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        x[n][i] *= kDown;
+        ss = fmaf(x[n][i], x[n][i], ss);
+      }
+      ss = warp_sum(ss);
+      eps = eps * kDown * kDown;
+    }
+    const float mul = rsqrtf(ss / D + eps) * (a.scale * 1.4426950408889634f);
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      x[n][i] *= mul * g[i];
+      if (q[n] == nullptr) x[n][i] = 0.f;
+      top = fmaxf(top, fabsf(x[n][i]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    int e = static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127;
+    e = e < -100 ? -100 : (e > 100 ? 100 : e);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float v = x[n][i] * up;
+      const __half hi = __float2half_rn(v);
+      const int at = ((c0 + i) & ~7) + ((c0 + i) & 3) * 2 + (((c0 + i) >> 2) & 1);   // pairs (i, i + 4) side by side
+      dst[n * kQTerms * D + at] = hi;
+      dst[n * kQTerms * D + D + at] = __float2half_rn(v - __half2float(hi));
+      sum += v;
+    }
+#pragma unroll
+    for (int o = 32 / E; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      f[4 * n] = __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23);
+      f[4 * n + 1] = sum;
+    }
+    if (D == 128 && lane == 16) f[4 * n + 2] = sum;
+  }
+}
+
+template <int D, int RW, bool kPolled>
+__global__ void __launch_bounds__(kAttnWarps * 32, tree_ctas_per_sm(D)) tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
+  using S = AttnShape<D>;
+  using M = TreeSmem<D, RW>;
+  constexpr int NG = S::NG, W = S::W, NQ = 16 * RW, KG = kAttnWarps / RW, ST = M::stages, E = D / 32;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int r = lane >> 2, j = lane & 3;
+  const int rw = wid % RW, kg = wid / RW;                  // rows 16 rw .., steps kg, kg + KG, ..
+  const int b = blockIdx.z, h = blockIdx.y / a.groups, qg = blockIdx.y - h * a.groups;
+  const int G = a.Hq / a.c.Hkv;
+  const long long cap = static_cast<long long>(a.max_pages) * a.c.page;
+  uint32_t bad = 0;
+  const TreeReq req = tree_req(a.cu, a.lens, b, a.N, a.max_new, cap);
+  if (req.bad) bad = DEV_ERR_BOUNDS;
+
+  // rows that hold nothing: those of a request that is refused, and those behind the last one
+  if (blockIdx.x == 0 && qg == 0) {
+    const int used = b == a.B - 1 ? a.cu[a.B] : a.N;
+    auto zero = [&](int row0, int row1) {
+      const float z[E] = {};
+      for (long long i = wid; i < static_cast<long long>(row1 - row0) * G; i += kAttnWarps) {
+        const long long at = (row0 + i / G) * a.Hq + h * G + i % G;
+        store_vec<E>(a.o + at * D + lane * E, z);
+        if (lane == 0) a.lse[at] = -INFINITY;
+      }
+    };
+    if (req.bad && req.rows > 0) zero(req.row0, req.row0 + req.rows);
+    if (used >= 0 && used < a.N) zero(used, a.N);
+  }
+  if (bad && tid == 0) atomicOr(a.status, bad);
+  const int row_q0 = qg * NQ;                              // first (token, head) row of this CTA
+  const int nq = min(NQ, req.n * G - row_q0);
+  if (nq <= 0) return;
+  const int len = req.ctx + req.n;
+  const int lo = a.window >= 0 && req.ctx - a.window > 0 ? req.ctx - a.window : 0;
+  const int t_lo = lo / kTile, t_hi = (len + kTile - 1) / kTile;     // tiles [t_lo, t_hi)
+  const int chunks = max(1, (t_hi - t_lo + a.chunk - 1) / a.chunk);
+  if (blockIdx.x >= chunks) return;
+  const int t0 = t_lo + blockIdx.x * a.chunk, t1 = min(t_hi, t0 + a.chunk);
+
+  const uint32_t bars = smem_u32(smem + M::bars) + kg * ST * 16, frees = bars + ST * 8;
+  uint32_t* flags = reinterpret_cast<uint32_t*>(smem + M::flags);    // [0] abort, [1] last
+  if (rw == 0 && lane == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(bars + 8 * s, 1);
+      mbar_init(frees + 8 * s, RW);
+    }
+    fence_mbar_init();
+  }
+  if (tid == 0) flags[0] = 0;
+  __syncwarp();
+
+  // Step n of a group of warps is the tiles t0 + 2 (kg + n KG) and the one
+  // behind it, which share a stage; its first warp fetches them. Pages are
+  // looked up 32 tiles at a time, a lane a tile.
+  const int steps = (t1 - t0 + 1) / 2;
+  const int n_mine = steps > kg ? (steps - kg + KG - 1) / KG : 0;
+  uint8_t* ring = smem + kg * M::ring1;
+  const uint32_t ring_u = smem_u32(ring);
+  const int per_page = a.c.page / kTile;
+  const long long head_off = static_cast<long long>(h) * per_page;
+  long long tile_at = -1;  // of the lane's tile in the cache; -1: none
+  uint32_t gone = 0;       // two bits per stage: tiles that are not there
+  // every warp of the group looks pages up, so that each knows which are gone
+  auto issue = [&](int n) {
+    if ((n & 15) == 0) {
+      const int t = t0 + 2 * (kg + (n + (lane >> 1)) * KG) + (lane & 1);
+      tile_at = -1;
+      if (t < t1) {
+        const int pi = t / per_page;
+        const int pg = a.table[static_cast<long long>(b) * a.max_pages + pi];
+        if (pg >= 0 && pg < a.c.n_pages)
+          tile_at = static_cast<long long>(pg) * a.c.Hkv * per_page + head_off + (t - pi * per_page);
+        else
+          bad = DEV_ERR_BOUNDS;
+      }
+    }
+    const int st = n % ST;
+    const long long at = __shfl_sync(0xffffffffu, tile_at, ((2 * n) & 31) + (lane & 1));
+    const uint32_t there = __ballot_sync(0xffffffffu, at >= 0) & 3u;
+    gone = (gone & ~(3u << (2 * st))) | ((there ^ 3u) << (2 * st));
+    if (rw != 0) return;
+    if (lane == 0) mbar_arrive_expect_tx(bars + 8 * st, __popc(there) * S::TB);
+    __syncwarp();
+    if (lane < 2 && at >= 0) bulk_load(ring_u + (st * 2 + lane) * S::TB, a.c.data + at * S::TB, S::TB, bars + 8 * st);
+  };
+  int issued = 0;
+  for (; issued < ST && issued < n_mine; ++issued) issue(issued);
+
+  // rows and queries
+  TreeRow* rows = reinterpret_cast<TreeRow*>(smem + M::row);
+  int* tpos = reinterpret_cast<int*>(smem + M::tpos);
+  __half* qs = reinterpret_cast<__half*>(smem + M::q);
+  float* qf = reinterpret_cast<float*>(smem + M::qf);
+  for (int i = tid; i < req.n; i += kAttnWarps * 32) tpos[i] = a.pos[req.row0 + i];
+  for (int i = tid; i < NQ; i += kAttnWarps * 32) {
+    TreeRow x{INT32_MAX, 0, 0};
+    if (i < nq) {
+      const int at = req.row0 + (row_q0 + i) / G;
+      x.pos = a.pos[at];
+      x.seen = static_cast<unsigned long long>(a.seen[at]);
+      // a row that sees nothing needs no position
+      const bool ok = x.pos >= req.ctx && (a.rcos == nullptr || x.pos < a.rows);
+      if (x.seen == 0) x.pos = 0;
+      else if (!ok) {
+        bad = DEV_ERR_BOUNDS;
+        x.seen = 0;
+        x.pos = 0;
+      } else {
+        x.lo = a.window >= 0 && x.pos - a.window > 0 ? x.pos - a.window : 0;
+      }
+    }
+    rows[i] = x;
+  }
+  __syncthreads();
+  constexpr int NR = 4;
+  for (int i = wid * NR; i < NQ; i += kAttnWarps * NR) {
+    const elem_t* q[NR];
+    int pos[NR];
+#pragma unroll
+    for (int k = 0; k < NR; ++k) {
+      const int row = row_q0 + i + k;
+      pos[k] = rows[i + k].pos;
+      q[k] = rows[i + k].lo != INT32_MAX ? a.q + (static_cast<long long>(req.row0 + row / G) * a.Hq + h * G + row % G) * D : nullptr;
+    }
+    query_rows<D, NR>(a, q, pos, qs + i * kQTerms * D, qf + i * 4);
+  }
+  __syncthreads();
+  uint32_t qa[kQTerms][2 * W][4];
+  float qfac[2], qsum[2][NG];
+  TreeRow my[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = 16 * rw + r + 8 * i;
+#pragma unroll
+    for (int s = 0; s < kQTerms; ++s) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const uint4 c = *reinterpret_cast<const uint4*>(qs + row * kQTerms * D + s * D + (w / 2) * 64 + j * 16 + (w & 1) * 8);
+        qa[s][2 * w][i] = c.x; qa[s][2 * w][i + 2] = c.y;
+        qa[s][2 * w + 1][i] = c.z; qa[s][2 * w + 1][i + 2] = c.w;
+      }
+    }
+    qfac[i] = qf[row * 4];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) qsum[i][g] = qf[row * 4 + 1 + g];
+    my[i] = rows[row];
+  }
+  // keys from here on are seen by every row of the warp, up to the context's end
+  int all_lo = max(my[0].lo == INT32_MAX ? 0 : my[0].lo, my[1].lo == INT32_MAX ? 0 : my[1].lo);
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, o));
+
+  const WaitCtl<kPolled> ctl{flags, a.status, a.wait_limit_ns};
+  float acc[4 * W][4] = {};
+  float m[2] = {-1e30f, -1e30f}, l[2] = {}, zs[2][NG] = {};
+  int n = 0;
+  for (; n < n_mine; ++n) {
+    const int st = n % ST;
+    if (!mbar_wait_warp(bars + 8 * st, (n / ST) & 1, ctl)) break;
+    const uint8_t* tile = ring + st * 2 * S::TB;
+    const int key0 = (t0 + 2 * (kg + n * KG)) * kTile;
+    const uint32_t miss = gone >> (2 * st) & 3u;
+    float s[2][2][4];        // logits (base 2): tile, eight keys, (row, key) as the product leaves them
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        uint32_t kw[W];
+        ld_words<W>(tile + q * S::TB + (r + 8 * t) * (D / 2) + j * (D / 8), kw);
+        float d[NG][4] = {};
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          uint32_t x[4];
+          widen_f16(kw[w], x);
+#pragma unroll
+          for (int u = kQTerms - 1; u >= 0; --u) {
+            const uint32_t(&p)[4] = qa[u][2 * w], (&z)[4] = qa[u][2 * w + 1];
+            mma_f16(d[w / 2], p[0], p[1], p[2], p[3], x[0], x[1]);
+            mma_f16(d[w / 2], z[0], z[1], z[2], z[3], x[2], x[3]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float sk[NG], zk[NG];
+          ld_scales<NG>(tile + q * S::TB + 16 * D + (8 * t + 2 * j + e) * (4 * NG), sk, zk);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float v = 0.f;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) v = fmaf(sk[g], d[g][2 * i + e], fmaf(zk[g], qsum[i][g], v));
+            s[q][t][2 * i + e] = v * qfac[i];
+          }
+        }
+      }
+    }
+    const bool edge = key0 < all_lo || key0 + 2 * kTile > req.ctx || miss;
+    if (edge) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int key = key0 + q * kTile + 8 * t + 2 * j + e, d = key - req.ctx;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              bool on = my[i].lo != INT32_MAX && !(miss >> q & 1u);
+              if (d < 0) on = on && key >= my[i].lo;
+              else
+                on = on && d < req.n && (my[i].seen >> d & 1ull) &&
+                     (a.window < 0 || static_cast<long long>(my[i].pos) - tpos[d] <= a.window);
+              if (!on) s[q][t][2 * i + e] = -INFINITY;
+            }
+          }
+    }
+    float top[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      top[i] = fmaxf(fmax3(s[0][0][2 * i], s[0][0][2 * i + 1], fmaxf(s[0][1][2 * i], s[0][1][2 * i + 1])),
+                     fmax3(s[1][0][2 * i], s[1][0][2 * i + 1], fmaxf(s[1][1][2 * i], s[1][1][2 * i + 1])));
+    if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = top[i];
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        const float mn = fmaxf(m[i], x), al = ex2_approx(m[i] - mn);
+        m[i] = mn;
+        l[i] *= al;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) zs[i][g] *= al;
+#pragma unroll
+        for (int k = 0; k < 4 * W; ++k) {
+          acc[k][2 * i] *= al;
+          acc[k][2 * i + 1] *= al;
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint8_t* at = tile + q * S::TB;
+      uint32_t pa[kThreeTerms ? 3 : 1][NG][4];     // P times the values' steps, as operand registers
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        float sv[2][NG], zv[2][NG];
+        ld_scales<NG>(at + 17 * D + (8 * t + 2 * j) * (4 * NG), sv[0], zv[0]);
+        ld_scales<NG>(at + 17 * D + (8 * t + 2 * j + 1) * (4 * NG), sv[1], zv[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float p0 = ex2_approx(s[q][t][2 * i] - m[i]), p1 = ex2_approx(s[q][t][2 * i + 1] - m[i]);
+          l[i] += p0 + p1;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            float w0 = p0 * sv[0][g], w1 = p1 * sv[1][g], z0 = p0 * zv[0][g], z1 = p1 * zv[1][g];
+            if (edge) {        // another row may see the key: what it holds, a NaN even, is not this row's
+              if (s[q][t][2 * i] == -INFINITY) w0 = z0 = 0.f;
+              if (s[q][t][2 * i + 1] == -INFINITY) w1 = z1 = 0.f;
+            }
+            zs[i][g] += z0 + z1;
+            const uint32_t hi = pack_bf16x2(w0, w1);
+            pa[0][g][2 * t + i] = hi;
+            if constexpr (kThreeTerms) {
+              const float e0 = w0 - __uint_as_float(hi << 16), e1 = w1 - __uint_as_float(hi & 0xFFFF0000u);
+              const uint32_t mid = pack_bf16x2(e0, e1);
+              pa[1][g][2 * t + i] = mid;
+              pa[2][g][2 * t + i] = pack_bf16x2(e0 - __uint_as_float(mid << 16), e1 - __uint_as_float(mid & 0xFFFF0000u));
+            }
+          }
+        }
+      }
+      uint32_t va[W], vb[W];
+      ld_words<W>(at + 8 * D + j * D + r * (D / 8), va);
+      ld_words<W>(at + 8 * D + (j + 4) * D + r * (D / 8), vb);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        uint32_t x[4], y[4];
+        widen_bf16(va[w], x);
+        widen_bf16(vb[w], y);
+#pragma unroll
+        for (int u = (kThreeTerms ? 3 : 1) - 1; u >= 0; --u) {
+          const uint32_t(&p)[4] = pa[u][w / 2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma_bf16(acc[4 * w + i], p[0], p[1], p[2], p[3], x[i], y[i]);
+        }
+      }
+    }
+    __syncwarp();
+    if constexpr (RW == 1) {
+      if (issued < n_mine) issue(issued++);
+    } else {
+      // a stage is free once every warp of the group is through with it; the one
+      // of the step before is filled again, so that the wait is seldom one
+      if (lane == 0) mbar_arrive(frees + 8 * st);
+      if (n > 0 && issued < n_mine) {
+        if (rw == 0 && !mbar_wait_warp(frees + 8 * ((n - 1) % ST), ((n - 1) / ST) & 1, ctl)) {
+          ++n;
+          break;
+        }
+        issue(issued++);
+      }
+    }
+  }
+  // a wait that ran out: the copies still on their way land before the memory is used again
+  for (int k = n; k < issued; ++k) mbar_wait_drain(bars + 8 * (k % ST), (k / ST) & 1, kDrainLimitNs);
+  if (bad) atomicOr(a.status, bad);
+
+  // join the groups of warps: O, M, L of each row into shared memory
+  __syncthreads();
+  float* jo = reinterpret_cast<float*>(smem);                    // [warp][16][D]
+  float* jm = jo + kAttnWarps * 16 * D;                          // [warp][16][2]: M, L
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      zs[i][g] += __shfl_xor_sync(0xffffffffu, zs[i][g], 1);
+      zs[i][g] += __shfl_xor_sync(0xffffffffu, zs[i][g], 2);
+    }
+    const int row = wid * 16 + r + 8 * i;
+    // channel 64 g + 16 j + 8 e + 4 u + k is entry (2 i + e) of sum 4 (2 g + u) + k
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float z = zs[i][w / 2];
+        const int c = 2 * i + e;
+        *reinterpret_cast<float4*>(jo + row * D + (w / 2) * 64 + 16 * j + 8 * e + 4 * (w & 1)) =
+            make_float4(acc[4 * w][c] + z, acc[4 * w + 1][c] + z, acc[4 * w + 2][c] + z, acc[4 * w + 3][c] + z);
+      }
+    if (j == 0) {
+      jm[2 * row] = m[i];
+      jm[2 * row + 1] = l[i];
+    }
+  }
+  __syncthreads();
+  auto head_of = [&](int i) {       // index of row i's head in o and lse
+    const int row = row_q0 + i;
+    return static_cast<long long>(req.row0 + row / G) * a.Hq + h * G + row % G;
+  };
+  const long long item = (static_cast<long long>(b) * a.c.Hkv + h) * a.groups + qg;
+  const long long part0 = item * a.splits * NQ;
+  for (int i = wid; i < nq; i += kAttnWarps) {      // a warp a row, E channels a lane
+    float top = -1e30f, sum = 0.f, o[E] = {};
+#pragma unroll
+    for (int k = 0; k < KG; ++k) top = fmaxf(top, jm[2 * (k * NQ + i)]);
+#pragma unroll
+    for (int k = 0; k < KG; ++k) {
+      const float f = ex2_approx(jm[2 * (k * NQ + i)] - top);
+      sum = fmaf(f, jm[2 * (k * NQ + i) + 1], sum);
+      float x[E];
+      load_vec<E>(jo + (k * NQ + i) * D + lane * E, x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(f, x[e], o[e]);
+    }
+    if (rows[i].lo == INT_MAX) {     // sees nothing: tiles that every other row sees were not masked for it
+      top = -1e30f;
+      sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = 0.f;
+    }
+    if (chunks == 1) {
+      finish_head<D>(a, head_of(i), o, top, sum);
+    } else {
+      const long long at = part0 + static_cast<long long>(blockIdx.x) * NQ + i;
+      store_vec<E>(a.part + at * D + lane * E, o);
+      if (lane == 0) a.part_ml[at] = make_float2(top, sum);
+    }
+  }
+  if (chunks == 1) return;
+  __syncthreads();
+  if (tid == 0) {
+    __threadfence();      // after the barrier it covers what the CTA wrote
+    flags[1] = atomicAdd(a.count + item, 1u) == static_cast<unsigned>(chunks - 1);
+  }
+  __syncthreads();
+  if (!flags[1]) return;
+  __threadfence();
+  if (tid == 0) a.count[item] = 0;        // for the next call
+
+  // join the chunks in their order: a warp a row
+  for (int i = wid; i < nq; i += kAttnWarps) {
+    float top = -1e30f, sum = 0.f, o[E] = {};
+    for (int k = lane; k < chunks; k += 32) top = fmaxf(top, __ldcg(a.part_ml + part0 + static_cast<long long>(k) * NQ + i).x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+#pragma unroll 4
+    for (int k = 0; k < chunks; ++k) {
+      const long long at = part0 + static_cast<long long>(k) * NQ + i;
+      const float2 ml = __ldcg(a.part_ml + at);
+      float x[E];
+      if constexpr (E == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + at * D + lane * E));
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part + at * D + lane * E));
+        x[0] = v.x; x[1] = v.y;
+      }
+      const float f = ex2_approx(ml.x - top);
+      sum = fmaf(f, ml.y, sum);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(f, x[e], o[e]);
+    }
+    finish_head<D>(a, head_of(i), o, top, sum);
+  }
+}
+
+// Warps over rows, chunks and CTAs of a call, from what the host knows. Partial
+// results of split requests have to fit the decode workspace.
+struct TreeSplit {
+  int rw, groups, chunk, splits;
+  long long items;
+};
+inline TreeSplit tree_split(int B, int Hq, int Hkv, int d, int page, int max_pages, int window, int max_new, long long part_floats) {
+  constexpr long long kSetup = 24, kJoin = 8, kStep = 2 * kAttnWarps;
+  TreeSplit s;
+  const int rows = Hq / Hkv * max_new;
+  s.rw = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
+  const int nq = 16 * s.rw;
+  s.groups = (rows + nq - 1) / nq;
+  s.items = static_cast<long long>(B) * Hkv * s.groups;
+  const long long cap = static_cast<long long>(max_pages) * page;
+  long long keys = cap;
+  if (window >= 0 && static_cast<long long>(window) + max_new + kTile < cap) keys = static_cast<long long>(window) + max_new + kTile;
+  const long long tiles = (keys + kTile - 1) / kTile;
+  const long long slots = 152LL * tree_ctas_per_sm(d);
+  long long best = 0, chunk = tiles;
+  for (long long n = 1; n <= kMaxSplits; ++n) {
+    const long long c = ((tiles + n - 1) / n + kStep - 1) / kStep * kStep, real = (tiles + c - 1) / c;
+    if (real > 1 && s.items * real * nq * (d + 2) > part_floats) break;
+    const long long own = (c < tiles ? c : tiles) + kSetup;
+    const long long t = (s.items * real + slots - 1) / slots * own + (real > 1 ? kJoin + real / 2 : 0);
+    if (n == 1 || t < best) {
+      best = t;
+      chunk = c;
+    }
+    if (c == kStep) break;
+  }
+  s.chunk = static_cast<int>(chunk);
+  s.splits = static_cast<int>((tiles + chunk - 1) / chunk);
+  return s;
+}
+
+}  // namespace kv4
+}  // namespace swa

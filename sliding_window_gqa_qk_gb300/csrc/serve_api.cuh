@@ -1,0 +1,250 @@
+// Host side of the norm, of the 4-bit projections and of the drafted tokens'
+// entry points of include/swa_attn.h: argument checks and launches. Included
+// at the end of swa_attn.cu, behind decode_api.cuh, whose helpers it uses.
+#pragma once
+
+#include "kv4_tree.cuh"
+#include "norm.cuh"
+#include "w4.cuh"
+
+namespace {
+
+swa_status check_norm(long long rows, int C) {
+  if (rows < 0 || C < 8 || C % 8 != 0) return SWA_ERR_INVALID_ARG;
+  return C > norm::kMaxC || rows > INT32_MAX ? SWA_ERR_UNSUPPORTED : SWA_OK;
+}
+
+swa_status check_w4(int N, int K) {
+  if (N < 1 || K < 8 || K % 8 != 0) return SWA_ERR_INVALID_ARG;
+  return N > w4::kMaxN || K > w4::kMaxK ? SWA_ERR_UNSUPPORTED : SWA_OK;
+}
+long long w4_tiles(int N, int K) {
+  return static_cast<long long>((N + w4::kRows - 1) / w4::kRows) * ((K + w4::kCols - 1) / w4::kCols);
+}
+
+template <w4::XKind X>
+swa_status launch_linear(const w4::LinArgs& a, cudaStream_t st) {
+  const long long panels = (a.N + w4::kRows - 1) / w4::kRows;
+  auto go = [&](auto kern, int nt) {
+    const long long blocks = panels * ((a.M + 8 * nt - 1) / (8 * nt));
+    if (blocks > INT32_MAX) return SWA_ERR_UNSUPPORTED;
+    kern<<<static_cast<unsigned>(blocks), w4::kLinWarps * 32, 0, st>>>(a);
+    return launched();
+  };
+  if (a.M <= 8) return go(w4::linear_kernel<X, 1>, 1);
+  if (a.M <= 16) return go(w4::linear_kernel<X, 2>, 2);
+  return go(w4::linear_kernel<X, 4>, 4);
+}
+
+swa_status check_tokens(int B, int n_tokens, int max_new) {
+  if (B < 0 || n_tokens < 0 || max_new < 1) return SWA_ERR_INVALID_ARG;
+  if (B == 0 && n_tokens > 0) return SWA_ERR_INVALID_ARG;
+  return max_new > kv4::kTreeTokens ? SWA_ERR_UNSUPPORTED : SWA_OK;
+}
+
+constexpr long long kTreePartFloats = static_cast<long long>((kKv4Bytes - kKv4Part) / sizeof(float)) - 64;
+
+template <int D, int RW, bool kPolled>
+swa_status launch_tree(const kv4::TreeAttnArgs& a, cudaStream_t st) {
+  auto kern = kv4::tree_attn_kernel<D, RW, kPolled>;
+  constexpr int smem = kv4::TreeSmem<D, RW>::bytes;
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    cudaGetLastError();
+    return SWA_ERR_CUDA;
+  }
+  kern<<<dim3(a.splits, a.c.Hkv * a.groups, a.B), kv4::kAttnWarps * 32, smem, st>>>(a);
+  return launched();
+}
+template <bool kPolled>
+swa_status launch_tree(const kv4::TreeAttnArgs& a, int d, int rw, cudaStream_t st) {
+  if (d == 64)
+    return rw == 1 ? launch_tree<64, 1, kPolled>(a, st) : rw == 2 ? launch_tree<64, 2, kPolled>(a, st) : launch_tree<64, 4, kPolled>(a, st);
+  return rw == 1 ? launch_tree<128, 1, kPolled>(a, st) : rw == 2 ? launch_tree<128, 2, kPolled>(a, st) : launch_tree<128, 4, kPolled>(a, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+swa_status swa_rms_norm(long long rows, int C, float eps, const void* x, const void* add, const float* gain, void* h, void* y,
+                        void* y8, float* scale, float* rstd, void* stream) {
+  swa_status s = check_norm(rows, C);
+  if (s != SWA_OK) return s;
+  if (!std::isfinite(eps) || eps < 0.f) return SWA_ERR_INVALID_ARG;
+  if ((y == nullptr) == (y8 == nullptr) || (y8 != nullptr) != (scale != nullptr)) return SWA_ERR_INVALID_ARG;
+  if (rows == 0) return SWA_OK;
+  if (x == nullptr || (add != nullptr && h == nullptr) || (h != nullptr && (h == y || h == y8))) return SWA_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(add, 16) || !aligned(gain, 16) || !aligned(h, 16) || !aligned(y, 16) || !aligned(y8, 16) ||
+      !aligned(scale, 4) || !aligned(rstd, 4))
+    return SWA_ERR_INVALID_ARG;
+  if ((s = check_device()) != SWA_OK) return s;
+  norm::FwdArgs a{};
+  a.rows = rows; a.C = C; a.eps = eps;
+  a.x = static_cast<const elem_t*>(x); a.add = static_cast<const elem_t*>(add); a.gain = gain;
+  a.h = static_cast<elem_t*>(h == x ? (add != nullptr ? h : nullptr) : h);   // h is x already where nothing is added
+  a.y = static_cast<elem_t*>(y); a.y8 = static_cast<uint8_t*>(y8); a.scale = scale; a.rstd = rstd;
+  const int blocks = norm::row_blocks(rows, C, norm::kFwdThreadsPerSm);
+  norm::by_width(C, [&](auto tpr, auto vpt) {
+    constexpr int T = decltype(tpr)::value, V = decltype(vpt)::value;
+    const int threads = T == 32 ? 256 : T;
+    if (y8 != nullptr) norm::fwd_kernel<T, V, true><<<blocks, threads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    else norm::fwd_kernel<T, V, false><<<blocks, threads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  });
+  return launched();
+}
+
+size_t swa_rms_norm_workspace_size(long long rows, int C) {
+  if (check_norm(rows, C) != SWA_OK) return 0;
+  return (static_cast<size_t>(norm::row_blocks(rows, C, norm::kBwdThreadsPerSm)) * C * sizeof(float) + 255) / 256 * 256;
+}
+
+swa_status swa_rms_norm_bwd(long long rows, int C, const void* h, const float* rstd, const float* gain, const void* dy,
+                            const void* dh, void* dx, float* dgain, void* workspace, size_t ws_bytes, void* stream) {
+  swa_status s = check_norm(rows, C);
+  if (s != SWA_OK) return s;
+  if (!aligned(h, 16) || !aligned(rstd, 4) || !aligned(gain, 16) || !aligned(dy, 16) || !aligned(dh, 16) || !aligned(dx, 16) ||
+      !aligned(dgain, 4))
+    return SWA_ERR_INVALID_ARG;
+  if (rows > 0 && (h == nullptr || rstd == nullptr || dy == nullptr || dx == nullptr)) return SWA_ERR_INVALID_ARG;
+  if (dgain != nullptr && rows > 0) {
+    if (workspace == nullptr || !aligned(workspace, 256)) return SWA_ERR_INVALID_ARG;
+    if (ws_bytes < swa_rms_norm_workspace_size(rows, C)) return SWA_ERR_WORKSPACE;
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    if (dgain != nullptr && cudaMemsetAsync(dgain, 0, static_cast<size_t>(C) * sizeof(float), st) != cudaSuccess) return SWA_ERR_CUDA;
+    return SWA_OK;
+  }
+  if ((s = check_device()) != SWA_OK) return s;
+  norm::BwdArgs a{};
+  a.rows = rows; a.C = C;
+  a.h = static_cast<const elem_t*>(h); a.rstd = rstd; a.gain = gain;
+  a.dy = static_cast<const elem_t*>(dy); a.dh = static_cast<const elem_t*>(dh); a.dx = static_cast<elem_t*>(dx);
+  a.part = dgain != nullptr ? static_cast<float*>(workspace) : nullptr;
+  const int blocks = norm::row_blocks(rows, C, norm::kBwdThreadsPerSm);
+  norm::by_width(C, [&](auto tpr, auto vpt) {
+    constexpr int T = decltype(tpr)::value, V = decltype(vpt)::value;
+    norm::bwd_kernel<T, V><<<blocks, T == 32 ? 256 : T, T == 32 ? C * sizeof(float) : 0, st>>>(a);
+  });
+  if ((s = launched()) != SWA_OK || dgain == nullptr) return s;
+  norm::gain_kernel<<<(C + 31) / 32, 256, 0, st>>>(a.part, blocks, C, dgain);
+  return launched();
+}
+
+size_t swa_w4_size(int N, int K) { return check_w4(N, K) != SWA_OK ? 0 : static_cast<size_t>(w4_tiles(N, K)) * w4::kTileBytes; }
+
+swa_status swa_w4_pack(int N, int K, const void* w, void* w4, void* stream) {
+  swa_status s = check_w4(N, K);
+  if (s != SWA_OK) return s;
+  if (!tensor_ok(w) || !tensor_ok(w4)) return SWA_ERR_INVALID_ARG;
+  if ((s = check_device()) != SWA_OK) return s;
+  const w4::PackArgs a{N, K, static_cast<const elem_t*>(w), static_cast<uint8_t*>(w4)};
+  w4::pack_kernel<<<flat_grid(w4_tiles(N, K), 8, num_sms() * 8LL), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return launched();
+}
+
+swa_status swa_w4_unpack(int N, int K, const void* w4, void* w, void* stream) {
+  swa_status s = check_w4(N, K);
+  if (s != SWA_OK) return s;
+  if (!tensor_ok(w) || !tensor_ok(w4)) return SWA_ERR_INVALID_ARG;
+  if ((s = check_device()) != SWA_OK) return s;
+  w4::unpack_kernel<<<flat_grid(w4_tiles(N, K), 8, num_sms() * 8LL), 256, 0, static_cast<cudaStream_t>(stream)>>>(
+      N, K, static_cast<const uint8_t*>(w4), static_cast<elem_t*>(w));
+  return launched();
+}
+
+swa_status swa_w4_linear(int M, int N, int K, const void* x, const float* x_scale, const void* w4, const void* add, void* y,
+                         void* stream) {
+  swa_status s = check_w4(N, K);
+  if (s != SWA_OK) return s;
+  if (M < 0) return SWA_ERR_INVALID_ARG;
+  if (M == 0) return SWA_OK;
+  if (!tensor_ok(x) || !tensor_ok(w4) || !tensor_ok(y) || !aligned(add, 16) || !aligned(x_scale, 4)) return SWA_ERR_INVALID_ARG;
+  if (x == y) return SWA_ERR_INVALID_ARG;
+  if ((s = check_device()) != SWA_OK) return s;
+  const w4::LinArgs a{M, N, K, x, x_scale, static_cast<const uint8_t*>(w4), static_cast<const elem_t*>(add), static_cast<elem_t*>(y)};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return x_scale != nullptr ? launch_linear<w4::kX8>(a, st) : launch_linear<w4::kXElem>(a, st);
+}
+
+swa_status swa_kv4_tree(int B, int n_tokens, int max_new, const int32_t* parent, const int32_t* cu, const int32_t* lens,
+                        int32_t* pos, int64_t* seen, void* workspace, size_t ws_bytes, void* stream) {
+  swa_status s = check_tokens(B, n_tokens, max_new);
+  if (s != SWA_OK) return s;
+  if (!aligned(parent, 4) || !aligned(cu, 4) || !aligned(lens, 4) || !aligned(pos, 4) || !aligned(seen, 8)) return SWA_ERR_INVALID_ARG;
+  if ((s = check_header(workspace, ws_bytes)) != SWA_OK) return s;
+  if (n_tokens == 0) return SWA_OK;
+  if (parent == nullptr || cu == nullptr || lens == nullptr || pos == nullptr || seen == nullptr) return SWA_ERR_INVALID_ARG;
+  if ((s = check_device()) != SWA_OK) return s;
+  const kv4::TreeArgs a{B, n_tokens, max_new, parent, cu, lens, pos, seen, static_cast<uint32_t*>(workspace)};
+  kv4::tree_kernel<<<flat_grid(B, kv4::kTreeWarps, num_sms() * 8LL), kv4::kTreeWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return launched();
+}
+
+swa_status swa_kv4_move(const swa_params* p, const swa_kv4_cache* c, const int64_t* src, const int64_t* dst, void* workspace,
+                        size_t ws_bytes, void* stream) {
+  swa_status s = check_rows(p);
+  if (s != SWA_OK) return s;
+  kv4::MoveArgs a{};
+  if ((s = check_cache(p, c, a.c)) != SWA_OK) return s;
+  if (p->T > kv4::kTreeTokens) return SWA_ERR_UNSUPPORTED;
+  if (!aligned(src, 8) || !aligned(dst, 8)) return SWA_ERR_INVALID_ARG;
+  if ((s = check_header(workspace, ws_bytes)) != SWA_OK) return s;
+  if (p->B == 0 || p->T == 0) return SWA_OK;
+  if (src == nullptr || dst == nullptr) return SWA_ERR_INVALID_ARG;
+  if ((s = check_device()) != SWA_OK) return s;
+  a.B = p->B; a.T = p->T; a.src = src; a.dst = dst;
+  a.status = static_cast<uint32_t*>(workspace);
+  const int grid = flat_grid(static_cast<long long>(p->B) * p->Hkv, 1, num_sms() * 64LL);
+  by_head_dim(p->d, [&] { kv4::move_kernel<64><<<grid, kv4::kMoveThreads, 0, static_cast<cudaStream_t>(stream)>>>(a); },
+              [&] { kv4::move_kernel<128><<<grid, kv4::kMoveThreads, 0, static_cast<cudaStream_t>(stream)>>>(a); });
+  return launched();
+}
+
+swa_status swa_kv4_tree_attn(const swa_params* p, const swa_extras* ex, const swa_kv4_cache* c, const swa_rope* r,
+                             int n_tokens, int max_new, const void* q, const float* gq, const int32_t* table, int max_pages,
+                             const int32_t* lens, const int32_t* cu, const int32_t* pos, const int64_t* seen, void* o,
+                             float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  swa_status s = check_params(p);
+  if (s != SWA_OK) return s;
+  if (p->T != 1 || p->causal != 1) return SWA_ERR_INVALID_ARG;
+  if ((s = check_tokens(p->B, n_tokens, max_new)) != SWA_OK) return s;
+  kv4::TreeAttnArgs a{};
+  if ((s = check_cache(p, c, a.c)) != SWA_OK) return s;
+  bool rope = false;
+  if ((s = check_rope(r, p->d, rope)) != SWA_OK) return s;
+  if (ex != nullptr && (ex->rope_cos != nullptr || ex->rope_sin != nullptr)) return SWA_ERR_INVALID_ARG;
+  if (!width_ok(max_pages, c->page)) return SWA_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned(workspace, 256)) return SWA_ERR_INVALID_ARG;
+  if (ws_bytes < kKv4Bytes) return SWA_ERR_WORKSPACE;
+  if (n_tokens == 0) return SWA_OK;
+  if (!tensor_ok(q) || !tensor_ok(o) || lse == nullptr || table == nullptr || lens == nullptr || cu == nullptr || pos == nullptr ||
+      seen == nullptr)
+    return SWA_ERR_INVALID_ARG;
+  if (!aligned(lse, 4) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(gq, 16) || !aligned(cu, 4) || !aligned(pos, 4) ||
+      !aligned(seen, 8))
+    return SWA_ERR_INVALID_ARG;
+  const kv4::TreeSplit sp = kv4::tree_split(p->B, p->Hq, p->Hkv, p->d, c->page, max_pages, p->window, max_new, kTreePartFloats);
+  // (groups of at least 64 rows of at most 64 tokens: no more items than B * Hq, and than the workspace's counters)
+  if ((s = check_device()) != SWA_OK) return s;
+  a.B = p->B; a.Hq = p->Hq; a.max_pages = max_pages; a.window = p->window;
+  a.scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt(static_cast<float>(p->d));
+  a.eps = p->eps;
+  a.q = static_cast<const elem_t*>(q); a.gq = gq;
+  if (rope) {
+    a.rcos = r->cos; a.rsin = r->sin; a.rows = r->rows; a.rot = r->rot; a.interleaved = r->interleaved;
+  }
+  a.table = table; a.lens = lens; a.cu = cu; a.pos = pos; a.seen = seen;
+  a.N = n_tokens; a.max_new = max_new;
+  a.o = static_cast<elem_t*>(o); a.lse = lse;
+  a.status = static_cast<uint32_t*>(workspace);
+  a.chunk = sp.chunk; a.splits = sp.splits; a.groups = sp.groups;
+  a.count = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(workspace) + kKv4Count);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kKv4Part);
+  a.part_ml = reinterpret_cast<float2*>(a.part + sp.items * sp.splits * 16 * sp.rw * p->d);
+  a.wait_limit_ns = ex != nullptr && ex->wait_limit_ns != 0 ? ex->wait_limit_ns : kWaitLimitNs;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return a.wait_limit_ns < kPollBelowNs ? launch_tree<true>(a, p->d, sp.rw, st) : launch_tree<false>(a, p->d, sp.rw, st);
+}
+
+}  // extern "C"

@@ -997,3 +997,4 @@ const char* swa_build_info(void) {
 }  // extern "C"
 
 #include "decode_api.cuh"
+#include "serve_api.cuh"
