@@ -679,13 +679,16 @@ swa_status swa_rms_norm_bwd(long long rows, int C, const void* h, const float* r
  *
  * swa_w4_linear: x [M][K] elem, or e4m3 where x_scale (fp32 [M]) is given: the pair
  * that swa_rms_norm makes. add [M][N] or NULL; it may be y. x, add and y are 16-byte
- * aligned. Products are exact, sums fp32.
+ * aligned. Sums are fp32. Products are exact in calls of up to 32 rows and in the
+ * fp32 library; in larger bf16 calls a weight s (n - 8) enters rounded to bf16.
+ * workspace: as in swa_rope_apply (the pipeline waits of larger bf16 calls report
+ * there). K is cut into parts that are added in a fixed order.
  */
 size_t swa_w4_size(int N, int K);
 swa_status swa_w4_pack(int N, int K, const void* w, void* w4, void* stream);
 swa_status swa_w4_unpack(int N, int K, const void* w4, void* w, void* stream);
 swa_status swa_w4_linear(int M, int N, int K, const void* x, const float* x_scale, const void* w4, const void* add, void* y,
-                         void* stream);
+                         void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * Synchronises `stream`, reads the workspace status word, clears it, and

@@ -190,7 +190,7 @@ def load(kind: str = "bf16") -> ctypes.CDLL:
             ("swa_rms_norm_bwd", [L, I] + [_vp] * 8 + [Z, _vp]),
             ("swa_w4_pack", [I, I] + [_vp] * 3),
             ("swa_w4_unpack", [I, I] + [_vp] * 3),
-            ("swa_w4_linear", [I] * 3 + [_vp] * 6)):
+            ("swa_w4_linear", [I] * 3 + [_vp] * 5 + [_vp, Z, _vp])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = I
     for name, args in (("swa_kv4_cache_size", [P, I, I]), ("swa_kv4_workspace_size", [P, I, I]),
@@ -509,9 +509,9 @@ def swa_w4_unpack(N, K, w4, w, stream=None, kind=None) -> int:
     return int(load(kind or _kind_of(w)).swa_w4_unpack(int(N), int(K), _ptr(w4), _ptr(w), _stream(stream)))
 
 
-def swa_w4_linear(M, N, K, x, x_scale, w4, add, y, stream=None, kind=None) -> int:
+def swa_w4_linear(M, N, K, x, x_scale, w4, add, y, stream=None, kind=None, ws=None, ws_bytes=None) -> int:
     return int(load(kind or _kind_of(y)).swa_w4_linear(int(M), int(N), int(K), _ptr(x), _ptr(x_scale), _ptr(w4), _ptr(add), _ptr(y),
-                                                       _stream(stream)))
+                                                       _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream)))
 
 
 def swa_attn_check_status(ws, stream=None, kind: str = "bf16") -> int:
@@ -1165,11 +1165,13 @@ def w4_unpack(w4, out_features: int, in_features: int, *, dtype=torch.bfloat16, 
     return w
 
 
-def w4_linear(x, w4, *, out_features: Optional[int] = None, scale=None, add=None, dtype=None, out=None, stream=None):
+def w4_linear(x, w4, *, out_features: Optional[int] = None, scale=None, add=None, dtype=None, out=None, workspace=None,
+              stream=None):
     """y = x W^T (+ add) [..., out_features] for x [..., K] and weights of w4_pack
     (out_features: N; None: a multiple of 16, all that w4 holds). x is bf16 or fp32, or
     float8_e4m3fn with ``scale`` fp32 [...] (rms_norm's pair); then ``dtype`` is y's
-    (bf16 by default). ``out``: y, which may be ``add``."""
+    (bf16 by default). ``out``: y, which may be ``add``. ``workspace``: where a wait
+    that ran out is reported (swa_attn_check_status)."""
     M, K = _rows_of("x", x)
     dev = x.device
     if w4.dim() != 3:
@@ -1185,13 +1187,15 @@ def w4_linear(x, w4, *, out_features: Optional[int] = None, scale=None, add=None
     shape = (*x.shape[:-1], N)
     xa, wa = _at("x", x, dt if scale is None else _F8, x.shape, dev), _at("w4", w4, _U8, _w4_tiles(N, K), dev)
     sa, aa, oa = _at("scale", scale, _F32, x.shape[:-1], dev), _at("add", add, dt, shape, dev), _at("out", out, dt, shape, dev)
+    ws, nws = _ws_at(workspace, dev)
     st = _stream_here(dev, stream)
     if st is None:
-        return _there(dev, stream, lambda: w4_linear(x, w4, out_features=N, scale=scale, add=add, dtype=dt, out=out))
+        return _there(dev, stream, lambda: w4_linear(x, w4, out_features=N, scale=scale, add=add, dtype=dt, out=out,
+                                                     workspace=workspace))
     if out is None:
         out = torch.empty(shape, dtype=dt, device=dev)
         oa = out.data_ptr()
-    s = lib.swa_w4_linear(M, N, K, xa, sa, wa, aa, oa, st)
+    s = lib.swa_w4_linear(M, N, K, xa, sa, wa, aa, oa, ws, nws, st)
     if s:
         raise SwaError(s, "swa_w4_linear")
     return out

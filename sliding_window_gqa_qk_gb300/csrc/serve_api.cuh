@@ -6,6 +6,9 @@
 #include "kv4_tree.cuh"
 #include "norm.cuh"
 #include "w4.cuh"
+#if !defined(SWA_ELEM_FP32)
+#include "w4_tc.cuh"
+#endif
 
 namespace {
 
@@ -22,18 +25,66 @@ long long w4_tiles(int N, int K) {
   return static_cast<long long>((N + w4::kRows - 1) / w4::kRows) * ((K + w4::kCols - 1) / w4::kCols);
 }
 
-template <w4::XKind X>
-swa_status launch_linear(const w4::LinArgs& a, cudaStream_t st) {
+// Which form a call takes in the bf16 library (GB300, us):
+//   up to kFewRows rows   products with the weights as the 16-row operand (32 rows at 8192 x 8192 22.3; the
+//                         tcgen05 form takes 22.9 from 33 to 64 rows, and from 9 on)
+//   of these, long rows   x in shared memory, K over a cluster: from K = 4096 on (8 rows: 4096 x 4096 6.9 for 7.6,
+//                         1536 x 16384 14 for 28; but 16384 x 1536 10.1 for 6.2, 2048 x 2048 5.7 for 4.3), and for
+//                         25 to 32 rows of large layers (16384 x 1536 13.6 for 17.6; 2048 x 2048 7.0 for 6.6)
+constexpr int kFewRows = 32;
+bool wide_form(const w4::LinArgs& a) { return a.K >= 4096 || (a.M > 24 && w4_tiles(a.N, a.K) >= 16384); }
+
+#if !defined(SWA_ELEM_FP32)
+template <w4::XKind X, int NT, int PN>
+swa_status launch_wide(const w4::LinArgs& l, cudaStream_t st) {
+  using S = w4::WideShape<X, NT, PN>;
+  const long long groups = (l.N + S::RN - 1) / S::RN;
+  const int chunks = (l.K + w4::kChunk - 1) / w4::kChunk;
+  w4::WideArgs a{l, 1, 0};
+  while (a.splits < 8 && groups * a.splits * 2 <= 2 * 152 && chunks >= 2 * a.splits) a.splits *= 2;
+  a.per = (chunks + a.splits - 1) / a.splits;
+  auto kern = w4::linear_wide_kernel<X, NT, PN>;
+  if (S::bytes > 48 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes) != cudaSuccess) {
+    cudaGetLastError();
+    return SWA_ERR_CUDA;
+  }
+  return w4::launch_cluster(kern, groups * a.splits, w4::kWideWarps * 32, S::bytes, a.splits, st, a);
+}
+#endif
+
+template <w4::XKind X, int NT>
+swa_status launch_few(const w4::LinArgs& a, cudaStream_t st) {
   const long long panels = (a.N + w4::kRows - 1) / w4::kRows;
-  auto go = [&](auto kern, int nt) {
-    const long long blocks = panels * ((a.M + 8 * nt - 1) / (8 * nt));
-    if (blocks > INT32_MAX) return SWA_ERR_UNSUPPORTED;
-    kern<<<static_cast<unsigned>(blocks), w4::kLinWarps * 32, 0, st>>>(a);
-    return launched();
-  };
-  if (a.M <= 8) return go(w4::linear_kernel<X, 1>, 1);
-  if (a.M <= 16) return go(w4::linear_kernel<X, 2>, 2);
-  return go(w4::linear_kernel<X, 4>, 4);
+#if !defined(SWA_ELEM_FP32)
+  // two panels a warp where the CTAs of their groups still fill the GPU and the sums the registers
+  if (a.M <= 8 * NT && wide_form(a)) {
+    if constexpr (NT <= 2) {
+      if (panels >= 2 * 8 * 19) return launch_wide<X, NT, 2>(a, st);
+    }
+    return launch_wide<X, NT, 1>(a, st);
+  }
+#endif
+  const long long grid = panels * ((a.M + 8 * NT - 1) / (8 * NT));
+  if (grid > INT32_MAX) return SWA_ERR_UNSUPPORTED;
+  if (a.K < 32 * w4::kCols) w4::linear_kernel<X, NT, 4><<<static_cast<unsigned>(grid), 128, 0, st>>>(a);
+  else w4::linear_kernel<X, NT, 8><<<static_cast<unsigned>(grid), 256, 0, st>>>(a);
+  return launched();
+}
+
+template <w4::XKind X>
+swa_status launch_linear(const w4::LinArgs& a, uint32_t* status, cudaStream_t st) {
+#if !defined(SWA_ELEM_FP32)
+  constexpr bool x8 = X == w4::kX8;
+  if (a.M > kFewRows && (!x8 || a.K % 16 == 0)) {      // (e4m3 rows come by TMA, whose strides are multiples of 16 bytes)
+    if (a.M <= 64) return w4::launch_linear_tc<64, x8>(a, status, kWaitLimitNs, st);
+    if (x8 || a.M <= 128) return w4::launch_linear_tc<128, x8>(a, status, kWaitLimitNs, st);
+    return w4::launch_linear_tc<256, false>(a, status, kWaitLimitNs, st);
+  }
+#endif
+  if (a.M <= 8) return launch_few<X, 1>(a, st);
+  if (a.M <= 16) return launch_few<X, 2>(a, st);
+  if (a.M <= 24) return launch_few<X, 3>(a, st);
+  return launch_few<X, 4>(a, st);
 }
 
 swa_status check_tokens(int B, int n_tokens, int max_new) {
@@ -154,17 +205,19 @@ swa_status swa_w4_unpack(int N, int K, const void* w4, void* w, void* stream) {
 }
 
 swa_status swa_w4_linear(int M, int N, int K, const void* x, const float* x_scale, const void* w4, const void* add, void* y,
-                         void* stream) {
+                         void* workspace, size_t ws_bytes, void* stream) {
   swa_status s = check_w4(N, K);
   if (s != SWA_OK) return s;
   if (M < 0) return SWA_ERR_INVALID_ARG;
+  if ((s = check_header(workspace, ws_bytes)) != SWA_OK) return s;
   if (M == 0) return SWA_OK;
   if (!tensor_ok(x) || !tensor_ok(w4) || !tensor_ok(y) || !aligned(add, 16) || !aligned(x_scale, 4)) return SWA_ERR_INVALID_ARG;
   if (x == y) return SWA_ERR_INVALID_ARG;
   if ((s = check_device()) != SWA_OK) return s;
   const w4::LinArgs a{M, N, K, x, x_scale, static_cast<const uint8_t*>(w4), static_cast<const elem_t*>(add), static_cast<elem_t*>(y)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return x_scale != nullptr ? launch_linear<w4::kX8>(a, st) : launch_linear<w4::kXElem>(a, st);
+  uint32_t* status = static_cast<uint32_t*>(workspace);
+  return x_scale != nullptr ? launch_linear<w4::kX8>(a, status, st) : launch_linear<w4::kXElem>(a, status, st);
 }
 
 swa_status swa_kv4_tree(int B, int n_tokens, int max_new, const int32_t* parent, const int32_t* cu, const int32_t* lens,

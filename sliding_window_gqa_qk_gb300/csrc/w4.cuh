@@ -125,8 +125,10 @@ __global__ void __launch_bounds__(256) unpack_kernel(int N, int K, const uint8_t
 // them once a tile, in fp32.
 //   x bf16: as it is.   x e4m3: widened to fp16 (exact), with fp16 numbers.
 //   x fp32: three bf16 terms of 8 bits each, cut off, which hold it exactly.
-// The warps of a CTA take every kWarps-th tile of the same 16 weight rows and
-// add their sums up in shared memory, in their order.
+// Small layers (linear_kernel, and all of the fp32 library): the warps of a CTA
+// take every fourth (eighth) tile of the same 16 weight rows, x straight from
+// memory, and add their sums up in shared memory, in their order. This is
+// latency: one token through 1536 x 768 weights takes 2.2 us.
 // ---------------------------------------------------------------------------
 enum XKind { kXElem, kX8 };
 
@@ -139,7 +141,6 @@ struct LinArgs {
   elem_t* y;                  // [M, N]
 };
 
-constexpr int kLinWarps = 4;
 constexpr int kTerms = sizeof(elem_t) == 4 ? 3 : 1;
 
 // 16 entries of a row of x as operand registers: b[term][word][2].
@@ -201,6 +202,13 @@ __device__ __forceinline__ void load_x(const LinArgs& a, int m, int k, XFrag<X>&
   }
 }
 
+// 16 bytes that no one else reads.
+__device__ __forceinline__ uint4 ld_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 template <XKind X>
 __device__ __forceinline__ void widen(uint32_t w, uint32_t (&h)[4]) {
   if constexpr (X == kX8) kv4::widen_f16(w, h); else kv4::widen_bf16(w, h);
@@ -211,57 +219,290 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&h)[4], const
   else kv4::mma_bf16(c, h[0], h[1], h[2], h[3], b[0], b[1]);
 }
 
-// NT operands of eight rows of x.
-template <XKind X, int NT>
-__global__ void __launch_bounds__(kLinWarps * 32) linear_kernel(const __grid_constant__ LinArgs a) {
-  constexpr int MB = 8 * NT;
-  __shared__ float part[kLinWarps][MB][kRows + 1];
+// Eight sums of row m of x and weight rows n .. n + 7 into y.
+template <XKind X>
+__device__ __forceinline__ void finish8(const LinArgs& a, int m, int n, bool wide, float (&y)[8]) {
+  const float xs = X == kX8 ? a.xs[m] : 1.0f;
+  const long long at = static_cast<long long>(m) * a.N + n;
+#if !defined(SWA_ELEM_FP32)
+  if (wide) {
+    float b[8] = {};
+    if (a.add != nullptr) unpack16(ld16(a.add + at), b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = fmaf(y[e], xs, b[e]);
+    st16(a.y + at, pack16(y));
+    return;
+  }
+#endif
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (n + e < a.N) a.y[at + e] = from_f32<elem_t>(fmaf(y[e], xs, a.add != nullptr ? to_f32(a.add[at + e]) : 0.f));
+}
+
+// NT operands of eight rows of x, NW warps.
+template <XKind X, int NT, int NW>
+__global__ void __launch_bounds__(NW * 32) linear_kernel(const __grid_constant__ LinArgs a) {
+  constexpr int MB = 8 * NT, kAhead = 2;
+  __shared__ float part[NW][MB][kRows + 1];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, r = lane >> 2, j = lane & 3;
   const int P = (a.N + kRows - 1) / kRows, Q = (a.K + kCols - 1) / kCols;
   const int panel = static_cast<int>(blockIdx.x % P), m0 = static_cast<int>(blockIdx.x / P) * MB;
   const uint8_t* w = a.w4 + static_cast<long long>(panel) * Q * kTileBytes;
+  uint4 v[kAhead];
+  uint32_t sc[kAhead];
+  auto load = [&](int i, int q) {
+    if (q < Q) {
+      const uint8_t* tile = w + static_cast<long long>(q) * kTileBytes;
+      v[i] = ld_once(tile + 16 * lane);
+      sc[i] = *reinterpret_cast<const uint32_t*>(tile + 512 + 4 * r);
+    }
+  };
   float acc[NT][4] = {};
-  for (int q = wid; q < Q; q += kLinWarps) {
-    const uint8_t* tile = w + static_cast<long long>(q) * kTileBytes;
-    const uint4 v = ld16(tile + 16 * lane);
-    const uint32_t sc = *reinterpret_cast<const uint32_t*>(tile + 512 + 4 * r);
-    const uint32_t word[4] = {v.x, v.y, v.z, v.w};
-    uint32_t h[4][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) widen<X>(word[i], h[i]);
-    const float s0 = __uint_as_float(sc << 16), s1 = __uint_as_float(sc & 0xFFFF0000u);
+  for (int i = 0; i < kAhead; ++i) load(i, wid + i * NW);
+  for (int q0 = wid; q0 < Q; q0 += NW * kAhead) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      XFrag<X> f;
-      load_x<X>(a, m0 + 8 * t + r, q * kCols + 16 * j, f);
-      float d[4] = {};
+    for (int i = 0; i < kAhead; ++i) {
+      const int q = q0 + i * NW;
+      if (q >= Q) break;
+      XFrag<X> f[NT];
 #pragma unroll
-      for (int s = XFrag<X>::T - 1; s >= 0; --s)
+      for (int t = 0; t < NT; ++t) load_x<X>(a, m0 + 8 * t + r, q * kCols + 16 * j, f[t]);
+      const uint32_t word[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      uint32_t h[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mma<X>(d, h[i], f.b[s][i]);
-      acc[t][0] = fmaf(s0, d[0], acc[t][0]);
-      acc[t][1] = fmaf(s0, d[1], acc[t][1]);
-      acc[t][2] = fmaf(s1, d[2], acc[t][2]);
-      acc[t][3] = fmaf(s1, d[3], acc[t][3]);
+      for (int k = 0; k < 4; ++k) widen<X>(word[k], h[k]);
+      const float s0 = __uint_as_float(sc[i] << 16), s1 = __uint_as_float(sc[i] & 0xFFFF0000u);
+      load(i, q + NW * kAhead);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float d[4] = {};
+#pragma unroll
+        for (int s = XFrag<X>::T - 1; s >= 0; --s)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma<X>(d, h[k], f[t].b[s][k]);
+        acc[t][0] = fmaf(s0, d[0], acc[t][0]);
+        acc[t][1] = fmaf(s0, d[1], acc[t][1]);
+        acc[t][2] = fmaf(s1, d[2], acc[t][2]);
+        acc[t][3] = fmaf(s1, d[3], acc[t][3]);
+      }
     }
   }
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) part[wid][8 * t + 2 * j + (e & 1)][r + 8 * (e >> 1)] = acc[t][e];
-  }
   __syncthreads();
-  for (int i = tid; i < MB * kRows; i += kLinWarps * 32) {
+  for (int i = tid; i < MB * kRows; i += NW * 32) {
     const int m = m0 + i / kRows, n = panel * kRows + i % kRows;
     if (m >= a.M || n >= a.N) continue;
-    float v = part[0][i / kRows][i % kRows];
+    float y = part[0][i / kRows][i % kRows];
 #pragma unroll
-    for (int k = 1; k < kLinWarps; ++k) v += part[k][i / kRows][i % kRows];
-    if (a.xs != nullptr) v *= a.xs[m];
+    for (int k = 1; k < NW; ++k) y += part[k][i / kRows][i % kRows];
+    if (a.xs != nullptr) y *= a.xs[m];
     const long long at = static_cast<long long>(m) * a.N + n;
-    if (a.add != nullptr) v += to_f32(a.add[at]);
-    a.y[at] = from_f32<elem_t>(v);
+    if (a.add != nullptr) y += to_f32(a.add[at]);
+    a.y[at] = from_f32<elem_t>(y);
   }
+}
+
+#if !defined(SWA_ELEM_FP32)
+// ---------------------------------------------------------------------------
+// Large layers: the same products, bound by the weights' bytes up to the rows
+// whose products take longer (a product takes 2.5 clocks of an SM, a tile four of
+// them for every eight rows of x, and its bytes 24 clocks).
+//   - The eight warps of a CTA hold different panels (PN each) and go through the
+//     same columns, of which x is in shared memory, 512 at a time, two buffers:
+//     straight from memory every tile waited for L2 (15.6 us at 8192 x 8192 and one
+//     row, 27 us from nine on, for 12.4 and 16 here).
+//   - kAhead tiles a panel are in flight in registers, straight from memory.
+//   - K is split over a cluster of up to 8 CTAs, which add their sums up through
+//     distributed shared memory, in rank order.
+// ---------------------------------------------------------------------------
+constexpr int kWideWarps = 8, kChunk = 512, kAhead = 4;
+
+template <XKind X, int NT, int PN>
+struct WideShape {
+  static constexpr int row = kChunk * 2 + 16;          // bytes of a row of x: lanes 4 r + j meet no bank twice
+  static constexpr int buf = 8 * NT * row;
+  static constexpr int RN = kWideWarps * PN * kRows;
+  static constexpr int sums = 8 * NT * RN * 4;
+  static constexpr int bytes = 2 * buf > sums ? 2 * buf : sums;
+};
+struct WideArgs {
+  LinArgs l;
+  int splits, per;      // CTAs of a group of panels (the cluster), chunks of each
+};
+
+template <XKind X, int NT, int PN>
+__global__ void __launch_bounds__(kWideWarps * 32, 2) linear_wide_kernel(const __grid_constant__ WideArgs a) {
+  using S = WideShape<X, NT, PN>;
+  constexpr int MB = 8 * NT, RN = S::RN, kTiles = kChunk / kCols;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, r = lane >> 2, j = lane & 3;
+  const int P = (a.l.N + kRows - 1) / kRows, Q = (a.l.K + kCols - 1) / kCols;
+  const int rank = static_cast<int>(blockIdx.x) % a.splits, group = static_cast<int>(blockIdx.x) / a.splits;
+  const int q0 = rank * a.per * kTiles, q1 = min(Q, q0 + a.per * kTiles);
+  const uint8_t* w[PN];
+#pragma unroll
+  for (int p = 0; p < PN; ++p)      // (a panel behind the last: the last again, not stored)
+    w[p] = a.l.w4 + static_cast<long long>(min((group * kWideWarps + wid) * PN + p, P - 1)) * Q * kTileBytes;
+  uint4 v[kAhead][PN];
+  uint32_t sc[kAhead][PN];
+  auto load = [&](int i, int q) {
+    if (q < q1) {
+#pragma unroll
+      for (int p = 0; p < PN; ++p) {
+        const uint8_t* tile = w[p] + static_cast<long long>(q) * kTileBytes;
+        v[i][p] = ld_once(tile + 16 * lane);
+        sc[i][p] = *reinterpret_cast<const uint32_t*>(tile + 512 + 4 * r);
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) load(i, q0 + i);
+  // x of chunk c into its buffer, in pieces of 8 columns (K is a multiple of 8); zeros beyond M and K. e4m3 is
+  // widened to fp16 on the way, through registers: get() before the chunk in front of it is worked on, put() after.
+  constexpr int kPieces = kChunk / 8, kMine = X == kX8 ? MB * kPieces / (kWideWarps * 32) : 1;
+  uint2 x8[kMine];
+  auto get = [&](int c) {
+    if constexpr (X == kX8) {
+#pragma unroll
+      for (int u = 0; u < kMine; ++u) {
+        const int i = tid + u * kWideWarps * 32, m = i / kPieces, k = (q0 + c * kTiles) * kCols + i % kPieces * 8;
+        x8[u] = make_uint2(0u, 0u);
+        if (m < a.l.M && k < a.l.K) x8[u] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.l.x) + static_cast<long long>(m) * a.l.K + k);
+      }
+    } else {
+      for (int i = tid; i < MB * kPieces; i += kWideWarps * 32) {
+        const int m = i / kPieces, k = (q0 + c * kTiles) * kCols + i % kPieces * 8;
+        const bool on = m < a.l.M && k < a.l.K;
+        const elem_t* src = static_cast<const elem_t*>(a.l.x) + (on ? static_cast<long long>(m) * a.l.K + k : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sbase + (c & 1) * S::buf + m * S::row + i % kPieces * 16), "l"(src),
+                     "r"(on ? 16 : 0)
+                     : "memory");
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+  auto put = [&](int c) {
+    if constexpr (X == kX8) {
+#pragma unroll
+      for (int u = 0; u < kMine; ++u) {
+        const int i = tid + u * kWideWarps * 32;
+        const uint32_t e[4] = {x8[u].x & 0xFFFFu, x8[u].x >> 16, x8[u].y & 0xFFFFu, x8[u].y >> 16};
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __half2_raw t = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(e[k]), __NV_E4M3);
+          h[k] = static_cast<uint32_t>(t.x) | static_cast<uint32_t>(t.y) << 16;
+        }
+        st_shared_v4(sbase + (c & 1) * S::buf + i / kPieces * S::row + i % kPieces * 16, h[0], h[1], h[2], h[3]);
+      }
+    }
+  };
+  float acc[PN][NT][4] = {};
+  const int chunks = (q1 - q0 + kTiles - 1) / kTiles;      // (below 1: this rank has no columns)
+  if (chunks > 0) get(0);
+  for (int c = 0; c < chunks; ++c) {
+    put(c);
+    if (c + 1 < chunks) {
+      get(c + 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    __syncthreads();
+    const uint8_t* xb = smem + (c & 1) * S::buf;
+#pragma unroll
+    for (int tq = 0; tq < kTiles; ++tq) {
+      const int q = q0 + c * kTiles + tq, i = tq % kAhead;
+      if (q >= q1) break;
+      uint32_t h[PN][4][4];
+      float s0[PN], s1[PN];
+#pragma unroll
+      for (int p = 0; p < PN; ++p) {
+        const uint32_t word[4] = {v[i][p].x, v[i][p].y, v[i][p].z, v[i][p].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) widen<X>(word[k], h[p][k]);
+        s0[p] = __uint_as_float(sc[i][p] << 16);
+        s1[p] = __uint_as_float(sc[i][p] & 0xFFFF0000u);
+      }
+      load(i, q + kAhead);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        uint32_t b[4][2];
+        const uint8_t* at = xb + (8 * t + r) * S::row + (tq * kCols + 16 * j) * 2;
+        const uint4 u = *reinterpret_cast<const uint4*>(at), z = *reinterpret_cast<const uint4*>(at + 16);
+        b[0][0] = u.x; b[0][1] = u.y; b[1][0] = u.z; b[1][1] = u.w;
+        b[2][0] = z.x; b[2][1] = z.y; b[3][0] = z.z; b[3][1] = z.w;
+#pragma unroll
+        for (int p = 0; p < PN; ++p) {
+          float d[4] = {};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma<X>(d, h[p][k], b[k]);
+          acc[p][t][0] = fmaf(s0[p], d[0], acc[p][t][0]);
+          acc[p][t][1] = fmaf(s0[p], d[1], acc[p][t][1]);
+          acc[p][t][2] = fmaf(s1[p], d[2], acc[p][t][2]);
+          acc[p][t][3] = fmaf(s1[p], d[3], acc[p][t][3]);
+        }
+      }
+    }
+    __syncthreads();       // the buffer is free
+  }
+  // the sums, [MB][RN]
+  float* part = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int p = 0; p < PN; ++p)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        part[(8 * t + 2 * j + (e & 1)) * RN + (wid * PN + p) * kRows + r + 8 * (e >> 1)] = acc[p][t][e];
+  if (a.splits > 1)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else
+    __syncthreads();
+  // this CTA's share of them, eight weight rows a thread
+  const int share = (MB * RN / 8 + a.splits - 1) / a.splits;
+  const bool wide = a.l.N % 8 == 0;
+  for (int i = rank * share + tid; i < min((rank + 1) * share, MB * RN / 8); i += kWideWarps * 32) {
+    const int m = i / (RN / 8), f = i % (RN / 8) * 8, n = group * RN + f;
+    if (m >= a.l.M || n >= a.l.N) continue;
+    float y[8] = {};
+    const uint32_t mine = sbase + static_cast<uint32_t>(m * RN + f) * 4;
+    for (int s = 0; s < a.splits; ++s) {
+      uint32_t there;
+      float4 u, z;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(mine), "r"(s));
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(u.x), "=f"(u.y), "=f"(u.z), "=f"(u.w) : "r"(there) : "memory");
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(z.x), "=f"(z.y), "=f"(z.z), "=f"(z.w) : "r"(there + 16) : "memory");
+      y[0] += u.x; y[1] += u.y; y[2] += u.z; y[3] += u.w;
+      y[4] += z.x; y[5] += z.y; y[6] += z.z; y[7] += z.w;
+    }
+    finish8<X>(a.l, m, n, wide, y);
+  }
+  if (a.splits > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+#endif
+
+// A launch in clusters of `size` CTAs.
+template <typename K, typename... A>
+swa_status launch_cluster(K kern, long long grid, int threads, int smem, int size, cudaStream_t st, const A&... args) {
+  if (grid > INT32_MAX) return SWA_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = static_cast<unsigned>(size);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess && cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 
 }  // namespace w4

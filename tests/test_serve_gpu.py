@@ -11,7 +11,8 @@ bf16, 2^-11 in fp16, relative to the value):
   backward  the sum of C products likewise: see back_bounds.
   linear    products are exact; K additions in fp32, of which a product
             instruction may cut rather than round (2 U each): 2 K U of the sum of
-            sizes, and half a step of y.
+            sizes, and half a step of y. bf16 calls of more than 32 rows meet weights
+            rounded to bf16: 2^-8 of that sum more.
   tree      as the decode attention (a logit's products sum to at most 30 in
             absolute value; the query's two fp16 terms, norm and accumulation make it
             wrong by 8e-5): lse within 1e-4. In bf16 calls P is one bf16 term, 2^-8: o
@@ -302,6 +303,8 @@ def linear_case(kind, M, N, K, x8=False, add=False, seed=50):
 
 def check_linear(y, kind, want, size, M, K, x8):
     tol = 2 * (K + 8) * U * size + HALF[kind] * np.abs(want)
+    if kind == "bf16" and M > 32:
+        tol = tol + 2.0 ** -8 * size
     err = np.abs(f64(y) - want)
     assert np.all(err <= tol), float((err - tol).max())
     assert np.linalg.norm(err) <= (1e-2 if kind == "bf16" else 2e-6) * np.linalg.norm(want)
