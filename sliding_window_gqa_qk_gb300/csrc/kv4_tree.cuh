@@ -213,11 +213,103 @@ struct TreeRow {
   unsigned long long seen;
 };
 
+// What the CTA's rows see, and the drafted tokens' positions, into shared memory.
+template <int NQ, int kThreads>
+__device__ __forceinline__ void tree_rows(const TreeAttnArgs& a, const TreeReq& req, int row_q0, int nq, int G, TreeRow* rows, int* tpos,
+                                          uint32_t& bad) {
+  for (int i = threadIdx.x; i < req.n; i += kThreads) tpos[i] = a.pos[req.row0 + i];
+  for (int i = threadIdx.x; i < NQ; i += kThreads) {
+    TreeRow x{INT32_MAX, 0, 0};
+    if (i < nq) {
+      const int at = req.row0 + (row_q0 + i) / G;
+      x.pos = a.pos[at];
+      x.seen = static_cast<unsigned long long>(a.seen[at]);
+      // a row that sees nothing needs no position
+      const bool ok = x.pos >= req.ctx && (a.rcos == nullptr || x.pos < a.rows);
+      if (x.seen == 0) x.pos = 0;
+      else if (!ok) {
+        bad = DEV_ERR_BOUNDS;
+        x.seen = 0;
+        x.pos = 0;
+      } else {
+        x.lo = a.window >= 0 && x.pos - a.window > 0 ? x.pos - a.window : 0;
+      }
+    }
+    rows[i] = x;
+  }
+}
+
+// Rows that hold nothing, by the CTA that answers for them: those of a request
+// that is refused, and those behind the last one.
+template <int D, int kWarps>
+__device__ __forceinline__ void tree_zero(const TreeAttnArgs& a, const TreeReq& req, int b, int h, int G) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int used = b == a.B - 1 ? a.cu[a.B] : a.N;
+  auto zero = [&](int row0, int row1) {
+    const float z[E] = {};
+    for (long long i = wid; i < static_cast<long long>(row1 - row0) * G; i += kWarps) {
+      const long long at = (row0 + i / G) * a.Hq + h * G + i % G;
+      store_vec<E>(a.o + at * D + lane * E, z);
+      if (lane == 0) a.lse[at] = -INFINITY;
+    }
+  };
+  if (req.bad && req.rows > 0) zero(req.row0, req.row0 + req.rows);
+  if (used >= 0 && used < a.N) zero(used, a.N);
+}
+
+// A row's sums o (relative to top, base 2), joined over the warps of a CTA by one
+// warp: into o and lse, or beside the other chunks'. part0: of the CTA's item.
+template <int D>
+__device__ __forceinline__ void tree_row_out(const TreeAttnArgs& a, int chunks, long long part0, int nq_slot, int i, long long head,
+                                             float (&o)[D / 32], float top, float sum) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  if (chunks == 1) {
+    finish_head<D>(a, head, o, top, sum);
+  } else {
+    const long long at = part0 + static_cast<long long>(blockIdx.x) * nq_slot + i;
+    store_vec<E>(a.part + at * D + lane * E, o);
+    if (lane == 0) a.part_ml[at] = make_float2(top, sum);
+  }
+}
+// Row i of all chunks, joined in their order by one warp.
+template <int D>
+__device__ __forceinline__ void tree_join(const TreeAttnArgs& a, int chunks, long long part0, int nq_slot, int i, long long head) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  float top = -1e30f, sum = 0.f, o[E] = {};
+  for (int k = lane; k < chunks; k += 32) top = fmaxf(top, __ldcg(a.part_ml + part0 + static_cast<long long>(k) * nq_slot + i).x);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+#pragma unroll 4
+  for (int k = 0; k < chunks; ++k) {
+    const long long at = part0 + static_cast<long long>(k) * nq_slot + i;
+    const float2 ml = __ldcg(a.part_ml + at);
+    float x[E];
+    if constexpr (E == 4) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + at * D + lane * E));
+      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part + at * D + lane * E));
+      x[0] = v.x; x[1] = v.y;
+    }
+    const float f = ex2_approx(ml.x - top);
+    sum = fmaf(f, ml.y, sum);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fmaf(f, x[e], o[e]);
+  }
+  finish_head<D>(a, head, o, top, sum);
+}
+
 // NR query rows by one warp at once (query_row's arithmetic, row after row the
-// same; their loads wait together).
-template <int D, int NR>
-__device__ __forceinline__ void query_rows(const AttnArgs& a, const elem_t* const (&q)[NR], const int (&pos)[NR], __half* dst,
-                                           float* f) {
+// same; their loads wait together). Entries times a power of two that brings
+// them below 2^14 (up; 0: each row's own): put(row, channel, hi, lo) as two fp16
+// terms, end(row, 1 / power) by lane 0 of each group of 64 channels with their
+// sum.
+template <int D, int NR, typename Put, typename End>
+__device__ __forceinline__ void query_rows(const AttnArgs& a, const elem_t* const (&q)[NR], const int (&pos)[NR], float up_all, Put put,
+                                           End end) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31, c0 = lane * E;
   float x[NR][E], y[NR][E], cs[NR][E], sn[NR][E], g[E];
@@ -291,24 +383,18 @@ __device__ __forceinline__ void query_rows(const AttnArgs& a, const elem_t* cons
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     int e = static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127;
     e = e < -100 ? -100 : (e > 100 ? 100 : e);
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23);
+    const float up = up_all != 0.f ? up_all : __uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23);
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       const float v = x[n][i] * up;
       const __half hi = __float2half_rn(v);
-      const int at = ((c0 + i) & ~7) + ((c0 + i) & 3) * 2 + (((c0 + i) >> 2) & 1);   // pairs (i, i + 4) side by side
-      dst[n * kQTerms * D + at] = hi;
-      dst[n * kQTerms * D + D + at] = __float2half_rn(v - __half2float(hi));
+      put(n, c0 + i, hi, __float2half_rn(v - __half2float(hi)));
       sum += v;
     }
 #pragma unroll
     for (int o = 32 / E; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) {
-      f[4 * n] = __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23);
-      f[4 * n + 1] = sum;
-    }
-    if (D == 128 && lane == 16) f[4 * n + 2] = sum;
+    if (lane % (64 / E) == 0) end(n, c0 / 64, __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23), sum);
   }
 }
 
@@ -328,20 +414,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, tree_ctas_per_sm(D)) tree_att
   const TreeReq req = tree_req(a.cu, a.lens, b, a.N, a.max_new, cap);
   if (req.bad) bad = DEV_ERR_BOUNDS;
 
-  // rows that hold nothing: those of a request that is refused, and those behind the last one
-  if (blockIdx.x == 0 && qg == 0) {
-    const int used = b == a.B - 1 ? a.cu[a.B] : a.N;
-    auto zero = [&](int row0, int row1) {
-      const float z[E] = {};
-      for (long long i = wid; i < static_cast<long long>(row1 - row0) * G; i += kAttnWarps) {
-        const long long at = (row0 + i / G) * a.Hq + h * G + i % G;
-        store_vec<E>(a.o + at * D + lane * E, z);
-        if (lane == 0) a.lse[at] = -INFINITY;
-      }
-    };
-    if (req.bad && req.rows > 0) zero(req.row0, req.row0 + req.rows);
-    if (used >= 0 && used < a.N) zero(used, a.N);
-  }
+  if (blockIdx.x == 0 && qg == 0) tree_zero<D, kAttnWarps>(a, req, b, h, G);
   if (bad && tid == 0) atomicOr(a.status, bad);
   const int row_q0 = qg * NQ;                              // first (token, head) row of this CTA
   const int nq = min(NQ, req.n * G - row_q0);
@@ -407,26 +480,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, tree_ctas_per_sm(D)) tree_att
   int* tpos = reinterpret_cast<int*>(smem + M::tpos);
   __half* qs = reinterpret_cast<__half*>(smem + M::q);
   float* qf = reinterpret_cast<float*>(smem + M::qf);
-  for (int i = tid; i < req.n; i += kAttnWarps * 32) tpos[i] = a.pos[req.row0 + i];
-  for (int i = tid; i < NQ; i += kAttnWarps * 32) {
-    TreeRow x{INT32_MAX, 0, 0};
-    if (i < nq) {
-      const int at = req.row0 + (row_q0 + i) / G;
-      x.pos = a.pos[at];
-      x.seen = static_cast<unsigned long long>(a.seen[at]);
-      // a row that sees nothing needs no position
-      const bool ok = x.pos >= req.ctx && (a.rcos == nullptr || x.pos < a.rows);
-      if (x.seen == 0) x.pos = 0;
-      else if (!ok) {
-        bad = DEV_ERR_BOUNDS;
-        x.seen = 0;
-        x.pos = 0;
-      } else {
-        x.lo = a.window >= 0 && x.pos - a.window > 0 ? x.pos - a.window : 0;
-      }
-    }
-    rows[i] = x;
-  }
+  tree_rows<NQ, kAttnWarps * 32>(a, req, row_q0, nq, G, rows, tpos, bad);
   __syncthreads();
   constexpr int NR = 4;
   for (int i = wid * NR; i < NQ; i += kAttnWarps * NR) {
@@ -438,7 +492,16 @@ __global__ void __launch_bounds__(kAttnWarps * 32, tree_ctas_per_sm(D)) tree_att
       pos[k] = rows[i + k].pos;
       q[k] = rows[i + k].lo != INT32_MAX ? a.q + (static_cast<long long>(req.row0 + row / G) * a.Hq + h * G + row % G) * D : nullptr;
     }
-    query_rows<D, NR>(a, q, pos, qs + i * kQTerms * D, qf + i * 4);
+    query_rows<D, NR>(a, q, pos, 0.f,
+        [&](int n, int c, __half hi, __half lo) {
+          __half* to = qs + (i + n) * kQTerms * D + (c & ~7) + (c & 3) * 2 + ((c >> 2) & 1);   // pairs (c, c + 4) side by side
+          to[0] = hi;
+          to[D] = lo;
+        },
+        [&](int n, int g, float down, float sum) {
+          if (g == 0) qf[(i + n) * 4] = down;
+          qf[(i + n) * 4 + 1 + g] = sum;
+        });
   }
   __syncthreads();
   uint32_t qa[kQTerms][2 * W][4];
@@ -675,13 +738,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, tree_ctas_per_sm(D)) tree_att
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = 0.f;
     }
-    if (chunks == 1) {
-      finish_head<D>(a, head_of(i), o, top, sum);
-    } else {
-      const long long at = part0 + static_cast<long long>(blockIdx.x) * NQ + i;
-      store_vec<E>(a.part + at * D + lane * E, o);
-      if (lane == 0) a.part_ml[at] = make_float2(top, sum);
-    }
+    tree_row_out<D>(a, chunks, part0, NQ, i, head_of(i), o, top, sum);
   }
   if (chunks == 1) return;
   __syncthreads();
@@ -695,51 +752,31 @@ __global__ void __launch_bounds__(kAttnWarps * 32, tree_ctas_per_sm(D)) tree_att
   if (tid == 0) a.count[item] = 0;        // for the next call
 
   // join the chunks in their order: a warp a row
-  for (int i = wid; i < nq; i += kAttnWarps) {
-    float top = -1e30f, sum = 0.f, o[E] = {};
-    for (int k = lane; k < chunks; k += 32) top = fmaxf(top, __ldcg(a.part_ml + part0 + static_cast<long long>(k) * NQ + i).x);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-#pragma unroll 4
-    for (int k = 0; k < chunks; ++k) {
-      const long long at = part0 + static_cast<long long>(k) * NQ + i;
-      const float2 ml = __ldcg(a.part_ml + at);
-      float x[E];
-      if constexpr (E == 4) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + at * D + lane * E));
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-      } else {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part + at * D + lane * E));
-        x[0] = v.x; x[1] = v.y;
-      }
-      const float f = ex2_approx(ml.x - top);
-      sum = fmaf(f, ml.y, sum);
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(f, x[e], o[e]);
-    }
-    finish_head<D>(a, head_of(i), o, top, sum);
-  }
+  for (int i = wid; i < nq; i += kAttnWarps) tree_join<D>(a, chunks, part0, NQ, i, head_of(i));
 }
 
 // Warps over rows, chunks and CTAs of a call, from what the host knows. Partial
 // results of split requests have to fit the decode workspace.
 struct TreeSplit {
-  int rw, groups, chunk, splits;
+  int nq;                // (token, head) rows of a CTA
+  bool tc;               // the tcgen05 form
+  int groups, chunk, splits;
   long long items;
 };
 inline TreeSplit tree_split(int B, int Hq, int Hkv, int d, int page, int max_pages, int window, int max_new, long long part_floats) {
-  constexpr long long kSetup = 24, kJoin = 8, kStep = 2 * kAttnWarps;
   TreeSplit s;
   const int rows = Hq / Hkv * max_new;
-  s.rw = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
-  const int nq = 16 * s.rw;
-  s.groups = (rows + nq - 1) / nq;
+  s.tc = !kThreeTerms && d == 128 && rows > 16;
+  s.nq = s.tc ? (rows <= 32 ? 32 : 64) : (rows <= 16 ? 16 : (rows <= 32 ? 32 : 64));
+  // in tiles of one CTA: its set-up and end, the join, and what a chunk is a multiple of
+  const long long kSetup = s.tc ? 48 : 24, kJoin = 8, kStep = 8, nq = s.nq;
+  s.groups = static_cast<int>((rows + nq - 1) / nq);
   s.items = static_cast<long long>(B) * Hkv * s.groups;
   const long long cap = static_cast<long long>(max_pages) * page;
   long long keys = cap;
   if (window >= 0 && static_cast<long long>(window) + max_new + kTile < cap) keys = static_cast<long long>(window) + max_new + kTile;
   const long long tiles = (keys + kTile - 1) / kTile;
-  const long long slots = 152LL * tree_ctas_per_sm(d);
+  const long long slots = 152LL * (s.tc ? 1 : tree_ctas_per_sm(d));
   long long best = 0, chunk = tiles;
   for (long long n = 1; n <= kMaxSplits; ++n) {
     const long long c = ((tiles + n - 1) / n + kStep - 1) / kStep * kStep, real = (tiles + c - 1) / c;

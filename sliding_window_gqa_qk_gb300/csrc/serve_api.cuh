@@ -7,6 +7,7 @@
 #include "norm.cuh"
 #include "w4.cuh"
 #if !defined(SWA_ELEM_FP32)
+#include "kv4_tree_tc.cuh"
 #include "w4_tc.cuh"
 #endif
 
@@ -106,11 +107,29 @@ swa_status launch_tree(const kv4::TreeAttnArgs& a, cudaStream_t st) {
   kern<<<dim3(a.splits, a.c.Hkv * a.groups, a.B), kv4::kAttnWarps * 32, smem, st>>>(a);
   return launched();
 }
+#if !defined(SWA_ELEM_FP32)
+template <int NR, bool kPolled>
+swa_status launch_tree_tc(const kv4::TreeAttnArgs& a, cudaStream_t st) {
+  using S = kv4::TtShape<NR>;
+  auto kern = kv4::tree_tc_kernel<NR, kPolled>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes) != cudaSuccess) {
+    cudaGetLastError();
+    return SWA_ERR_CUDA;
+  }
+  kern<<<dim3(a.splits, a.c.Hkv * a.groups, a.B), S::warps * 32, S::bytes, st>>>(a);
+  return launched();
+}
+#endif
 template <bool kPolled>
-swa_status launch_tree(const kv4::TreeAttnArgs& a, int d, int rw, cudaStream_t st) {
-  if (d == 64)
-    return rw == 1 ? launch_tree<64, 1, kPolled>(a, st) : rw == 2 ? launch_tree<64, 2, kPolled>(a, st) : launch_tree<64, 4, kPolled>(a, st);
-  return rw == 1 ? launch_tree<128, 1, kPolled>(a, st) : rw == 2 ? launch_tree<128, 2, kPolled>(a, st) : launch_tree<128, 4, kPolled>(a, st);
+swa_status launch_tree(const kv4::TreeAttnArgs& a, int d, const kv4::TreeSplit& sp, cudaStream_t st) {
+#if !defined(SWA_ELEM_FP32)
+  if (sp.tc) return sp.nq == 32 ? launch_tree_tc<32, kPolled>(a, st) : launch_tree_tc<64, kPolled>(a, st);
+  // (head dim 128 has more rows than 16 in that form only)
+  if (d == 128) return launch_tree<128, 1, kPolled>(a, st);
+#else
+  if (d == 128) return sp.nq == 16 ? launch_tree<128, 1, kPolled>(a, st) : sp.nq == 32 ? launch_tree<128, 2, kPolled>(a, st) : launch_tree<128, 4, kPolled>(a, st);
+#endif
+  return sp.nq == 16 ? launch_tree<64, 1, kPolled>(a, st) : sp.nq == 32 ? launch_tree<64, 2, kPolled>(a, st) : launch_tree<64, 4, kPolled>(a, st);
 }
 
 }  // namespace
@@ -294,10 +313,10 @@ swa_status swa_kv4_tree_attn(const swa_params* p, const swa_extras* ex, const sw
   a.chunk = sp.chunk; a.splits = sp.splits; a.groups = sp.groups;
   a.count = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(workspace) + kKv4Count);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kKv4Part);
-  a.part_ml = reinterpret_cast<float2*>(a.part + sp.items * sp.splits * 16 * sp.rw * p->d);
+  a.part_ml = reinterpret_cast<float2*>(a.part + sp.items * sp.splits * sp.nq * p->d);
   a.wait_limit_ns = ex != nullptr && ex->wait_limit_ns != 0 ? ex->wait_limit_ns : kWaitLimitNs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return a.wait_limit_ns < kPollBelowNs ? launch_tree<true>(a, p->d, sp.rw, st) : launch_tree<false>(a, p->d, sp.rw, st);
+  return a.wait_limit_ns < kPollBelowNs ? launch_tree<true>(a, p->d, sp, st) : launch_tree<false>(a, p->d, sp, st);
 }
 
 }  // extern "C"
