@@ -20,8 +20,10 @@
 //                         scales, cleaned: keys that are not there, or not finite, 0.
 //   values  4 warps       numbers to bf16, times step plus centre (rounded once, 2^-9,
 //                         as P is)
-//   mma     1 thread      products of 16: nine of S for the block ahead, eight of O
-//   load    1 warp        bulk copies of tiles, kRing blocks in flight
+//   mma     2 threads      products of 16: nine of S a block, eight of O. One after the
+//                         other by one thread they were 17 times 90 to 100 clocks of issue
+//                         a block, beside the other warps' work; S and O have one each
+//   load    1 warp        bulk copies of tiles, kTtRing blocks in flight
 // Maximum: a row's is that of the first block in which it sees a key, and is raised
 // only when a logit passes it by 2^40 (in base 2; P and its sums have fp32's
 // exponents), which the four warps of its 32 rows find out together; then they
@@ -39,12 +41,13 @@ namespace kv4 {
 
 constexpr int kTtD = 128, kTtKeys = 128, kTtTiles = kTtKeys / kTile;
 constexpr int kTtRing = 6;                       // blocks of packed tiles in flight
+constexpr int kTtScales = 8;                      // blocks whose scales are kept: see the keys' warps
 constexpr float kTtRaise = 40.f;
 
 template <int NR>
 struct TtShape {
-  static constexpr int soft = NR / 8, keys0 = soft, values0 = soft + 8, mma = soft + 12, load = soft + 13;
-  static constexpr int warps = soft + 16;        // whole groups of four, for the registers; the last two do nothing
+  static constexpr int soft = NR / 8, keys0 = soft, values0 = soft + 8, mma = soft + 12, mma_o = mma + 1, load = mma + 2;
+  static constexpr int warps = soft + 16;        // whole groups of four, for the registers; the last does nothing
   // registers of a thread: at launch, then softmax, keys and values, the rest (soft 128 threads for each 32 rows)
   static constexpr int regs0 = NR == 64 ? 80 : 96, regs_soft = 112, regs_convert = 72, regs_rest = 40;
   static_assert(128 * (NR / 32 * regs_soft + 3 * regs_convert + regs_rest) <= warps * 32 * regs0, "");
@@ -54,9 +57,9 @@ struct TtShape {
   // shared memory
   static constexpr int q_block = N * 128;        // 64 K elements of every row, 128-byte swizzle
   static constexpr int oQ = 0, oP = 3 * q_block, p_buf = kTtKeys * 128, oRing = oP + 2 * p_buf, block = kTtTiles * tile_bytes(kTtD);
-  static constexpr int oFk = oRing + kTtRing * block;          // [4][128] {factor, flags}
-  static constexpr int oVs = oFk + 4 * kTtKeys * 8;            // [4][2 groups][128] steps, then centres, bf16
-  static constexpr int oRow = oVs + 4 * 2 * 2 * kTtKeys * 2;   // TreeRow [NR]
+  static constexpr int oFk = oRing + kTtRing * block;          // [kTtScales][128] {factor, flags}
+  static constexpr int oVs = oFk + kTtScales * kTtKeys * 8;    // [kTtScales][2 groups][128] steps, then centres, bf16
+  static constexpr int oRow = oVs + kTtScales * 2 * 2 * kTtKeys * 2;   // TreeRow [NR]
   static constexpr int oM = oRow + NR * 16;                    // maxima, rescale factors [NR] each
   static constexpr int oRed = oM + 2 * NR * 4;                 // [4][NR]
   static constexpr int oNan = oRed + 4 * NR * 4;               // [NR]
@@ -65,7 +68,7 @@ struct TtShape {
   static constexpr int oMiss = oPos + kTreeTokens * 4;         // [kTtRing]
   static constexpr int oBar = (oMiss + kTtRing * 4 + 15) / 16 * 16;
   static constexpr int RAW = 0, RAWFREE = kTtRing, KFULL = 2 * kTtRing, KFREE = KFULL + 2, SFULL = KFREE + 2, SFREE = SFULL + 1,
-                       PFULL = SFREE + 1, VFULL = PFULL + 2, PVDONE = VFULL + 2, SCALES = PVDONE + 2, FINAL = SCALES + 4,
+                       PFULL = SFREE + 1, VFULL = PFULL + 2, PVDONE = VFULL + 2, SCALES = PVDONE + 2, FINAL = SCALES + kTtScales,
                        COUNT = FINAL + 1;
   static constexpr int bytes = oBar + COUNT * 8 + 32;
   static constexpr int oJoin = oRing;                          // [NR][128] fp32, over the ring
@@ -152,10 +155,10 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
       mbar_init(bar(S::VFULL + i), 4);
       mbar_init(bar(S::PVDONE + i), 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(bar(S::SCALES + i), 8);
+    for (int i = 0; i < kTtScales; ++i) mbar_init(bar(S::SCALES + i), 8);
     mbar_init(bar(S::SFULL), 1);
     mbar_init(bar(S::SFREE), S::soft);
-    mbar_init(bar(S::FINAL), 1);
+    mbar_init(bar(S::FINAL), 2);
     fence_mbar_init();
     flags[0] = 0;
     flags[3] = 0;
@@ -232,14 +235,14 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
 
   if (warp < S::mma) queries(warp, S::mma);
   // Q is written: the warps up to the issuer meet here (the loader has work of its own till the end)
-  if (warp <= S::mma) {
+  if (warp <= S::mma_o) {
     if (warp < S::mma && lane == 0) {
       int low = 0;
       for (int i = warp; i < NR; i += S::mma) low = max(low, rows[i].lo == INT32_MAX ? 0 : rows[i].lo);
       atomicMax(reinterpret_cast<int*>(flags + 3), low);
     }
     fence_async_smem();
-    named_bar_sync(1, (S::mma + 1) * 32);
+    named_bar_sync(1, (S::mma_o + 1) * 32);
   }
   const int all_lo = static_cast<int>(*reinterpret_cast<volatile uint32_t*>(flags + 3));
 
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
       const int key0 = (t0 + n * kTtTiles) * kTile, key = key0 + key_in;
       ok = ok && mbar_wait_warp(bar(S::SFULL), n & 1, ctl);
       tc_fence_after();
-      const float2 fk = *reinterpret_cast<const float2*>(smem + S::oFk + ((n & 3) * kTtKeys + key_in) * 8);
+      const float2 fk = *reinterpret_cast<const float2*>(smem + S::oFk + (n % kTtScales * kTtKeys + key_in) * 8);
       const uint32_t kflag = __float_as_uint(fk.y);
       float x[32];
       {
@@ -349,7 +352,7 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
           tmem_wait_st();
         }
       }
-      // (P's buffer is free: S of this block was issued behind O of the block two in front, and they complete in order)
+      if (n >= 2) ok = ok && mbar_wait_warp(bar(S::PVDONE + (n & 1)), ((n >> 1) - 1) & 1, ctl);
       const uint32_t p = sbase + S::oP + (n & 1) * S::p_buf + key_in * 128;
 #pragma unroll
       for (int i = 0; i < 32; i += 8) {
@@ -421,17 +424,18 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(S::RAWFREE + st));
-      // S of the block two in front is done, so O of the block four in front has been issued: its places here are free
+      // S of the block two in front is done, so the softmax is past the fourth in front, and O of the sixth is done: the
+      // places of the scales eight in front are free
       if (n >= 2 && !(ok = mbar_wait_warp(bar(S::KFREE + ks), ((n >> 1) - 1) & 1, ctl))) break;
       tc_fence_after();
       if (j == 0) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) *reinterpret_cast<float2*>(smem + S::oFk + ((n & 3) * kTtKeys + tile * kTile + r + 8 * i) * 8) = fk[i];
+        for (int i = 0; i < 2; ++i) *reinterpret_cast<float2*>(smem + S::oFk + (n % kTtScales * kTtKeys + tile * kTile + r + 8 * i) * 8) = fk[i];
       }
       {      // lane = (token, group): steps and centres of the values, 0 where they are not to be used
         const int token = lane >> 1, g = lane & 1, key = key_tile + token;
         const bool use = !(miss >> tile & 1u) && key >= lo && key < len && (w & 0x7F80u) != 0x7F80u && (w & 0x7F800000u) != 0x7F800000u;
-        uint16_t* to = reinterpret_cast<uint16_t*>(smem + S::oVs) + ((n & 3) * 2 + g) * 2 * kTtKeys + tile * kTile + token;
+        uint16_t* to = reinterpret_cast<uint16_t*>(smem + S::oVs) + (n % kTtScales * 2 + g) * 2 * kTtKeys + tile * kTile + token;
         to[0] = use ? static_cast<uint16_t>(w) : 0;
         to[kTtKeys] = use ? static_cast<uint16_t>(w >> 16) : 0;
       }
@@ -443,7 +447,7 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(S::KFULL + ks));
-        mbar_arrive(bar(S::SCALES + (n & 3)));
+        mbar_arrive(bar(S::SCALES + n % kTtScales));
       }
     }
   } else if (warp < S::mma) {
@@ -452,11 +456,11 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
     for (int n = 0; n < blocks; ++n) {
       const int st = n % kTtRing, vs = n & 1;
       if (!(ok = mbar_wait_warp(bar(S::RAW + st), (n / kTtRing) & 1, ctl))) break;
-      // a place for each of four blocks: the keys' warps may be two blocks ahead
-      if (!(ok = mbar_wait_warp(bar(S::SCALES + (n & 3)), (n >> 2) & 1, ctl))) break;
+      // a place for each of eight blocks: the keys' warps may be some blocks ahead
+      if (!(ok = mbar_wait_warp(bar(S::SCALES + n % kTtScales), (n / kTtScales) & 1, ctl))) break;
       if (n >= 2 && !(ok = mbar_wait_warp(bar(S::PVDONE + vs), ((n >> 1) - 1) & 1, ctl))) break;
       tc_fence_after();
-      const uint8_t* sc = smem + S::oVs + ((n & 3) * 2 + g) * 4 * kTtKeys;
+      const uint8_t* sc = smem + S::oVs + (n % kTtScales * 2 + g) * 4 * kTtKeys;
 #pragma unroll
       for (int t4 = 0; t4 < kTtTiles; t4 += 4) {
         uint32_t out[2][16];
@@ -522,9 +526,7 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
   } else if (warp == S::mma) {
     if (lane == 0) {
       constexpr uint32_t id_s = (1u << 4) | (static_cast<uint32_t>(S::N >> 3) << 17) | (8u << 24);      // fp16, M = 128
-      constexpr uint32_t id_o = idesc_bf16_f32(128, NR, 0, 1);
       const uint64_t dQ = sdesc_sw128(sbase + S::oQ, 16, 1024);
-      const uint64_t dP = sdesc_sw128(sbase + S::oP, 16, 1024);
       auto scores = [&](int n) {
         const int ks = n & 1;
         if (!(ok = mbar_wait(bar(S::KFULL + ks), (n >> 1) & 1, ctl))) return;
@@ -538,13 +540,18 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
         umma_commit(bar(S::SFULL));
         umma_commit(bar(S::KFREE + ks));
       };
-      scores(0);
-      for (int n = 0; n < blocks && ok; ++n) {
-        if (n + 1 < blocks) scores(n + 1);
-        if (!ok) break;
+      for (int n = 0; n < blocks && ok; ++n) scores(n);
+      umma_commit(bar(S::FINAL));         // every product issued has completed, after a wait that ran out too
+      mbar_wait_drain(bar(S::FINAL), 0, kDrainLimitNs);
+    }
+  } else if (warp == S::mma_o) {
+    if (lane == 0) {
+      constexpr uint32_t id_o = idesc_bf16_f32(128, NR, 0, 1);
+      const uint64_t dP = sdesc_sw128(sbase + S::oP, 16, 1024);
+      for (int n = 0; n < blocks; ++n) {
         const int ps = n & 1;
-        if (!(ok = mbar_wait(bar(S::PFULL + ps), (n >> 1) & 1, ctl))) break;
         if (!(ok = mbar_wait(bar(S::VFULL + ps), (n >> 1) & 1, ctl))) break;
+        if (!(ok = mbar_wait(bar(S::PFULL + ps), (n >> 1) & 1, ctl))) break;
         tc_fence_after();
         const uint32_t ta = tmem + S::cV + static_cast<uint32_t>(ps) * S::vstep;
         const uint64_t db = sdesc_add(dP, ps * S::p_buf);
@@ -554,7 +561,7 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
         });
         umma_commit(bar(S::PVDONE + ps));
       }
-      umma_commit(bar(S::FINAL));         // every product issued has completed, after a wait that ran out too
+      umma_commit(bar(S::FINAL));
       mbar_wait_drain(bar(S::FINAL), 0, kDrainLimitNs);
     }
   }
