@@ -691,6 +691,37 @@ swa_status swa_w4_linear(int M, int N, int K, const void* x, const float* x_scal
                          void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * A step of serving through the whole attention block (swa_block_fwd's, whose
+ * weights are held in 4 bits here): the tokens' norm, projections, append,
+ * attention and residual, as one call of the calls above:
+ *   h   = x + add                      [n_tokens, C] elem; add NULL: h = x
+ *   xn  = swa_rms_norm of h with `gain` (NULL: none, as in swa_block_fwd)
+ *   q, k, v = xn wq^T, xn wk^T, xn wv^T          (swa_w4_linear)
+ *   swa_kv4_append of k, v at slot, pos, with gk, ve, tok, and the learned gate of
+ *         ex (gate_w, gate_ch <= C; it reads xn's first channels; gate_x NULL)
+ *   o   = swa_kv4_attn of q, one token a request (cu and seen NULL, n_tokens = p->B;
+ *         its position in pos is lens[b] - 1), or swa_kv4_tree_attn (cu, seen, pos)
+ *   out = h + o wo^T
+ * p, c, r, gq, table, max_pages, lens, max_new are those of the attention (p->T 1),
+ * ex's wait_limit_ns too. out is none of x and add. lens counts the tokens of the
+ * call. The workspace: swa_kv4_block_workspace_size bytes for n_tokens or more,
+ * passed to swa_kv4_workspace_init once; it may serve the other decode calls too.
+ */
+typedef struct {
+  int C;                 /* model width                                        */
+  const void* wq;        /* swa_w4_pack of [Hq*d][C]                            */
+  const void* wk;        /* of [Hkv*d][C]                                       */
+  const void* wv;        /* of [Hkv*d][C]                                       */
+  const void* wo;        /* of [C][Hq*d]                                        */
+} swa_kv4_weights;
+size_t swa_kv4_block_workspace_size(const swa_params* p, int C, int n_tokens);
+swa_status swa_kv4_block(const swa_params* p, const swa_extras* ex, const swa_kv4_cache* c, const swa_rope* r,
+                         const swa_kv4_weights* w, int n_tokens, int max_new, const void* x, const void* add, const float* gain,
+                         const float* gq, const float* gk, const void* ve, const int32_t* tok, const int64_t* slot,
+                         const int32_t* pos, const int32_t* cu, const int64_t* seen, const int32_t* table, int max_pages,
+                         const int32_t* lens, void* out, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Synchronises `stream`, reads the workspace status word, clears it, and
  * returns SWA_OK, SWA_ERR_TIMEOUT or SWA_ERR_DEVICE_CHECK (timeout wins).
  * After a timeout it also drops the record of a zeroed dQ accumulator (a

@@ -50,7 +50,8 @@ __all__ = [
     "rope_tables", "rope_apply", "new_kv4_cache", "new_kv4_workspace", "kv4_plan", "kv4_append",
     "kv4_read", "kv4_attention",
     "swa_kv4_tree", "swa_kv4_tree_attn", "swa_kv4_move", "swa_rms_norm", "swa_rms_norm_workspace_size", "swa_rms_norm_bwd",
-    "swa_w4_size", "swa_w4_pack", "swa_w4_unpack", "swa_w4_linear",
+    "swa_w4_size", "swa_w4_pack", "swa_w4_unpack", "swa_w4_linear", "swa_kv4_weights", "swa_kv4_block_workspace_size",
+    "swa_kv4_block", "new_kv4_block_workspace", "kv4_block",
     "kv4_tree", "kv4_tree_attention", "kv4_move", "rms_norm", "rms_norm_backward", "w4_pack", "w4_unpack", "w4_linear",
     "SWA_OK", "SWA_ERR_INVALID_ARG", "SWA_ERR_UNSUPPORTED", "SWA_ERR_CUDA", "SWA_ERR_TIMEOUT",
     "SWA_ERR_WORKSPACE", "SWA_ERR_DEVICE_CHECK", "SWA_REUSE_PROLOGUE", "SWA_BWD_STAGE_PRE",
@@ -120,6 +121,11 @@ class swa_kv4_cache(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("page", ctypes.c_int)]
 
 
+class swa_kv4_weights(ctypes.Structure):
+    """Packed weights of swa_kv4_block (see include/swa_attn.h)."""
+    _fields_ = [("C", ctypes.c_int)] + [(n, ctypes.c_void_p) for n in ("wq", "wk", "wv", "wo")]
+
+
 _LIBS: dict = {}
 _vp = ctypes.c_void_p
 
@@ -186,6 +192,7 @@ def load(kind: str = "bf16") -> ctypes.CDLL:
             ("swa_kv4_tree", [I] * 3 + [_vp] * 6 + [Z, _vp]),
             ("swa_kv4_tree_attn", [P, R, C, F, I, I, _vp, _vp, _vp, I] + [_vp] * 7 + [Z, _vp]),
             ("swa_kv4_move", [P, C] + [_vp] * 3 + [Z, _vp]),
+            ("swa_kv4_block", [P, R, C, F, ctypes.POINTER(swa_kv4_weights), I, I] + [_vp] * 12 + [I] + [_vp] * 3 + [Z, _vp]),
             ("swa_rms_norm", [L, I, ctypes.c_float] + [_vp] * 9),
             ("swa_rms_norm_bwd", [L, I] + [_vp] * 8 + [Z, _vp]),
             ("swa_w4_pack", [I, I] + [_vp] * 3),
@@ -194,7 +201,7 @@ def load(kind: str = "bf16") -> ctypes.CDLL:
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = I
     for name, args in (("swa_kv4_cache_size", [P, I, I]), ("swa_kv4_workspace_size", [P, I, I]),
-                       ("swa_rms_norm_workspace_size", [L, I]), ("swa_w4_size", [I, I])):
+                       ("swa_rms_norm_workspace_size", [L, I]), ("swa_w4_size", [I, I]), ("swa_kv4_block_workspace_size", [P, I, I])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = Z
     lib.swa_attn_check_status.argtypes = [_vp, _vp]
@@ -214,6 +221,10 @@ def load(kind: str = "bf16") -> ctypes.CDLL:
         _fast.bind(0 if kind == "bf16" else 1, *(
             ctypes.cast(getattr(lib, f), _vp).value for f in (
                 "swa_rope_tables", "swa_rope_apply", "swa_kv4_plan", "swa_kv4_append", "swa_kv4_read", "swa_kv4_attn")))
+        _fast.bind_more(0 if kind == "bf16" else 1, *(
+            ctypes.cast(getattr(lib, f), _vp).value for f in (
+                "swa_rms_norm", "swa_rms_norm_workspace_size", "swa_rms_norm_bwd", "swa_w4_linear", "swa_kv4_tree",
+                "swa_kv4_tree_attn", "swa_kv4_move")))
     return lib
 
 
@@ -512,6 +523,19 @@ def swa_w4_unpack(N, K, w4, w, stream=None, kind=None) -> int:
 def swa_w4_linear(M, N, K, x, x_scale, w4, add, y, stream=None, kind=None, ws=None, ws_bytes=None) -> int:
     return int(load(kind or _kind_of(y)).swa_w4_linear(int(M), int(N), int(K), _ptr(x), _ptr(x_scale), _ptr(w4), _ptr(add), _ptr(y),
                                                        _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
+def swa_kv4_block_workspace_size(p: swa_params, C: int, n_tokens: int, kind: str = "bf16") -> int:
+    return int(load(kind).swa_kv4_block_workspace_size(ctypes.byref(p), int(C), int(n_tokens)))
+
+
+def swa_kv4_block(p, ex, c, r, w, n_tokens, max_new, x, add, gain, gq, gk, ve, tok, slot, pos, cu, seen, table, max_pages, lens, out,
+                  ws, ws_bytes=None, stream=None, kind=None) -> int:
+    kind = kind or _kind_of(x)
+    return int(load(kind).swa_kv4_block(
+        ctypes.byref(p), _ref(ex), _ref(c), _ref(r), _ref(w), int(n_tokens), int(max_new), _ptr(x), _ptr(add), _ptr(gain), _ptr(gq),
+        _ptr(gk), _ptr(ve), _ptr(tok), _ptr(slot), _ptr(pos), _ptr(cu), _ptr(seen), _ptr(table), int(max_pages), _ptr(lens), _ptr(out),
+        _ptr(ws), _ws_bytes(ws, ws_bytes), _stream(stream)))
 
 
 def swa_attn_check_status(ws, stream=None, kind: str = "bf16") -> int:
@@ -998,6 +1022,10 @@ def kv4_tree(parent, cu, lens, *, max_new: int, workspace=None, stream=None):
     (rows of the requests; rows behind cu[B] are padding) and lens int32 [B]
     (cached tokens, the drafted ones among them: cu and lens of kv4_plan). At
     most ``max_new`` (up to 64) tokens a request."""
+    if _fast is not None and stream is None:
+        r = _fast.kv4_tree(parent, cu, lens, max_new, workspace)
+        if r is not None:
+            return r
     dev = parent.device
     if parent.dim() != 1 or cu.dim() != 1 or cu.numel() < 1:
         raise ValueError("parent [N] and cu [B + 1] are expected")
@@ -1023,6 +1051,11 @@ def kv4_tree_attention(cache, q, table, lens, cu, pos, seen, *, max_new: int, ro
     and values are in the cache already. The other arguments are those of
     kv4_attention. Rows that see nothing (padding among them) are 0, their lse
     -infinity."""
+    if _fast is not None and stream is None:
+        r = _fast.kv4_tree_attention(cache, q, table, lens, cu, pos, seen, max_new, *(_NO_ROPE if rope is None else rope), interleaved,
+                                     gq, window, softmax_scale, eps, workspace)
+        if r is not None:
+            return r
     n_pages, Hkv, page, d = _cache_dims(cache)
     dev, dt = cache.device, q.dtype
     kind = _kind("q", dt)
@@ -1057,6 +1090,8 @@ def kv4_move(cache, src, dst, *, workspace=None, stream=None) -> None:
     dst. All of a row are read before any is written; rows must not write what
     others read or write. -1 in either skips a pair; slots outside the cache are
     skipped, which only a ``workspace`` tells."""
+    if _fast is not None and stream is None and _fast.kv4_move(cache, src, dst, workspace):
+        return
     n_pages, Hkv, page, d = _cache_dims(cache)
     dev = cache.device
     if src.dim() != 2:
@@ -1085,6 +1120,10 @@ def rms_norm(x, gain=None, *, add=None, eps: float = 1e-6, fp8: bool = False, in
     x (bf16 or fp32; gain fp32 [C]). Returns y, h (x itself without an ``add``) and
     rstd fp32 [...]; with ``fp8`` y is float8_e4m3fn and scale fp32 [...] the rows'
     factors (y ~ y * scale). ``inplace``: h is written over x."""
+    if _fast is not None and stream is None:
+        r = _fast.rms_norm(x, gain, add, eps, fp8, inplace)
+        if r is not None:
+            return r
     rows, C = _rows_of("x", x)
     dt, dev = x.dtype, x.device
     lib = load(_kind("x", dt))
@@ -1110,6 +1149,10 @@ def rms_norm_backward(h, rstd, dy, gain=None, *, dh=None, need_gain: bool = True
     (dy's, and dh where h is used elsewhere: the residual), and dgain fp32 [C] (None
     without ``need_gain``). ``workspace``: uint8, of swa_rms_norm_workspace_size
     bytes; None: one for this call."""
+    if _fast is not None and stream is None and need_gain:
+        r = _fast.rms_norm_backward(h, rstd, dy, gain, dh, workspace)
+        if r is not None:
+            return r
     rows, C = _rows_of("h", h)
     dt, dev = h.dtype, h.device
     kind = _kind("h", dt)
@@ -1172,6 +1215,11 @@ def w4_linear(x, w4, *, out_features: Optional[int] = None, scale=None, add=None
     float8_e4m3fn with ``scale`` fp32 [...] (rms_norm's pair); then ``dtype`` is y's
     (bf16 by default). ``out``: y, which may be ``add``. ``workspace``: where a wait
     that ran out is reported (swa_attn_check_status)."""
+    if _fast is not None and stream is None and (dtype is None or dtype is _BF16 or dtype is _F32):
+        r = _fast.w4_linear(x, w4, -1 if out_features is None else out_features, scale, add, 0 if dtype is None else (1 if dtype is _BF16 else 2),
+                            out, workspace)
+        if r is not None:
+            return r
     M, K = _rows_of("x", x)
     dev = x.device
     if w4.dim() != 3:
@@ -1198,4 +1246,76 @@ def w4_linear(x, w4, *, out_features: Optional[int] = None, scale=None, add=None
     s = lib.swa_w4_linear(M, N, K, xa, sa, wa, aa, oa, ws, nws, st)
     if s:
         raise SwaError(s, "swa_w4_linear")
+    return out
+
+
+def new_kv4_block_workspace(cache, n_tokens: int, C: int, Hq: int, *, kind: str = "bf16", stream=None):
+    """A workspace of kv4_block for steps of up to ``n_tokens`` tokens of width C,
+    initialised; the other decode calls may use it too."""
+    _, Hkv, _, d = _cache_dims(cache)
+    n = swa_kv4_block_workspace_size(make_params(1, 1, Hq, Hkv, d), C, n_tokens, kind)
+    if n == 0:
+        raise SwaError(SWA_ERR_INVALID_ARG, "workspace size")
+
+    def call():
+        ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
+        _check(swa_kv4_workspace_init(ws, n, None, kind), "workspace init")
+        return ws
+    return _there(cache.device, stream, call)
+
+
+def kv4_block(cache, x, weights, table, lens, slot, pos, *, Hq: int, cu=None, seen=None, max_new: int = 1, add=None, gain=None,
+              rope=None, interleaved: bool = False, gq=None, gk=None, ve=None, tok=None, gate_w=None, ve_scale: float = 0.5,
+              window: int = -1, softmax_scale: float = 0.0, eps: float = 1e-6, out=None, workspace=None, stream=None):
+    """out = h + c_proj(attention(norm(h))), h = x + add: a serving step of the whole
+    attention block over the 4-bit cache for the tokens x [N, C], with weights =
+    (wq, wk, wv, wo), each of w4_pack. slot int64 [N], pos int32 [N], lens: as
+    kv4_plan gives them. One token a request (N = B), or drafted tokens with cu, pos
+    and seen of kv4_tree and ``max_new``. gain fp32 [C]: of the pre-norm; gate_w fp32
+    [Hkv, C' <= 32]: the learned gate of value embeddings ve, tok [N]; the rest as in
+    kv4_append and kv4_attention. ``workspace``: of new_kv4_block_workspace (None: one
+    for this call, whose reports are lost)."""
+    n_pages, Hkv, page, d = _cache_dims(cache)
+    dev, dt = cache.device, x.dtype
+    kind = _kind("x", dt)
+    if x.dim() != 2 or table.dim() != 2 or len(weights) != 4:
+        raise ValueError("x [N, C], table [B, max_pages] and weights (wq, wk, wv, wo) are expected")
+    N, C = x.shape
+    B, max_pages = table.shape
+    if (cu is None) != (seen is None) or (cu is None and N != B):
+        raise ValueError("cu and seen, or one token a request, are expected")
+    nq, nk = Hq * d, Hkv * d
+    wa = [_at(n, w, _U8, _w4_tiles(*s), dev) for n, w, s in zip(("wq", "wk", "wv", "wo"), weights, ((nq, C), (nk, C), (nk, C), (C, nq)))]
+    xa, aa, oa = _at("x", x, dt, (N, C), dev), _at("add", add, dt, (N, C), dev), _at("out", out, dt, (N, C), dev)
+    na, qa, ka = _at("gain", gain, _F32, (C,), dev), _at("gq", gq, _F32, (d,), dev), _at("gk", gk, _F32, (d,), dev)
+    vocab, ea, ka2, ex = 0, None, None, None
+    if ve is not None:
+        vocab = ve.shape[0]
+        ea, ka2 = _at("ve", ve, dt, (vocab, nk), dev), _at("tok", tok, _I32, (N,), dev)
+        if gate_w is not None:
+            if gate_w.dim() != 2:
+                raise ValueError("gate_w: [Hkv, channels] is expected")
+            ex = swa_extras()
+            ex.gate_w, ex.gate_ch = _at("gate_w", gate_w, _F32, (Hkv, gate_w.shape[1]), dev), gate_w.shape[1]
+    sa, pa = _at("slot", slot, _I64, (N,), dev), _at("pos", pos, _I32, (N,), dev)
+    ta, la = _at("table", table, _I32, (B, max_pages), dev), _at("lens", lens, _I32, (B,), dev)
+    ca, va = _at("cu", cu, _I32, (B + 1,), dev), _at("seen", seen, _I64, (N,), dev)
+    r = _rope_at(rope, interleaved, dev)
+    st = _stream_here(dev, stream)
+    if st is None:
+        return _there(dev, stream, lambda: kv4_block(
+            cache, x, weights, table, lens, slot, pos, Hq=Hq, cu=cu, seen=seen, max_new=max_new, add=add, gain=gain, rope=rope,
+            interleaved=interleaved, gq=gq, gk=gk, ve=ve, tok=tok, gate_w=gate_w, ve_scale=ve_scale, window=window,
+            softmax_scale=softmax_scale, eps=eps, out=out, workspace=workspace))
+    if workspace is None:
+        workspace = new_kv4_block_workspace(cache, N, C, Hq, kind=kind)
+    ws, nws = _ws_at(workspace, dev)
+    if out is None:
+        out = torch.empty_like(x)
+        oa = out.data_ptr()
+    s = load(kind).swa_kv4_block(swa_params(B, 1, Hq, Hkv, d, window, 1, softmax_scale, eps, ve_scale, vocab), ex,
+                                 swa_kv4_cache(cache.data_ptr(), n_pages, page), r, swa_kv4_weights(C, *wa), N, max_new, xa, aa, na, qa,
+                                 ka, ea, ka2, sa, pa, ca, va, ta, max_pages, la, oa, ws, nws, st)
+    if s:
+        raise SwaError(s, "swa_kv4_block")
     return out

@@ -767,7 +767,7 @@ inline TreeSplit tree_split(int B, int Hq, int Hkv, int d, int page, int max_pag
   TreeSplit s;
   const int rows = Hq / Hkv * max_new;
   s.tc = !kThreeTerms && d == 128 && rows > 16;
-  s.nq = s.tc ? (rows <= 32 ? 32 : 64) : (rows <= 16 ? 16 : (rows <= 32 ? 32 : 64));
+  s.nq = rows <= 16 ? 16 : (rows <= 32 && !s.tc ? 32 : 64);
   // in tiles of one CTA: its set-up and end, the join, and what a chunk is a multiple of
   const long long kSetup = s.tc ? 48 : 24, kJoin = 8, kStep = 8, nq = s.nq;
   s.groups = static_cast<int>((rows + nq - 1) / nq);

@@ -60,7 +60,7 @@ struct TtShape {
   static constexpr int oFk = oRing + kTtRing * block;          // [kTtScales][128] {factor, flags}
   static constexpr int oVs = oFk + kTtScales * kTtKeys * 8;    // [kTtScales][2 groups][128] steps, then centres, bf16
   static constexpr int oRow = oVs + kTtScales * 2 * 2 * kTtKeys * 2;   // TreeRow [NR]
-  static constexpr int oM = oRow + NR * 16;                    // maxima, rescale factors [NR] each
+  static constexpr int oM = oRow + NR * 16;                    // maxima, negated, and their rises [NR] each
   static constexpr int oRed = oM + 2 * NR * 4;                 // [4][NR]
   static constexpr int oNan = oRed + 4 * NR * 4;               // [NR]
   static constexpr int oFresh = oNan + NR * 4;                 // [NR], then one for each 32 rows
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
   uint32_t* flags = reinterpret_cast<uint32_t*>(smem + S::oBar + S::COUNT * 8);    // abort, last, tensor memory, lowest key seen by all
   TreeRow* rows = reinterpret_cast<TreeRow*>(smem + S::oRow);
   int* tpos = reinterpret_cast<int*>(smem + S::oPos);
-  float* rowm = reinterpret_cast<float*>(smem + S::oM);          // maxima, then factors
+  float* rowm = reinterpret_cast<float*>(smem + S::oM);          // maxima, negated, then their last rises
   uint32_t* rownan = reinterpret_cast<uint32_t*>(smem + S::oNan);
   volatile int* fresh = reinterpret_cast<volatile int*>(smem + S::oFresh);
   const WaitCtl<kPolled> ctl{flags, a.status, a.wait_limit_ns};
@@ -282,8 +282,8 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
 #pragma unroll
       for (int i = 0; i < 32; i += 4) {       // relative to the rows' maxima from here on
         const float4 m = *reinterpret_cast<const float4*>(rowm + r0 + i);
-        ffma2(x[i], x[i + 1], x[i], x[i + 1], f, f, -m.x, -m.y);
-        ffma2(x[i + 2], x[i + 3], x[i + 2], x[i + 3], f, f, -m.z, -m.w);
+        ffma2(x[i], x[i + 1], x[i], x[i + 1], f, f, m.x, m.y);
+        ffma2(x[i + 2], x[i + 3], x[i + 2], x[i + 3], f, f, m.z, m.w);
       }
       const bool edge = key0 < all_lo || key0 + kTtKeys > req.ctx;        // of the block
       if (edge || (kflag & kKeyOff)) {
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
           const float top = unordered(t);
           const bool first = fresh[r0 + lane], none = first && top == -INFINITY;
           const float rise = none ? 0.f : (first ? top : fmaxf(top, 0.f));
-          rowm[r0 + lane] += rise;
+          rowm[r0 + lane] -= rise;
           rowm[NR + r0 + lane] = rise;
           fresh[r0 + lane] = none;
           const bool some = __any_sync(0xffffffffu, none);
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
   const long long part0 = item * a.splits * NR;
   const float* red = reinterpret_cast<const float*>(smem + S::oRed);
   for (int i = warp; i < nq; i += S::warps) {      // a warp a row
-    float o[E], top = rowm[i], sum = (red[i] + red[NR + i]) + (red[2 * NR + i] + red[3 * NR + i]);
+    float o[E], top = -rowm[i], sum = (red[i] + red[NR + i]) + (red[2 * NR + i] + red[3 * NR + i]);
     load_vec<E>(jo + i * D + lane * E, o);
     if (rows[i].lo == INT32_MAX) {       // sees nothing: blocks that every other row sees were not masked for it
       top = -1e30f;

@@ -1,4 +1,4 @@
-// The short way from Python to the rotary and decode entry points.
+// The short way from Python to the rotary, decode and serving entry points.
 //
 // A decode step is 4 to 15 us of GPU work, and the checks, allocations and
 // argument conversions of the binding's Python functions cost 16 to 30 us
@@ -19,6 +19,9 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <initializer_list>
+#include <utility>
+
 #include "../../include/swa_attn.h"
 
 namespace {
@@ -32,6 +35,16 @@ struct Lib {
   decltype(&swa_kv4_attn) attn;
 };
 Lib libs[2];   // bf16, fp32; filled by bind()
+struct More {
+  decltype(&swa_rms_norm) norm;
+  decltype(&swa_rms_norm_workspace_size) norm_ws;
+  decltype(&swa_rms_norm_bwd) norm_bwd;
+  decltype(&swa_w4_linear) linear;
+  decltype(&swa_kv4_tree) tree;
+  decltype(&swa_kv4_tree_attn) tree_attn;
+  decltype(&swa_kv4_move) move;
+};
+More more[2];  // likewise, by bind_more()
 
 struct Refused {};   // not the ordinary case; nothing is launched
 
@@ -192,6 +205,36 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                  reinterpret_cast<decltype(&swa_kv4_read)>(f[4]), reinterpret_cast<decltype(&swa_kv4_attn)>(f[5])};
     Py_RETURN_TRUE;
   });
+}
+
+PyObject* bind_more(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 8) Py_RETURN_NONE;
+  return guarded("bind_more", [&](Call&) -> PyObject* {
+    void* f[7];
+    for (int i = 0; i < 7; ++i) f[i] = PyLong_AsVoidPtr(a[i + 1]);
+    if (PyErr_Occurred()) throw Refused{};
+    more[int_of(a[0]) & 1] =
+        More{reinterpret_cast<decltype(&swa_rms_norm)>(f[0]),     reinterpret_cast<decltype(&swa_rms_norm_workspace_size)>(f[1]),
+             reinterpret_cast<decltype(&swa_rms_norm_bwd)>(f[2]), reinterpret_cast<decltype(&swa_w4_linear)>(f[3]),
+             reinterpret_cast<decltype(&swa_kv4_tree)>(f[4]),     reinterpret_cast<decltype(&swa_kv4_tree_attn)>(f[5]),
+             reinterpret_cast<decltype(&swa_kv4_move)>(f[6])};
+    Py_RETURN_TRUE;
+  });
+}
+// As kind_of, for the functions of More.
+int kind_more(at::ScalarType t) {
+  const int kind = t == at::kBFloat16 ? 0 : (t == at::kFloat ? 1 : -1);
+  if (kind < 0 || more[kind].move == nullptr) throw Refused{};
+  return kind;
+}
+PyObject* dict_of(std::initializer_list<std::pair<const char*, const at::Tensor*>> items) {
+  PyObject* dict = PyDict_New();
+  for (const auto& i : items) {
+    PyObject* v = i.second != nullptr && i.second->defined() ? THPVariable_Wrap(*i.second) : Py_NewRef(Py_None);
+    PyDict_SetItemString(dict, i.first, v);
+    Py_DECREF(v);
+  }
+  return dict;
 }
 
 PyObject* raises(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -406,9 +449,187 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// rms_norm(x, gain, add, eps, fp8, inplace)
+PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 6) Py_RETURN_NONE;
+  return guarded("swa_rms_norm", [&](Call& call) -> PyObject* {
+    const int dev = device_now();
+    const at::Tensor& x = tensor(a[0]);
+    if (x.dim() < 1 || x.numel() == 0) throw Refused{};
+    const auto type = x.scalar_type();
+    const int kind = kind_more(type);
+    const int64_t C = x.size(-1), rows = x.numel() / C;
+    void* xa = at_(a[0], type, dev, x.sizes());
+    const auto* g = static_cast<const float*>(at_(a[1], at::kFloat, dev, {C}));
+    const void* add = at_(a[2], type, dev, x.sizes());
+    const float eps = static_cast<float>(double_of(a[3]));
+    const bool fp8 = truth_of(a[4]), over = truth_of(a[5]);
+    const int width = small(C);
+    at::Tensor h = x, y, rstd, scale;
+    call([&] {
+      if (add != nullptr && !over) h = at::empty_like(x);
+      y = at::empty(x.sizes(), on(dev, fp8 ? at::kFloat8_e4m3fn : type));
+      rstd = at::empty(x.sizes().slice(0, x.dim() - 1), on(dev, at::kFloat));
+      if (fp8) scale = at::empty_like(rstd);
+      return more[kind].norm(rows, width, eps, xa, add, g, add != nullptr ? h.data_ptr() : nullptr, fp8 ? nullptr : y.data_ptr(),
+                             fp8 ? y.data_ptr() : nullptr, fp8 ? scale.data_ptr<float>() : nullptr, rstd.data_ptr<float>(), stream_now(dev));
+    });
+    PyObject* r = dict_of({{"y", &y}, {"scale", &scale}, {"rstd", &rstd}, {"h", &h}});
+    if (add == nullptr || over) PyDict_SetItemString(r, "h", a[0]);
+    return r;
+  });
+}
+
+// rms_norm_backward(h, rstd, dy, gain, dh, workspace)
+PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 6) Py_RETURN_NONE;
+  return guarded("swa_rms_norm_bwd", [&](Call& call) -> PyObject* {
+    const int dev = device_now();
+    const at::Tensor& h = tensor(a[0]);
+    if (h.dim() < 1 || h.numel() == 0) throw Refused{};
+    const auto type = h.scalar_type();
+    const int kind = kind_more(type);
+    const int64_t C = h.size(-1), rows = h.numel() / C;
+    const void* ha = at_(a[0], type, dev, h.sizes());
+    const auto* rs = static_cast<const float*>(at_(a[1], at::kFloat, dev, h.sizes().slice(0, h.dim() - 1)));
+    const void* dy = at_(a[2], type, dev, h.sizes());
+    const auto* g = static_cast<const float*>(at_(a[3], at::kFloat, dev, {C}));
+    const void* dh = at_(a[4], type, dev, h.sizes());
+    const Ws ws = ws_of(a[5], dev);
+    const int width = small(C);
+    if (rs == nullptr || dy == nullptr) throw Refused{};
+    at::Tensor dx, dg, part;
+    call([&] {
+      dx = at::empty_like(h);
+      dg = at::empty({C}, on(dev, at::kFloat));
+      void* at = ws.at;
+      size_t bytes = ws.bytes;
+      if (at == nullptr) {
+        bytes = more[kind].norm_ws(rows, width);
+        part = at::empty({static_cast<int64_t>(bytes)}, on(dev, at::kByte));
+        at = part.data_ptr();
+      }
+      return more[kind].norm_bwd(rows, width, ha, rs, g, dy, dh, dx.data_ptr(), dg.data_ptr<float>(), at, bytes, stream_now(dev));
+    });
+    return dict_of({{"dx", &dx}, {"dgain", &dg}});
+  });
+}
+
+// w4_linear(x, w4, out_features (-1: all), scale, add, dtype (0: x's, or bf16 with a scale; 1: bf16; 2: fp32), out, workspace)
+PyObject* w4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 8) Py_RETURN_NONE;
+  return guarded("swa_w4_linear", [&](Call& call) -> PyObject* {
+    const int dev = device_now();
+    const at::Tensor &x = tensor(a[0]), &w = tensor(a[1]);
+    if (x.dim() < 1 || x.numel() == 0 || w.dim() != 3) throw Refused{};
+    const bool x8 = a[3] != Py_None;
+    const int want = int_of(a[5]);
+    const auto type = want == 0 ? (x8 ? at::kBFloat16 : x.scalar_type()) : (want == 1 ? at::kBFloat16 : at::kFloat);
+    const int kind = kind_more(type);
+    const int64_t K = x.size(-1), M = x.numel() / K, given = int_of(a[2]), N = given < 0 ? 16 * w.size(0) : given;
+    const void* xa = at_(a[0], x8 ? at::kFloat8_e4m3fn : type, dev, x.sizes());
+    const void* wa = at_(a[1], at::kByte, dev, {(N + 15) / 16, (K + 63) / 64, 544});
+    const auto* sa = static_cast<const float*>(at_(a[3], at::kFloat, dev, x.sizes().slice(0, x.dim() - 1)));
+    at::DimVector shape(x.sizes().begin(), x.sizes().end());
+    shape.back() = N;
+    const void* add = at_(a[4], type, dev, shape);
+    void* to = at_(a[6], type, dev, shape);
+    const Ws ws = ws_of(a[7], dev);
+    const int m = small(M), nn = small(N), k = small(K);
+    if (to == nullptr && a[6] != Py_None) throw Refused{};
+    at::Tensor y;
+    if (to != nullptr) y = tensor(a[6]);
+    call([&] {
+      if (to == nullptr) {
+        y = at::empty(shape, on(dev, type));
+        to = y.data_ptr();
+      }
+      return more[kind].linear(m, nn, k, xa, sa, wa, add, to, ws.at, ws.bytes, stream_now(dev));
+    });
+    return a[6] != Py_None ? Py_NewRef(a[6]) : THPVariable_Wrap(y);
+  });
+}
+
+// kv4_tree(parent, cu, lens, max_new, workspace)
+PyObject* kv4_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 5 || more[0].tree == nullptr) Py_RETURN_NONE;
+  return guarded("swa_kv4_tree", [&](Call& call) -> PyObject* {
+    const int dev = device_now();
+    const at::Tensor &parent = tensor(a[0]), &cu = tensor(a[1]);
+    if (parent.dim() != 1 || cu.dim() != 1 || cu.numel() < 1 || parent.numel() < 1) throw Refused{};
+    const int64_t N = parent.size(0), B = cu.size(0) - 1;
+    const auto* pa = static_cast<const int32_t*>(at_(a[0], at::kInt, dev, {N}));
+    const auto* ca = static_cast<const int32_t*>(at_(a[1], at::kInt, dev, {B + 1}));
+    const auto* la = static_cast<const int32_t*>(at_(a[2], at::kInt, dev, {B}));
+    const int most = int_of(a[3]), b = small(B), rows = small(N);
+    const Ws ws = ws_of(a[4], dev);
+    at::Tensor pos, seen;
+    call([&] {
+      pos = at::empty({N}, on(dev, at::kInt));
+      seen = at::empty({N}, on(dev, at::kLong));
+      return more[0].tree(b, rows, most, pa, ca, la, pos.data_ptr<int32_t>(), seen.data_ptr<int64_t>(), ws.at, ws.bytes, stream_now(dev));
+    });
+    return pair(pos, seen);
+  });
+}
+
+// kv4_tree_attention(cache, q, table, lens, cu, pos, seen, max_new, cos, sin, interleaved, gq, window, softmax_scale, eps, workspace)
+PyObject* kv4_tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 16) Py_RETURN_NONE;
+  return guarded("swa_kv4_tree_attn", [&](Call& call) -> PyObject* {
+    const int dev = device_now();
+    const CacheDims c = cache_of(a[0], dev);
+    const at::Tensor &q = tensor(a[1]), &table = tensor(a[2]);
+    if (q.dim() != 3 || q.numel() == 0 || table.dim() != 2 || a[15] == Py_None) throw Refused{};
+    const auto type = q.scalar_type();
+    const int kind = kind_more(type);
+    const int64_t N = q.size(0), Hq = q.size(1), B = table.size(0), width = table.size(1);
+    const void* qa = at_(a[1], type, dev, {N, Hq, c.d});
+    const auto* ta = static_cast<const int32_t*>(at_(a[2], at::kInt, dev, {B, width}));
+    const auto* la = static_cast<const int32_t*>(at_(a[3], at::kInt, dev, {B}));
+    const auto* ca = static_cast<const int32_t*>(at_(a[4], at::kInt, dev, {B + 1}));
+    const auto* pa = static_cast<const int32_t*>(at_(a[5], at::kInt, dev, {N}));
+    const auto* sa = static_cast<const int64_t*>(at_(a[6], at::kLong, dev, {N}));
+    const int most = int_of(a[7]);
+    swa_rope r{};
+    const bool rope = rope_of(a[8], a[9], a[10], dev, r);
+    const auto* gq = static_cast<const float*>(at_(a[11], at::kFloat, dev, {c.d}));
+    const Ws ws = ws_of(a[15], dev);
+    const swa_params p{small(B), 1, small(Hq), c.Hkv, c.d, int_of(a[12]), 1, static_cast<float>(double_of(a[13])),
+                       static_cast<float>(double_of(a[14])), 0.f, 0};
+    const int max_pages = small(width), rows = small(N);
+    at::Tensor o, lse;
+    call([&] {
+      o = at::empty_like(q);
+      lse = at::empty({N, Hq}, on(dev, at::kFloat));
+      return more[kind].tree_attn(&p, nullptr, &c.c, rope ? &r : nullptr, rows, most, qa, gq, ta, max_pages, la, ca, pa, sa, o.data_ptr(),
+                                  lse.data_ptr<float>(), ws.at, ws.bytes, stream_now(dev));
+    });
+    return pair(o, lse);
+  });
+}
+
+// kv4_move(cache, src, dst, workspace)
+PyObject* kv4_move(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 4 || more[0].move == nullptr) Py_RETURN_NONE;
+  return guarded("swa_kv4_move", [&](Call& call) -> PyObject* {
+    const int dev = device_now();
+    const CacheDims c = cache_of(a[0], dev);
+    const at::Tensor& s = tensor(a[1]);
+    if (s.dim() != 2) throw Refused{};
+    const auto* sa = static_cast<const int64_t*>(at_(a[1], at::kLong, dev, s.sizes()));
+    const auto* da = static_cast<const int64_t*>(at_(a[2], at::kLong, dev, s.sizes()));
+    const Ws ws = ws_of(a[3], dev);
+    const swa_params p{small(s.size(0)), small(s.size(1)), c.Hkv, c.Hkv, c.d, -1, 1, 0.f, 0.f, 0.f, 0};
+    call([&] { return more[0].move(&p, &c.c, sa, da, ws.at, ws.bytes, stream_now(dev)); });
+    Py_RETURN_TRUE;
+  });
+}
+
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(bind),       FAST(raises),      FAST(rope_tables), FAST(rope_apply),    FAST(kv4_plan),
-                         FAST(kv4_append), FAST(kv4_read),    FAST(kv4_attention), {nullptr, nullptr, 0, nullptr}};
+                         FAST(kv4_append), FAST(kv4_read),    FAST(kv4_attention), FAST(bind_more), FAST(rms_norm), FAST(rms_norm_backward), FAST(w4_linear),
+                         FAST(kv4_tree),   FAST(kv4_tree_attention), FAST(kv4_move), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -123,13 +123,45 @@ swa_status launch_tree_tc(const kv4::TreeAttnArgs& a, cudaStream_t st) {
 template <bool kPolled>
 swa_status launch_tree(const kv4::TreeAttnArgs& a, int d, const kv4::TreeSplit& sp, cudaStream_t st) {
 #if !defined(SWA_ELEM_FP32)
-  if (sp.tc) return sp.nq == 32 ? launch_tree_tc<32, kPolled>(a, st) : launch_tree_tc<64, kPolled>(a, st);
+  if (sp.tc) return launch_tree_tc<64, kPolled>(a, st);
   // (head dim 128 has more rows than 16 in that form only)
   if (d == 128) return launch_tree<128, 1, kPolled>(a, st);
 #else
   if (d == 128) return sp.nq == 16 ? launch_tree<128, 1, kPolled>(a, st) : sp.nq == 32 ? launch_tree<128, 2, kPolled>(a, st) : launch_tree<128, 4, kPolled>(a, st);
 #endif
   return sp.nq == 16 ? launch_tree<64, 1, kPolled>(a, st) : sp.nq == 32 ? launch_tree<64, 2, kPolled>(a, st) : launch_tree<64, 4, kPolled>(a, st);
+}
+
+// Workspace of the serving block: that of the decode attention, then what lies
+// between its calls.
+struct ServeLayout {
+  size_t h, xn, q, k, v, o, lse, end;
+};
+ServeLayout serve_layout(const swa_params* p, int C, int n) {
+  ServeLayout L{};
+  const size_t es = sizeof(elem_t), t = static_cast<size_t>(n);
+  size_t at = align256(kKv4Bytes);
+  auto take = [&](size_t bytes) {
+    const size_t x = at;
+    at = align256(at + bytes);
+    return x;
+  };
+  L.h = take(t * C * es);
+  L.xn = take(t * C * es);
+  L.q = take(t * p->Hq * p->d * es);
+  L.k = take(t * p->Hkv * p->d * es);
+  L.v = take(t * p->Hkv * p->d * es);
+  L.o = take(t * p->Hq * p->d * es);
+  L.lse = take(t * p->Hq * sizeof(float));
+  L.end = at;
+  return L;
+}
+swa_status check_serve(const swa_params* p, int C, int n) {
+  swa_status s = check_params(p);
+  if (s != SWA_OK) return s;
+  if (p->T != 1 || p->causal != 1 || n < 0) return SWA_ERR_INVALID_ARG;
+  if ((s = check_norm(n, C)) != SWA_OK) return s;
+  return static_cast<long long>(p->Hq) * p->d > w4::kMaxN ? SWA_ERR_UNSUPPORTED : SWA_OK;
 }
 
 }  // namespace
@@ -317,6 +349,77 @@ swa_status swa_kv4_tree_attn(const swa_params* p, const swa_extras* ex, const sw
   a.wait_limit_ns = ex != nullptr && ex->wait_limit_ns != 0 ? ex->wait_limit_ns : kWaitLimitNs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return a.wait_limit_ns < kPollBelowNs ? launch_tree<true>(a, p->d, sp, st) : launch_tree<false>(a, p->d, sp, st);
+}
+
+size_t swa_kv4_block_workspace_size(const swa_params* p, int C, int n_tokens) {
+  return check_serve(p, C, n_tokens) == SWA_OK ? serve_layout(p, C, n_tokens).end : 0;
+}
+
+swa_status swa_kv4_block(const swa_params* p, const swa_extras* ex, const swa_kv4_cache* c, const swa_rope* r,
+                         const swa_kv4_weights* w, int n_tokens, int max_new, const void* x, const void* add, const float* gain,
+                         const float* gq, const float* gk, const void* ve, const int32_t* tok, const int64_t* slot,
+                         const int32_t* pos, const int32_t* cu, const int64_t* seen, const int32_t* table, int max_pages,
+                         const int32_t* lens, void* out, void* workspace, size_t ws_bytes, void* stream) {
+  if (p == nullptr || w == nullptr) return SWA_ERR_INVALID_ARG;
+  swa_status s = check_serve(p, w->C, n_tokens);
+  if (s != SWA_OK) return s;
+  const bool tree = seen != nullptr || cu != nullptr;
+  if ((seen == nullptr) != (cu == nullptr) || (!tree && n_tokens != p->B)) return SWA_ERR_INVALID_ARG;
+  if (ex != nullptr && (ex->gate_x != nullptr || ex->rope_cos != nullptr || ex->rope_sin != nullptr)) return SWA_ERR_INVALID_ARG;
+  if (ex != nullptr && ex->gate_w != nullptr && ex->gate_ch > w->C) return SWA_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned(workspace, 256)) return SWA_ERR_INVALID_ARG;
+  const ServeLayout L = serve_layout(p, w->C, n_tokens);
+  if (ws_bytes < L.end) return SWA_ERR_WORKSPACE;
+  if (n_tokens == 0) return SWA_OK;
+  if (!tensor_ok(x) || !tensor_ok(out) || out == x || (add != nullptr && out == add)) return SWA_ERR_INVALID_ARG;
+  for (const void* m : {w->wq, w->wk, w->wv, w->wo})
+    if (!tensor_ok(m)) return SWA_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const void* h = add != nullptr ? ws + L.h : x;
+  // everything that can be refused is, before the first launch: the calls below have their own checks, which these
+  // arguments pass, and those of the append and the attention come from outside
+  {
+    kv4::Cache cache{};
+    bool rope = false;
+    if ((s = check_cache(p, c, cache)) != SWA_OK || (s = check_rope(r, p->d, rope)) != SWA_OK) return s;
+    if ((s = check_tokens(p->B, n_tokens, tree ? max_new : 1)) != SWA_OK) return s;
+    if (!width_ok(max_pages, c->page) || slot == nullptr || pos == nullptr || table == nullptr || lens == nullptr) return SWA_ERR_INVALID_ARG;
+    if (!aligned(add, 16) || !aligned(gain, 16) || !aligned(gq, 16) || !aligned(gk, 4) || !aligned(tok, 4) || !aligned(slot, 8) ||
+        !aligned(pos, 4) || !aligned(cu, 4) || !aligned(seen, 8) || !aligned(table, 4) || !aligned(lens, 4))
+      return SWA_ERR_INVALID_ARG;
+    if (ve != nullptr && (!aligned(ve, 16) || tok == nullptr || p->vocab < 1)) return SWA_ERR_INVALID_ARG;
+    if (ex != nullptr && ex->gate_w != nullptr && (ex->gate_ch < 1 || ex->gate_ch > kMaxGateCh || p->Hkv > kMaxGateHeads))
+      return SWA_ERR_INVALID_ARG;
+  }
+  if ((s = swa_rms_norm(n_tokens, w->C, p->eps, x, add, gain, add != nullptr ? ws + L.h : nullptr, ws + L.xn, nullptr, nullptr,
+                        nullptr, stream)) != SWA_OK)
+    return s;
+  const int nq = p->Hq * p->d, nk = p->Hkv * p->d;
+  const struct { const void* w; int n; size_t to; } proj[] = {{w->wq, nq, L.q}, {w->wk, nk, L.k}, {w->wv, nk, L.v}};
+  for (const auto& m : proj)
+    if ((s = swa_w4_linear(n_tokens, m.n, w->C, ws + L.xn, nullptr, m.w, nullptr, ws + m.to, workspace, ws_bytes, stream)) != SWA_OK)
+      return s;
+  swa_params rows = *p;          // the tokens as rows of one, for the append
+  rows.B = n_tokens;
+  rows.Hq = p->Hkv;
+  swa_extras gate{};
+  if (ex != nullptr && ex->gate_w != nullptr && ve != nullptr) {
+    gate.gate_x = ws + L.xn;
+    gate.gate_x_stride = w->C;
+    gate.gate_w = ex->gate_w;
+    gate.gate_ch = ex->gate_ch;
+  }
+  if ((s = swa_kv4_append(&rows, gate.gate_w != nullptr ? &gate : nullptr, c, r, ws + L.k, ws + L.v, gk, ve, tok, nullptr, pos, slot,
+                          workspace, ws_bytes, stream)) != SWA_OK)
+    return s;
+  swa_extras wait{};
+  wait.wait_limit_ns = ex != nullptr ? ex->wait_limit_ns : 0;
+  float* lse = reinterpret_cast<float*>(ws + L.lse);
+  s = tree ? swa_kv4_tree_attn(p, &wait, c, r, n_tokens, max_new, ws + L.q, gq, table, max_pages, lens, cu, pos, seen, ws + L.o, lse,
+                               workspace, ws_bytes, stream)
+           : swa_kv4_attn(p, &wait, c, r, ws + L.q, gq, table, max_pages, lens, ws + L.o, lse, workspace, ws_bytes, stream);
+  if (s != SWA_OK) return s;
+  return swa_w4_linear(n_tokens, w->C, nq, ws + L.o, nullptr, w->wo, h, out, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

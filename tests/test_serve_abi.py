@@ -221,3 +221,35 @@ F32, I32, I64, U8, F8 = torch.float32, torch.int32, torch.int64, torch.uint8, to
 def test_python_refuses(call):
     with pytest.raises(ValueError):
         call()
+
+
+def block(kind="bf16", p=None, ex=None, c=None, r=None, w=None, **kw):
+    a = dict(n=10, max_new=8, x=A, add=None, gain=None, gq=None, gk=None, ve=None, tok=None, slot=A, pos=A, cu=A, seen=A, table=A,
+             max_pages=4, lens=A, out=X, ws=A, nws=1 << 28)
+    a.update(kw)
+    w = swa.swa_kv4_weights(64, A, A, A, A) if w is None else w
+    return swa.swa_kv4_block(params() if p is None else p, ex, cache() if c is None else c, r, w, *a.values(), None, kind)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("bad", [
+    dict(p=params(T=2)), dict(p=params(causal=0)), dict(p=params(Hq=3)), dict(w=swa.swa_kv4_weights(60, A, A, A, A)),
+    dict(w=swa.swa_kv4_weights(64, A, None, A, A)), dict(w=swa.swa_kv4_weights(64, A, A, A, A + 8)), dict(n=-1), dict(cu=None),
+    dict(seen=None), dict(cu=None, seen=None), dict(x=None), dict(out=None), dict(out=A), dict(add=X), dict(slot=None), dict(pos=None),
+    dict(table=None), dict(lens=None), dict(max_pages=0), dict(ws=None), dict(ws=A + 64), dict(gain=A + 4), dict(gq=A + 8),
+    dict(slot=A + 4), dict(seen=A + 4), dict(ve=A), dict(ve=A, tok=A), dict(max_new=0), dict(c=cache(page=8)), dict(c=cache(data=None)),
+    dict(r=swa.swa_rope(A, A, 0, 64, 0)), dict(ex=swa.swa_extras(gate_w=A, gate_ch=65)), dict(ex=swa.swa_extras(gate_w=A, gate_ch=33)),
+    dict(ex=swa.swa_extras(gate_x=A)), dict(ex=swa.swa_extras(rope_cos=A)),
+])
+def test_block_refuses(kind, bad):
+    assert block(kind, **bad) == BAD
+
+
+def test_block_limits():
+    n = swa.swa_kv4_block_workspace_size(params(), 64, 10)
+    assert n > swa.swa_kv4_workspace_size(params(), 32, 4)
+    assert block(nws=n - 1) == WS and block(n=0, x=None, nws=1 << 28) == OK and block(max_new=65) == UNS
+    assert block(w=swa.swa_kv4_weights(65544, A, A, A, A)) == UNS
+    assert swa.swa_kv4_block_workspace_size(params(T=2), 64, 10) == 0 and swa.swa_kv4_block_workspace_size(params(), 60, 10) == 0
+    if not torch.cuda.is_available():
+        assert block() in PAST and block(n=2, cu=None, seen=None) in PAST
