@@ -108,11 +108,20 @@ constexpr int kMoveThreads = 128;
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ MoveArgs a) {
   constexpr int KW = D / 8, VW = D / 4, SW = D / 64;       // words of a key row, 16-bit pieces of a value row, pairs of each
-  constexpr int RB = D + 8 * SW;                           // bytes of a token
-  __shared__ __align__(16) uint8_t held[kTreeTokens * RB];
+  constexpr int UNITS = KW + VW + 2 * SW;
+  __shared__ uint32_t held[kTreeTokens * UNITS];
   __shared__ long long to[kTreeTokens];
   __shared__ long long from[kTreeTokens];
   const long long slots = static_cast<long long>(a.c.n_pages) * a.c.page;
+  const int n = a.T * UNITS;
+  // where piece k of token o of a tile starts, and whether it has 16 bits
+  auto piece = [](int k, int o) {
+    if (k < KW) return o * (D / 2) + 4 * k;
+    if (k < KW + VW) return 8 * D + (o >> 1) * D + 4 * (k - KW) + 2 * (o & 1);
+    const int i = k - KW - VW, kv = i / SW, g = i - kv * SW;
+    return 16 * D + kv * D + o * (4 * SW) + 4 * g;
+  };
+  auto half = [](int k) { return k >= KW && k < KW + VW; };
   uint32_t bad = 0;
   const long long items = static_cast<long long>(a.B) * a.c.Hkv;
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
@@ -127,37 +136,28 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
       to[t] = d;
     }
     __syncthreads();
-    constexpr int UNITS = KW + VW + 2 * SW;
-    for (int u = threadIdx.x; u < a.T * UNITS; u += kMoveThreads) {
-      const int t = u / UNITS, k = u - t * UNITS;
-      if (from[t] < 0) continue;
-      const uint8_t* tile = tile_of<D>(a.c, from[t], h);
-      const int o = static_cast<int>(from[t] & 15);
-      uint8_t* x = held + t * RB;
-      if (k < KW) *reinterpret_cast<uint32_t*>(x + 4 * k) = *reinterpret_cast<const uint32_t*>(tile + o * (D / 2) + 4 * k);
-      else if (k < KW + VW)
-        *reinterpret_cast<uint16_t*>(x + D / 2 + 2 * (k - KW)) =
-            *reinterpret_cast<const uint16_t*>(tile + 8 * D + (o >> 1) * D + 4 * (k - KW) + 2 * (o & 1));
-      else {
-        const int i = k - KW - VW, kv = i / SW, g = i - kv * SW;
-        *reinterpret_cast<uint32_t*>(x + D + 4 * i) = *reinterpret_cast<const uint32_t*>(tile + 16 * D + kv * D + o * (4 * SW) + 4 * g);
+    // four pieces of a thread in flight
+    for (int u0 = threadIdx.x; u0 < n; u0 += 4 * kMoveThreads) {
+      uint32_t x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int u = u0 + i * kMoveThreads, t = u / UNITS, k = u - t * UNITS;
+        if (u >= n || from[t] < 0) continue;
+        const uint8_t* at = tile_of<D>(a.c, from[t], h) + piece(k, static_cast<int>(from[t] & 15));
+        if (half(k)) x[i] = *reinterpret_cast<const uint16_t*>(at);
+        else x[i] = *reinterpret_cast<const uint32_t*>(at);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (u0 + i * kMoveThreads < n) held[u0 + i * kMoveThreads] = x[i];
     }
     __syncthreads();
-    for (int u = threadIdx.x; u < a.T * UNITS; u += kMoveThreads) {
+    for (int u = threadIdx.x; u < n; u += kMoveThreads) {
       const int t = u / UNITS, k = u - t * UNITS;
       if (to[t] < 0) continue;
-      uint8_t* tile = tile_of<D>(a.c, to[t], h);
-      const int o = static_cast<int>(to[t] & 15);
-      const uint8_t* x = held + t * RB;
-      if (k < KW) *reinterpret_cast<uint32_t*>(tile + o * (D / 2) + 4 * k) = *reinterpret_cast<const uint32_t*>(x + 4 * k);
-      else if (k < KW + VW)
-        *reinterpret_cast<uint16_t*>(tile + 8 * D + (o >> 1) * D + 4 * (k - KW) + 2 * (o & 1)) =
-            *reinterpret_cast<const uint16_t*>(x + D / 2 + 2 * (k - KW));
-      else {
-        const int i = k - KW - VW, kv = i / SW, g = i - kv * SW;
-        *reinterpret_cast<uint32_t*>(tile + 16 * D + kv * D + o * (4 * SW) + 4 * g) = *reinterpret_cast<const uint32_t*>(x + D + 4 * i);
-      }
+      uint8_t* at = tile_of<D>(a.c, to[t], h) + piece(k, static_cast<int>(to[t] & 15));
+      if (half(k)) *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(held[u]);
+      else *reinterpret_cast<uint32_t*>(at) = held[u];
     }
     __syncthreads();
   }
@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
 struct TreeAttnArgs : AttnArgs {
   int N, max_new;
   const int32_t* cu; const int32_t* pos; const int64_t* seen;
+  int slots, setup;                  // CTAs that run at once (0: chunk is given), and their set-up in tiles
 };
 
 constexpr int kQTerms = 2;
@@ -212,6 +213,118 @@ struct TreeRow {
   int pos;
   unsigned long long seen;
 };
+
+// A CTA's share of a call: the chunk'th chunk of `chunk` tiles of group qg of
+// request b's rows under kv head h. Either as the host laid them out (grid x of
+// chunks, y of kv heads and groups, z of requests: nothing to be computed), or, for
+// long contexts, a flat grid whose CTAs look at all the lengths and find the chunk
+// for which the call should end first: the host knows only the longest possible
+// request, and a batch that is ragged, or far below its tables' width, left most of
+// the GPU idle (64 ragged requests of at most 16384 tokens, 16 query heads on 2: 165 us
+// against 70; 16 in fp32 of at most 5000: 39 against 27). Every CTA comes to the same answer: integers, and
+// fp32 of them.
+struct TreeShare {
+  int b, h, qg, ci, chunk;
+  long long item, part0;             // its counter, and the first of its chunks' rows in part
+  bool none;
+};
+constexpr int kShareB = 128;         // requests of a call whose CTAs do so
+constexpr int kShareN = 128;         // chunks of the longest request that are tried
+constexpr int kJoinTiles = 8;        // what a join costs, in tiles
+constexpr int kShareTiles = 256;     // tables of at least so many tiles a request
+
+template <int NQ, int kThreads>
+__device__ __forceinline__ TreeShare tree_share(const TreeAttnArgs& a) {
+  TreeShare x;
+  x.none = false;
+  if (a.slots == 0) {
+    x.b = blockIdx.z;
+    x.h = blockIdx.y / a.groups;
+    x.qg = blockIdx.y - x.h * a.groups;
+    x.ci = blockIdx.x;
+    x.chunk = a.chunk;
+    x.item = (static_cast<long long>(x.b) * a.c.Hkv + x.h) * a.groups + x.qg;
+    x.part0 = x.item * a.splits * NQ;
+    return x;
+  }
+  __shared__ int tiles[kShareB], items[kShareB];
+  __shared__ float2 bests[kShareN / 32];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, G = a.Hq / a.c.Hkv;
+  for (int b = tid; b < a.B; b += kThreads) {
+    const TreeReq req = tree_req(a.cu, a.lens, b, a.N, a.max_new, static_cast<long long>(a.max_pages) * a.c.page);
+    const int len = req.ctx + req.n, lo = a.window >= 0 && req.ctx - a.window > 0 ? req.ctx - a.window : 0;
+    tiles[b] = req.n > 0 ? max(1, (len + kTile - 1) / kTile - lo / kTile) : 1;
+    items[b] = a.c.Hkv * max(1, (req.n * G + NQ - 1) / NQ);        // (rows to be zeroed take a CTA a kv head)
+  }
+  __syncthreads();
+  // n / c, rounded up, for quotients of a few hundred: the product is off by less than one
+  auto div_up = [](int n, int c, float inv) {
+    n += c - 1;
+    int q = static_cast<int>(static_cast<float>(n) * inv);
+    const long long rest = n - static_cast<long long>(q) * c;
+    return q + (rest >= c) - (rest < 0);
+  };
+  int longest = 1;
+  float total = 0.f;                 // (the same sum in every lane: the exchange adds the same pairs)
+  for (int b = lane; b < a.B; b += 32) {
+    longest = max(longest, tiles[b]);
+    total += static_cast<float>(tiles[b]) * static_cast<float>(items[b]);
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  static_assert(kShareN <= kThreads, "");
+  if (tid < kShareN) {               // thread n: the longest request in n + 1 chunks
+    const int c = ((longest + tid) / (tid + 1) + 7) / 8 * 8;
+    const float inv = 1.0f / static_cast<float>(c);
+    int k = 0;
+#pragma unroll 4
+    for (int b = 0; b < a.B; ++b) k += items[b] * div_up(tiles[b], c, inv);
+    const float own = static_cast<float>((c < longest ? c : longest) + a.setup), per = 1.0f / static_cast<float>(a.slots);
+    // whole rounds of equal CTAs, or as short ones fill up: both are bounds
+    const float even = ceilf(static_cast<float>(k) * per) * own;
+    const float filled = (total + static_cast<float>(k) * a.setup) * per + own;
+    const int n = div_up(longest, c, inv);
+    float t = fminf(even, filled) + (n > 1 ? kJoinTiles + n / 2 : 0);
+    if (k > static_cast<int>(gridDim.x)) t = INFINITY;
+    const unsigned least = __reduce_min_sync(0xffffffffu, __float_as_uint(t));        // (positive)
+    const int at = __ffs(__ballot_sync(0xffffffffu, __float_as_uint(t) == least)) - 1;
+    if (lane == at) bests[wid] = make_float2(t, __int_as_float(c));
+  }
+  __syncthreads();
+  float2 best = bests[0];
+#pragma unroll
+  for (int i = 1; i < kShareN / 32; ++i)
+    if (bests[i].x < best.x) best = bests[i];
+  x.chunk = __float_as_int(best.y);
+  const float inv = 1.0f / static_cast<float>(x.chunk);
+  int first = 0;                     // CTAs of the requests in front of b0
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane, per = b < a.B ? div_up(tiles[b], x.chunk, inv) : 1, k = b < a.B ? items[b] * per : 0;
+    int end = k;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += v;
+    }
+    const int at = static_cast<int>(blockIdx.x) - first - (end - k);
+    const unsigned here = __ballot_sync(0xffffffffu, at >= 0 && at < k);
+    if (here) {
+      const int src = __ffs(here) - 1, mine = __shfl_sync(0xffffffffu, at, src), p = __shfl_sync(0xffffffffu, per, src);
+      x.b = b0 + src;
+      const int it = mine / p, groups = items[x.b] / a.c.Hkv;
+      x.h = it / groups;
+      x.qg = it - x.h * groups;
+      x.ci = mine - it * p;
+      x.item = static_cast<int>(blockIdx.x) - x.ci;
+      x.part0 = x.item * NQ;
+      return x;
+    }
+    first += __shfl_sync(0xffffffffu, end, 31);
+  }
+  x.none = true;
+  return x;
+}
 
 // What the CTA's rows see, and the drafted tokens' positions, into shared memory.
 template <int NQ, int kThreads>
@@ -261,45 +374,80 @@ __device__ __forceinline__ void tree_zero(const TreeAttnArgs& a, const TreeReq& 
 // A row's sums o (relative to top, base 2), joined over the warps of a CTA by one
 // warp: into o and lse, or beside the other chunks'. part0: of the CTA's item.
 template <int D>
-__device__ __forceinline__ void tree_row_out(const TreeAttnArgs& a, int chunks, long long part0, int nq_slot, int i, long long head,
+__device__ __forceinline__ void tree_row_out(const TreeAttnArgs& a, int chunks, int ci, long long part0, int nq_slot, int i, long long head,
                                              float (&o)[D / 32], float top, float sum) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   if (chunks == 1) {
     finish_head<D>(a, head, o, top, sum);
   } else {
-    const long long at = part0 + static_cast<long long>(blockIdx.x) * nq_slot + i;
+    const long long at = part0 + static_cast<long long>(ci) * nq_slot + i;
     store_vec<E>(a.part + at * D + lane * E, o);
     if (lane == 0) a.part_ml[at] = make_float2(top, sum);
   }
 }
-// Row i of all chunks, joined in their order by one warp.
-template <int D>
-__device__ __forceinline__ void tree_join(const TreeAttnArgs& a, int chunks, long long part0, int nq_slot, int i, long long head) {
+// Rows i0, i0 + step .. below nq of all chunks, joined in their order by one warp:
+// R rows and U chunks of each in flight, since each load waits out the L2's
+// latency (32 requests in a window of 1024 keys, three chunks each: 26.6 us with one row
+// after the other, 24.4 so).
+template <int D, int R, int U, typename Head>
+__device__ __forceinline__ void tree_join(const TreeAttnArgs& a, int chunks, long long part0, int nq_slot, int i0, int step, int nq,
+                                          Head head_of) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
-  float top = -1e30f, sum = 0.f, o[E] = {};
-  for (int k = lane; k < chunks; k += 32) top = fmaxf(top, __ldcg(a.part_ml + part0 + static_cast<long long>(k) * nq_slot + i).x);
+  for (int i = i0; i < nq; i += R * step) {
+    float top[R], sum[R], o[R][E];
+    long long at[R];
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-#pragma unroll 4
-  for (int k = 0; k < chunks; ++k) {
-    const long long at = part0 + static_cast<long long>(k) * nq_slot + i;
-    const float2 ml = __ldcg(a.part_ml + at);
-    float x[E];
-    if constexpr (E == 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + at * D + lane * E));
-      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-    } else {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part + at * D + lane * E));
-      x[0] = v.x; x[1] = v.y;
+    for (int r = 0; r < R; ++r) {
+      at[r] = part0 + (i + r * step < nq ? i + r * step : i);
+      top[r] = -1e30f;
+      sum[r] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[r][e] = 0.f;
     }
-    const float f = ex2_approx(ml.x - top);
-    sum = fmaf(f, ml.y, sum);
+    for (int k = lane; k < chunks; k += 32)
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(f, x[e], o[e]);
+      for (int r = 0; r < R; ++r) top[r] = fmaxf(top[r], __ldcg(a.part_ml + at[r] + static_cast<long long>(k) * nq_slot).x);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], x));
+    for (int k0 = 0; k0 < chunks; k0 += U) {
+      float2 ml[U][R];
+      float x[U][R][E];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const long long k = static_cast<long long>(k0 + u < chunks ? k0 + u : k0) * nq_slot;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          ml[u][r] = __ldcg(a.part_ml + at[r] + k);
+          const float* from = a.part + (at[r] + k) * D + lane * E;
+          if constexpr (E == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(from));
+            x[u][r][0] = v.x; x[u][r][1] = v.y; x[u][r][2] = v.z; x[u][r][3] = v.w;
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(from));
+            x[u][r][0] = v.x; x[u][r][1] = v.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (k0 + u >= chunks) continue;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float f = ex2_approx(ml[u][r].x - top[r]);
+          sum[r] = fmaf(f, ml[u][r].y, sum[r]);
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[r][e] = fmaf(f, x[u][r][e], o[r][e]);
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (i + r * step < nq) finish_head<D>(a, head_of(i + r * step), o[r], top[r], sum[r]);
   }
-  finish_head<D>(a, head, o, top, sum);
 }
 
 // NR query rows by one warp at once (query_row's arithmetic, row after row the
@@ -407,14 +555,16 @@ __global__ void __launch_bounds__(kAttnWarps * 32, tree_ctas_per_sm(D)) tree_att
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int r = lane >> 2, j = lane & 3;
   const int rw = wid % RW, kg = wid / RW;                  // rows 16 rw .., steps kg, kg + KG, ..
-  const int b = blockIdx.z, h = blockIdx.y / a.groups, qg = blockIdx.y - h * a.groups;
+  const TreeShare share = tree_share<NQ, kAttnWarps * 32>(a);
+  if (share.none) return;
+  const int b = share.b, h = share.h, qg = share.qg;
   const int G = a.Hq / a.c.Hkv;
   const long long cap = static_cast<long long>(a.max_pages) * a.c.page;
   uint32_t bad = 0;
   const TreeReq req = tree_req(a.cu, a.lens, b, a.N, a.max_new, cap);
   if (req.bad) bad = DEV_ERR_BOUNDS;
 
-  if (blockIdx.x == 0 && qg == 0) tree_zero<D, kAttnWarps>(a, req, b, h, G);
+  if (share.ci == 0 && qg == 0) tree_zero<D, kAttnWarps>(a, req, b, h, G);
   if (bad && tid == 0) atomicOr(a.status, bad);
   const int row_q0 = qg * NQ;                              // first (token, head) row of this CTA
   const int nq = min(NQ, req.n * G - row_q0);
@@ -422,9 +572,9 @@ __global__ void __launch_bounds__(kAttnWarps * 32, tree_ctas_per_sm(D)) tree_att
   const int len = req.ctx + req.n;
   const int lo = a.window >= 0 && req.ctx - a.window > 0 ? req.ctx - a.window : 0;
   const int t_lo = lo / kTile, t_hi = (len + kTile - 1) / kTile;     // tiles [t_lo, t_hi)
-  const int chunks = max(1, (t_hi - t_lo + a.chunk - 1) / a.chunk);
-  if (blockIdx.x >= chunks) return;
-  const int t0 = t_lo + blockIdx.x * a.chunk, t1 = min(t_hi, t0 + a.chunk);
+  const int chunks = max(1, (t_hi - t_lo + share.chunk - 1) / share.chunk);
+  if (share.ci >= chunks) return;
+  const int t0 = t_lo + share.ci * share.chunk, t1 = min(t_hi, t0 + share.chunk);
 
   const uint32_t bars = smem_u32(smem + M::bars) + kg * ST * 16, frees = bars + ST * 8;
   uint32_t* flags = reinterpret_cast<uint32_t*>(smem + M::flags);    // [0] abort, [1] last
@@ -717,8 +867,6 @@ __global__ void __launch_bounds__(kAttnWarps * 32, tree_ctas_per_sm(D)) tree_att
     const int row = row_q0 + i;
     return static_cast<long long>(req.row0 + row / G) * a.Hq + h * G + row % G;
   };
-  const long long item = (static_cast<long long>(b) * a.c.Hkv + h) * a.groups + qg;
-  const long long part0 = item * a.splits * NQ;
   for (int i = wid; i < nq; i += kAttnWarps) {      // a warp a row, E channels a lane
     float top = -1e30f, sum = 0.f, o[E] = {};
 #pragma unroll
@@ -738,21 +886,20 @@ __global__ void __launch_bounds__(kAttnWarps * 32, tree_ctas_per_sm(D)) tree_att
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = 0.f;
     }
-    tree_row_out<D>(a, chunks, part0, NQ, i, head_of(i), o, top, sum);
+    tree_row_out<D>(a, chunks, share.ci, share.part0, NQ, i, head_of(i), o, top, sum);
   }
   if (chunks == 1) return;
   __syncthreads();
   if (tid == 0) {
     __threadfence();      // after the barrier it covers what the CTA wrote
-    flags[1] = atomicAdd(a.count + item, 1u) == static_cast<unsigned>(chunks - 1);
+    flags[1] = atomicAdd(a.count + share.item, 1u) == static_cast<unsigned>(chunks - 1);
   }
   __syncthreads();
   if (!flags[1]) return;
   __threadfence();
-  if (tid == 0) a.count[item] = 0;        // for the next call
+  if (tid == 0) a.count[share.item] = 0;        // for the next call
 
-  // join the chunks in their order: a warp a row
-  for (int i = wid; i < nq; i += kAttnWarps) tree_join<D>(a, chunks, part0, NQ, i, head_of(i));
+  tree_join<D, 4, 4>(a, chunks, share.part0, NQ, wid, kAttnWarps, nq, head_of);
 }
 
 // Warps over rows, chunks and CTAs of a call, from what the host knows. Partial
@@ -762,14 +909,16 @@ struct TreeSplit {
   bool tc;               // the tcgen05 form
   int groups, chunk, splits;
   long long items;
+  int grid, slots, setup;   // grid > 0: a flat one, whose CTAs find their shares
+  long long parts;          // rows of partial results
 };
 inline TreeSplit tree_split(int B, int Hq, int Hkv, int d, int page, int max_pages, int window, int max_new, long long part_floats) {
   TreeSplit s;
   const int rows = Hq / Hkv * max_new;
   s.tc = !kThreeTerms && d == 128 && rows > 16;
   s.nq = rows <= 16 ? 16 : (rows <= 32 && !s.tc ? 32 : 64);
-  // in tiles of one CTA: its set-up and end, the join, and what a chunk is a multiple of
-  const long long kSetup = s.tc ? 48 : 24, kJoin = 8, kStep = 8, nq = s.nq;
+  s.setup = s.tc ? 48 : 24;          // set-up and end of a CTA, in tiles that it could have done
+  const long long nq = s.nq;
   s.groups = static_cast<int>((rows + nq - 1) / nq);
   s.items = static_cast<long long>(B) * Hkv * s.groups;
   const long long cap = static_cast<long long>(max_pages) * page;
@@ -777,20 +926,34 @@ inline TreeSplit tree_split(int B, int Hq, int Hkv, int d, int page, int max_pag
   if (window >= 0 && static_cast<long long>(window) + max_new + kTile < cap) keys = static_cast<long long>(window) + max_new + kTile;
   const long long tiles = (keys + kTile - 1) / kTile;
   const long long slots = 152LL * (s.tc ? 1 : tree_ctas_per_sm(d));
+  const long long room = part_floats / (nq * (d + 2));      // partial results of CTAs
+  // The CTAs look for their shares where that can spare more than the microsecond
+  // that it takes (16 equal requests of 32768: 180 us without, 186 so; of 1500: 19.2,
+  // 20.6), and where there is room to split a request.
+  s.grid = 0;
+  s.slots = 0;
+  if (tiles >= kShareTiles && B <= kShareB && s.items < (room < 65536 ? room : 65536 - slots)) {
+    s.grid = static_cast<int>(s.items + slots < room ? s.items + slots : room);
+    s.slots = static_cast<int>(slots);
+    s.chunk = s.splits = 0;
+    s.parts = s.grid * nq;
+    return s;
+  }
   long long best = 0, chunk = tiles;
   for (long long n = 1; n <= kMaxSplits; ++n) {
-    const long long c = ((tiles + n - 1) / n + kStep - 1) / kStep * kStep, real = (tiles + c - 1) / c;
-    if (real > 1 && s.items * real * nq * (d + 2) > part_floats) break;
-    const long long own = (c < tiles ? c : tiles) + kSetup;
-    const long long t = (s.items * real + slots - 1) / slots * own + (real > 1 ? kJoin + real / 2 : 0);
+    const long long c = ((tiles + n - 1) / n + 7) / 8 * 8, real = (tiles + c - 1) / c;
+    if (real > 1 && s.items * real > room) break;
+    const long long own = (c < tiles ? c : tiles) + s.setup;
+    const long long t = (s.items * real + slots - 1) / slots * own + (real > 1 ? kJoinTiles + real / 2 : 0);
     if (n == 1 || t < best) {
       best = t;
       chunk = c;
     }
-    if (c == kStep) break;
+    if (c == 8) break;
   }
   s.chunk = static_cast<int>(chunk);
   s.splits = static_cast<int>((tiles + chunk - 1) / chunk);
+  s.parts = s.items * s.splits * nq;
   return s;
 }
 

@@ -2,8 +2,12 @@
 // library, head dim 128): more than 16 (token, head) rows of a kv head.
 //
 // With many rows the m16n8k16 form (kv4_tree.cuh) is held by its products and by
-// the softmax beside them: 64 rows take it 548 us where the cache's bytes take the
-// memory 43. Here a block is 128 keys (eight tiles), the lanes of tensor memory:
+// the softmax beside them: 16 requests of 32768 tokens, 64 rows for each of 4 kv
+// heads, took it 548 us where the cache's bytes take the memory 43 and the products
+// 34. This form takes 181, and is held by the softmax warps' round of a block, 2600
+// clocks: their exponentials, P's stores, and the waits for S around them. (With 32
+// rows a CTA 201; with a thread's 16 rows instead of 32 its registers spill, 335.)
+// Here a block is 128 keys (eight tiles), the lanes of tensor memory:
 //   S^T[keys x rows]     = K Q^T    K from tensor memory (a lane a key), Q from
 //                                   shared memory, rows twice: q's two fp16 terms
 //   O^T[channels x rows] += V^T P^T V^T from tensor memory (a lane a channel), P
@@ -49,7 +53,7 @@ struct TtShape {
   static constexpr int soft = NR / 8, keys0 = soft, values0 = soft + 8, mma = soft + 12, mma_o = mma + 1, load = mma + 2;
   static constexpr int warps = soft + 16;        // whole groups of four, for the registers; the last does nothing
   // registers of a thread: at launch, then softmax, keys and values, the rest (soft 128 threads for each 32 rows)
-  static constexpr int regs0 = NR == 64 ? 80 : 96, regs_soft = 112, regs_convert = 72, regs_rest = 40;
+  static constexpr int regs0 = 80, regs_soft = 112, regs_convert = 72, regs_rest = 40;
   static_assert(128 * (NR / 32 * regs_soft + 3 * regs_convert + regs_rest) <= warps * 32 * regs0, "");
   static constexpr int N = 2 * NR;               // columns of S: both terms
   // tensor memory
@@ -118,21 +122,23 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.z, h = blockIdx.y / a.groups, qg = blockIdx.y - h * a.groups;
+  const TreeShare share = tree_share<NR, S::warps * 32>(a);
+  if (share.none) return;
+  const int b = share.b, h = share.h, qg = share.qg;
   const int G = a.Hq / a.c.Hkv;
   uint32_t bad = 0;
   const TreeReq req = tree_req(a.cu, a.lens, b, a.N, a.max_new, static_cast<long long>(a.max_pages) * a.c.page);
   if (req.bad || (sbase & 1023u)) bad = DEV_ERR_BOUNDS;      // (swizzle atoms need 1024-byte aligned tiles)
-  if (blockIdx.x == 0 && qg == 0) tree_zero<D, S::warps>(a, req, b, h, G);
+  if (share.ci == 0 && qg == 0) tree_zero<D, S::warps>(a, req, b, h, G);
   if (bad && tid == 0) atomicOr(a.status, bad);
   const int row_q0 = qg * NR, nq = min(NR, req.n * G - row_q0);
   if (nq <= 0 || (sbase & 1023u)) return;
   const int len = req.ctx + req.n;
   const int lo = a.window >= 0 && req.ctx - a.window > 0 ? req.ctx - a.window : 0;
   const int t_lo = lo / kTile, t_hi = (len + kTile - 1) / kTile;     // tiles [t_lo, t_hi)
-  const int chunks = max(1, (t_hi - t_lo + a.chunk - 1) / a.chunk);
-  if (blockIdx.x >= chunks) return;
-  const int t0 = t_lo + blockIdx.x * a.chunk, t1 = min(t_hi, t0 + a.chunk);
+  const int chunks = max(1, (t_hi - t_lo + share.chunk - 1) / share.chunk);
+  if (share.ci >= chunks) return;
+  const int t0 = t_lo + share.ci * share.chunk, t1 = min(t_hi, t0 + share.chunk);
   const int blocks = (t1 - t0 + kTtTiles - 1) / kTtTiles;
 
   auto bar = [&](int i) { return sbase + S::oBar + 8u * static_cast<uint32_t>(i); };
@@ -591,8 +597,6 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
     const int row = row_q0 + i;
     return static_cast<long long>(req.row0 + row / G) * a.Hq + h * G + row % G;
   };
-  const long long item = (static_cast<long long>(b) * a.c.Hkv + h) * a.groups + qg;
-  const long long part0 = item * a.splits * NR;
   const float* red = reinterpret_cast<const float*>(smem + S::oRed);
   for (int i = warp; i < nq; i += S::warps) {      // a warp a row
     float o[E], top = -rowm[i], sum = (red[i] + red[NR + i]) + (red[2 * NR + i] + red[3 * NR + i]);
@@ -603,19 +607,19 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = 0.f;
     }
-    tree_row_out<D>(a, chunks, part0, NR, i, head_of(i), o, top, sum);
+    tree_row_out<D>(a, chunks, share.ci, share.part0, NR, i, head_of(i), o, top, sum);
   }
   if (chunks == 1) return;
   __syncthreads();
   if (tid == 0) {
     __threadfence();      // after the barrier it covers what the CTA wrote
-    flags[1] = atomicAdd(a.count + item, 1u) == static_cast<unsigned>(chunks - 1);
+    flags[1] = atomicAdd(a.count + share.item, 1u) == static_cast<unsigned>(chunks - 1);
   }
   __syncthreads();
   if (!flags[1]) return;
   __threadfence();
-  if (tid == 0) a.count[item] = 0;        // for the next call
-  for (int i = warp; i < nq; i += S::warps) tree_join<D>(a, chunks, part0, NR, i, head_of(i));
+  if (tid == 0) a.count[share.item] = 0;        // for the next call
+  tree_join<D, 1, 4>(a, chunks, share.part0, NR, warp, S::warps, nq, head_of);
 }
 
 }  // namespace kv4

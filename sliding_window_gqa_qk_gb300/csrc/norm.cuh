@@ -278,10 +278,17 @@ struct BwdArgs {
   float* part;                          // [blocks][C], or NULL: no gradient of the gain
 };
 
+// A row's three tensors are loaded together and its products with the gain are
+// kept, so that the gain is read once a row (32768 x 768 in bf16: 66 us with dh loaded
+// behind the sum and the gain read twice, 42 so; its bytes take 30). Rows of many
+// threads meet at a barrier, with nothing in flight but what was asked for before
+// it: the next row is, where registers hold it (5001 x 8192 in fp32: 106 us without,
+// 86 so, its bytes 73; 8192 x 4096 in bf16 51, its bytes 40). The blocks are as many
+// as run at once with 128 registers a thread.
 template <int TPR, int VPT>
-__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) bwd_kernel(const __grid_constant__ BwdArgs a) {
+__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, TPR == 32 ? 2 : 512 / TPR) bwd_kernel(const __grid_constant__ BwdArgs a) {
   constexpr int RPB = TPR == 32 ? 8 : 1;
-  constexpr bool kLoop = VPT == 0;
+  constexpr bool kLoop = VPT == 0, kNext = !kLoop && TPR > 32 && (kEpl == 4 || VPT < 3);
   constexpr int V = kLoop ? 1 : VPT;
   __shared__ float buf[TPR == 32 ? 1 : 2 * TPR / 32];
   extern __shared__ float sums[];        // TPR == 32: [C] of the block
@@ -291,74 +298,99 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) bwd_kernel(const __grid
   float acc[V][kEpl] = {};
   float* mine = a.part != nullptr ? a.part + static_cast<long long>(blockIdx.x) * a.C : nullptr;
   bool first = true;
-  for (long long r = static_cast<long long>(blockIdx.x) * RPB + (TPR == 32 ? threadIdx.x >> 5 : 0); r < a.rows;
-       r += static_cast<long long>(gridDim.x) * RPB) {
+  uint4 hv[V], dv[V], ev[V];
+  float rs = 0.f;
+  auto load = [&](long long r) {
     const long long base = r * a.C;
-    const float rs = a.rstd[r];
-    uint4 hv[V], dv[V];
-    auto load = [&](int k, int i) {
-      hv[k] = ld16(a.h + base + static_cast<long long>(i) * kEpl);
-      dv[k] = ld16(a.dy + base + static_cast<long long>(i) * kEpl);
-    };
-    auto dots = [&](int k, int i, float& dot) {
-      float x[kEpl], d[kEpl], g[kEpl];
-      unpack16(hv[k], x);
-      unpack16(dv[k], d);
-      if (a.gain != nullptr) ldf<kEpl>(a.gain + i * kEpl, g);
+    rs = a.rstd[r];
 #pragma unroll
-      for (int e = 0; e < kEpl; ++e) {
-        const float n = x[e] * rs;
-        dot = fmaf(a.gain != nullptr ? d[e] * g[e] : d[e], n, dot);
-        x[e] = d[e] * n;
-      }
-      if (kLoop) {
-        if (mine != nullptr) {
-          float s[kEpl] = {};
-          if (!first) ldf<kEpl>(mine + i * kEpl, s);
+    for (int k = 0; k < V; ++k) {
+      if (t + k * TPR >= nv) continue;
+      const long long at = base + static_cast<long long>(t + k * TPR) * kEpl;
+      hv[k] = ld16(a.h + at);
+      dv[k] = ld16(a.dy + at);
+      if (a.dh != nullptr) ev[k] = ld16(a.dh + at);
+    }
+  };
+  // (dy xh) into the gain's sums; d = g dy and its product with xh
+  auto products = [&](const uint4& hr, const uint4& dr, int c, float rstd, float (&d)[kEpl], float (&w)[kEpl], float& dot) {
+    float x[kEpl], g[kEpl];
+    unpack16(hr, x);
+    unpack16(dr, d);
+    gains(a.gain, c, g);
 #pragma unroll
-          for (int e = 0; e < kEpl; ++e) s[e] += x[e];
-          stf<kEpl>(mine + i * kEpl, s);
-        }
-      } else {
+    for (int e = 0; e < kEpl; ++e) {
+      const float n = x[e] * rstd;
+      w[e] = d[e] * n;
+      d[e] *= g[e];
+      dot = fmaf(d[e], n, dot);
+    }
+  };
+  auto write = [&](const uint4& hr, const uint4& er, long long at, float rstd, float mean, float (&d)[kEpl]) {
+    float x[kEpl];
+    unpack16(hr, x);
 #pragma unroll
-        for (int e = 0; e < kEpl; ++e) acc[k][e] += x[e];
-      }
-    };
-    auto write = [&](int k, int i, float mean) {
-      float x[kEpl], d[kEpl], g[kEpl];
-      unpack16(hv[k], x);
-      unpack16(dv[k], d);
-      if (a.gain != nullptr) {
-        ldf<kEpl>(a.gain + i * kEpl, g);
+    for (int e = 0; e < kEpl; ++e) d[e] = rstd * fmaf(-x[e] * rstd, mean, d[e]);
+    if (a.dh != nullptr) {
+      unpack16(er, x);
 #pragma unroll
-        for (int e = 0; e < kEpl; ++e) d[e] *= g[e];
-      }
-#pragma unroll
-      for (int e = 0; e < kEpl; ++e) d[e] = rs * fmaf(-x[e] * rs, mean, d[e]);
-      if (a.dh != nullptr) {
-        unpack16(ld16(a.dh + base + static_cast<long long>(i) * kEpl), g);
-#pragma unroll
-        for (int e = 0; e < kEpl; ++e) d[e] += g[e];
-      }
-      st16(a.dx + base + static_cast<long long>(i) * kEpl, pack16(d));
-    };
+      for (int e = 0; e < kEpl; ++e) d[e] += x[e];
+    }
+    st16(a.dx + at, pack16(d));
+  };
+  const long long stride = static_cast<long long>(gridDim.x) * RPB;
+  long long r = static_cast<long long>(blockIdx.x) * RPB + (TPR == 32 ? threadIdx.x >> 5 : 0);
+  if (kNext && r < a.rows) load(r);
+  for (; r < a.rows; r += stride) {
+    const long long base = r * a.C;
     float dot = 0.f;
     if constexpr (kLoop) {
-      for (int i = t; i < nv; i += TPR) { load(0, i); dots(0, i, dot); }
+      const float rstd = a.rstd[r];
+      for (int i = t; i < nv; i += TPR) {
+        const long long at = base + static_cast<long long>(i) * kEpl;
+        float d[kEpl], w[kEpl];
+        products(ld16(a.h + at), ld16(a.dy + at), i * kEpl, rstd, d, w, dot);
+        if (mine != nullptr) {
+          float sum[kEpl] = {};
+          if (!first) ldf<kEpl>(mine + i * kEpl, sum);
+#pragma unroll
+          for (int e = 0; e < kEpl; ++e) sum[e] += w[e];
+          stf<kEpl>(mine + i * kEpl, sum);
+        }
+      }
+      const float mean = row_reduce<TPR, false>(dot, buf, turn) / a.C;
+      for (int i = t; i < nv; i += TPR) {
+        const long long at = base + static_cast<long long>(i) * kEpl;
+        const uint4 x = ld16(a.h + at);
+        float d[kEpl], w[kEpl], none = 0.f;
+        products(x, ld16(a.dy + at), i * kEpl, rstd, d, w, none);
+        write(x, a.dh != nullptr ? ld16(a.dh + at) : x, at, rstd, mean, d);
+      }
+      first = false;
     } else {
+      if (!kNext) load(r);
+      float d[V][kEpl];
 #pragma unroll
-      for (int k = 0; k < V; ++k) if (t + k * TPR < nv) load(k, t + k * TPR);
+      for (int k = 0; k < V; ++k) {
+        if (t + k * TPR >= nv) continue;
+        float w[kEpl];
+        products(hv[k], dv[k], (t + k * TPR) * kEpl, rs, d[k], w, dot);
 #pragma unroll
-      for (int k = 0; k < V; ++k) if (t + k * TPR < nv) dots(k, t + k * TPR, dot);
+        for (int e = 0; e < kEpl; ++e) acc[k][e] += w[e];
+      }
+      uint4 h0[V], e0[V];
+      const float rs0 = rs;
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        h0[k] = hv[k];
+        e0[k] = ev[k];
+      }
+      if (kNext && r + stride < a.rows) load(r + stride);
+      const float mean = row_reduce<TPR, false>(dot, buf, turn) / a.C;
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (t + k * TPR < nv) write(h0[k], e0[k], base + static_cast<long long>(t + k * TPR) * kEpl, rs0, mean, d[k]);
     }
-    const float mean = row_reduce<TPR, false>(dot, buf, turn) / a.C;
-    if constexpr (kLoop) {
-      for (int i = t; i < nv; i += TPR) { load(0, i); write(0, i, mean); }
-    } else {
-#pragma unroll
-      for (int k = 0; k < V; ++k) if (t + k * TPR < nv) write(k, t + k * TPR, mean);
-    }
-    first = false;
   }
   if (mine == nullptr || kLoop) return;
   if constexpr (TPR == 32) {             // the block's eight rows of sums, warp after warp
@@ -404,10 +436,11 @@ __global__ void __launch_bounds__(256) gain_kernel(const float* __restrict__ par
   }
 }
 
-// Threads of a row and vectors of a thread: f(integral constants TPR, VPT).
+// Threads of a row and vectors of a thread: f(integral constants TPR, VPT). The
+// backward pass, which holds a row three times, takes more threads for long ones.
 template <int N>
 struct Int { static constexpr int value = N; };
-template <typename F>
+template <bool kBwd, typename F>
 void by_width(int C, F f) {
   const int nv = C / kEpl;
   if (nv <= 32) f(Int<32>{}, Int<1>{});
@@ -415,21 +448,26 @@ void by_width(int C, F f) {
   else if (nv <= 96) f(Int<32>{}, Int<3>{});
   else if (nv <= 128) f(Int<32>{}, Int<4>{});
   else if (nv <= 256) f(Int<128>{}, Int<2>{});
-  else if (nv <= 384) f(Int<128>{}, Int<3>{});
-  else if (nv <= 512) f(Int<128>{}, Int<4>{});
+  else if (nv <= 512) {
+    if constexpr (kBwd) f(Int<256>{}, Int<2>{});
+    else if (nv <= 384) f(Int<128>{}, Int<3>{});
+    else f(Int<128>{}, Int<4>{});
+  }
   else if (nv <= 1024) f(Int<512>{}, Int<2>{});
   else if (nv <= 1536) f(Int<512>{}, Int<3>{});
   else if (nv <= 2048) f(Int<512>{}, Int<4>{});
   else f(Int<kLoopThreads>{}, Int<0>{});
 }
 // Blocks of a call: a wave of the GPU's, by threads an SM holds.
-inline int row_blocks(long long rows, int C, int threads_per_sm) {
-  const int nv = C / kEpl, tpr = nv <= 128 ? 32 : (nv <= 512 ? 128 : 512);
+template <bool kBwd>
+int row_blocks(long long rows, int C) {
+  int tpr = 0;
+  by_width<kBwd>(C, [&](auto t, auto) { tpr = decltype(t)::value; });
+  const int threads_per_sm = kBwd ? 512 : 2048;
   const long long want = tpr == 32 ? (rows + 7) / 8 : rows;
   const long long cap = 152LL * (threads_per_sm / (tpr == 32 ? 256 : tpr));
   return static_cast<int>(want < 1 ? 1 : (want < cap ? want : cap));
 }
-constexpr int kFwdThreadsPerSm = 2048, kBwdThreadsPerSm = 1024;
 
 }  // namespace norm
 }  // namespace swa

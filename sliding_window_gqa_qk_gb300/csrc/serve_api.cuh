@@ -97,39 +97,40 @@ swa_status check_tokens(int B, int n_tokens, int max_new) {
 constexpr long long kTreePartFloats = static_cast<long long>((kKv4Bytes - kKv4Part) / sizeof(float)) - 64;
 
 template <int D, int RW, bool kPolled>
-swa_status launch_tree(const kv4::TreeAttnArgs& a, cudaStream_t st) {
+swa_status launch_tree(const kv4::TreeAttnArgs& a, dim3 grid, cudaStream_t st) {
   auto kern = kv4::tree_attn_kernel<D, RW, kPolled>;
   constexpr int smem = kv4::TreeSmem<D, RW>::bytes;
   if (smem > 48 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
     cudaGetLastError();
     return SWA_ERR_CUDA;
   }
-  kern<<<dim3(a.splits, a.c.Hkv * a.groups, a.B), kv4::kAttnWarps * 32, smem, st>>>(a);
+  kern<<<grid, kv4::kAttnWarps * 32, smem, st>>>(a);
   return launched();
 }
 #if !defined(SWA_ELEM_FP32)
 template <int NR, bool kPolled>
-swa_status launch_tree_tc(const kv4::TreeAttnArgs& a, cudaStream_t st) {
+swa_status launch_tree_tc(const kv4::TreeAttnArgs& a, dim3 grid, cudaStream_t st) {
   using S = kv4::TtShape<NR>;
   auto kern = kv4::tree_tc_kernel<NR, kPolled>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes) != cudaSuccess) {
     cudaGetLastError();
     return SWA_ERR_CUDA;
   }
-  kern<<<dim3(a.splits, a.c.Hkv * a.groups, a.B), S::warps * 32, S::bytes, st>>>(a);
+  kern<<<grid, S::warps * 32, S::bytes, st>>>(a);
   return launched();
 }
 #endif
 template <bool kPolled>
 swa_status launch_tree(const kv4::TreeAttnArgs& a, int d, const kv4::TreeSplit& sp, cudaStream_t st) {
+  const dim3 grid = sp.grid > 0 ? dim3(sp.grid) : dim3(sp.splits, a.c.Hkv * sp.groups, a.B);
 #if !defined(SWA_ELEM_FP32)
-  if (sp.tc) return launch_tree_tc<64, kPolled>(a, st);
+  if (sp.tc) return launch_tree_tc<64, kPolled>(a, grid, st);
   // (head dim 128 has more rows than 16 in that form only)
-  if (d == 128) return launch_tree<128, 1, kPolled>(a, st);
+  if (d == 128) return launch_tree<128, 1, kPolled>(a, grid, st);
 #else
-  if (d == 128) return sp.nq == 16 ? launch_tree<128, 1, kPolled>(a, st) : sp.nq == 32 ? launch_tree<128, 2, kPolled>(a, st) : launch_tree<128, 4, kPolled>(a, st);
+  if (d == 128) return sp.nq == 16 ? launch_tree<128, 1, kPolled>(a, grid, st) : sp.nq == 32 ? launch_tree<128, 2, kPolled>(a, grid, st) : launch_tree<128, 4, kPolled>(a, grid, st);
 #endif
-  return sp.nq == 16 ? launch_tree<64, 1, kPolled>(a, st) : sp.nq == 32 ? launch_tree<64, 2, kPolled>(a, st) : launch_tree<64, 4, kPolled>(a, st);
+  return sp.nq == 16 ? launch_tree<64, 1, kPolled>(a, grid, st) : sp.nq == 32 ? launch_tree<64, 2, kPolled>(a, grid, st) : launch_tree<64, 4, kPolled>(a, grid, st);
 }
 
 // Workspace of the serving block: that of the decode attention, then what lies
@@ -185,8 +186,8 @@ swa_status swa_rms_norm(long long rows, int C, float eps, const void* x, const v
   a.x = static_cast<const elem_t*>(x); a.add = static_cast<const elem_t*>(add); a.gain = gain;
   a.h = static_cast<elem_t*>(h == x ? (add != nullptr ? h : nullptr) : h);   // h is x already where nothing is added
   a.y = static_cast<elem_t*>(y); a.y8 = static_cast<uint8_t*>(y8); a.scale = scale; a.rstd = rstd;
-  const int blocks = norm::row_blocks(rows, C, norm::kFwdThreadsPerSm);
-  norm::by_width(C, [&](auto tpr, auto vpt) {
+  const int blocks = norm::row_blocks<false>(rows, C);
+  norm::by_width<false>(C, [&](auto tpr, auto vpt) {
     constexpr int T = decltype(tpr)::value, V = decltype(vpt)::value;
     const int threads = T == 32 ? 256 : T;
     if (y8 != nullptr) norm::fwd_kernel<T, V, true><<<blocks, threads, 0, static_cast<cudaStream_t>(stream)>>>(a);
@@ -197,7 +198,7 @@ swa_status swa_rms_norm(long long rows, int C, float eps, const void* x, const v
 
 size_t swa_rms_norm_workspace_size(long long rows, int C) {
   if (check_norm(rows, C) != SWA_OK) return 0;
-  return (static_cast<size_t>(norm::row_blocks(rows, C, norm::kBwdThreadsPerSm)) * C * sizeof(float) + 255) / 256 * 256;
+  return (static_cast<size_t>(norm::row_blocks<true>(rows, C)) * C * sizeof(float) + 255) / 256 * 256;
 }
 
 swa_status swa_rms_norm_bwd(long long rows, int C, const void* h, const float* rstd, const float* gain, const void* dy,
@@ -223,8 +224,8 @@ swa_status swa_rms_norm_bwd(long long rows, int C, const void* h, const float* r
   a.h = static_cast<const elem_t*>(h); a.rstd = rstd; a.gain = gain;
   a.dy = static_cast<const elem_t*>(dy); a.dh = static_cast<const elem_t*>(dh); a.dx = static_cast<elem_t*>(dx);
   a.part = dgain != nullptr ? static_cast<float*>(workspace) : nullptr;
-  const int blocks = norm::row_blocks(rows, C, norm::kBwdThreadsPerSm);
-  norm::by_width(C, [&](auto tpr, auto vpt) {
+  const int blocks = norm::row_blocks<true>(rows, C);
+  norm::by_width<true>(C, [&](auto tpr, auto vpt) {
     constexpr int T = decltype(tpr)::value, V = decltype(vpt)::value;
     norm::bwd_kernel<T, V><<<blocks, T == 32 ? 256 : T, T == 32 ? C * sizeof(float) : 0, st>>>(a);
   });
@@ -343,9 +344,10 @@ swa_status swa_kv4_tree_attn(const swa_params* p, const swa_extras* ex, const sw
   a.o = static_cast<elem_t*>(o); a.lse = lse;
   a.status = static_cast<uint32_t*>(workspace);
   a.chunk = sp.chunk; a.splits = sp.splits; a.groups = sp.groups;
+  a.slots = sp.slots; a.setup = sp.setup;
   a.count = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(workspace) + kKv4Count);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kKv4Part);
-  a.part_ml = reinterpret_cast<float2*>(a.part + sp.items * sp.splits * sp.nq * p->d);
+  a.part_ml = reinterpret_cast<float2*>(a.part + sp.parts * p->d);
   a.wait_limit_ns = ex != nullptr && ex->wait_limit_ns != 0 ? ex->wait_limit_ns : kWaitLimitNs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return a.wait_limit_ns < kPollBelowNs ? launch_tree<true>(a, p->d, sp, st) : launch_tree<false>(a, p->d, sp, st);

@@ -376,3 +376,91 @@ def test_tree_over_a_cache_past_32_bits(T):
     swa.kv4_move(cache, far, slot[:, 1030:1033].contiguous())
     moved = swa.kv4_read(cache, slot[:, 1030:1033].contiguous(), dtype=torch.float32)
     assert np.array_equal(f64(moved[0])[0], kh[-3:]) and np.array_equal(f64(moved[1])[0], vh[-3:])
+
+
+# Tables of 4096 tokens and more: CTAs that find their shares from all the lengths.
+RAGGED = [  # lens, new, Hq, Hkv, d, page, window, rot, interleaved
+    ([4200, 0, 1, 17, 4100, 900, 2500], [4, 0, 1, 3, 2, 4, 4], 8, 2, 128, 64, -1, 128, False),
+    ([4200, 0, 1, 17, 4100, 900, 2500], [4, 0, 1, 3, 2, 4, 4], 4, 4, 64, 16, -1, 64, False),
+    ([17, 4200, 33, 64, 0], [16, 20, 33, 1, 0], 8, 2, 128, 64, -1, 0, False),           # two groups of 64 rows
+    ([17, 4200, 33, 64, 0], [16, 20, 30, 1, 0], 6, 2, 64, 64, -1, 0, True),
+    ([5000, 4999, 4097, 30], [8, 8, 7, 8], 2, 1, 128, 256, 4500, 64, False),
+    ([9000], [3], 1, 1, 64, 64, -1, 64, False),
+    ([9000], [64], 4, 1, 128, 64, -1, 128, False),
+    ([1] * 60 + [4200] + [40 + i for i in range(67)], [1] * 128, 2, 1, 64, 16, -1, 0, False),        # 128 requests
+    ([1] * 60 + [4200] + [40 + i for i in range(68)], [1] * 129, 2, 1, 64, 16, -1, 0, False),        # one more: the host's grid
+]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("case", range(len(RAGGED)))
+def test_ragged_long_batches(kind, case):
+    tree_case(kind, *RAGGED[case])
+
+
+@pytest.mark.parametrize("T", [3, 12])
+@pytest.mark.parametrize("kind", KINDS)
+def test_shares_of_refused_requests_and_of_a_wide_table(kind, T):
+    # a table far wider than its requests; two of them refused; lengths of a
+    # captured call that grow between its replays
+    B, Hq, Hkv, d, page = 5, 4, 2, 128, 16
+    lens = [300, 260, 310, 5, 1200]
+    new = [T, T, T, 0, T]
+    cache, table, rows = build_cache(lens, Hkv, d, page, 61)
+    wide = torch.full((B, 700), -1, dtype=torch.int32)
+    wide[:, : table.shape[1]] = table
+    cd, wide = cache.to(dev()), wide.to(dev())
+    cu = np.concatenate([[0], np.cumsum(new)])
+    trees = [serve.tree(random_parents(n, 62), m - n) for n, m in zip(new, lens)]
+    seen = torch.tensor(np.array([s for t in trees for s in t[1]] + [0] * 3, dtype=np.uint64).view(np.int64), device=dev())
+    q = randn(63, sum(new) + 3, Hq, d, dtype=DT[kind]).to(dev())
+    ws = swa.new_kv4_workspace(cd, B, Hq, max_pages=700, kind=kind)
+    held, where = i32(*lens), i32(*np.concatenate([t[0] for t in trees] + [[0] * 3]))
+
+    def call():
+        return swa.kv4_tree_attention(cd, q, wide, held, i32cu, where, seen, max_new=T, workspace=ws)
+
+    i32cu = i32(*cu)
+
+    def check(o, lse, dead=(), less=0):
+        od, ld = f64(o), f64(lse)
+        for b in range(B):
+            at = slice(cu[b], cu[b + 1])
+            if b in dead or b == 3:
+                assert not od[at].any() and np.all(ld[at] == -np.inf)
+                continue
+            pos, vis = trees[b]
+            n = lens[b] - less if b == 4 else lens[b]
+            ro, rl = serve.tree_attend(f64(q)[at], rows[b][0][:n], rows[b][1][:n], np.asarray(pos) - (lens[b] - n), vis)
+            top = np.abs(rows[b][1]).max()
+            assert np.abs(ld[at] - rl).max() <= 1e-4
+            assert np.all(np.abs(od[at] - ro) <= (1.7e-4 + 2.0 ** -8) * top + 2.0 ** -8 * np.abs(ro))
+        assert not od[cu[-1]:].any() and np.all(ld[cu[-1]:] == -np.inf)
+
+    o, lse = call()
+    check(o, lse)
+    assert swa.swa_attn_check_status(ws, kind=kind) == swa.SWA_OK
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        go, gl = call()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(go, o) and torch.equal(gl, lse)
+    full, at_full = held.clone(), where.clone()
+    held[4] -= 900                                   # an earlier state of the long request
+    where[cu[4]:cu[5]] -= 900
+    g.replay()
+    torch.cuda.synchronize()
+    check(go, gl, less=900)
+    held.copy_(full)
+    where.copy_(at_full)
+    held[0], held[2] = -1, 700 * page + 1            # refused
+    g.replay()
+    torch.cuda.synchronize()
+    assert swa.swa_attn_check_status(ws, kind=kind) == swa.SWA_ERR_DEVICE_CHECK
+    check(go, gl, dead=(0, 2))
+    held.copy_(full)
+    g.replay()
+    torch.cuda.synchronize()
+    assert swa.swa_attn_check_status(ws, kind=kind) == swa.SWA_OK
+    assert torch.equal(go, o) and torch.equal(gl, lse)
