@@ -95,7 +95,10 @@ __global__ void __launch_bounds__(kTreeWarps * 32) tree_kernel(const __grid_cons
 
 // ---------------------------------------------------------------------------
 // Move: the tokens of slots src[b][t] become those of dst[b][t]. All of a row b
-// are read before any is written. A block a (row, kv head).
+// are read before any is written. A block a (row, kv head). Held by instructions
+// more than by bytes (2048 rows of 32 tokens, 4 kv heads of 128: 27 us with a
+// thread for every four bytes of a key and two of a value, 16 with 16 bytes each; the
+// bytes take 14.5), and by the sectors that 2 bytes of every 4 touch.
 // ---------------------------------------------------------------------------
 struct MoveArgs {
   Cache c;
@@ -107,57 +110,73 @@ constexpr int kMoveThreads = 128;
 
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ MoveArgs a) {
-  constexpr int KW = D / 8, VW = D / 4, SW = D / 64;       // words of a key row, 16-bit pieces of a value row, pairs of each
-  constexpr int UNITS = KW + VW + 2 * SW;
-  __shared__ uint32_t held[kTreeTokens * UNITS];
-  __shared__ long long to[kTreeTokens];
-  __shared__ long long from[kTreeTokens];
+  constexpr int SW = D / 64, KU = D / 32, VU = D / 16, UNITS = KU + VU + 2;      // 16-byte pieces of a key and of a pair of values; scales
+  __shared__ uint4 held[kTreeTokens * UNITS];
+  __shared__ long long from[kTreeTokens], to[kTreeTokens];      // tiles, in bytes; -1: skipped
+  __shared__ uint8_t in_from[kTreeTokens], in_to[kTreeTokens];  // tokens of theirs
   const long long slots = static_cast<long long>(a.c.n_pages) * a.c.page;
   const int n = a.T * UNITS;
-  // where piece k of token o of a tile starts, and whether it has 16 bits
+  // where piece k of token o of a tile starts
   auto piece = [](int k, int o) {
-    if (k < KW) return o * (D / 2) + 4 * k;
-    if (k < KW + VW) return 8 * D + (o >> 1) * D + 4 * (k - KW) + 2 * (o & 1);
-    const int i = k - KW - VW, kv = i / SW, g = i - kv * SW;
-    return 16 * D + kv * D + o * (4 * SW) + 4 * g;
+    if (k < KU) return o * (D / 2) + 16 * k;
+    if (k < KU + VU) return 8 * D + (o >> 1) * D + 16 * (k - KU);
+    return 16 * D + (k - KU - VU) * D + o * (4 * SW);
   };
-  auto half = [](int k) { return k >= KW && k < KW + VW; };
   uint32_t bad = 0;
   const long long items = static_cast<long long>(a.B) * a.c.Hkv;
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
     const long long b = it / a.c.Hkv;
     const int h = static_cast<int>(it - b * a.c.Hkv);
     for (int t = threadIdx.x; t < a.T; t += kMoveThreads) {
-      long long s = a.src[b * a.T + t], d = a.dst[b * a.T + t];
-      const bool skip = s == -1 || d == -1;
-      if (!skip && (s < 0 || s >= slots || d < 0 || d >= slots)) bad = DEV_ERR_BOUNDS;
-      if (skip || s < 0 || s >= slots || d < 0 || d >= slots || s == d) s = d = -1;
-      from[t] = s;
-      to[t] = d;
+      const long long s = a.src[b * a.T + t], d = a.dst[b * a.T + t];
+      const bool skip = s == -1 || d == -1, out = s < 0 || s >= slots || d < 0 || d >= slots;
+      if (!skip && out) bad = DEV_ERR_BOUNDS;
+      from[t] = to[t] = -1;
+      if (!out && s != d) {
+        from[t] = tile_of<D>(a.c, s, h) - a.c.data;
+        to[t] = tile_of<D>(a.c, d, h) - a.c.data;
+        in_from[t] = static_cast<uint8_t>(s & 15);
+        in_to[t] = static_cast<uint8_t>(d & 15);
+      }
     }
     __syncthreads();
-    // four pieces of a thread in flight
-    for (int u0 = threadIdx.x; u0 < n; u0 += 4 * kMoveThreads) {
-      uint32_t x[4];
+    // two pieces of a thread in flight
+    for (int u0 = threadIdx.x; u0 < n; u0 += 2 * kMoveThreads) {
+      uint4 x[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         const int u = u0 + i * kMoveThreads, t = u / UNITS, k = u - t * UNITS;
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
         if (u >= n || from[t] < 0) continue;
-        const uint8_t* at = tile_of<D>(a.c, from[t], h) + piece(k, static_cast<int>(from[t] & 15));
-        if (half(k)) x[i] = *reinterpret_cast<const uint16_t*>(at);
-        else x[i] = *reinterpret_cast<const uint32_t*>(at);
+        const uint8_t* at = a.c.data + from[t] + piece(k, in_from[t]);
+        if (k < KU + VU) x[i] = ld16(at);
+        else if constexpr (SW == 2) *reinterpret_cast<uint2*>(&x[i]) = *reinterpret_cast<const uint2*>(at);
+        else x[i].x = *reinterpret_cast<const uint32_t*>(at);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 2; ++i)
         if (u0 + i * kMoveThreads < n) held[u0 + i * kMoveThreads] = x[i];
     }
     __syncthreads();
     for (int u = threadIdx.x; u < n; u += kMoveThreads) {
       const int t = u / UNITS, k = u - t * UNITS;
       if (to[t] < 0) continue;
-      uint8_t* at = tile_of<D>(a.c, to[t], h) + piece(k, static_cast<int>(to[t] & 15));
-      if (half(k)) *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(held[u]);
-      else *reinterpret_cast<uint32_t*>(at) = held[u];
+      uint8_t* at = a.c.data + to[t] + piece(k, in_to[t]);
+      const uint4 x = held[u];
+      if (k < KU) {
+        st16(at, x);
+      } else if (k < KU + VU) {          // words of a pair of tokens, 16 bits of each: the other's stay as they are
+        const int down = 16 * (in_from[t] & 1);
+        uint16_t* y = reinterpret_cast<uint16_t*>(at) + (in_to[t] & 1);
+        y[0] = static_cast<uint16_t>(x.x >> down);
+        y[2] = static_cast<uint16_t>(x.y >> down);
+        y[4] = static_cast<uint16_t>(x.z >> down);
+        y[6] = static_cast<uint16_t>(x.w >> down);
+      } else if constexpr (SW == 2) {
+        *reinterpret_cast<uint2*>(at) = make_uint2(x.x, x.y);
+      } else {
+        *reinterpret_cast<uint32_t*>(at) = x.x;
+      }
     }
     __syncthreads();
   }

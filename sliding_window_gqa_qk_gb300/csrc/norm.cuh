@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) fwd_kernel(const __grid
       }
     };
     if constexpr (kLoop) {
-      if (a.add != nullptr)
+      if (a.h != nullptr)
         for (int i = t; i < nv; i += TPR) st16(a.h + base + static_cast<long long>(i) * kEpl, take(a, base + static_cast<long long>(i) * kEpl));
     } else {
 #pragma unroll

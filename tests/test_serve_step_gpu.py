@@ -464,3 +464,42 @@ def test_shares_of_refused_requests_and_of_a_wide_table(kind, T):
     torch.cuda.synchronize()
     assert swa.swa_attn_check_status(ws, kind=kind) == swa.SWA_OK
     assert torch.equal(go, o) and torch.equal(gl, lse)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("C", [96, 40000])
+def test_norm_copies_its_input_where_h_is_wanted_without_an_addition(kind, C):
+    x = randn(70, 5, C, dtype=DT[kind]).to(dev())
+    want = swa.rms_norm(x)
+    h, y = torch.zeros_like(x), torch.zeros_like(x)
+    assert swa.swa_rms_norm(5, C, 1e-6, x, None, None, h, y, None, None, None, kind=kind) == swa.SWA_OK
+    assert torch.equal(h, x) and torch.equal(y, want["y"])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("C", [248, 1000, 2048, 3000, 4096, 6008, 8192, 12000, 16384, 20000])
+def test_norm_backward_of_more_rows_than_blocks(kind, C):
+    # every width of row, blocks with several rows whose loads overlap, in place.
+    # dx: half a step of its type (2^-8 or 2^-24) and fp32's own few roundings of
+    # terms of size rstd (|d| + |xh mean|) + |dh|: 1e-6 of them; its mean over C of
+    # products of size |d xh| is a sum of C / threads and then log terms: 1e-5.
+    # dgain: at most ~700 additions in a row, 700 * 2^-24 of the sum of sizes.
+    rows = 6000 if C <= 1000 else (1300 if C < 4096 else 700)
+    h, dy, dh = (randn(71 + i, rows, C, dtype=DT[kind]).to(dev()) for i in range(3))
+    g = (1 + 0.1 * randn(74, C)).to(dev())
+    rstd = swa.rms_norm(h)["rstd"]
+    r = swa.rms_norm_backward(h, rstd, dy, g, dh=dh)
+    xh, d = h.double() * rstd.double()[:, None], dy.double() * g.double()
+    mean = (d * xh).mean(-1, keepdim=True)
+    want = rstd.double()[:, None] * (d - xh * mean) + dh.double()
+    size = rstd.double()[:, None] * (d.abs() + xh.abs() * ((d * xh).abs().mean(-1, keepdim=True))) + dh.double().abs()
+    half = 2.0 ** -8 if kind == "bf16" else 2.0 ** -24
+    assert bool(((r["dx"].double() - want).abs() <= half * want.abs() + 1.1e-5 * size).all())
+    dg, top = (dy.double() * xh).sum(0), (dy.double() * xh).abs().sum(0)
+    assert bool(((r["dgain"].double() - dg).abs() <= 700 * 2.0 ** -24 * top).all())
+    ws = torch.empty(swa.swa_rms_norm_workspace_size(rows, C, kind), dtype=torch.uint8, device=dev())
+    for at in range(3):
+        t = [h.clone(), dy.clone(), dh.clone()]
+        dgain = torch.empty_like(g)
+        assert swa.swa_rms_norm_bwd(rows, C, t[0], rstd, g, t[1], t[2], t[at], dgain, ws, kind=kind) == swa.SWA_OK
+        assert torch.equal(t[at], r["dx"]) and torch.equal(dgain, r["dgain"])
