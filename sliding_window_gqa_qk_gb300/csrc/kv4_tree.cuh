@@ -469,99 +469,120 @@ __device__ __forceinline__ void tree_join(const TreeAttnArgs& a, int chunks, lon
   }
 }
 
-// NR query rows by one warp at once (query_row's arithmetic, row after row the
-// same; their loads wait together). Entries times a power of two that brings
-// them below 2^14 (up; 0: each row's own): put(row, channel, hi, lo) as two fp16
-// terms, end(row, 1 / power) by lane 0 of each group of 64 channels with their
-// sum.
-template <int D, int NR, typename Put, typename End>
-__device__ __forceinline__ void query_rows(const AttnArgs& a, const elem_t* const (&q)[NR], const int (&pos)[NR], float up_all, Put put,
-                                           End end) {
+// Query rows i0, i0 + step .. below i1 by one warp (query_row's arithmetic), the
+// next row's loads in flight beside a row's arithmetic. src(i, pos): row i and its
+// position; NULL: a row of zeros. Entries times a power of two that brings them
+// below 2^14 (up; 0: each row's own): put(i, channel, hi, lo) as two fp16 terms,
+// end(i, group, 1 / power, sum) by lane 0 of each group of 64 channels with their
+// sum. A loop, for instructions that run once each wait to be fetched: four
+// rows unrolled beside each other took 5800 clocks where four in turn take QA (a
+// call for one request of 32 tokens: QB us of QC).
+template <int D, typename Src, typename Put, typename End>
+__device__ __forceinline__ void query_rows(const AttnArgs& a, int i0, int i1, int step, float up_all, Src src, Put put, End end) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31, c0 = lane * E;
-  float x[NR][E], y[NR][E], cs[NR][E], sn[NR][E], g[E];
+  struct Row {
+    bool on;
+    float x[E], y[E], cs[E], sn[E];
+  };
+  float g[E];
   const bool turned = a.rcos != nullptr && c0 < a.rot;
   const int half = a.rot / 2;
   const bool first = c0 < half;
 #pragma unroll
   for (int i = 0; i < E; ++i) g[i] = 1.0f;
   if (a.gq != nullptr) load_vec<E>(a.gq + c0, g);
+  auto load = [&](int i) {
+    Row r;
+    int pos = 0;
+    const elem_t* q = src(i, pos);
+    r.on = q != nullptr;
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) x[n][i] = y[n][i] = sn[n][i] = 0.f, cs[n][i] = 1.f;
-    if (q[n] == nullptr) continue;
-    load_vec<E>(q[n] + c0, x[n]);
+    for (int k = 0; k < E; ++k) r.x[k] = r.y[k] = r.sn[k] = 0.f, r.cs[k] = 1.f;
+    if (!r.on) return r;
+    load_vec<E>(q + c0, r.x);
     if (turned) {
-      const long long row = static_cast<long long>(pos[n]) * half;
+      const long long row = static_cast<long long>(pos) * half;
       if (a.interleaved) {
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-          cs[n][2 * i] = cs[n][2 * i + 1] = a.rcos[row + c0 / 2 + i];
-          sn[n][2 * i] = sn[n][2 * i + 1] = a.rsin[row + c0 / 2 + i];
+        for (int k = 0; k < E / 2; ++k) {
+          r.cs[2 * k] = r.cs[2 * k + 1] = a.rcos[row + c0 / 2 + k];
+          r.sn[2 * k] = r.sn[2 * k + 1] = a.rsin[row + c0 / 2 + k];
         }
       } else {
-        load_vec<E>(q[n] + (first ? c0 + half : c0 - half), y[n]);
-        load_vec<E>(a.rcos + row + (first ? c0 : c0 - half), cs[n]);
-        load_vec<E>(a.rsin + row + (first ? c0 : c0 - half), sn[n]);
+        load_vec<E>(q + (first ? c0 + half : c0 - half), r.y);
+        load_vec<E>(a.rcos + row + (first ? c0 : c0 - half), r.cs);
+        load_vec<E>(a.rsin + row + (first ? c0 : c0 - half), r.sn);
       }
     }
-  }
+    return r;
+  };
+  if (i0 >= i1) return;
+  Row next = load(i0);
+#pragma unroll 1
+  for (int i = i0; i < i1; i += step) {
+    Row r = next;
+    if (i + step < i1) next = load(i + step);
+    float down = 1.f, sum = 0.f;
+    if (!r.on) {                 // (the warp's lanes alike)
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    float ss = 0.f;
-    if (turned) {
-      if (a.interleaved) {
+      for (int k = 0; k < E; ++k) put(i, c0 + k, __half(0.f), __half(0.f));
+    } else {
+      if (turned) {
+        if (a.interleaved) {
 #pragma unroll
-        for (int i = 0; i < E; i += 2) {
-          const float u = x[n][i], v = x[n][i + 1];
-          x[n][i] = fmaf(u, cs[n][i], v * sn[n][i]);
-          x[n][i + 1] = fmaf(v, cs[n][i], -u * sn[n][i]);
+          for (int k = 0; k < E; k += 2) {
+            const float u = r.x[k], v = r.x[k + 1];
+            r.x[k] = fmaf(u, r.cs[k], v * r.sn[k]);
+            r.x[k + 1] = fmaf(v, r.cs[k], -u * r.sn[k]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < E; ++k) r.x[k] = fmaf(r.x[k], r.cs[k], (first ? r.y[k] : -r.y[k]) * r.sn[k]);
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) x[n][i] = fmaf(x[n][i], cs[n][i], (first ? y[n][i] : -y[n][i]) * sn[n][i]);
       }
-    }
+      float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < E; ++i) ss = fmaf(x[n][i], x[n][i], ss);
-    ss = warp_sum(ss);
-    float eps = a.eps;
-    if (ss == INFINITY) {      // the squares pass fp32: the same of 2^-80 of the row
-      constexpr float kDown = 0x1p-80f;
-      ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        x[n][i] *= kDown;
-        ss = fmaf(x[n][i], x[n][i], ss);
-      }
+      for (int k = 0; k < E; ++k) ss = fmaf(r.x[k], r.x[k], ss);
       ss = warp_sum(ss);
-      eps = eps * kDown * kDown;
-    }
-    const float mul = rsqrtf(ss / D + eps) * (a.scale * 1.4426950408889634f);
-    float top = 0.f;
+      float eps = a.eps;
+      if (ss == INFINITY) {      // the squares pass fp32: the same of 2^-80 of the row
+        constexpr float kDown = 0x1p-80f;
+        ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      x[n][i] *= mul * g[i];
-      if (q[n] == nullptr) x[n][i] = 0.f;
-      top = fmaxf(top, fabsf(x[n][i]));
-    }
+        for (int k = 0; k < E; ++k) {
+          r.x[k] *= kDown;
+          ss = fmaf(r.x[k], r.x[k], ss);
+        }
+        ss = warp_sum(ss);
+        eps = eps * kDown * kDown;
+      }
+      const float mul = rsqrtf(ss / D + eps) * (a.scale * 1.4426950408889634f);
+      float up = up_all;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    int e = static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127;
-    e = e < -100 ? -100 : (e > 100 ? 100 : e);
-    const float up = up_all != 0.f ? up_all : __uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23);
-    float sum = 0.f;
+      for (int k = 0; k < E; ++k) r.x[k] *= mul * g[k];
+      if (up_all == 0.f) {
+        float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float v = x[n][i] * up;
-      const __half hi = __float2half_rn(v);
-      put(n, c0 + i, hi, __float2half_rn(v - __half2float(hi)));
-      sum += v;
+        for (int k = 0; k < E; ++k) top = fmaxf(top, fabsf(r.x[k]));
+        // (of floats that are not negative the bits are in their order, a NaN above all)
+        const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+        int e = static_cast<int>((bits >> 23) & 255u) - 127;
+        e = e < -100 ? -100 : (e > 100 ? 100 : e);
+        up = __uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23);
+        down = __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23);
+      }
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        const float v = r.x[k] * up;
+        const __half hi = __float2half_rn(v);
+        put(i, c0 + k, hi, __float2half_rn(v - __half2float(hi)));
+        sum += v;
+      }
     }
 #pragma unroll
     for (int o = 32 / E; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane % (64 / E) == 0) end(n, c0 / 64, __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23), sum);
+    if (lane % (64 / E) == 0) end(i, c0 / 64, down, sum);
   }
 }
 
@@ -651,27 +672,21 @@ __global__ void __launch_bounds__(kAttnWarps * 32, tree_ctas_per_sm(D)) tree_att
   float* qf = reinterpret_cast<float*>(smem + M::qf);
   tree_rows<NQ, kAttnWarps * 32>(a, req, row_q0, nq, G, rows, tpos, bad);
   __syncthreads();
-  constexpr int NR = 4;
-  for (int i = wid * NR; i < NQ; i += kAttnWarps * NR) {
-    const elem_t* q[NR];
-    int pos[NR];
-#pragma unroll
-    for (int k = 0; k < NR; ++k) {
-      const int row = row_q0 + i + k;
-      pos[k] = rows[i + k].pos;
-      q[k] = rows[i + k].lo != INT32_MAX ? a.q + (static_cast<long long>(req.row0 + row / G) * a.Hq + h * G + row % G) * D : nullptr;
-    }
-    query_rows<D, NR>(a, q, pos, 0.f,
-        [&](int n, int c, __half hi, __half lo) {
-          __half* to = qs + (i + n) * kQTerms * D + (c & ~7) + (c & 3) * 2 + ((c >> 2) & 1);   // pairs (c, c + 4) side by side
-          to[0] = hi;
-          to[D] = lo;
-        },
-        [&](int n, int g, float down, float sum) {
-          if (g == 0) qf[(i + n) * 4] = down;
-          qf[(i + n) * 4 + 1 + g] = sum;
-        });
-  }
+  query_rows<D>(a, wid, NQ, kAttnWarps, 0.f,
+      [&](int i, int& pos) -> const elem_t* {
+        const int row = row_q0 + i;
+        pos = rows[i].pos;
+        return rows[i].lo != INT32_MAX ? a.q + (static_cast<long long>(req.row0 + row / G) * a.Hq + h * G + row % G) * D : nullptr;
+      },
+      [&](int i, int c, __half hi, __half lo) {
+        __half* to = qs + i * kQTerms * D + (c & ~7) + (c & 3) * 2 + ((c >> 2) & 1);   // pairs (c, c + 4) side by side
+        to[0] = hi;
+        to[D] = lo;
+      },
+      [&](int i, int g, float down, float sum) {
+        if (g == 0) qf[i * 4] = down;
+        qf[i * 4 + 1 + g] = sum;
+      });
   __syncthreads();
   uint32_t qa[kQTerms][2 * W][4];
   float qfac[2], qsum[2][NG];

@@ -209,37 +209,28 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
     up = __uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23);
   }
   const float down = 1.0f / up;                                  // a power of two
-  auto queries = [&](int w, int n_warps) {
-    constexpr int NQR = 4;
-    for (int i = w * NQR; i < NR; i += n_warps * NQR) {
-      const elem_t* q[NQR];
-      int pos[NQR];
-#pragma unroll
-      for (int k = 0; k < NQR; ++k) {
-        const int row = row_q0 + i + k;
-        pos[k] = rows[i + k].pos;
-        q[k] = rows[i + k].lo != INT32_MAX ? a.q + (static_cast<long long>(req.row0 + row / G) * a.Hq + h * G + row % G) * D : nullptr;
-      }
-      auto at = [&](int n, int k) {                              // K element k of row n of Q
-        return reinterpret_cast<__half*>(smem + S::oQ + (k >> 6) * S::q_block + n * 128 + (((k & 63) >> 3) ^ (n & 7)) * 16 + (k & 7) * 2);
-      };
-      query_rows<D, NQR>(a, q, pos, up,
-          [&](int n, int c, __half hi, __half lo2) {
-            // the order in which a lane's numbers of a key make its operand: pair k of lane j in column 4 k + j
-            const int k = 4 * (2 * (c >> 6) + ((c & 15) >> 3)) + (c & 3), j = (c & 63) >> 4, e = 2 * (4 * k + j) + ((c & 7) >> 2);
-            *at(i + n, e) = hi;
-            *at(NR + i + n, e) = lo2;
-          },
-          [&](int n, int g, float, float sum) {
-            const float v = sum * 0.015625f;                     // below 2^14 again
-            const __half hi = __float2half_rn(v);
-            *at(i + n, 128 + g) = hi;
-            *at(NR + i + n, 128 + g) = __float2half_rn(v - __half2float(hi));
-          });
-    }
+  auto at = [&](int n, int k) {                                  // K element k of row n of Q
+    return reinterpret_cast<__half*>(smem + S::oQ + (k >> 6) * S::q_block + n * 128 + (((k & 63) >> 3) ^ (n & 7)) * 16 + (k & 7) * 2);
   };
-
-  if (warp < S::mma) queries(warp, S::mma);
+  if (warp < S::mma)
+    query_rows<D>(a, warp, NR, S::mma, up,
+        [&](int i, int& pos) -> const elem_t* {
+          const int row = row_q0 + i;
+          pos = rows[i].pos;
+          return rows[i].lo != INT32_MAX ? a.q + (static_cast<long long>(req.row0 + row / G) * a.Hq + h * G + row % G) * D : nullptr;
+        },
+        [&](int i, int c, __half hi, __half lo2) {
+          // the order in which a lane's numbers of a key make its operand: pair k of lane j in column 4 k + j
+          const int k = 4 * (2 * (c >> 6) + ((c & 15) >> 3)) + (c & 3), j = (c & 63) >> 4, e = 2 * (4 * k + j) + ((c & 7) >> 2);
+          *at(i, e) = hi;
+          *at(NR + i, e) = lo2;
+        },
+        [&](int i, int g, float, float sum) {
+          const float v = sum * 0.015625f;                       // below 2^14 again
+          const __half hi = __float2half_rn(v);
+          *at(i, 128 + g) = hi;
+          *at(NR + i, 128 + g) = __float2half_rn(v - __half2float(hi));
+        });
   // Q is written: the warps up to the issuer meet here (the loader has work of its own till the end)
   if (warp <= S::mma_o) {
     if (warp < S::mma && lane == 0) {
