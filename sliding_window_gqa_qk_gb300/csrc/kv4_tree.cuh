@@ -240,7 +240,7 @@ struct TreeRow {
 // for which the call should end first: the host knows only the longest possible
 // request, and a batch that is ragged, or far below its tables' width, left most of
 // the GPU idle (64 ragged requests of at most 16384 tokens, 16 query heads on 2: 165 us
-// against 70; 16 in fp32 of at most 5000: 39 against 27). Every CTA comes to the same answer: integers, and
+// against 66; 16 in fp32 of at most 5000: 39 against 25). Every CTA comes to the same answer: integers, and
 // fp32 of them.
 struct TreeShare {
   int b, h, qg, ci, chunk;
@@ -371,6 +371,21 @@ __device__ __forceinline__ void tree_rows(const TreeAttnArgs& a, const TreeReq& 
   }
 }
 
+// Then, by kWarps warps behind a barrier: of seen only the request's tokens within the
+// row's window stay, so that a mask is one bit of it (tested in full per key and row
+// it was 2000 clocks of the first step's 3700, and one request of 32 tokens 8.5 us for
+// 7.7; of 64 rows in the tcgen05 form 16.4 for 13.2).
+template <int NQ, int kWarps>
+__device__ __forceinline__ void tree_sight(const TreeAttnArgs& a, const TreeReq& req, TreeRow* rows, const int* tpos, int w) {
+  const int lane = threadIdx.x & 31;
+  for (int i = w; i < NQ; i += kWarps) {
+    auto near = [&](int t) { return t < req.n && (a.window < 0 || static_cast<long long>(rows[i].pos) - tpos[t] <= a.window); };
+    const unsigned lo = __ballot_sync(0xffffffffu, near(lane)), hi = __ballot_sync(0xffffffffu, near(lane + 32));
+    if (lane == 0) rows[i].seen &= lo | static_cast<unsigned long long>(hi) << 32;
+    __syncwarp();
+  }
+}
+
 // Rows that hold nothing, by the CTA that answers for them: those of a request
 // that is refused, and those behind the last one.
 template <int D, int kWarps>
@@ -475,8 +490,8 @@ __device__ __forceinline__ void tree_join(const TreeAttnArgs& a, int chunks, lon
 // below 2^14 (up; 0: each row's own): put(i, channel, hi, lo) as two fp16 terms,
 // end(i, group, 1 / power, sum) by lane 0 of each group of 64 channels with their
 // sum. A loop, for instructions that run once each wait to be fetched: four
-// rows unrolled beside each other took 5800 clocks where four in turn take QA (a
-// call for one request of 32 tokens: QB us of QC).
+// rows unrolled beside each other took 5800 clocks where four in turn take 4100 (one
+// request of 32 tokens, the whole kernel: 9.2 us for 8.5).
 template <int D, typename Src, typename Put, typename End>
 __device__ __forceinline__ void query_rows(const AttnArgs& a, int i0, int i1, int step, float up_all, Src src, Put put, End end) {
   constexpr int E = D / 32;
@@ -672,6 +687,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, tree_ctas_per_sm(D)) tree_att
   float* qf = reinterpret_cast<float*>(smem + M::qf);
   tree_rows<NQ, kAttnWarps * 32>(a, req, row_q0, nq, G, rows, tpos, bad);
   __syncthreads();
+  tree_sight<NQ, kAttnWarps>(a, req, rows, tpos, wid);
   query_rows<D>(a, wid, NQ, kAttnWarps, 0.f,
       [&](int i, int& pos) -> const elem_t* {
         const int row = row_q0 + i;
@@ -767,11 +783,9 @@ __global__ void __launch_bounds__(kAttnWarps * 32, tree_ctas_per_sm(D)) tree_att
             const int key = key0 + q * kTile + 8 * t + 2 * j + e, d = key - req.ctx;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              bool on = my[i].lo != INT32_MAX && !(miss >> q & 1u);
-              if (d < 0) on = on && key >= my[i].lo;
-              else
-                on = on && d < req.n && (my[i].seen >> d & 1ull) &&
-                     (a.window < 0 || static_cast<long long>(my[i].pos) - tpos[d] <= a.window);
+              const bool old = (d < 0) & (key >= my[i].lo);
+              const bool drafted = (d >= 0) & (d < kTreeTokens) & static_cast<bool>(my[i].seen >> (d & 63) & 1ull);
+              const bool on = (old | drafted) & !(miss >> q & 1u);
               if (!on) s[q][t][2 * i + e] = -INFINITY;
             }
           }

@@ -212,7 +212,8 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
   auto at = [&](int n, int k) {                                  // K element k of row n of Q
     return reinterpret_cast<__half*>(smem + S::oQ + (k >> 6) * S::q_block + n * 128 + (((k & 63) >> 3) ^ (n & 7)) * 16 + (k & 7) * 2);
   };
-  if (warp < S::mma)
+  if (warp < S::mma) {
+    tree_sight<NR, S::mma>(a, req, rows, tpos, warp);
     query_rows<D>(a, warp, NR, S::mma, up,
         [&](int i, int& pos) -> const elem_t* {
           const int row = row_q0 + i;
@@ -231,6 +232,7 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
           *at(i, 128 + g) = hi;
           *at(NR + i, 128 + g) = __float2half_rn(v - __half2float(hi));
         });
+  }
   // Q is written: the warps up to the issuer meet here (the loader has work of its own till the end)
   if (warp <= S::mma_o) {
     if (warp < S::mma && lane == 0) {
@@ -288,12 +290,8 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const int4 w = *reinterpret_cast<const int4*>(rows + r0 + i);    // lo, pos, seen
-          bool on = w.x != INT32_MAX && !(kflag & kKeyOff);
-          if (d < 0) on = on && key >= w.x;
-          else {
-            const unsigned long long seen = static_cast<uint32_t>(w.z) | static_cast<unsigned long long>(static_cast<uint32_t>(w.w)) << 32;
-            on = on && d < req.n && (seen >> d & 1ull) && (a.window < 0 || static_cast<long long>(w.y) - tpos[d < kTreeTokens ? d : 0] <= a.window);
-          }
+          const uint32_t word = static_cast<uint32_t>(d & 32 ? w.w : w.z);
+          const bool on = (d < 0 ? key >= w.x : (d < kTreeTokens) & static_cast<bool>(word >> (d & 31) & 1u)) & !(kflag & kKeyOff);
           if (!on) x[i] = -INFINITY;
         }
       }
