@@ -595,6 +595,8 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
       sum = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = 0.f;
+    } else if (fresh[i]) {               // nothing of this chunk: no maximum for the join (its sums are 0, or a key's NaN)
+      top = -1e30f;
     }
     tree_row_out<D>(a, chunks, share.ci, share.part0, NR, i, head_of(i), o, top, sum);
   }
