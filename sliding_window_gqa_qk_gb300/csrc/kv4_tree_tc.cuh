@@ -515,9 +515,9 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
       __syncwarp();
       if (lane < 8 && at >= 0) bulk_load(sbase + S::oRing + st * S::block + lane * TB, a.c.data + at * TB, TB, bar(S::RAW + st));
     }
-    // a wait that ran out: the copies still on their way land before the memory is used again
-    if (n < blocks)
-      for (int i = max(0, n - kTtRing); i < n; ++i) mbar_wait_drain(bar(S::RAW + i % kTtRing), (i / kTtRing) & 1, kDrainLimitNs);
+    // the copies still on their way land before the memory is used again (also where all are issued: the warps that wait
+    // for them may have given up)
+    for (int i = max(0, n - kTtRing); i < n; ++i) mbar_wait_drain(bar(S::RAW + i % kTtRing), (i / kTtRing) & 1, kDrainLimitNs);
   } else if (warp == S::mma) {
     if (lane == 0) {
       constexpr uint32_t id_s = (1u << 4) | (static_cast<uint32_t>(S::N >> 3) << 17) | (8u << 24);      // fp16, M = 128
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
   }
   __syncwarp();
   if (bad) atomicOr(a.status, bad);
-  __syncthreads();                        // (every copy has landed: its block was used, or the loader waited for it)
+  __syncthreads();                        // (every copy has landed: the loader waited for the last ones)
   tc_fence_after();
 
   // O^T into rows [row][channel]

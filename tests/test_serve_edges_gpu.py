@@ -1,5 +1,7 @@
 """Edges of the serving calls that the other files' cases do not reach."""
 
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -53,3 +55,62 @@ def test_rows_that_see_nothing_of_the_last_chunk(kind, Hq, T, ahead, chunks, wid
     assert np.all(np.abs(f64(lse) - rl) <= slip + 2e-6 * np.abs(rl)), (float(np.abs(f64(lse) - rl).max()), slip)
     top = np.abs(vals).max()
     assert np.all(np.abs(f64(o) - ro) <= (2 * slip + 2.0 ** -8 + 2e-4) * top + 2.0 ** -8 * np.abs(ro))
+
+
+def long_batch(kind, B, T, Hq, Hkv, d, n, page=64):
+    """Arguments of the tree attention of B requests of n cached tokens, T of them drafted in a chain, and their workspace."""
+    per = -(-n // page)
+    cache = torch.randint(0, 256, (B * per, Hkv, page // 16, 18 * d), dtype=torch.uint8, device=dev())
+    sc = cache[..., 16 * d:].view(torch.bfloat16)
+    sc[..., 0::2], sc[..., 1::2] = 0.2, 0.1
+    table = torch.arange(B * per, dtype=torch.int32, device=dev()).view(B, per)
+    lens = torch.full((B,), n, dtype=torch.int32, device=dev())
+    cu = torch.arange(B + 1, dtype=torch.int32, device=dev()) * T
+    pos, seen = swa.kv4_tree(torch.arange(-1, T - 1, dtype=torch.int32, device=dev()).repeat(B), cu, lens, max_new=T)
+    q = randn(31, B * T, Hq, d, dtype=DT[kind]).to(dev())
+    return cache, q, table, lens, cu, pos, seen, swa.new_kv4_workspace(cache, B, Hq, max_pages=per, kind=kind)
+
+
+def out_of_time(call, check, ws, kind, tries=20):
+    """Runs call under a limit of 1 ns, while another stream keeps the memory busy, until a wait has run out; check()
+    after each. Whether one did, and the longest that a call took, in seconds."""
+    side, big = torch.cuda.Stream(), [torch.zeros(1 << 28, device=dev()) for _ in range(2)]
+    longest = 0.0
+    for _ in range(tries):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(3):
+                big[0].copy_(big[1])
+        start = time.perf_counter()
+        assert call(swa.make_extras(wait_limit_ns=1)) == swa.SWA_OK
+        st = swa.swa_attn_check_status(ws, kind=kind)
+        longest = max(longest, time.perf_counter() - start)
+        assert st in (swa.SWA_OK, swa.SWA_ERR_TIMEOUT)
+        assert swa.swa_attn_check_status(ws, kind=kind) == swa.SWA_OK      # read and cleared
+        check()
+        if st == swa.SWA_ERR_TIMEOUT:
+            return True, longest
+    return False, longest
+
+
+@pytest.mark.parametrize("n", [100, 700, 768, 900])
+@pytest.mark.parametrize("Hq,T", [(4, 16), (4, 5)])
+def test_tree_waits_that_run_out_in_short_requests(n, Hq, T):
+    # One to eight blocks a CTA, so that the loader has issued its last copies when the others give up. They land before
+    # the CTA ends: calls behind it on the same SMs, and on the same workspace, give their bits.
+    B = 600
+    cache, q, table, lens, cu, pos, seen, ws = long_batch("bf16", B, T, Hq, 1, 128, n)
+    want = swa.kv4_tree_attention(cache, q, table, lens, cu, pos, seen, max_new=T, workspace=ws)
+    p, c = swa.make_params(B, 1, Hq, 1, 128), swa.swa_kv4_cache(cache.data_ptr(), cache.shape[0], 64)
+    o, lse = torch.empty_like(q), torch.empty(B * T, Hq, device=dev())
+
+    def call(ex):
+        return swa.swa_kv4_tree_attn(p, ex, c, None, B * T, T, q, None, table, table.shape[1], lens, cu, pos, seen, o, lse, ws)
+
+    def check():
+        got = swa.kv4_tree_attention(cache, q, table, lens, cu, pos, seen, max_new=T, workspace=ws)
+        assert swa.swa_attn_check_status(ws) == swa.SWA_OK
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    ran_out, longest = out_of_time(call, check, ws, "bf16")
+    assert ran_out
+    assert longest < 1.0          # the copies land in microseconds; nothing waits for what never comes
