@@ -877,8 +877,10 @@ __global__ void __launch_bounds__(kAttnWarps * 32, tree_ctas_per_sm(D)) tree_att
       }
     }
   }
-  // a wait that ran out: the copies still on their way land before the memory is used again
-  for (int k = n; k < issued; ++k) mbar_wait_drain(bars + 8 * (k % ST), (k / ST) & 1, kDrainLimitNs);
+  // a wait that ran out: the copies still on their way land before the memory is used again. (Only the warp that asked
+  // for them knows which were: a stage that another has counted and this one gave up on never fills.)
+  if (rw == 0)
+    for (int k = n; k < issued; ++k) mbar_wait_drain(bars + 8 * (k % ST), (k / ST) & 1, kDrainLimitNs);
   if (bad) atomicOr(a.status, bad);
 
   // join the groups of warps: O, M, L of each row into shared memory

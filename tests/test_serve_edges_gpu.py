@@ -114,3 +114,25 @@ def test_tree_waits_that_run_out_in_short_requests(n, Hq, T):
     ran_out, longest = out_of_time(call, check, ws, "bf16")
     assert ran_out
     assert longest < 1.0          # the copies land in microseconds; nothing waits for what never comes
+
+
+@pytest.mark.parametrize("kind,d,Hq,T", [("fp32", 128, 4, 8), ("fp32", 128, 4, 16), ("bf16", 64, 4, 8), ("bf16", 64, 4, 16)])
+def test_tree_waits_that_run_out_among_warps_that_share_stages(kind, d, Hq, T):
+    # 32 and 64 rows of the m16n8k16 form: two and four warps wait for each other's stages. None waits for one that was
+    # never asked for (2 s each, and there are more CTAs than run at once).
+    B, n = 32, 8192
+    cache, q, table, lens, cu, pos, seen, ws = long_batch(kind, B, T, Hq, 1, d, n)
+    want = swa.kv4_tree_attention(cache, q, table, lens, cu, pos, seen, max_new=T, workspace=ws)
+    p, c = swa.make_params(B, 1, Hq, 1, d), swa.swa_kv4_cache(cache.data_ptr(), cache.shape[0], 64)
+    o, lse = torch.empty_like(q), torch.empty(B * T, Hq, device=dev())
+
+    def call(ex):
+        return swa.swa_kv4_tree_attn(p, ex, c, None, B * T, T, q, None, table, table.shape[1], lens, cu, pos, seen, o, lse, ws)
+
+    def check():
+        got = swa.kv4_tree_attention(cache, q, table, lens, cu, pos, seen, max_new=T, workspace=ws)
+        assert swa.swa_attn_check_status(ws, kind=kind) == swa.SWA_OK
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    ran_out, longest = out_of_time(call, check, ws, kind)
+    assert ran_out
+    assert longest < 1.0
