@@ -49,9 +49,11 @@ constexpr uint32_t kTcAcol = 256;                // their first column, behind t
 template <int MB, bool X8>
 struct TcShape {
   static constexpr int kB = MB * kCols * 2;      // x as operand, of a step
-  // Stages of x. Up to 128 rows they go with those of the weights, under the same barriers: the issuer then has
-  // one wait and one commit a stage beside its eight products, which take 45 to 64 clocks each to issue however
-  // narrow they are (a wait and a commit of their own for every 64 columns of x: 27 us for 22).
+  // Stages of x. Up to 128 rows they go with those of the weights: the issuer then has one wait and one commit a
+  // stage beside its eight products, which take 45 to 64 clocks each to issue however narrow they are (a wait and a
+  // commit of their own for every 64 columns of x: 27 us for 22). The warps that turn the stage's weights wait for its
+  // x too, and arrive for both: a copy that the issuer's barrier counted itself could not be waited for on the way out,
+  // once warps that give up arrive there no more.
   static constexpr bool kJoint = MB <= 128;
   static constexpr int kXs = kJoint ? kTcStages : 3;
   // A stage's place in either ring is always the same group's: a wait for a
@@ -64,7 +66,7 @@ struct TcShape {
   static constexpr int FULL = 0, EMPTY = kTcStages, XFULL = 2 * kTcStages, XEMPTY = XFULL + kXs, RAW = XEMPTY + kXs,
                        RAWFREE = RAW + kRaws, ACC = RAWFREE + kRaws, COUNT = ACC + 1;
   static_assert(kBytes <= 232448 && COUNT * 8 + 8 <= 512 && oRawW % 1024 == 0 && oRawX % 128 == 0 && oRawS % 128 == 0, "");
-  static_assert(kRaws % kTcGroups == 0 && kTcStages % kTcGroups == 0, "");
+  static_assert(kRaws % kTcGroups == 0 && kTcStages % kTcGroups == 0 && (!kJoint || kXs == kTcStages), "");
   static_assert(MB * kTcRows * 4 <= oRawS && MB <= static_cast<int>(kTcAcol), "the sums fit shared memory and their columns");
 };
 
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (tid == 0) {
     *abort_flag = 0;
     for (int s = 0; s < ST; ++s) {
-      mbar_init(bar(S::FULL + s), kTcGroup + (!X8 && S::kJoint ? 1 : 0));
+      mbar_init(bar(S::FULL + s), kTcGroup);
       mbar_init(bar(S::EMPTY + s), 1);
     }
     for (int s = 0; s < XS; ++s) {
@@ -201,6 +203,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         fence_async_smem();
       }
       tmem_wait_st();
+      if (!X8 && S::kJoint && !(ok = mbar_wait_warp(bar(S::XFULL + st), (k / ST) & 1, ctl))) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else if (warp == kTcTma) {
     if (!X8 && lane == 0) {
       tma_prefetch_desc(&tmX);
-      constexpr int full = S::kJoint ? S::FULL : S::XFULL, empty = S::kJoint ? S::EMPTY : S::XEMPTY;
+      constexpr int full = S::XFULL, empty = S::kJoint ? S::EMPTY : S::XEMPTY;
       int k = 0;
       for (; k < stages; ++k) {
         const int st = k % XS;
@@ -220,10 +223,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int u = 0; u < kSub; ++u)
           tma_load_2d(sbase + static_cast<uint32_t>(st * kSub + u) * S::kB, &tmX, bar(full + st), (q0 + k * kSub + u) * kCols, m0);
       }
-      // after a wait that ran out: what was issued lands before the memory is given back (joint barriers also wait
-      // for the weights' warps, which may have given up; then these waits give up too, after 2 s each)
-      if (k < stages)
-        for (int i = max(0, k - XS); i < k; ++i) mbar_wait_drain(bar(full + i % XS), (i / XS) & 1, kDrainLimitNs);
+      // what was issued lands before the memory is given back (those who wait for it may have given up)
+      for (int i = max(0, k - XS); i < k; ++i) mbar_wait_drain(bar(full + i % XS), (i / XS) & 1, kDrainLimitNs);
     }
   } else if (warp == kTcRaw) {
     if (lane == 0) {
@@ -241,8 +242,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int e = 0; e < kSub; ++e)
             tma_load_2d(sbase + S::oRawX + st * S::kRawX + e * (MB * kCols), &tmX, bar(S::RAW + st), (k + e) * kCols, m0);
       }
-      if (i < stages)       // after a wait that ran out, as above
-        for (int e = max(0, i - RS); e < i; ++e) mbar_wait_drain(bar(S::RAW + e % RS), (e / RS) & 1, kDrainLimitNs);
+      for (int e = max(0, i - RS); e < i; ++e) mbar_wait_drain(bar(S::RAW + e % RS), (e / RS) & 1, kDrainLimitNs);   // as above
     }
   } else if (lane == 0) {
     constexpr uint32_t id = idesc_bf16_f32(kTcRows, MB, 0, 0);

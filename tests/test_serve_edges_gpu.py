@@ -10,7 +10,7 @@ import sliding_window_gqa_qk_gb300 as swa
 from oracle import serve
 from test_decode_gpu import build_cache, f64, numbers_of, randn, scales_of
 from oracle import decode as dec
-from test_serve_gpu import DT, KINDS, dev, i32
+from test_serve_gpu import DT, KINDS, check_linear, dev, i32, linear_case
 
 pytestmark = pytest.mark.gpu
 
@@ -136,3 +136,16 @@ def test_tree_waits_that_run_out_among_warps_that_share_stages(kind, d, Hq, T):
     ran_out, longest = out_of_time(call, check, ws, kind)
     assert ran_out
     assert longest < 1.0
+
+
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("M,N,K", [(33, 48, 4104), (64, 128, 8192), (65, 20000, 640), (100, 160, 6464), (128, 2048, 2048), (129, 130, 5000)])
+def test_linear_rings_that_go_round(x8, M, N, K):
+    # the pipelines of the form for many rows: more stages than their rings hold, parts of K of different lengths, more
+    # tiles than CTAs run at once; every call gives the same bits
+    w4, x, scale, r, want, size = linear_case("bf16", M, N, K, x8, True, 40)
+    a = [t if t is None else t.to(dev()) for t in (x, w4, scale, r)]
+    ws = torch.zeros(256, dtype=torch.uint8, device=dev())
+    ys = [swa.w4_linear(a[0], a[1], out_features=N, scale=a[2], add=a[3], dtype=torch.bfloat16, workspace=ws) for _ in range(4)]
+    check_linear(ys[0], "bf16", want, size, M, K, x8)
+    assert all(torch.equal(y, ys[0]) for y in ys) and swa.swa_attn_check_status(ws) == swa.SWA_OK
