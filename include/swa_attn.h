@@ -702,8 +702,8 @@ swa_status swa_w4_linear(int M, int N, int K, const void* x, const float* x_scal
  *   o   = swa_kv4_attn of q, one token a request (cu and seen NULL, n_tokens = p->B;
  *         its position in pos is lens[b] - 1), or swa_kv4_tree_attn (cu, seen, pos)
  *   out = h + o wo^T
- * p, c, r, gq, table, max_pages, lens, max_new are those of the attention (p->T 1),
- * ex's wait_limit_ns too. out is none of x and add. lens counts the tokens of the
+ * p, c, r, gq, table, max_pages, lens, max_new are those of the attention (p->T 1).
+ * ex's wait_limit_ns holds for the projections too. out is none of x and add. lens counts the tokens of the
  * call. The workspace: swa_kv4_block_workspace_size bytes for n_tokens or more,
  * passed to swa_kv4_workspace_init once; it may serve the other decode calls too.
  */

@@ -73,19 +73,36 @@ swa_status launch_few(const w4::LinArgs& a, cudaStream_t st) {
 }
 
 template <w4::XKind X>
-swa_status launch_linear(const w4::LinArgs& a, uint32_t* status, cudaStream_t st) {
+swa_status launch_linear(const w4::LinArgs& a, uint32_t* status, uint64_t wait_ns, cudaStream_t st) {
 #if !defined(SWA_ELEM_FP32)
   constexpr bool x8 = X == w4::kX8;
   if (a.M > kFewRows && (!x8 || a.K % 16 == 0)) {      // (e4m3 rows come by TMA, whose strides are multiples of 16 bytes)
-    if (a.M <= 64) return w4::launch_linear_tc<64, x8>(a, status, kWaitLimitNs, st);
-    if (x8 || a.M <= 128) return w4::launch_linear_tc<128, x8>(a, status, kWaitLimitNs, st);
-    return w4::launch_linear_tc<256, false>(a, status, kWaitLimitNs, st);
+    if (a.M <= 64) return w4::launch_linear_tc<64, x8>(a, status, wait_ns, st);
+    if (x8 || a.M <= 128) return w4::launch_linear_tc<128, x8>(a, status, wait_ns, st);
+    return w4::launch_linear_tc<256, false>(a, status, wait_ns, st);
   }
 #endif
   if (a.M <= 8) return launch_few<X, 1>(a, st);
   if (a.M <= 16) return launch_few<X, 2>(a, st);
   if (a.M <= 24) return launch_few<X, 3>(a, st);
   return launch_few<X, 4>(a, st);
+}
+
+// swa_w4_linear under a time limit of its pipeline waits (which the form for few rows, and the fp32 library, do not have).
+swa_status linear_call(int M, int N, int K, const void* x, const float* x_scale, const void* w4, const void* add, void* y,
+                       void* workspace, size_t ws_bytes, uint64_t wait_ns, void* stream) {
+  swa_status s = check_w4(N, K);
+  if (s != SWA_OK) return s;
+  if (M < 0) return SWA_ERR_INVALID_ARG;
+  if ((s = check_header(workspace, ws_bytes)) != SWA_OK) return s;
+  if (M == 0) return SWA_OK;
+  if (!tensor_ok(x) || !tensor_ok(w4) || !tensor_ok(y) || !aligned(add, 16) || !aligned(x_scale, 4)) return SWA_ERR_INVALID_ARG;
+  if (x == y) return SWA_ERR_INVALID_ARG;
+  if ((s = check_device()) != SWA_OK) return s;
+  const w4::LinArgs a{M, N, K, x, x_scale, static_cast<const uint8_t*>(w4), static_cast<const elem_t*>(add), static_cast<elem_t*>(y)};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint32_t* status = static_cast<uint32_t*>(workspace);
+  return x_scale != nullptr ? launch_linear<w4::kX8>(a, status, wait_ns, st) : launch_linear<w4::kXElem>(a, status, wait_ns, st);
 }
 
 swa_status check_tokens(int B, int n_tokens, int max_new) {
@@ -258,18 +275,7 @@ swa_status swa_w4_unpack(int N, int K, const void* w4, void* w, void* stream) {
 
 swa_status swa_w4_linear(int M, int N, int K, const void* x, const float* x_scale, const void* w4, const void* add, void* y,
                          void* workspace, size_t ws_bytes, void* stream) {
-  swa_status s = check_w4(N, K);
-  if (s != SWA_OK) return s;
-  if (M < 0) return SWA_ERR_INVALID_ARG;
-  if ((s = check_header(workspace, ws_bytes)) != SWA_OK) return s;
-  if (M == 0) return SWA_OK;
-  if (!tensor_ok(x) || !tensor_ok(w4) || !tensor_ok(y) || !aligned(add, 16) || !aligned(x_scale, 4)) return SWA_ERR_INVALID_ARG;
-  if (x == y) return SWA_ERR_INVALID_ARG;
-  if ((s = check_device()) != SWA_OK) return s;
-  const w4::LinArgs a{M, N, K, x, x_scale, static_cast<const uint8_t*>(w4), static_cast<const elem_t*>(add), static_cast<elem_t*>(y)};
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  uint32_t* status = static_cast<uint32_t*>(workspace);
-  return x_scale != nullptr ? launch_linear<w4::kX8>(a, status, st) : launch_linear<w4::kXElem>(a, status, st);
+  return linear_call(M, N, K, x, x_scale, w4, add, y, workspace, ws_bytes, kWaitLimitNs, stream);
 }
 
 swa_status swa_kv4_tree(int B, int n_tokens, int max_new, const int32_t* parent, const int32_t* cu, const int32_t* lens,
@@ -397,9 +403,12 @@ swa_status swa_kv4_block(const swa_params* p, const swa_extras* ex, const swa_kv
                         nullptr, stream)) != SWA_OK)
     return s;
   const int nq = p->Hq * p->d, nk = p->Hkv * p->d;
+  swa_extras wait{};
+  wait.wait_limit_ns = ex != nullptr ? ex->wait_limit_ns : 0;
+  const uint64_t wait_ns = wait.wait_limit_ns != 0 ? wait.wait_limit_ns : kWaitLimitNs;
   const struct { const void* w; int n; size_t to; } proj[] = {{w->wq, nq, L.q}, {w->wk, nk, L.k}, {w->wv, nk, L.v}};
   for (const auto& m : proj)
-    if ((s = swa_w4_linear(n_tokens, m.n, w->C, ws + L.xn, nullptr, m.w, nullptr, ws + m.to, workspace, ws_bytes, stream)) != SWA_OK)
+    if ((s = linear_call(n_tokens, m.n, w->C, ws + L.xn, nullptr, m.w, nullptr, ws + m.to, workspace, ws_bytes, wait_ns, stream)) != SWA_OK)
       return s;
   swa_params rows = *p;          // the tokens as rows of one, for the append
   rows.B = n_tokens;
@@ -414,14 +423,12 @@ swa_status swa_kv4_block(const swa_params* p, const swa_extras* ex, const swa_kv
   if ((s = swa_kv4_append(&rows, gate.gate_w != nullptr ? &gate : nullptr, c, r, ws + L.k, ws + L.v, gk, ve, tok, nullptr, pos, slot,
                           workspace, ws_bytes, stream)) != SWA_OK)
     return s;
-  swa_extras wait{};
-  wait.wait_limit_ns = ex != nullptr ? ex->wait_limit_ns : 0;
   float* lse = reinterpret_cast<float*>(ws + L.lse);
   s = tree ? swa_kv4_tree_attn(p, &wait, c, r, n_tokens, max_new, ws + L.q, gq, table, max_pages, lens, cu, pos, seen, ws + L.o, lse,
                                workspace, ws_bytes, stream)
            : swa_kv4_attn(p, &wait, c, r, ws + L.q, gq, table, max_pages, lens, ws + L.o, lse, workspace, ws_bytes, stream);
   if (s != SWA_OK) return s;
-  return swa_w4_linear(n_tokens, w->C, nq, ws + L.o, nullptr, w->wo, h, out, workspace, ws_bytes, stream);
+  return linear_call(n_tokens, w->C, nq, ws + L.o, nullptr, w->wo, h, out, workspace, ws_bytes, wait_ns, stream);
 }
 
 }  // extern "C"

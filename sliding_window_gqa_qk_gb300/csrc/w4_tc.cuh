@@ -97,7 +97,7 @@ __device__ __forceinline__ uint32_t e4m3_bf16x2(uint32_t two) {
   return pack_bf16x2(f.x, f.y);
 }
 
-template <int MB, bool X8>
+template <int MB, bool X8, bool kPolled>
 __global__ void __launch_bounds__(kTcThreads, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                      const __grid_constant__ CUtensorMap tmS, const __grid_constant__ TcArgs a) {
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint32_t* abort_flag = tmem_sh + 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t* status = a.status != nullptr ? a.status : &g_unreported;
-  const WaitCtl<false> ctl{abort_flag, status, a.wait_limit_ns};
+  const WaitCtl<kPolled> ctl{abort_flag, status, a.wait_limit_ns};
   auto bar = [&](int i) { return sbase + S::oBar + 8u * static_cast<uint32_t>(i); };
   const int rank = static_cast<int>(blockIdx.x) % a.splits, tile = static_cast<int>(blockIdx.x) / a.splits;
   const int m0 = tile % a.mt * MB, n0 = tile / a.mt * kTcRows;
@@ -362,12 +362,14 @@ swa_status launch_linear_tc(const LinArgs& l, uint32_t* status, uint64_t wait_ns
   a.per = (stages + a.splits - 1) / a.splits;
   a.status = status;
   a.wait_limit_ns = wait_ns;
-  auto kern = linear_tc_kernel<MB, X8>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess) {
-    cudaGetLastError();
-    return SWA_ERR_CUDA;
-  }
-  return launch_cluster(kern, tiles * a.splits, kTcThreads, S::kBytes, a.splits, st, map, wmap, smap, a);
+  auto launch = [&](auto kern) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess) {
+      cudaGetLastError();
+      return SWA_ERR_CUDA;
+    }
+    return launch_cluster(kern, tiles * a.splits, kTcThreads, S::kBytes, a.splits, st, map, wmap, smap, a);
+  };
+  return wait_ns < kPollBelowNs ? launch(linear_tc_kernel<MB, X8, true>) : launch(linear_tc_kernel<MB, X8, false>);
 }
 
 }  // namespace w4

@@ -10,7 +10,7 @@ import sliding_window_gqa_qk_gb300 as swa
 from oracle import serve
 from test_decode_gpu import build_cache, f64, numbers_of, randn, scales_of
 from oracle import decode as dec
-from test_serve_gpu import DT, KINDS, check_linear, dev, i32, linear_case
+from test_serve_gpu import DT, KINDS, check_linear, dev, i32, linear_case, random_w4
 
 pytestmark = pytest.mark.gpu
 
@@ -149,3 +149,32 @@ def test_linear_rings_that_go_round(x8, M, N, K):
     ys = [swa.w4_linear(a[0], a[1], out_features=N, scale=a[2], add=a[3], dtype=torch.bfloat16, workspace=ws) for _ in range(4)]
     check_linear(ys[0], "bf16", want, size, M, K, x8)
     assert all(torch.equal(y, ys[0]) for y in ys) and swa.swa_attn_check_status(ws) == swa.SWA_OK
+
+
+@pytest.mark.parametrize("N", [40, 100, 300])
+def test_projections_of_the_block_call_keep_its_wait_limit(N):
+    # requests without a cached token, so that the attention has nothing to wait for: what runs out is the projections'
+    # (N rows: each tile of x that they have). Calls behind it give their bits.
+    C, Hq, Hkv, d = 4096, 8, 8, 64
+    cache = swa.new_kv4_cache(2, 16, Hkv, d, dev())
+    w = [random_w4(50 + i, n, k).to(dev()) for i, (n, k) in enumerate(((Hq * d, C), (Hkv * d, C), (Hkv * d, C), (C, Hq * d)))]
+    x = randn(55, N, C, dtype=torch.bfloat16).to(dev())
+    table, lens = torch.zeros(N, 1, dtype=torch.int32, device=dev()), torch.zeros(N, dtype=torch.int32, device=dev())
+    slot, pos = torch.full((N,), -1, dtype=torch.int64, device=dev()), torch.zeros(N, dtype=torch.int32, device=dev())
+    ws = swa.new_kv4_block_workspace(cache, N, C, Hq)
+    p, c = swa.make_params(N, 1, Hq, Hkv, d), swa.swa_kv4_cache(cache.data_ptr(), 2, 16)
+    weights, out = swa.swa_kv4_weights(C, *(t.data_ptr() for t in w)), torch.empty_like(x)
+    want = [swa.w4_linear(x, w[0]), swa.w4_linear(x[:, :Hq * d].contiguous(), w[3])]
+
+    def call(ex):
+        return swa.swa_kv4_block(p, ex, c, None, weights, N, 1, x, None, None, None, None, None, None, slot, pos, None, None, table, 1,
+                                 lens, out, ws)
+
+    def check():
+        got = [swa.w4_linear(x, w[0], workspace=ws), swa.w4_linear(x[:, :Hq * d].contiguous(), w[3], workspace=ws)]
+        assert call(None) == swa.SWA_OK and swa.swa_attn_check_status(ws) == swa.SWA_OK
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(out, x)
+    check()
+    ran_out, longest = out_of_time(call, check, ws, "bf16")
+    assert ran_out
+    assert longest < 1.0
