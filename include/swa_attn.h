@@ -637,7 +637,8 @@ swa_status swa_kv4_move(const swa_params* p, const swa_kv4_cache* c, const int64
  *   gain   fp32 [C], or NULL (1)
  *   h      elem [rows, C]; NULL only where add is NULL. May be x or add.
  *   y      elem [rows, C], may be x or add; or
- *   y8, scale  y in 8 bits: e4m3 numbers [rows, C], fp32 [rows]; y ~ y8 * scale.
+ *   y8, scale  y in 8 bits: e4m3 numbers [rows, C], fp32 [rows]; y ~ y8 * scale. y8 is
+ *          none of x, add and h.
  *          y8 = e4m3(448 u / max|u|), scale = max|u| rstd / 448 with u = gain h,
  *          to nearest, ties to even, exactly so. A row that holds a NaN or an
  *          infinity is NaN in both; one whose entries are all 0 is 0 in both (so is one

@@ -194,6 +194,8 @@ swa_status swa_rms_norm(long long rows, int C, float eps, const void* x, const v
   if ((y == nullptr) == (y8 == nullptr) || (y8 != nullptr) != (scale != nullptr)) return SWA_ERR_INVALID_ARG;
   if (rows == 0) return SWA_OK;
   if (x == nullptr || (add != nullptr && h == nullptr) || (h != nullptr && (h == y || h == y8))) return SWA_ERR_INVALID_ARG;
+  // (y takes the place of the entries that it is made of; 8-bit rows are shorter, and would lie over other rows)
+  if (y8 != nullptr && (y8 == x || y8 == add)) return SWA_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(add, 16) || !aligned(gain, 16) || !aligned(h, 16) || !aligned(y, 16) || !aligned(y8, 16) ||
       !aligned(scale, 4) || !aligned(rstd, 4))
     return SWA_ERR_INVALID_ARG;
