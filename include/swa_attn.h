@@ -664,7 +664,7 @@ swa_status swa_rms_norm_bwd(long long rows, int C, const void* h, const float* r
 /*
  * Projections whose weights are held in 4 bits, for serving:
  *   y[m][n] = x_scale[m] sum_k x[m][k] W[n][k] + add[m][n]
- * K a multiple of 8; N, K at most 2^24. The weights are swa_w4_size(N, K) bytes,
+ * K a multiple of 8; N, K at most 2^24, M at most 2^31 - 256. The weights are swa_w4_size(N, K) bytes,
  * 16-byte aligned: [ceil(N / 16)][ceil(K / 64)] tiles of 544 bytes, 512 of numbers
  * and 16 steps (bf16). A number n = 0..15 stands for s (n - 8), with a step s per
  * row and 64 columns. Lane = 4 r + j (r 0..7, j 0..3) of a tile has its bytes 16

@@ -22,6 +22,11 @@ swa_status check_w4(int N, int K) {
   if (N < 1 || K < 8 || K % 8 != 0) return SWA_ERR_INVALID_ARG;
   return N > w4::kMaxN || K > w4::kMaxK ? SWA_ERR_UNSUPPORTED : SWA_OK;
 }
+// Rows of x, whose tiles of up to 256 are counted in 31 bits.
+swa_status check_w4_rows(int M) {
+  if (M < 0) return SWA_ERR_INVALID_ARG;
+  return M > w4::kMaxM ? SWA_ERR_UNSUPPORTED : SWA_OK;
+}
 long long w4_tiles(int N, int K) {
   return static_cast<long long>((N + w4::kRows - 1) / w4::kRows) * ((K + w4::kCols - 1) / w4::kCols);
 }
@@ -92,8 +97,7 @@ swa_status launch_linear(const w4::LinArgs& a, uint32_t* status, uint64_t wait_n
 swa_status linear_call(int M, int N, int K, const void* x, const float* x_scale, const void* w4, const void* add, void* y,
                        void* workspace, size_t ws_bytes, uint64_t wait_ns, void* stream) {
   swa_status s = check_w4(N, K);
-  if (s != SWA_OK) return s;
-  if (M < 0) return SWA_ERR_INVALID_ARG;
+  if (s != SWA_OK || (s = check_w4_rows(M)) != SWA_OK) return s;
   if ((s = check_header(workspace, ws_bytes)) != SWA_OK) return s;
   if (M == 0) return SWA_OK;
   if (!tensor_ok(x) || !tensor_ok(w4) || !tensor_ok(y) || !aligned(add, 16) || !aligned(x_scale, 4)) return SWA_ERR_INVALID_ARG;
@@ -178,7 +182,7 @@ swa_status check_serve(const swa_params* p, int C, int n) {
   swa_status s = check_params(p);
   if (s != SWA_OK) return s;
   if (p->T != 1 || p->causal != 1 || n < 0) return SWA_ERR_INVALID_ARG;
-  if ((s = check_norm(n, C)) != SWA_OK) return s;
+  if ((s = check_norm(n, C)) != SWA_OK || (s = check_w4_rows(n)) != SWA_OK) return s;
   return static_cast<long long>(p->Hq) * p->d > w4::kMaxN ? SWA_ERR_UNSUPPORTED : SWA_OK;
 }
 

@@ -25,7 +25,7 @@ namespace w4 {
 
 constexpr int kRows = 16, kCols = 64;
 constexpr int kTileBytes = 544;
-constexpr int kMaxN = 1 << 24, kMaxK = 1 << 24;
+constexpr int kMaxN = 1 << 24, kMaxK = 1 << 24, kMaxM = INT32_MAX - 255;
 
 // ---------------------------------------------------------------------------
 // Packing. A warp a tile: lane 4 r + j reads its two rows' 16 columns.

@@ -2,9 +2,10 @@
 Nothing here runs on a GPU; the addresses are never followed."""
 
 import pytest
+import torch
 
 import sliding_window_gqa_qk_gb300 as swa
-from test_serve_abi import A, BAD, KINDS, X, built_libraries, norm  # noqa: F401  (a fixture)
+from test_serve_abi import A, BAD, KINDS, X, block, built_libraries, lin, norm, params  # noqa: F401  (a fixture)
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -14,3 +15,15 @@ def test_norm_refuses_8_bit_rows_over_what_it_reads(kind):
     for bad in (dict(x=A, y8=A), dict(x=A, add=add, h=X, y8=add), dict(x=A, add=add, h=A, y8=A), dict(x=A, add=add, h=X, y8=X)):
         assert norm(kind, y=None, scale=A, **bad) == BAD
         assert norm(kind, y=None, scale=A, rows=0, **bad) == swa.SWA_OK
+
+
+def test_rows_of_a_projection_have_a_limit():
+    # tiles of up to 256 rows, counted in 31 bits
+    for kind in KINDS:
+        for M in (2 ** 31 - 1, 2 ** 31 - 255):
+            assert lin(kind, M=M) == swa.SWA_ERR_UNSUPPORTED and lin(kind, M=M, x_scale=A) == swa.SWA_ERR_UNSUPPORTED
+            assert block(kind, n=M, nws=1 << 62) == swa.SWA_ERR_UNSUPPORTED
+            assert swa.swa_kv4_block_workspace_size(params(), 64, M, kind) == 0
+        if not torch.cuda.is_available():
+            assert lin(kind, M=2 ** 31 - 256) == swa.SWA_ERR_CUDA
+        assert swa.swa_kv4_block_workspace_size(params(), 64, 2 ** 31 - 256, kind) > 2 ** 38
