@@ -1216,7 +1216,7 @@ def w4_linear(x, w4, *, out_features: Optional[int] = None, scale=None, add=None
     (bf16 by default). ``out``: y, which may be ``add``. ``workspace``: where a wait
     that ran out is reported (swa_attn_check_status)."""
     if _fast is not None and stream is None and (dtype is None or dtype is _BF16 or dtype is _F32):
-        r = _fast.w4_linear(x, w4, -1 if out_features is None else out_features, scale, add, 0 if dtype is None else (1 if dtype is _BF16 else 2),
+        r = _fast.w4_linear(x, w4, out_features, scale, add, 0 if dtype is None else (1 if dtype is _BF16 else 2),
                             out, workspace)
         if r is not None:
             return r

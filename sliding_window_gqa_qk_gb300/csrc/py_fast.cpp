@@ -515,7 +515,7 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// w4_linear(x, w4, out_features (-1: all), scale, add, dtype (0: x's, or bf16 with a scale; 1: bf16; 2: fp32), out, workspace)
+// w4_linear(x, w4, out_features (None: all), scale, add, dtype (0: x's, or bf16 with a scale; 1: bf16; 2: fp32), out, workspace)
 PyObject* w4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 8) Py_RETURN_NONE;
   return guarded("swa_w4_linear", [&](Call& call) -> PyObject* {
@@ -526,7 +526,8 @@ PyObject* w4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int want = int_of(a[5]);
     const auto type = want == 0 ? (x8 ? at::kBFloat16 : x.scalar_type()) : (want == 1 ? at::kBFloat16 : at::kFloat);
     const int kind = kind_more(type);
-    const int64_t K = x.size(-1), M = x.numel() / K, given = int_of(a[2]), N = given < 0 ? 16 * w.size(0) : given;
+    const int64_t K = x.size(-1), M = x.numel() / K, N = a[2] == Py_None ? 16 * w.size(0) : int_of(a[2]);
+    if (N < 1) throw Refused{};
     const void* xa = at_(a[0], x8 ? at::kFloat8_e4m3fn : type, dev, x.sizes());
     const void* wa = at_(a[1], at::kByte, dev, {(N + 15) / 16, (K + 63) / 64, 544});
     const auto* sa = static_cast<const float*>(at_(a[3], at::kFloat, dev, x.sizes().slice(0, x.dim() - 1)));

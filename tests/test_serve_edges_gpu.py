@@ -178,3 +178,11 @@ def test_projections_of_the_block_call_keep_its_wait_limit(N):
     ran_out, longest = out_of_time(call, check, ws, "bf16")
     assert ran_out
     assert longest < 1.0
+
+
+def test_the_short_way_leaves_numbers_that_are_no_size():
+    x, w4 = randn(24, 3, 64, dtype=torch.bfloat16).to(dev()), torch.zeros(2, 1, 544, dtype=torch.uint8, device=dev())
+    for n in (-1, -5, -(2 ** 31)):
+        with pytest.raises(ValueError):
+            swa.w4_linear(x, w4, out_features=n)
+    assert swa.w4_linear(x, w4).shape == (3, 32)
