@@ -580,8 +580,8 @@ swa_status swa_kv4_attn(const swa_params* p, const swa_extras* ex, const swa_kv4
  * them, each the continuation of its parent. A step's tokens lie one request
  * behind the other, as swa_kv4_plan lays them out: those of request b are rows
  * cu[b] .. cu[b + 1] - 1 (at most max_new, 1 .. 64), their slots are the last ones
- * of its lens[b], in order. The rest of lens[b] is its context. Rows behind
- * cu[B] are padding.
+ * of its lens[b], in order. The rest of lens[b] is its context. Rows in front of
+ * cu[0] and behind cu[B] are padding.
  *
  * swa_kv4_tree: what the tokens see, and where they stand, from their parents.
  *   parent  int32 [n_tokens], the index of the token's parent among its request's

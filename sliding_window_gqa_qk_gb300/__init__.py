@@ -1019,7 +1019,7 @@ def kv4_tree(parent, cu, lens, *, max_new: int, workspace=None, stream=None):
     """pos, seen = kv4_tree(parent, cu, lens): positions (int32) and visibility
     (int64 bits) of a step's drafted tokens, from parent int32 [N] (the index of
     each token's parent among its request's, -1: the context), cu int32 [B + 1]
-    (rows of the requests; rows behind cu[B] are padding) and lens int32 [B]
+    (rows of the requests; those in front of cu[0] and behind cu[B] are padding) and lens int32 [B]
     (cached tokens, the drafted ones among them: cu and lens of kv4_plan). At
     most ``max_new`` (up to 64) tokens a request."""
     if _fast is not None and stream is None:

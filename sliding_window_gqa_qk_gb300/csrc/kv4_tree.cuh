@@ -49,6 +49,12 @@ __device__ __forceinline__ TreeReq tree_req(const int32_t* cu, const int32_t* le
   return r;
 }
 
+// Rows in front of the first request; none where its rows are not plausible.
+__device__ __forceinline__ int tree_front(const int32_t* cu, int N) {
+  const int row0 = cu[0], end = cu[1];
+  return row0 > 0 && end >= row0 && end <= N ? row0 : 0;
+}
+
 constexpr int kTreeWarps = 4;
 __global__ void __launch_bounds__(kTreeWarps * 32) tree_kernel(const __grid_constant__ TreeArgs a) {
   __shared__ int up[kTreeWarps][kTreeTokens];
@@ -81,15 +87,18 @@ __global__ void __launch_bounds__(kTreeWarps * 32) tree_kernel(const __grid_cons
     }
     __syncwarp();
   }
-  // rows behind the last request
-  const int used = a.cu[a.B];
-  if (used < 0 || used > a.N) bad = DEV_ERR_BOUNDS;
-  else
-    for (long long i = used + static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < a.N;
+  // rows of no request: in front of the first and behind the last one
+  auto none = [&](long long from, long long to) {
+    for (long long i = from + static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < to;
          i += static_cast<long long>(gridDim.x) * blockDim.x) {
       a.seen[i] = 0;
       a.pos[i] = 0;
     }
+  };
+  const int used = a.cu[a.B];
+  none(0, tree_front(a.cu, a.N));
+  if (used < 0 || used > a.N) bad = DEV_ERR_BOUNDS;
+  else none(used, a.N);
   if (bad && a.status) atomicOr(a.status, bad);
 }
 
@@ -387,7 +396,7 @@ __device__ __forceinline__ void tree_sight(const TreeAttnArgs& a, const TreeReq&
 }
 
 // Rows that hold nothing, by the CTA that answers for them: those of a request
-// that is refused, and those behind the last one.
+// that is refused, those in front of the first one and those behind the last.
 template <int D, int kWarps>
 __device__ __forceinline__ void tree_zero(const TreeAttnArgs& a, const TreeReq& req, int b, int h, int G) {
   constexpr int E = D / 32;
@@ -402,6 +411,7 @@ __device__ __forceinline__ void tree_zero(const TreeAttnArgs& a, const TreeReq& 
     }
   };
   if (req.bad && req.rows > 0) zero(req.row0, req.row0 + req.rows);
+  if (b == 0) zero(0, tree_front(a.cu, a.N));
   if (used >= 0 && used < a.N) zero(used, a.N);
 }
 

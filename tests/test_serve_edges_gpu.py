@@ -186,3 +186,34 @@ def test_the_short_way_leaves_numbers_that_are_no_size():
         with pytest.raises(ValueError):
             swa.w4_linear(x, w4, out_features=n)
     assert swa.w4_linear(x, w4).shape == (3, 32)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Hq,d,T", [(2, 128, 3), (4, 128, 12), (2, 64, 9)])
+def test_rows_in_front_of_the_first_request_are_padding(kind, Hq, d, T):
+    # some requests of a larger step: the rows of the others, in front and behind, hold nothing
+    lens, page, front, behind = [40, 33], 16, 5, 3
+    cache, table, rows = build_cache(lens, 1, d, page, 21)
+    cd, td = cache.to(dev()), table.to(dev())
+    N = front + 2 * T + behind
+    cu = i32(front, front + T, front + 2 * T)
+    parent = torch.arange(-1, T - 1).repeat(2)
+    parent = torch.cat([torch.full((front,), 7), parent, torch.full((behind,), -1)]).int().to(dev())
+    ws = swa.new_kv4_workspace(cd, 2, Hq, max_pages=td.shape[1], kind=kind)
+    # (outputs of the C calls, so that what they leave alone is seen)
+    pos, seen = torch.full((N,), 77, dtype=torch.int32, device=dev()), torch.full((N,), 77, dtype=torch.int64, device=dev())
+    assert swa.swa_kv4_tree(2, N, T, parent, cu, i32(*lens), pos, seen, ws) == swa.SWA_OK
+    assert pos[:front].tolist() == [0] * front and seen[:front].tolist() == [0] * front
+    assert pos[-behind:].tolist() == [0] * behind and seen[-behind:].tolist() == [0] * behind
+    q = randn(22, N, Hq, d, dtype=DT[kind]).to(dev())
+    o, lse = torch.full_like(q, 5.0), torch.full((N, Hq), 5.0, device=dev())
+    p, c = swa.make_params(2, 1, Hq, 1, d), swa.swa_kv4_cache(cd.data_ptr(), cd.shape[0], page)
+    assert swa.swa_kv4_tree_attn(p, None, c, None, N, T, q, None, td, td.shape[1], i32(*lens), cu, pos, seen, o, lse, ws) == swa.SWA_OK
+    assert swa.swa_attn_check_status(ws, kind=kind) == swa.SWA_OK
+    for at in (slice(0, front), slice(N - behind, N)):
+        assert not o[at].any() and torch.isneginf(lse[at]).all()
+    for b, n in enumerate(lens):
+        at = slice(front + b * T, front + (b + 1) * T)
+        ro, rl = serve.tree_attend(f64(q)[at], *rows[b], *serve.tree(list(range(-1, T - 1)), n - T))
+        assert np.abs(f64(lse)[at] - rl).max() <= 1e-4
+        assert np.linalg.norm(f64(o)[at] - ro) <= (9e-3 if kind == "bf16" else 1e-5) * np.linalg.norm(ro)
