@@ -238,8 +238,9 @@ swa_status swa_rms_norm_bwd(long long rows, int C, const void* h, const float* r
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (rows == 0) {
-    if (dgain != nullptr && cudaMemsetAsync(dgain, 0, static_cast<size_t>(C) * sizeof(float), st) != cudaSuccess) return SWA_ERR_CUDA;
-    return SWA_OK;
+    if (dgain == nullptr) return SWA_OK;
+    cudaMemsetAsync(dgain, 0, static_cast<size_t>(C) * sizeof(float), st);
+    return launched();
   }
   if ((s = check_device()) != SWA_OK) return s;
   norm::BwdArgs a{};

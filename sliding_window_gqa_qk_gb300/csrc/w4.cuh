@@ -502,7 +502,8 @@ swa_status launch_cluster(K kern, long long grid, int threads, int smem, int siz
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess && cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+  const bool ok = cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess;
+  return cudaGetLastError() == cudaSuccess && ok ? SWA_OK : SWA_ERR_CUDA;      // (told here, and not again by the next launch)
 }
 
 }  // namespace w4

@@ -1,5 +1,6 @@
 """Edges of the serving calls that the other files' cases do not reach."""
 
+import ctypes
 import time
 
 import numpy as np
@@ -217,3 +218,30 @@ def test_rows_in_front_of_the_first_request_are_padding(kind, Hq, d, T):
         ro, rl = serve.tree_attend(f64(q)[at], *rows[b], *serve.tree(list(range(-1, T - 1)), n - T))
         assert np.abs(f64(lse)[at] - rl).max() <= 1e-4
         assert np.linalg.norm(f64(o)[at] - ro) <= (9e-3 if kind == "bf16" else 1e-5) * np.linalg.norm(ro)
+
+
+def test_a_failed_launch_is_not_told_again():
+    # A launch into a capture that is no longer valid fails on the host. The next call, which has nothing to do with it,
+    # succeeds. (The capture is begun and ended by the driver's functions, so that torch knows nothing of it.)
+    cu = ctypes.CDLL("libcuda.so.1")
+    w4 = torch.randint(0, 128, (256, 64, 544), dtype=torch.uint8, device=dev())
+    g = torch.ones(4096, device=dev())
+    for M in (4, 40, 0):         # in a cluster, each form
+        x = randn(23, max(M, 1), 4096, dtype=torch.bfloat16).to(dev())
+        y = torch.empty_like(x)
+        assert swa.swa_w4_linear(M, 4096, 4096, x, None, w4, None, y) == swa.SWA_OK
+        torch.cuda.synchronize()
+        stream = torch.cuda.Stream()
+        h = ctypes.c_void_p(stream.cuda_stream)
+        assert cu.cuStreamBeginCapture_v2(h, 2) == 0
+        assert cu.cuStreamSynchronize(h) != 0                  # not allowed in a capture, which ends it
+        if M:
+            failed = swa.swa_w4_linear(M, 4096, 4096, x, None, w4, None, y, stream=stream)
+        else:                    # the gradient of no rows: a memset
+            failed = swa.swa_rms_norm_bwd(0, 4096, None, None, None, None, None, None, g, None, 0, stream=stream, kind="bf16")
+        graph = ctypes.c_void_p()
+        assert cu.cuStreamEndCapture(h, ctypes.byref(graph)) != 0 and not graph.value
+        assert failed == swa.SWA_ERR_CUDA
+        out = torch.empty_like(x)
+        assert swa.swa_rms_norm(1, 4096, 1e-6, x, None, g, None, out, None, None, None) == swa.SWA_OK
+        torch.cuda.synchronize()
