@@ -72,7 +72,35 @@ SWA_BWD_STAGE_MAIN = 4
 SWA_BWD_STAGE_POST = 8
 
 
-class swa_params(ctypes.Structure):
+def _int32(value):
+    """value, where it fits 32 bits: ctypes would cut it to them without a word."""
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{value} does not fit 32 bits")
+    return value
+
+
+class _Int(ctypes.c_int):
+    """An int argument of the library."""
+
+    @classmethod
+    def from_param(cls, value):
+        return value if isinstance(value, ctypes.c_int) else ctypes.c_int(_int32(value))
+
+
+class _Struct(ctypes.Structure):
+    def __init_subclass__(cls):
+        cls._ints = {name: i for i, (name, kind) in enumerate(cls._fields_) if kind is ctypes.c_int}
+
+    def __init__(self, *args, **kw):
+        n = len(args)
+        for name, i in self._ints.items():
+            value = args[i] if i < n else kw.get(name, 0)
+            if value > 0x7fffffff or value < -0x80000000:
+                _int32(value)
+        super().__init__(*args, **kw)
+
+
+class swa_params(_Struct):
     _fields_ = [
         ("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int),
         ("d", ctypes.c_int), ("window", ctypes.c_int), ("causal", ctypes.c_int),
@@ -87,7 +115,7 @@ class SwaError(RuntimeError):
         self.status = status
 
 
-class swa_extras(ctypes.Structure):
+class swa_extras(_Struct):
     """Extras of the _ex entry points: rotary tables, the learned
     value-embedding gate and the pipeline-wait limit (see include/swa_attn.h)."""
     _fields_ = [("rope_cos", ctypes.c_void_p), ("rope_sin", ctypes.c_void_p), ("rope_rows", ctypes.c_int),
@@ -97,31 +125,31 @@ class swa_extras(ctypes.Structure):
                 ("wait_limit_ns", ctypes.c_ulonglong)]
 
 
-class swa_block_weights(ctypes.Structure):
+class swa_block_weights(_Struct):
     """Weights of the block calls: model width C and the four projection
     matrices in the torch.nn.Linear layout (see include/swa_attn.h)."""
     _fields_ = [("C", ctypes.c_int), ("wq", ctypes.c_void_p), ("wk", ctypes.c_void_p),
                 ("wv", ctypes.c_void_p), ("wo", ctypes.c_void_p)]
 
 
-class swa_rope(ctypes.Structure):
+class swa_rope(_Struct):
     """Rotary tables of the rope and kv4 calls (see include/swa_attn.h)."""
     _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("rows", ctypes.c_int),
                 ("rot", ctypes.c_int), ("interleaved", ctypes.c_int)]
 
 
-class swa_rope_freq(ctypes.Structure):
+class swa_rope_freq(_Struct):
     """Frequencies of swa_rope_tables (see include/swa_attn.h)."""
     _fields_ = [("rot", ctypes.c_int), ("scaling", ctypes.c_int)] + [
         (n, ctypes.c_double) for n in ("base", "factor", "orig_len", "slow", "fast", "amplitude")]
 
 
-class swa_kv4_cache(ctypes.Structure):
+class swa_kv4_cache(_Struct):
     """A 4-bit paged cache: device buffer, pages, tokens per page."""
     _fields_ = [("data", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("page", ctypes.c_int)]
 
 
-class swa_kv4_weights(ctypes.Structure):
+class swa_kv4_weights(_Struct):
     """Packed weights of swa_kv4_block (see include/swa_attn.h)."""
     _fields_ = [("C", ctypes.c_int)] + [(n, ctypes.c_void_p) for n in ("wq", "wk", "wv", "wo")]
 
@@ -180,7 +208,7 @@ def load(kind: str = "bf16") -> ctypes.CDLL:
     lib.swa_block_fwd.restype = ctypes.c_int
     lib.swa_block_bwd.argtypes = [P, R, W] + [_vp] * 15 + [ctypes.c_size_t, _vp]
     lib.swa_block_bwd.restype = ctypes.c_int
-    C, F, I, L, Z = (ctypes.POINTER(swa_kv4_cache), ctypes.POINTER(swa_rope), ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t)
+    C, F, I, L, Z = (ctypes.POINTER(swa_kv4_cache), ctypes.POINTER(swa_rope), _Int, ctypes.c_longlong, ctypes.c_size_t)
     for name, args in (
             ("swa_rope_tables", [ctypes.POINTER(swa_rope_freq), I, I, _vp, _vp, _vp]),
             ("swa_rope_apply", [P, F] + [_vp] * 5 + [I, _vp, Z, _vp]),
@@ -199,7 +227,7 @@ def load(kind: str = "bf16") -> ctypes.CDLL:
             ("swa_w4_unpack", [I, I] + [_vp] * 3),
             ("swa_w4_linear", [I] * 3 + [_vp] * 5 + [_vp, Z, _vp])):
         getattr(lib, name).argtypes = args
-        getattr(lib, name).restype = I
+        getattr(lib, name).restype = ctypes.c_int
     for name, args in (("swa_kv4_cache_size", [P, I, I]), ("swa_kv4_workspace_size", [P, I, I]),
                        ("swa_rms_norm_workspace_size", [L, I]), ("swa_w4_size", [I, I]), ("swa_kv4_block_workspace_size", [P, I, I])):
         getattr(lib, name).argtypes = args

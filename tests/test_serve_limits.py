@@ -1,6 +1,8 @@
 """Refusals and limits of the serving calls beside those of test_serve_abi.py.
 Nothing here runs on a GPU; the addresses are never followed."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -27,3 +29,26 @@ def test_rows_of_a_projection_have_a_limit():
         if not torch.cuda.is_available():
             assert lin(kind, M=2 ** 31 - 256) == swa.SWA_ERR_CUDA
         assert swa.swa_kv4_block_workspace_size(params(), 64, 2 ** 31 - 256, kind) > 2 ** 38
+
+
+FAR = [2 ** 31, 2 ** 32 + 5, 2 ** 40, -2 ** 31 - 1, -2 ** 40]
+
+
+@pytest.mark.parametrize("n", FAR)
+def test_numbers_that_do_not_fit_32_bits_are_refused(n):
+    # (ctypes cuts them: a window of 2^40 became one of 0 keys)
+    for call in (lambda: swa.make_params(1, 1, 2, 1, 128, window=n), lambda: swa.make_params(n, 1, 2, 1, 128),
+                 lambda: swa.make_params(1, 1, 2, 1, 128, vocab=n), lambda: swa.swa_params(window=n), lambda: swa.swa_rope(A, A, n, 64, 0),
+                 lambda: swa.swa_kv4_cache(A, n, 32), lambda: swa.swa_kv4_cache(A, 10, page=n), lambda: swa.swa_kv4_weights(n, A, A, A, A),
+                 lambda: swa.swa_block_weights(n, A, A, A, A), lambda: swa.swa_rope_freq(rot=n)):
+        with pytest.raises(ValueError):
+            call()
+    m = n + 64 if n > 0 else n - 64       # cut, some would be sizes that there are
+    for call in (lambda: swa.swa_w4_size(m, 64), lambda: swa.swa_kv4_tree(2, 10, m, A, A, A, X, X),
+                 lambda: swa.swa_w4_pack(m, 64, A, X, None, "bf16"), lambda: lin(M=m), lambda: norm(C=m),
+                 lambda: swa.swa_kv4_block_workspace_size(params(), m, 10)):
+        with pytest.raises((ValueError, ctypes.ArgumentError)):
+            call()
+    assert swa.make_params(1, 1, 2, 1, 128, window=2 ** 31 - 1).window == 2 ** 31 - 1
+    e = swa.make_extras(wait_limit_ns=2 ** 40)
+    assert e.wait_limit_ns == 2 ** 40
