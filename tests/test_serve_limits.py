@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import sliding_window_gqa_qk_gb300 as swa
-from test_serve_abi import A, BAD, KINDS, X, block, built_libraries, lin, norm, params  # noqa: F401  (a fixture)
+from test_serve_abi import A, BAD, KINDS, X, attn, back, block, built_libraries, lin, move, norm, params, tree  # noqa: F401  (a fixture)
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -52,3 +52,25 @@ def test_numbers_that_do_not_fit_32_bits_are_refused(n):
     assert swa.make_params(1, 1, 2, 1, 128, window=2 ** 31 - 1).window == 2 ** 31 - 1
     e = swa.make_extras(wait_limit_ns=2 ** 40)
     assert e.wait_limit_ns == 2 ** 40
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses would be used")
+@pytest.mark.parametrize("kind", KINDS)
+def test_calls_that_pass_every_check_end_at_the_device_and_nowhere_else(kind):
+    # asking for a device fails here; a check that refused a legal call as unsupported would answer otherwise
+    end = swa.SWA_ERR_CUDA
+    for bad in (dict(), dict(y=None, y8=X, scale=A), dict(C=65536), dict(rows=2 ** 31 - 1), dict(C=8), dict(y=A), dict(add=X, h=A, y=X)):
+        assert norm(kind, **bad) == end
+    for bad in (dict(), dict(dgain=None, ws=None), dict(dx=A), dict(C=65536, n=1 << 40)):
+        assert back(kind, **bad) == end
+    for bad in (dict(), dict(x_scale=A), dict(add=X), dict(M=1, N=1, K=8), dict(M=2 ** 31 - 256), dict(N=1 << 24, K=1 << 24)):
+        assert lin(kind, **bad) == end
+    assert swa.swa_w4_pack(1 << 24, 8, A, X, None, kind) == end and swa.swa_w4_unpack(16, 1 << 24, A, X, None, kind) == end
+    assert tree() == end and tree(max_new=64, B=1) == end and tree(ws=A, nws=256) == end
+    assert move() == end and move(p=params(T=64)) == end and move(ws=A, nws=256) == end
+    for bad in (dict(), dict(max_new=64), dict(p=params(Hq=32, B=2047, Hkv=1), max_new=64, n=2047), dict(p=params(window=0)),
+                dict(p=params(d=64)), dict(r=swa.swa_rope(A, A, 64, 64, 0)), dict(p=params(B=65535, Hq=1, Hkv=1), n=65535, max_new=1)):
+        assert attn(kind, **bad) == end
+    for bad in (dict(), dict(n=2, cu=None, seen=None), dict(add=A + 4096), dict(ve=A, tok=A, p=params(vocab=3)), dict(max_new=64),
+                dict(ex=swa.swa_extras(wait_limit_ns=1)), dict(ex=swa.swa_extras(gate_w=A, gate_ch=32))):
+        assert block(kind, **bad) == end
