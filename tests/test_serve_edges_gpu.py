@@ -245,3 +245,54 @@ def test_a_failed_launch_is_not_told_again():
         out = torch.empty_like(x)
         assert swa.swa_rms_norm(1, 4096, 1e-6, x, None, g, None, out, None, None, None) == swa.SWA_OK
         torch.cuda.synchronize()
+
+
+def test_the_short_way_takes_the_ordinary_calls():
+    # each of its functions itself, with what the Python functions pass: a result, and the long way's bits
+    swa.load("fp32")
+    f = swa._fast
+    assert f is not None
+    for dt in (torch.bfloat16, torch.float32):
+        x, add = (randn(90 + i, 5, 264, dtype=dt).to(dev()) for i in range(2))
+        g, w4 = (1 + 0.1 * randn(92, 264)).to(dev()), random_w4(93, 104, 264).to(dev())
+        s = torch.cuda.current_stream()            # asked for by name: the long way
+
+        def same(a, b):
+            assert a is not None
+            a, b = ([t[k] for k in sorted(t)] if isinstance(t, dict) else list(t) if isinstance(t, tuple) else [t] for t in (a, b))
+            assert len(a) == len(b)
+            for u, v in zip(a, b):
+                assert (u is None) == (v is None) and (u is None or u.dtype is v.dtype and torch.equal(u.float(), v.float()))
+        n = f.rms_norm(x, g, add, 1e-6, False, False)
+        e = f.rms_norm(x, None, add, 1e-6, True, False)
+        same(n, swa.rms_norm(x, g, add=add, stream=s))
+        same(e, swa.rms_norm(x, add=add, fp8=True, stream=s))
+        y = x.clone()
+        assert f.rms_norm(y, g, add, 1e-6, False, True)["h"] is y and torch.equal(y, n["h"])
+        ws = torch.empty(swa.swa_rms_norm_workspace_size(5, 264), dtype=torch.uint8, device=dev())
+        for w in (None, ws):
+            same(f.rms_norm_backward(n["h"], n["rstd"], add, g, x, w), swa.rms_norm_backward(n["h"], n["rstd"], add, g, dh=x, stream=s))
+        which = 1 if dt is torch.bfloat16 else 2
+        for args, kw in (((None, None, None, 0, None, None), dict()), ((97, None, add[:, :97].contiguous(), which, None, None),
+                                                                      dict(out_features=97, add=add[:, :97].contiguous(), dtype=dt))):
+            same(f.w4_linear(x, w4, *args) if args[0] else f.w4_linear(x, w4, None, None, None, 0, None, None)[:, :97],
+                 swa.w4_linear(x, w4, stream=s, **kw)[:, :97])
+        out, r = torch.empty(5, 104, dtype=dt, device=dev()), add[:, :104].contiguous()
+        assert f.w4_linear(e["y"], w4, 104, e["scale"], r, which, out, None) is out
+        same(out, swa.w4_linear(e["y"], w4, out_features=104, scale=e["scale"], add=r, dtype=dt, stream=s))
+        cache, table, _ = build_cache([50, 33], 2, 128, 16, 94)
+        cd, td, lens, cu = cache.to(dev()), table.to(dev()), i32(50, 33), i32(0, 3, 5)
+        parent, q = i32(-1, 0, 0, -1, 0, 0), randn(95, 6, 4, 128, dtype=dt).to(dev())
+        ws, rope, gq = swa.new_kv4_workspace(cd, 2, 4, max_pages=td.shape[1]), swa.rope_tables(64, 64), (1 + 0.1 * randn(96, 128)).to(dev())
+        for w in (None, ws):
+            tree = f.kv4_tree(parent, cu, lens, 3, w)
+            same(tree, swa.kv4_tree(parent, cu, lens, max_new=3, workspace=w, stream=s))
+        for pair in ((None, None), rope):
+            same(f.kv4_tree_attention(cd, q, td, lens, cu, *tree, 3, *pair, False, gq, 40, 0.0, 1e-6, ws),
+                 swa.kv4_tree_attention(cd, q, td, lens, cu, *tree, max_new=3, rope=None if pair[0] is None else pair, gq=gq, window=40,
+                                        workspace=ws, stream=s))
+        src, dst = torch.tensor([[3, 4]], device=dev()), torch.tensor([[5, -1]], device=dev())
+        a, b = cd.clone(), cd.clone()
+        assert f.kv4_move(a, src, dst, ws) is True
+        swa.kv4_move(b, src, dst, workspace=ws, stream=s)
+        assert torch.equal(a, b) and not torch.equal(a, cd)
