@@ -610,7 +610,11 @@ swa_status swa_kv4_attn(const swa_params* p, const swa_extras* ex, const swa_kv4
  * (swa_kv4_workspace_size, and what is said there of sharing one). Limit: B * Hq
  * at most 65535.
  * Rounding: in bf16 calls the probabilities count 8 bits where they multiply
- * the values (not in their sum, nor in lse). Sums are fp32, joined in a fixed order.
+ * the values (not in their sum, nor in lse; swa_kv4_attn keeps 16, so a single
+ * drafted token's o is less exact than plain decoding's), and with d = 128 and more
+ * than 16 (token, head) rows of a kv head the values do too. Sums are fp32, joined
+ * in a fixed order; a row's are relative to a logit that others pass by up to 2^40:
+ * values above 2^70 may leave fp32.
  *
  * swa_kv4_move: the tokens of slots src[b][t] become those of dst[b][t] (int64 [p->B,
  * p->T], T <= 64), in the whole cache of a layer: the accepted path of a tree put
@@ -681,7 +685,8 @@ swa_status swa_rms_norm_bwd(long long rows, int C, const void* h, const float* r
  * swa_w4_linear: x [M][K] elem, or e4m3 where x_scale (fp32 [M]) is given: the pair
  * that swa_rms_norm makes. add [M][N] or NULL; it may be y. x, add and y are 16-byte
  * aligned. Sums are fp32. Products are exact in calls of up to 32 rows and in the
- * fp32 library; in larger bf16 calls a weight s (n - 8) enters rounded to bf16.
+ * fp32 library; in larger bf16 calls a weight s (n - 8) enters rounded to bf16 (2^-8
+ * of it, so of the sum of sizes |x W|: a row's result may change with M).
  * workspace: as in swa_rope_apply (the pipeline waits of larger bf16 calls report
  * there). K is cut into parts that are added in a fixed order.
  */

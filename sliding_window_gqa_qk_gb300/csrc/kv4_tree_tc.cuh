@@ -22,8 +22,8 @@
 //                         out again. Centres are a ninth product of 16: <q, k> =
 //                         sum_g s_g <q, n - 8>_g + z_g sum(q)_g. Also the values'
 //                         scales, cleaned: keys that are not there, or not finite, 0.
-//   values  4 warps       numbers to bf16, times step plus centre (rounded once, 2^-9,
-//                         as P is)
+//   values  4 warps       numbers to bf16, times step plus centre (rounded once, as P
+//                         is: up to 2^-8 of it)
 //   mma     2 threads      products of 16: nine of S a block, eight of O. One after the
 //                         other by one thread they were 17 times 90 to 100 clocks of issue
 //                         a block, beside the other warps' work; S and O have one each

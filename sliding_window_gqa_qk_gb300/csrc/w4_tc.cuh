@@ -25,9 +25,10 @@
 // 128 rows the issue of the products bounds it, 45 to 64 clocks each (eight a
 // stage) however narrow they are; with 256 rows the products themselves, 128 each.
 // Rounding: a weight enters as bf16(s (n - 8)): its 11 bits lose up to three,
-// 2^-9 of the weight at most, below what y's own bf16 rounding costs. (The form
-// for few rows keeps s out of the products; here that would take the sums out of
-// tensor memory every 64 columns.)
+// less than 2^-8 of the weight (3.9e-3 for s = 148 / 128, n - 8 = 7). The error is
+// relative to the sum of sizes |x w|: as y's own bf16 rounding where that sum does
+// not cancel, above it where it does. (The form for few rows keeps s out of the
+// products; here that would take the sums out of tensor memory every 64 columns.)
 // Few tiles: K is split over a cluster of up to 8 CTAs, which add their sums up
 // through distributed shared memory, in rank order.
 #pragma once

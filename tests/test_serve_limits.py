@@ -74,3 +74,13 @@ def test_calls_that_pass_every_check_end_at_the_device_and_nowhere_else(kind):
     for bad in (dict(), dict(n=2, cu=None, seen=None), dict(add=A + 4096), dict(ve=A, tok=A, p=params(vocab=3)), dict(max_new=64),
                 dict(ex=swa.swa_extras(wait_limit_ns=1)), dict(ex=swa.swa_extras(gate_w=A, gate_ch=32))):
         assert block(kind, **bad) == end
+
+
+def test_what_a_weight_loses_as_bf16():
+    # s (n - 8) for every step of one binade, as the calls of more than 32 rows round it: below 2^-8 of it (half a step of
+    # 8 bits), and for some more than 2^-9. In sums that cancel, 2^-8 of the sum of sizes can exceed y's own rounding.
+    s = (torch.arange(128, 256).float() / 128).view(-1, 1)
+    assert torch.equal(s, s.bfloat16().float())
+    exact = s.double() * torch.arange(1, 9).double()
+    lost = ((exact.bfloat16().double() - exact).abs() / exact).max().item()
+    assert 2.0 ** -9 < lost < 2.0 ** -8
