@@ -611,10 +611,9 @@ swa_status swa_kv4_attn(const swa_params* p, const swa_extras* ex, const swa_kv4
  * at most 65535.
  * Rounding: in bf16 calls the probabilities count 8 bits where they multiply
  * the values (not in their sum, nor in lse; swa_kv4_attn keeps 16, so a single
- * drafted token's o is less exact than plain decoding's), and with d = 128 and more
- * than 16 (token, head) rows of a kv head the values do too. Sums are fp32, joined
- * in a fixed order; a row's are relative to a logit that others pass by up to 2^40:
- * values above 2^70 may leave fp32.
+ * drafted token's o is less exact than plain decoding's). With d = 128 and more than
+ * 16 (token, head) rows of a kv head they count 11 bits, and the values 11 (of a
+ * key's largest; values below 2^-97 lose more). Sums are fp32, joined in a fixed order.
  *
  * swa_kv4_move: the tokens of slots src[b][t] become those of dst[b][t] (int64 [p->B,
  * p->T], T <= 64), in the whole cache of a layer: the accepted path of a tree put

@@ -4,7 +4,7 @@
 // With many rows the m16n8k16 form (kv4_tree.cuh) is held by its products and by
 // the softmax beside them: 16 requests of 32768 tokens, 64 rows for each of 4 kv
 // heads, took it 548 us where the cache's bytes take the memory 43 and the products
-// 34. This form takes 181, and is held by the softmax warps' round of a block, 2600
+// 34. This form takes 173, and is held by the softmax warps' round of a block, 2600
 // clocks: their exponentials, P's stores, and the waits for S around them. (With 32
 // rows a CTA 201; with a thread's 16 rows instead of 32 its registers spill, 335.)
 // Here a block is 128 keys (eight tiles), the lanes of tensor memory:
@@ -22,16 +22,21 @@
 //                         out again. Centres are a ninth product of 16: <q, k> =
 //                         sum_g s_g <q, n - 8>_g + z_g sum(q)_g. Also the values'
 //                         scales, cleaned: keys that are not there, or not finite, 0.
-//   values  4 warps       numbers to bf16, times step plus centre (rounded once, as P
-//                         is: up to 2^-8 of it)
+//   values  4 warps       numbers to fp16, times step plus centre: 11 bits, as P has
+//                         (with 8 of each, in bf16, o was up to 2.5e-3 off where its own
+//                         rounding makes 1.7e-3). A key whose values are far from 1
+//                         (2^13 above, 2^12 below) has them brought there by a power of
+//                         two that P takes on and its sum takes off: see value_shift
 //   mma     2 threads      products of 16: nine of S a block, eight of O. One after the
 //                         other by one thread they were 17 times 90 to 100 clocks of issue
 //                         a block, beside the other warps' work; S and O have one each
 //   load    1 warp        bulk copies of tiles, kTtRing blocks in flight
-// Maximum: a row's is that of the first block in which it sees a key, and is raised
-// only when a logit passes it by 2^40 (in base 2; P and its sums have fp32's
-// exponents), which the four warps of its 32 rows find out together; then they
-// rescale O in tensor memory themselves.
+// Maximum: a row's is that of the first block in which it sees a key, where P is 2^4,
+// and is raised only when P would pass 2^15, which the four warps of its 32 rows find
+// out together; then they rescale O in tensor memory themselves. So P leaves fp16 2^29
+// below that first maximum (what a million keys there would count is below o's own
+// rounding), and has 2^11 above it: logits of a standard deviation of 1 to 3 take 173
+// to 180 us, of 4 195 (from 2^8: 173 to 210, 231; from 2^2: 173 to 175, 184).
 // A key whose scales are not finite counts as 0 in the products, for a product would
 // bring a NaN to rows that do not see it: the rows that see it are made NaN at the
 // end (keys' scales: through S, per row).
@@ -46,7 +51,7 @@ namespace kv4 {
 constexpr int kTtD = 128, kTtKeys = 128, kTtTiles = kTtKeys / kTile;
 constexpr int kTtRing = 6;                       // blocks of packed tiles in flight
 constexpr int kTtScales = 8;                      // blocks whose scales are kept: see the keys' warps
-constexpr float kTtRaise = 40.f;
+constexpr float kTtBase = 4.f, kTtRaise = 15.f;
 
 template <int NR>
 struct TtShape {
@@ -62,7 +67,7 @@ struct TtShape {
   static constexpr int q_block = N * 128;        // 64 K elements of every row, 128-byte swizzle
   static constexpr int oQ = 0, oP = 3 * q_block, p_buf = kTtKeys * 128, oRing = oP + 2 * p_buf, block = kTtTiles * tile_bytes(kTtD);
   static constexpr int oFk = oRing + kTtRing * block;          // [kTtScales][128] {factor, flags}
-  static constexpr int oVs = oFk + kTtScales * kTtKeys * 8;    // [kTtScales][2 groups][128] steps, then centres, bf16
+  static constexpr int oVs = oFk + kTtScales * kTtKeys * 8;    // [kTtScales][2 groups][128] steps, then centres, fp16
   static constexpr int oRow = oVs + kTtScales * 2 * 2 * kTtKeys * 2;   // TreeRow [NR]
   static constexpr int oM = oRow + NR * 16;                    // maxima, negated, and their rises [NR] each
   static constexpr int oRed = oM + 2 * NR * 4;                 // [4][NR]
@@ -108,12 +113,28 @@ __device__ __forceinline__ uint32_t hmul2_u(uint32_t a, __half2 b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-__device__ __forceinline__ uint32_t bfma2_u(uint32_t a, uint32_t s, uint32_t z) {
-  const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&s),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&z));
+__device__ __forceinline__ uint32_t hfma2_u(uint32_t a, uint32_t s, uint32_t z) {
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&s), *reinterpret_cast<const __half2*>(&z));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 r = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 constexpr uint32_t kKeyOff = 4u;                 // flags of a key: no such key; 1, 2: values of group 0, 1 not finite
+// Size of a group's values, whose step and centre are w (bf16), as an exponent of fp32; 0: nothing, -1: not finite. The
+// values are below four times it.
+__device__ __forceinline__ int value_size(uint32_t w) {
+  const int es = w >> 7 & 255u, ez = w >> 23 & 255u;
+  return max(es, ez) == 255 ? -1 : max(es > 0 ? es + 3 : 0, ez);
+}
+// Power of two e by which a key's values of size `top` are taken down (up below 0), so that they fit fp16: 0 for those
+// of 2^-12 to 2^13, and never below -85, so that P's sum, whose terms are P 2^-e, stays in fp32.
+__device__ __forceinline__ int value_shift(int top) {
+  const int e = top - 127;
+  return top <= 0 ? 0 : (e > 12 ? e - 12 : (e < -12 ? max(e + 12, -85) : 0));
+}
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 template <int NR, bool kPolled>
 __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(const __grid_constant__ TreeAttnArgs a) {
@@ -285,14 +306,15 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
         ffma2(x[i + 2], x[i + 3], x[i + 2], x[i + 3], f, f, m.z, m.w);
       }
       const bool edge = key0 < all_lo || key0 + kTtKeys > req.ctx;        // of the block
-      if (edge || (kflag & kKeyOff)) {
+      if (edge || (kflag & ~3u)) {        // off, or values of another size, whose power of two P takes on
         const int d = key - req.ctx;
+        const float shift = static_cast<float>(static_cast<int>(kflag) >> 8);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const int4 w = *reinterpret_cast<const int4*>(rows + r0 + i);    // lo, pos, seen
           const uint32_t word = static_cast<uint32_t>(d & 32 ? w.w : w.z);
           const bool on = (d < 0 ? key >= w.x : (d < kTreeTokens) & static_cast<bool>(word >> (d & 31) & 1u)) & !(kflag & kKeyOff);
-          if (!on) x[i] = -INFINITY;
+          x[i] = on ? x[i] + shift : -INFINITY;
         }
       }
       if (kflag & 3u) {                 // values that are not finite: the rows that see them say so at the end
@@ -320,7 +342,7 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
           // by how much the row's maximum rises; a first one may be below 0, where it starts
           const float top = unordered(t);
           const bool first = fresh[r0 + lane], none = first && top == -INFINITY;
-          const float rise = none ? 0.f : (first ? top : fmaxf(top, 0.f));
+          const float rise = none ? 0.f : (first ? top - kTtBase : fmaxf(top - kTtBase, 0.f));
           rowm[r0 + lane] -= rise;
           rowm[NR + r0 + lane] = rise;
           fresh[r0 + lane] = none;
@@ -349,14 +371,16 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
       }
       if (n >= 2) ok = ok && mbar_wait_warp(bar(S::PVDONE + (n & 1)), ((n >> 1) - 1) & 1, ctl);
       const uint32_t p = sbase + S::oP + (n & 1) * S::p_buf + key_in * 128;
+      // (read again: a register that is kept till here is one that spills)
+      const float back = exp2i(-(*reinterpret_cast<volatile int*>(smem + S::oFk + (n % kTtScales * kTtKeys + key_in) * 8 + 4) >> 8));
 #pragma unroll
       for (int i = 0; i < 32; i += 8) {
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
           const float p0 = ex2_approx(x[i + e]), p1 = ex2_approx(x[i + e + 1]);
-          fadd2_acc(l[i + e], l[i + e + 1], p0, p1);
-          w[e / 2] = pack_bf16x2(p0, p1);
+          ffma2(l[i + e], l[i + e + 1], p0, p1, back, back, l[i + e], l[i + e + 1]);
+          w[e / 2] = pack_f16x2(p0, p1);
         }
         st_shared_v4(p + static_cast<uint32_t>(((r0 + i) >> 3) ^ (key_in & 7)) * 16, w[0], w[1], w[2], w[3]);
       }
@@ -385,17 +409,25 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
       const uint32_t miss = *reinterpret_cast<volatile uint32_t*>(smem + S::oMiss + 4 * st);
       const uint8_t* at = smem + S::oRing + st * S::block + tile * TB;
       uint32_t kw[2][4];
-      float s[2][2], z[2][2], vs[2][2], vz[2][2];
+      float s[2][2], z[2][2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         ld_words<4>(at + (r + 8 * i) * (D / 2) + j * 16, kw[i]);
         ld_scales<2>(at + 16 * D + (r + 8 * i) * 8, s[i], z[i]);
-        ld_scales<2>(at + 17 * D + (r + 8 * i) * 8, vs[i], vz[i]);
       }
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(at + 17 * D + lane * 4);
       const int key_tile = (t0 + n * kTtTiles + tile) * kTile;
+      // lane = (token, group): steps and centres of the values, in fp16, 0 where they are not to be used, and the token's flags
+      uint32_t value = *reinterpret_cast<const uint32_t*>(at + 17 * D + lane * 4), flags_v;
+      {
+        const int mine = value_size(value), other = __shfl_xor_sync(0xffffffffu, mine, 1), key = key_tile + (lane >> 1);
+        const int shift = value_shift(max(mine, other));
+        const bool off = (miss >> tile & 1u) || key < lo || key >= len;
+        const float fit = exp2i(-shift);
+        value = off || mine < 0 ? 0u : pack_f16x2(__uint_as_float(value << 16) * fit, __uint_as_float(value & 0xFFFF0000u) * fit);
+        flags_v = off ? kKeyOff : static_cast<uint32_t>(shift) << 8 | static_cast<uint32_t>(mine) >> 31 | static_cast<uint32_t>(other) >> 31 << 1;
+      }
       uint32_t out[32], zw[2];
-      float2 fk[2];
+      float fk[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float top = fmaxf(fmaxf(fabsf(s[i][0]), fabsf(s[i][1])) * 8.f, fmaxf(fabsf(z[i][0]), fabsf(z[i][1])));
@@ -405,10 +437,7 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
         const __half2 s0 = __float2half2_rn(s[i][0] * fit), s1 = __float2half2_rn(s[i][1] * fit);
         const __half2 zz = __floats2half2_rn(z[i][0] * fit * 64.f, z[i][1] * fit * 64.f);
         zw[i] = j == 0 ? *reinterpret_cast<const uint32_t*>(&zz) : 0u;
-        const int key = key_tile + r + 8 * i;
-        uint32_t f = (miss >> tile & 1u) || key < lo || key >= len ? kKeyOff : 0u;
-        if (!f) f = (isfinite(vs[i][0]) && isfinite(vz[i][0]) ? 0u : 1u) | (isfinite(vs[i][1]) && isfinite(vz[i][1]) ? 0u : 2u);
-        fk[i] = make_float2(__uint_as_float(static_cast<uint32_t>(127 - 8 + e) << 23), __uint_as_float(f));
+        fk[i] = __uint_as_float(static_cast<uint32_t>(127 - 8 + e) << 23);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           uint32_t t[4];
@@ -423,16 +452,16 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
       // places of the scales eight in front are free
       if (n >= 2 && !(ok = mbar_wait_warp(bar(S::KFREE + ks), ((n >> 1) - 1) & 1, ctl))) break;
       tc_fence_after();
+      float* kfac = reinterpret_cast<float*>(smem + S::oFk + (n % kTtScales * kTtKeys + tile * kTile) * 8);
       if (j == 0) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) *reinterpret_cast<float2*>(smem + S::oFk + (n % kTtScales * kTtKeys + tile * kTile + r + 8 * i) * 8) = fk[i];
+        for (int i = 0; i < 2; ++i) kfac[2 * (r + 8 * i)] = fk[i];
       }
-      {      // lane = (token, group): steps and centres of the values, 0 where they are not to be used
-        const int token = lane >> 1, g = lane & 1, key = key_tile + token;
-        const bool use = !(miss >> tile & 1u) && key >= lo && key < len && (w & 0x7F80u) != 0x7F80u && (w & 0x7F800000u) != 0x7F800000u;
-        uint16_t* to = reinterpret_cast<uint16_t*>(smem + S::oVs) + (n % kTtScales * 2 + g) * 2 * kTtKeys + tile * kTile + token;
-        to[0] = use ? static_cast<uint16_t>(w) : 0;
-        to[kTtKeys] = use ? static_cast<uint16_t>(w >> 16) : 0;
+      if (!(lane & 1)) kfac[lane + 1] = __uint_as_float(flags_v);
+      {
+        uint16_t* to = reinterpret_cast<uint16_t*>(smem + S::oVs) + (n % kTtScales * 2 + (lane & 1)) * 2 * kTtKeys + tile * kTile + (lane >> 1);
+        to[0] = static_cast<uint16_t>(value);
+        to[kTtKeys] = static_cast<uint16_t>(value >> 16);
       }
       const uint32_t to = tmem + lanes + (static_cast<uint32_t>(16 * u) << 16) + S::cK + static_cast<uint32_t>(ks) * S::kstep;
       tmem_st_16x128_x16(to, out);
@@ -468,9 +497,9 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
             const uint32_t w = *reinterpret_cast<const uint32_t*>(at + (j + 4 * half) * D + r * 16 + q4 * 4);
             const int pair = (t4 + t) * 8 + j + 4 * half;
             const uint32_t s2 = *reinterpret_cast<const uint32_t*>(sc + 4 * pair), z2 = *reinterpret_cast<const uint32_t*>(sc + 2 * kTtKeys + 4 * pair);
-            widen_bf16(w, x);
+            widen_f16(w, x);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) out[i >> 1][4 * t + 2 * half + (i & 1)] = bfma2_u(x[i], s2, z2);
+            for (int i = 0; i < 4; ++i) out[i >> 1][4 * t + 2 * half + (i & 1)] = hfma2_u(x[i], s2, z2);
           }
         }
 #pragma unroll
@@ -541,7 +570,7 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
     }
   } else if (warp == S::mma_o) {
     if (lane == 0) {
-      constexpr uint32_t id_o = idesc_bf16_f32(128, NR, 0, 1);
+      constexpr uint32_t id_o = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(NR >> 3) << 17) | (8u << 24);    // fp16, P^T by rows
       const uint64_t dP = sdesc_sw128(sbase + S::oP, 16, 1024);
       for (int n = 0; n < blocks; ++n) {
         const int ps = n & 1;

@@ -11,7 +11,7 @@ import sliding_window_gqa_qk_gb300 as swa
 from oracle import serve
 from test_decode_gpu import build_cache, f64, numbers_of, randn, scales_of
 from oracle import decode as dec
-from test_serve_gpu import DT, KINDS, check_linear, dev, i32, linear_case, random_w4
+from test_serve_gpu import DT, KINDS, check_linear, dev, i32, linear_case, random_parents, random_w4
 
 pytestmark = pytest.mark.gpu
 
@@ -296,3 +296,81 @@ def test_the_short_way_takes_the_ordinary_calls():
         assert f.kv4_move(a, src, dst, ws) is True
         swa.kv4_move(b, src, dst, workspace=ws, stream=s)
         assert torch.equal(a, b) and not torch.equal(a, cd)
+
+
+MANY = [  # lens, new, Hq, Hkv, page: more than 16 (token, head) rows of a kv head, d = 128
+    ([700, 40, 129], [16, 16, 5], 4, 1, 64),
+    ([2500, 2499], [20, 24], 8, 2, 32),
+    ([5000, 300], [30, 9], 2, 2, 64),
+    ([9000], [64], 4, 4, 128),
+]
+
+
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_tree_of_many_rows_keeps_its_bits(case):
+    # P and the values have 11 bits each: beside o's own rounding they count little. A rounding to 8 bits has an rms of
+    # 2^-8 / sqrt(3) times that of 1 / mantissa, 0.74 where mantissas are spread by their logarithm: 1.66e-3. One to 11
+    # bits is an eighth of it, twice, of a sum's terms: 3e-4. Together 1.69e-3, and a tenth for how mantissas are spread.
+    lens, new, Hq, Hkv, page = MANY[case]
+    cache, table, rows = build_cache(lens, Hkv, 128, page, 60 + case)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    trees = [serve.tree(random_parents(n, 61 + b), m - n) for b, (n, m) in enumerate(zip(new, lens))]
+    q = randn(62, int(cu[-1]), Hq, 128, dtype=torch.bfloat16)
+    o, _ = swa.kv4_tree_attention(cache.to(dev()), q.to(dev()), table.to(dev()), i32(*lens), i32(*cu), i32(*sum((t[0] for t in trees), [])),
+                                  torch.tensor(np.array(sum((t[1] for t in trees), []), dtype=np.uint64).view(np.int64), device=dev()),
+                                  max_new=max(new))
+    want = np.concatenate([serve.tree_attend(f64(q)[cu[b]:cu[b + 1]], *rows[b], *trees[b])[0] for b in range(len(lens))])
+    assert np.linalg.norm(f64(o) - want) <= 1.9e-3 * np.linalg.norm(want), np.linalg.norm(f64(o) - want) / np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("Hq,T", [(4, 16), (2, 40), (4, 3)])
+@pytest.mark.parametrize("powers", [[0], [-14], [12], [13, 14], [-90, -60], [60], [100, 0], [-30, -13, -12, 0, 11, 12, 13, 14, 40], [110, 108]])
+def test_tree_of_values_of_every_size(Hq, T, powers):
+    # values of each key, or of some, times a power of two: far from fp16's range, in which more than 16 rows hold them
+    d, page, n = 128, 64, 900
+    cache, table, _ = build_cache([n], 1, d, page, 70)
+    sc = cache[..., 16 * d:].view(torch.bfloat16).view(*cache.shape[:3], 2, 16, 2, 2)
+    keys, vals, size = [], [], []
+    for j in range(n):
+        slot = int(table[0, j // page]) * page + j % page
+        v = sc[slot // page, :, slot % page // 16, 1, j % 16]
+        v *= 2.0 ** powers[(j * 7 + j // 128) % len(powers)]
+        s = scales_of(cache, page, slot)
+        nk, nv = numbers_of(cache, page, slot)
+        keys.append(dec.dequantise(nk, s[0, :, :, 0], s[0, :, :, 1]))
+        vals.append(dec.dequantise(nv, s[1, :, :, 0], s[1, :, :, 1]))
+        size.append(np.repeat(8 * np.abs(s[1, :, :, 0]) + np.abs(s[1, :, :, 1]), 64, -1))
+    keys, vals, size = (np.array(t).reshape(n, 1, d) for t in (keys, vals, size))
+    pos, seen = serve.tree(random_parents(T, 71), n - T)
+    q = randn(72, T, Hq, d, dtype=torch.bfloat16)
+    o, lse = swa.kv4_tree_attention(cache.to(dev()), q.to(dev()), table.to(dev()), i32(n), i32(0, T), i32(*pos),
+                                    torch.tensor(np.array(seen, dtype=np.uint64).view(np.int64), device=dev()), max_new=T)
+    ro, rl = serve.tree_attend(f64(q), keys, vals, pos, seen)
+    so = serve.tree_attend(f64(q), keys, size, pos, seen)[0]          # what a row's terms sum to
+    assert np.all(np.abs(f64(lse) - rl) <= 1e-4)
+    # P: 2^-8 up to 16 rows, 2^-11 above; a value: exact up to 16 rows, half a step of 2^-11 of four times a key's size
+    # above (times size, which is at least a quarter of that); logits 2 * 8e-5
+    each = 2.0 ** -8 if Hq * T <= 16 else 2.0 ** -11 + 2.0 ** -10
+    assert np.all(np.abs(f64(o) - ro) <= (1.7e-4 + each) * so + 2.0 ** -8 * np.abs(ro))
+
+
+@pytest.mark.parametrize("Hq,T", [(4, 16), (4, 3)])
+def test_tree_of_one_key_far_above_many(Hq, T):
+    # one key 25 powers of two above 20000 others, which together still count 6e-4: no P may be lost
+    d, page, n = 128, 64, 20000
+    per = -(-n // page)
+    cache = torch.zeros(per, 1, page // 16, 18 * d, dtype=torch.uint8)
+    cache[..., :16 * d] = 0x88                                           # n - 8 = 0 everywhere: keys and values are their centres
+    sc = cache[..., 16 * d:].view(torch.bfloat16).view(per, 1, page // 16, 2, 16, 2, 2)
+    sc[..., 0, :, :, 1], sc[..., 1, :, :, 1] = 0.0, 1.0
+    sc[0, 0, 0, 0, 5, :, 1], sc[0, 0, 0, 1, 5, :, 1] = 1.53125, 0.0      # logits 128 * 1.53 / sqrt(128) = 17.3 and 0
+    q = torch.ones(T, Hq, d, dtype=torch.bfloat16)
+    pos, seen = serve.tree(list(range(-1, T - 1)), n - T)
+    o, lse = swa.kv4_tree_attention(cache.to(dev()), q.to(dev()), torch.arange(per, dtype=torch.int32, device=dev())[None].contiguous(),
+                                    i32(n), i32(0, T), i32(*pos), torch.tensor(seen, device=dev()), max_new=T)
+    top = 1.53125 * 128 / np.sqrt(128) / np.sqrt(1 + 1e-6)
+    count = n - T + np.arange(1, T + 1) - 1.0                             # keys at 0 that a token sees
+    want = count * np.exp(-top) / (1 + count * np.exp(-top))
+    assert np.abs(f64(lse)[:, 0] - (top + np.log1p(count * np.exp(-top)))).max() <= 1e-4
+    # (the logit's 2.6e-6 of 17.3, o's rounding)
+    assert np.all(np.abs(f64(o) - want[:, None, None]) <= (2.0 ** -8 + 1e-3) * want[:, None, None])
