@@ -24,9 +24,9 @@
 //                         scales, cleaned: keys that are not there, or not finite, 0.
 //   values  4 warps       numbers to fp16, times step plus centre: 11 bits, as P has
 //                         (with 8 of each, in bf16, o was up to 2.5e-3 off where its own
-//                         rounding makes 1.7e-3). A key whose values are far from 1
-//                         (2^13 above, 2^12 below) has them brought there by a power of
-//                         two that P takes on and its sum takes off: see value_shift
+//                         rounding makes 1.7e-3). A key whose values are not about 1
+//                         has them brought there by a power of two that P takes on and
+//                         its sum takes off: see value_shift
 //   mma     2 threads      products of 16: nine of S a block, eight of O. One after the
 //                         other by one thread they were 17 times 90 to 100 clocks of issue
 //                         a block, beside the other warps' work; S and O have one each
@@ -128,11 +128,13 @@ __device__ __forceinline__ int value_size(uint32_t w) {
   const int es = w >> 7 & 255u, ez = w >> 23 & 255u;
   return max(es, ez) == 255 ? -1 : max(es > 0 ? es + 3 : 0, ez);
 }
-// Power of two e by which a key's values of size `top` are taken down (up below 0), so that they fit fp16: 0 for those
-// of 2^-12 to 2^13, and never below -85, so that P's sum, whose terms are P 2^-e, stays in fp32.
+// Power of two e by which a key's values of size `top` are taken down (up below 0). 0 for those of 2^-4 to 2^5, which
+// need none of it: with P beside them as little as 2^-29 of a row's largest, what is cut off P (2^-25) is below 2^-19 of
+// the row's sum there; values of all that fp16 holds, 2^-12 to 2^13, would make it 2^-3. Never below -85, so that P's sum,
+// whose terms are P 2^-e, stays in fp32. (Keys whose values lie 2^120 apart leave it.)
 __device__ __forceinline__ int value_shift(int top) {
   const int e = top - 127;
-  return top <= 0 ? 0 : (e > 12 ? e - 12 : (e < -12 ? max(e + 12, -85) : 0));
+  return top <= 0 ? 0 : (e > 4 ? e - 4 : (e < -4 ? max(e + 4, -85) : 0));
 }
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
@@ -306,15 +308,22 @@ __global__ void __launch_bounds__(TtShape<NR>::warps * 32, 1) tree_tc_kernel(con
         ffma2(x[i + 2], x[i + 3], x[i + 2], x[i + 3], f, f, m.z, m.w);
       }
       const bool edge = key0 < all_lo || key0 + kTtKeys > req.ctx;        // of the block
-      if (edge || (kflag & ~3u)) {        // off, or values of another size, whose power of two P takes on
-        const int d = key - req.ctx;
-        const float shift = static_cast<float>(static_cast<int>(kflag) >> 8);
+      // (one branch for both that are seldom: with one of their own for the shifts 178 us for 173)
+      if (edge || (kflag & ~3u)) {
+        if (kflag >> 8) {
+          const float shift = static_cast<float>(static_cast<int>(kflag) >> 8);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int4 w = *reinterpret_cast<const int4*>(rows + r0 + i);    // lo, pos, seen
-          const uint32_t word = static_cast<uint32_t>(d & 32 ? w.w : w.z);
-          const bool on = (d < 0 ? key >= w.x : (d < kTreeTokens) & static_cast<bool>(word >> (d & 31) & 1u)) & !(kflag & kKeyOff);
-          x[i] = on ? x[i] + shift : -INFINITY;
+          for (int i = 0; i < 32; i += 2) fadd2_acc(x[i], x[i + 1], shift, shift);
+        }
+        if (edge || (kflag & kKeyOff)) {
+          const int d = key - req.ctx;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int4 w = *reinterpret_cast<const int4*>(rows + r0 + i);    // lo, pos, seen
+            const uint32_t word = static_cast<uint32_t>(d & 32 ? w.w : w.z);
+            const bool on = (d < 0 ? key >= w.x : (d < kTreeTokens) & static_cast<bool>(word >> (d & 31) & 1u)) & !(kflag & kKeyOff);
+            if (!on) x[i] = -INFINITY;
+          }
         }
       }
       if (kflag & 3u) {                 // values that are not finite: the rows that see them say so at the end
