@@ -207,7 +207,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
 //        4 / RW - 1 groups of warps take other steps of two tiles.
 // Precision: q is two fp16 terms (22 bits: lse is an fp32 output; one term left it
 // 2e-4 off). P is one bf16 term in bf16 calls, whose o has 8 bits itself (as in the
-// training forward), and three in fp32 ones. The products with n - 8 are exact,
+// training forward; two take 153 us for 134, 16 requests of 32768 and one token),
+// and three in fp32 ones. The products with n - 8 are exact,
 // steps and centres multiply the sums in fp32.
 // ---------------------------------------------------------------------------
 struct TreeAttnArgs : AttnArgs {

@@ -35,8 +35,9 @@
 // and is raised only when P would pass 2^15, which the four warps of its 32 rows find
 // out together; then they rescale O in tensor memory themselves. So P leaves fp16 2^29
 // below that first maximum (what a million keys there would count is below o's own
-// rounding), and has 2^11 above it: logits of a standard deviation of 1 to 3 take 173
-// to 180 us, of 4 195 (from 2^8: 173 to 210, 231; from 2^2: 173 to 175, 184).
+// rounding), and has 2^11 above it: logits of a standard deviation of 0.9 and 2.3 take
+// 173 us, of 3.7 181, of 4.6 193, of 9.2 254 (from 2^8: 173 and 178, 210, 231, 279; from 2^2: 173, 175,
+// 184, 239). 183 where every key's values are shifted.
 // A key whose scales are not finite counts as 0 in the products, for a product would
 // bring a NaN to rows that do not see it: the rows that see it are made NaN at the
 // end (keys' scales: through S, per row).
