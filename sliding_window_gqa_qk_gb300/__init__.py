@@ -87,17 +87,24 @@ class _Int(ctypes.c_int):
         return value if isinstance(value, ctypes.c_int) else ctypes.c_int(_int32(value))
 
 
+_init = ctypes.Structure.__init__
+
+
 class _Struct(ctypes.Structure):
     def __init_subclass__(cls):
         cls._ints = {name: i for i, (name, kind) in enumerate(cls._fields_) if kind is ctypes.c_int}
+        cls._at = tuple(cls._ints.values())
 
     def __init__(self, *args, **kw):
-        n = len(args)
-        for name, i in self._ints.items():
-            value = args[i] if i < n else kw.get(name, 0)
-            if value > 0x7fffffff or value < -0x80000000:
-                _int32(value)
-        super().__init__(*args, **kw)
+        if kw or len(args) < len(self._fields_):
+            for name, i in self._ints.items():
+                _int32(args[i] if i < len(args) else kw.get(name, 0))
+            _init(self, *args, **kw)
+        else:                       # (in a hurry: the calls of a decode step make four of these)
+            for i in self._at:
+                if not -0x80000000 <= args[i] <= 0x7fffffff:
+                    _int32(args[i])
+            _init(self, *args)
 
 
 class swa_params(_Struct):
