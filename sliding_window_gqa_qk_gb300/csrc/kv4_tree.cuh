@@ -40,6 +40,7 @@ __device__ __forceinline__ TreeReq tree_req(const int32_t* cu, const int32_t* le
   const int end = cu[b + 1], len = lens[b];
   if (r.row0 < 0 || end < r.row0 || end > N) {
     r.bad = true;
+    r.row0 = 0;
     return r;
   }
   r.rows = end - r.row0;
@@ -402,18 +403,25 @@ template <int D, int kWarps>
 __device__ __forceinline__ void tree_zero(const TreeAttnArgs& a, const TreeReq& req, int b, int h, int G) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int used = b == a.B - 1 ? a.cu[a.B] : a.N;
-  auto zero = [&](int row0, int row1) {
+#pragma unroll 1
+  for (int k = 0; k < 3; ++k) {          // (one loop: instructions that few CTAs run are fetched by all)
+    int row0 = 0, row1 = 0;
+    if (k == 0 && req.bad) {
+      row0 = req.row0;
+      row1 = row0 + req.rows;
+    } else if (k == 1 && b == 0) {
+      row1 = req.row0;                   // (0 where cu is not plausible)
+    } else if (k == 2 && b == a.B - 1) {
+      row0 = a.cu[a.B];
+      row1 = row0 >= 0 ? a.N : row0;
+    }
     const float z[E] = {};
     for (long long i = wid; i < static_cast<long long>(row1 - row0) * G; i += kWarps) {
       const long long at = (row0 + i / G) * a.Hq + h * G + i % G;
       store_vec<E>(a.o + at * D + lane * E, z);
       if (lane == 0) a.lse[at] = -INFINITY;
     }
-  };
-  if (req.bad && req.rows > 0) zero(req.row0, req.row0 + req.rows);
-  if (b == 0) zero(0, tree_front(a.cu, a.N));
-  if (used >= 0 && used < a.N) zero(used, a.N);
+  }
 }
 
 // A row's sums o (relative to top, base 2), joined over the warps of a CTA by one
